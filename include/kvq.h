@@ -213,6 +213,97 @@ int kvq_append(kvq_handle* h, void* pool, int num_pool_pages,
                const int32_t* seq_idx, const int32_t* positions, int n,
                const int32_t* page_table, int batch, int max_pages, void* stream);
 
+/* ---- rotary positions ------------------------------------------------------
+ * A row's first rot_dim elements are rotated pair by pair, by its position:
+ *     a' = a cos - b sin,   b' = b cos + a sin
+ * with cos, sin of pair i at position p from a table that kvq_rope_table (or the
+ * caller) makes:  table[p][i] = cos, table[p][rot_dim / 2 + i] = sin.  Pair i is
+ *     KVQ_ROPE_HALF:         elements i and i + rot_dim / 2
+ *     KVQ_ROPE_INTERLEAVED:  elements 2i and 2i + 1
+ * and elements rot_dim .. 127 stay as they are.  The arithmetic is fixed: each
+ * product is rounded to fp32, then their difference or sum, then the result to
+ * bf16, so that kvq_rope and the appends below give the same bits. */
+#define KVQ_ROPE_HALF 0
+#define KVQ_ROPE_INTERLEAVED 1
+
+typedef struct kvq_rope_spec {
+  const float* table;    /* device fp32 [table_len][rot_dim], 16-byte aligned      */
+  int32_t table_len;     /* positions in [0, table_len) can be rotated             */
+  int32_t rot_dim;       /* even, 2 .. 128                                         */
+  int32_t style;         /* KVQ_ROPE_HALF or KVQ_ROPE_INTERLEAVED                  */
+} kvq_rope_spec;
+
+/* How the frequencies f_i = base^(-2i / rot_dim) (radians per position) are
+ * scaled for contexts longer than the trained one:
+ *   NONE    f_i
+ *   LINEAR  f_i / factor
+ *   NTK     the base becomes base * factor^(rot_dim / (rot_dim - 2)) (rot_dim >= 4)
+ *   YARN    f_i (1 - r) + f_i / factor r, r = (i - first) / (last - first) in [0, 1],
+ *           first / last the pairs that make high_turns / low_turns turns in
+ *           orig_len positions (rounded outwards, clamped to [0, rot_dim - 1])
+ *   BANDED  f_i s + f_i / factor (1 - s), s = (t_i - low_turns) / (high_turns -
+ *           low_turns) in [0, 1], t_i the turns pair i makes in orig_len positions */
+#define KVQ_ROPE_SCALE_NONE 0
+#define KVQ_ROPE_SCALE_LINEAR 1
+#define KVQ_ROPE_SCALE_NTK 2
+#define KVQ_ROPE_SCALE_YARN 3
+#define KVQ_ROPE_SCALE_BANDED 4
+
+typedef struct kvq_rope_scaling {
+  double base;           /* > 1                                                    */
+  double factor;         /* >= 1 (unused by NONE)                                  */
+  double orig_len;       /* YARN, BANDED: trained context, >= 1                    */
+  double low_turns;      /* YARN, BANDED: > 0 (usually 1)                          */
+  double high_turns;     /* YARN, BANDED: > low_turns (usually 32 and 4)           */
+  double amplitude;      /* factor on cos and sin; 0: 0.1 ln(factor) + 1 for YARN,
+                            1 for the others                                       */
+  int32_t kind;          /* KVQ_ROPE_SCALE_*                                       */
+} kvq_rope_scaling;
+
+/* Write the table of positions 0 .. table_len - 1: device fp32
+ * [table_len][rot_dim], 16-byte aligned.  The angle is reduced exactly (a 64-bit
+ * fraction of a turn), so far positions are as accurate as near ones.  Needs no
+ * handle: runs on the current device. */
+int kvq_rope_table(float* table, int table_len, int rot_dim, const kvq_rope_scaling* scaling,
+                   void* stream);
+
+/* Rotate n rows of `heads` heads: y[i][h] = rotation of x[i][h] by positions[i].
+ *   x, y      : device bf16, row i at x + i * x_stride (elements), heads adjacent
+ *               (128 elements each).  16-byte aligned, strides multiples of 8 and
+ *               >= heads * 128, so that x may be a slice of a fused projection.
+ *               y == x (with the same stride) rotates in place; otherwise they
+ *               must not overlap.
+ *   positions : device int32 [n]; a position outside [0, table_len) sets
+ *               KVQ_STATUS_BAD_POS and leaves the row of y as it was.
+ *   inverse   : nonzero rotates by minus the angle.  That is the transposed map:
+ *               the gradient of x from that of y.
+ * 1 <= heads <= 1024.  n == 0 is a no-op. */
+int kvq_rope(kvq_handle* h, const uint16_t* x, long long x_stride, uint16_t* y, long long y_stride,
+             int heads, const int32_t* positions, int n, const kvq_rope_spec* rope, int inverse,
+             void* stream);
+
+/* ---- append with rotary positions ----------------------------------------------
+ * kvq_append / kvq_bf16_append of keys that still lack their position: equal, byte
+ * for byte, to kvq_rope of K and then that append, without a pass over HBM for the
+ * rotated keys.  Values are not rotated.
+ *   K, V      : device bf16, token i at K + i * k_stride (elements), KV heads
+ *               adjacent; alignment and strides as for kvq_rope.
+ *   positions : the tokens' places in the cache, and their angles unless
+ *   rope_positions (device int32 [n], may be NULL) gives other ones.
+ * A rotation position outside the table sets KVQ_STATUS_BAD_POS and the token is
+ * skipped (key and value).  Other arguments, errors and status bits as for
+ * kvq_append. */
+int kvq_append_rope(kvq_handle* h, void* pool, int num_pool_pages, const uint16_t* K,
+                    long long k_stride, const uint16_t* V, long long v_stride,
+                    const int32_t* seq_idx, const int32_t* positions, int n,
+                    const int32_t* page_table, int batch, int max_pages,
+                    const kvq_rope_spec* rope, const int32_t* rope_positions, void* stream);
+int kvq_bf16_append_rope(kvq_handle* h, void* pool, int num_pool_pages, const uint16_t* K,
+                         long long k_stride, const uint16_t* V, long long v_stride,
+                         const int32_t* seq_idx, const int32_t* positions, int n,
+                         const int32_t* page_table, int batch, int max_pages,
+                         const kvq_rope_spec* rope, const int32_t* rope_positions, void* stream);
+
 /* ---- decode attention ----------------------------------------------------
  * Bytes of workspace kvq_decode needs for `batch` sequences and `num_splits`
  * splits (num_splits == 0: the automatic choice for that batch).  The

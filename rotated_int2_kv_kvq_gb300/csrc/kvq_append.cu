@@ -65,7 +65,9 @@ struct AppendSmem {
   static constexpr int kSZ = kMu + kDim * 4;                    // u32 [kTile]
   static constexpr int kRec = kSZ + kTile * 4;                  // long long [kTile]
   static constexpr int kBar = kRec + kTile * 8;                 // mbarrier
-  static constexpr int kBytes = kBar + 16;
+  static constexpr int kAng = kBar + 16;                        // int [kTile] (ROPE)
+  static constexpr int kBytes = kAng;
+  static constexpr int kBytesRope = kAng + kTile * 4;
 };
 
 __device__ __forceinline__ float bf16_to_f32(uint32_t bits16) {
@@ -75,7 +77,13 @@ __device__ __forceinline__ float bf16_to_f32(uint32_t bits16) {
 // Quantise tiles of tokens for one (KV head, K|V).  TPW = tokens per warp.
 // Warp w owns tokens [w*TPW, (w+1)*TPW) of a tile; lane L owns output elements
 // 4L..4L+3 of each of them.
-template <int TPW, int NW>
+//
+// ROPE: keys are first rotated by their position (rope_pair, rounded to bf16 as
+// the rotated key that kvq_rope writes), in the staged tile between its load and
+// the centring: 64 pairs per token beside the 16,384 products of the rotation
+// into the cache's basis, so it is not worth a pass of its own over HBM.  K and
+// V rows may be strided (slices of a fused projection).
+template <int TPW, int NW, bool ROPE>
 __global__ void __launch_bounds__(NW * 32) append_int2_kernel(AppendArgs a) {
   constexpr int kAppThreads = NW * 32;
   using S = AppendSmem<TPW, NW>;
@@ -88,6 +96,7 @@ __global__ void __launch_bounds__(NW * 32) append_int2_kernel(AppendArgs a) {
   uint32_t* sz = reinterpret_cast<uint32_t*>(smem + S::kSZ);
   long long* rec = reinterpret_cast<long long*>(smem + S::kRec);
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + S::kBar);
+  int* ang = reinterpret_cast<int*>(smem + S::kAng);   // ROPE: the rotation's position, or -1
 
   const int kv = blockIdx.y;
   const int which = blockIdx.z;            // 0 keys, 1 values
@@ -95,6 +104,8 @@ __global__ void __launch_bounds__(NW * 32) append_int2_kernel(AppendArgs a) {
   const float* R = a.R + (static_cast<size_t>(which) * a.Hkv + kv) * kDim * kDim;
   const float* mu = which ? nullptr : a.mu + static_cast<size_t>(kv) * kDim;
   const uint16_t* X = which ? a.V : a.K;
+  const size_t row = ROPE ? static_cast<size_t>(which ? a.v_stride : a.k_stride)
+                          : static_cast<size_t>(a.Hkv) * kDim;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // A following decode call's query preparation reads neither the pool nor
   // this kernel's inputs: let it start now (it waits for this grid before it
@@ -129,7 +140,7 @@ __global__ void __launch_bounds__(NW * 32) append_int2_kernel(AppendArgs a) {
       const int tok = t0 + k;
       pre[r] = make_uint4(0u, 0u, 0u, 0u);
       if (idx < kPieces && tok < a.n)
-        pre[r] = *reinterpret_cast<const uint4*>(X + (static_cast<size_t>(tok) * a.Hkv + kv) * kDim +
+        pre[r] = *reinterpret_cast<const uint4*>(X + static_cast<size_t>(tok) * row + kv * kDim +
                                                  ch * 8);
     }
   };
@@ -156,6 +167,17 @@ __global__ void __launch_bounds__(NW * 32) append_int2_kernel(AppendArgs a) {
             r = ((static_cast<long long>(page) * a.Hkv + kv) * kInt2Rec) * kPage + (p % kPage);
           }
         }
+        if constexpr (ROPE) {
+          const int w = a.rope_positions ? a.rope_positions[tok] : p;
+          const bool in = w >= 0 && w < a.rope.table_len;
+          if (!in) {
+            atomicOr(a.status, KVQ_STATUS_BAD_POS);
+            r = -1;
+          }
+          ang[tid] = in ? w : -1;
+        }
+      } else if constexpr (ROPE) {
+        ang[tid] = -1;
       }
       rec[tid] = r;      // record byte offset * 16 + slot
     }
@@ -177,10 +199,29 @@ __global__ void __launch_bounds__(NW * 32) append_int2_kernel(AppendArgs a) {
           const float4 m1 = *reinterpret_cast<const float4*>(mus + ch * 8 + 4);
           const float mv[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = __fsub_rn(v[e], mv[e]);
+          for (int e = 0; e < 8; ++e)
+            if (!ROPE || ch * 8 + e >= a.rope.rot_dim) v[e] = __fsub_rn(v[e], mv[e]);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) Cs[(ch * 8 + e) * kTile + k] = v[e];
+      }
+    }
+    if constexpr (ROPE) {
+      if (which == 0) {
+        __syncthreads();
+        const int half = a.rope.rot_dim >> 1;
+        for (int idx = tid; idx < half * kTile; idx += kAppThreads) {
+          const int k = idx % kTile, i = idx / kTile;
+          const int w = ang[k];
+          if (w < 0) continue;
+          const float* t = a.rope.table + static_cast<size_t>(w) * a.rope.rot_dim + i;
+          const bool inter = a.rope.style == KVQ_ROPE_INTERLEAVED;
+          const int d0 = inter ? 2 * i : i, d1 = inter ? 2 * i + 1 : i + half;
+          float p, q;
+          rope_pair(Cs[d0 * kTile + k], Cs[d1 * kTile + k], t[0], t[half], p, q);
+          Cs[d0 * kTile + k] = __fsub_rn(__bfloat162float(__float2bfloat16_rn(p)), mus[d0]);
+          Cs[d1 * kTile + k] = __fsub_rn(__bfloat162float(__float2bfloat16_rn(q)), mus[d1]);
+        }
       }
     }
     if (!r_ready) {
@@ -379,15 +420,16 @@ __global__ void __launch_bounds__(128) append_bf16_kernel(AppendArgs a) {
   }
 }
 
-template <int TPW, int NW>
+template <int TPW, int NW, bool ROPE>
 cudaError_t launch_tpw(const AppendArgs& a, int num_sms, cudaStream_t st) {
   using S = AppendSmem<TPW, NW>;
   static bool attr_set[64] = {};       // per device: the attribute is per context
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(append_int2_kernel<TPW, NW>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+    cudaError_t e = cudaFuncSetAttribute(append_int2_kernel<TPW, NW, ROPE>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         ROPE ? S::kBytesRope : S::kBytes);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
@@ -401,7 +443,8 @@ cudaError_t launch_tpw(const AppendArgs& a, int num_sms, cudaStream_t st) {
   if (gx > tiles) gx = tiles;
   if (gx < 1) gx = 1;
   dim3 grid(gx, a.Hkv, 2);
-  append_int2_kernel<TPW, NW><<<grid, NW * 32, S::kBytes, st>>>(a);
+  append_int2_kernel<TPW, NW, ROPE>
+      <<<grid, NW * 32, ROPE ? S::kBytesRope : S::kBytes, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -411,8 +454,13 @@ cudaError_t launch_append_int2(const AppendArgs& a, int num_sms, cudaStream_t st
   // Few tokens (decode-time appends): one token per warp keeps the dependent
   // fmaf chains short in wall time.  Many tokens (prefill): eight tokens per
   // warp reuse each staged rotation row eight times.
-  if (a.n <= 8 * num_sms / (a.Hkv > 0 ? a.Hkv : 1)) return launch_tpw<1, 8>(a, num_sms, st);
-  return launch_tpw<8, 8>(a, num_sms, st);
+  if (a.n <= 8 * num_sms / (a.Hkv > 0 ? a.Hkv : 1)) return launch_tpw<1, 8, false>(a, num_sms, st);
+  return launch_tpw<8, 8, false>(a, num_sms, st);
+}
+
+cudaError_t launch_append_int2_rope(const AppendArgs& a, int num_sms, cudaStream_t st) {
+  if (a.n <= 8 * num_sms / (a.Hkv > 0 ? a.Hkv : 1)) return launch_tpw<1, 8, true>(a, num_sms, st);
+  return launch_tpw<8, 8, true>(a, num_sms, st);
 }
 
 cudaError_t launch_append_bf16(const AppendArgs& a, cudaStream_t st) {

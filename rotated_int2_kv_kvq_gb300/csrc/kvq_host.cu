@@ -314,10 +314,48 @@ int decode_common(kvq_handle* h, bool int2, const void* pool, int num_pool_pages
   return cuda_rc(kvq::launch_combine(a, st));
 }
 
+// A caller's rotary-position table as the kernels take it, or false.
+bool rope_ok(const kvq_rope_spec* r, kvq::RopeArgs* out) {
+  if (!r || !r->table || r->table_len < 1) return false;
+  if (r->rot_dim < 2 || r->rot_dim > kDim || r->rot_dim % 2 != 0) return false;
+  if (r->style != KVQ_ROPE_HALF && r->style != KVQ_ROPE_INTERLEAVED) return false;
+  if (reinterpret_cast<uintptr_t>(r->table) % 16 != 0) return false;
+  out->table = r->table;
+  out->table_len = r->table_len;
+  out->rot_dim = r->rot_dim;
+  out->style = r->style;
+  return true;
+}
+
+// Rows of `heads` x 128 bf16 elements, `stride` elements apart, read and
+// written in 16-byte pieces.
+bool rows_ok(const void* p, long long stride, int heads) {
+  return p && reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0 &&
+         stride >= static_cast<long long>(heads) * kDim;
+}
+
+// The strided, rotating form of an append (absent for the plain appends).
+struct RopeAppend {
+  const kvq_rope_spec* spec = nullptr;
+  const int32_t* positions = nullptr;
+  long long k_stride = 0, v_stride = 0;
+};
+
 int append_common(kvq_handle* h, bool int2, void* pool, int num_pool_pages, const uint16_t* K,
                   const uint16_t* V, const int32_t* seq_idx, const int32_t* positions, int n,
-                  const int32_t* page_table, int batch, int max_pages, void* stream) {
+                  const int32_t* page_table, int batch, int max_pages, void* stream,
+                  const RopeAppend* rope = nullptr) {
   if (!h || n < 0) return KVQ_EINVAL;
+  kvq::AppendArgs a;
+  if (rope) {
+    if (!rope_ok(rope->spec, &a.rope)) return KVQ_EINVAL;
+    if (n > 0 && (!rows_ok(K, rope->k_stride, h->L.num_kv_heads) ||
+                  !rows_ok(V, rope->v_stride, h->L.num_kv_heads)))
+      return KVQ_EINVAL;
+    a.rope_positions = rope->positions;
+    a.k_stride = rope->k_stride;
+    a.v_stride = rope->v_stride;
+  }
   if (n == 0) return KVQ_OK;
   if (!pool || !K || !V || !seq_idx || !positions || !page_table) return KVQ_EINVAL;
   if (num_pool_pages < 1 || batch < 1 || max_pages < 1) return KVQ_EINVAL;
@@ -327,7 +365,6 @@ int append_common(kvq_handle* h, bool int2, void* pool, int num_pool_pages, cons
   if (int2 && !h->ready) return KVQ_ENOTREADY;
   kvq::DeviceGuard dev_guard(h->device);
   if (!dev_guard.ok()) return KVQ_ECUDA;
-  kvq::AppendArgs a;
   a.pool = static_cast<uint8_t*>(pool);
   a.num_pool_pages = num_pool_pages;
   a.K = K;
@@ -344,9 +381,60 @@ int append_common(kvq_handle* h, bool int2, void* pool, int num_pool_pages, cons
   a.clip_k = h->L.clip_k;
   a.clip_v = h->L.clip_v;
   a.status = h->status;
+  if (rope)
+    return cuda_rc(int2 ? kvq::launch_append_int2_rope(a, h->num_sms, S(stream))
+                        : kvq::launch_append_bf16_rope(a, h->num_sms, S(stream)));
   cudaError_t e = int2 ? kvq::launch_append_int2(a, h->num_sms, S(stream))
                        : kvq::launch_append_bf16(a, S(stream));
   return cuda_rc(e);
+}
+
+// Each pair's turns per position as a 64-bit fraction, from the base and the
+// scaling (include/kvq.h); false for parameters outside their ranges.
+bool rope_turns(int rot_dim, const kvq_rope_scaling* sc, uint64_t* turns, float* amplitude) {
+  const double kTwoPi = 6.283185307179586476925286766559;
+  if (rot_dim < 2 || rot_dim > kDim || rot_dim % 2 != 0) return false;
+  // comparisons that NaN fails
+  if (!(sc->base > 1.0) || !(sc->base < 1e30)) return false;
+  if (sc->kind < KVQ_ROPE_SCALE_NONE || sc->kind > KVQ_ROPE_SCALE_BANDED) return false;
+  if (!(sc->amplitude >= 0.0) || !(sc->amplitude < 1e6)) return false;
+  const bool scaled = sc->kind != KVQ_ROPE_SCALE_NONE;
+  if (scaled && (!(sc->factor >= 1.0) || !(sc->factor < 1e6))) return false;
+  if (sc->kind == KVQ_ROPE_SCALE_NTK && rot_dim < 4) return false;
+  const bool by_turns = sc->kind == KVQ_ROPE_SCALE_YARN || sc->kind == KVQ_ROPE_SCALE_BANDED;
+  if (by_turns && (!(sc->orig_len >= 1.0) || !(sc->orig_len < 1e9) || !(sc->low_turns > 0.0) ||
+                   !(sc->high_turns > sc->low_turns) || !(sc->high_turns < 1e9)))
+    return false;
+  const double rot = rot_dim;
+  double base = sc->base;
+  if (sc->kind == KVQ_ROPE_SCALE_NTK) base *= pow(sc->factor, rot / (rot - 2.0));
+  double first = 0.0, last = 0.0;       // the pairs between which YARN blends
+  if (sc->kind == KVQ_ROPE_SCALE_YARN) {
+    const double den = 2.0 * log(base);
+    first = floor(rot * log(sc->orig_len / (sc->high_turns * kTwoPi)) / den);
+    last = ceil(rot * log(sc->orig_len / (sc->low_turns * kTwoPi)) / den);
+    if (first < 0.0) first = 0.0;
+    if (last > rot - 1.0) last = rot - 1.0;
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double inv = pow(base, -2.0 * i / rot);
+    if (sc->kind == KVQ_ROPE_SCALE_LINEAR) {
+      inv /= sc->factor;
+    } else if (sc->kind == KVQ_ROPE_SCALE_YARN) {
+      double ramp = (i - first) / fmax(last - first, 1e-3);
+      ramp = fmin(fmax(ramp, 0.0), 1.0);
+      inv = inv / sc->factor * ramp + inv * (1.0 - ramp);
+    } else if (sc->kind == KVQ_ROPE_SCALE_BANDED) {
+      double smooth = (sc->orig_len * inv / kTwoPi - sc->low_turns) / (sc->high_turns - sc->low_turns);
+      smooth = fmin(fmax(smooth, 0.0), 1.0);
+      inv = (1.0 - smooth) * inv / sc->factor + smooth * inv;
+    }
+    turns[i] = static_cast<uint64_t>(inv / kTwoPi * 18446744073709551616.0);   // inv <= 1: below a turn
+  }
+  double amp = sc->amplitude;
+  if (amp == 0.0) amp = sc->kind == KVQ_ROPE_SCALE_YARN ? 0.1 * log(sc->factor) + 1.0 : 1.0;
+  *amplitude = static_cast<float>(amp);
+  return true;
 }
 
 }  // namespace
@@ -458,6 +546,52 @@ int kvq_bf16_append(kvq_handle* h, void* pool, int num_pool_pages, const uint16_
                     const int32_t* page_table, int batch, int max_pages, void* stream) {
   return append_common(h, false, pool, num_pool_pages, K, V, seq_idx, positions, n, page_table,
                        batch, max_pages, stream);
+}
+
+int kvq_rope_table(float* table, int table_len, int rot_dim, const kvq_rope_scaling* scaling,
+                   void* stream) {
+  if (!table || !scaling || table_len < 1 || reinterpret_cast<uintptr_t>(table) % 16 != 0)
+    return KVQ_EINVAL;
+  uint64_t turns[kDim / 2] = {};
+  float amplitude = 1.0f;
+  if (!rope_turns(rot_dim, scaling, turns, &amplitude)) return KVQ_EINVAL;
+  return cuda_rc(kvq::launch_rope_table(table, table_len, rot_dim, turns, amplitude, S(stream)));
+}
+
+int kvq_rope(kvq_handle* h, const uint16_t* x, long long x_stride, uint16_t* y, long long y_stride,
+             int heads, const int32_t* positions, int n, const kvq_rope_spec* rope, int inverse,
+             void* stream) {
+  if (!h || n < 0 || heads < 1 || heads > 1024) return KVQ_EINVAL;
+  kvq::RopeArgs r;
+  if (!rope_ok(rope, &r)) return KVQ_EINVAL;
+  if (n == 0) return KVQ_OK;
+  if (!positions || !rows_ok(x, x_stride, heads) || !rows_ok(y, y_stride, heads))
+    return KVQ_EINVAL;
+  if (x == y && x_stride != y_stride) return KVQ_EINVAL;
+  kvq::DeviceGuard dev_guard(h->device);
+  if (!dev_guard.ok()) return KVQ_ECUDA;
+  return cuda_rc(kvq::launch_rope(x, x_stride, y, y_stride, heads, positions, n, r, inverse != 0,
+                                  h->status, S(stream)));
+}
+
+int kvq_append_rope(kvq_handle* h, void* pool, int num_pool_pages, const uint16_t* K,
+                    long long k_stride, const uint16_t* V, long long v_stride,
+                    const int32_t* seq_idx, const int32_t* positions, int n,
+                    const int32_t* page_table, int batch, int max_pages,
+                    const kvq_rope_spec* rope, const int32_t* rope_positions, void* stream) {
+  const RopeAppend ra{rope, rope_positions, k_stride, v_stride};
+  return append_common(h, true, pool, num_pool_pages, K, V, seq_idx, positions, n, page_table,
+                       batch, max_pages, stream, &ra);
+}
+
+int kvq_bf16_append_rope(kvq_handle* h, void* pool, int num_pool_pages, const uint16_t* K,
+                         long long k_stride, const uint16_t* V, long long v_stride,
+                         const int32_t* seq_idx, const int32_t* positions, int n,
+                         const int32_t* page_table, int batch, int max_pages,
+                         const kvq_rope_spec* rope, const int32_t* rope_positions, void* stream) {
+  const RopeAppend ra{rope, rope_positions, k_stride, v_stride};
+  return append_common(h, false, pool, num_pool_pages, K, V, seq_idx, positions, n, page_table,
+                       batch, max_pages, stream, &ra);
 }
 
 size_t kvq_workspace_bytes(const kvq_handle* h, int batch, int num_splits) {

@@ -74,6 +74,14 @@ struct DecodeArgs {
   const int32_t* bf16_page_table;   // [B][max_pages]
 };
 
+// The rotary-position table of a call (kvq_rope_spec, checked on the host).
+struct RopeArgs {
+  const float* table = nullptr;   // [table_len][rot_dim]: cos, then sin
+  int table_len = 0;
+  int rot_dim = 0;
+  int style = 0;                  // KVQ_ROPE_HALF or KVQ_ROPE_INTERLEAVED
+};
+
 struct AppendArgs {
   uint8_t* pool;
   int num_pool_pages;
@@ -88,6 +96,10 @@ struct AppendArgs {
   const float* mu;           // [Hkv][D]
   float clip_k, clip_v;
   uint32_t* status;
+  // kvq_append_rope and kvq_bf16_append_rope only
+  RopeArgs rope;
+  const int32_t* rope_positions = nullptr;   // the rotation's positions; nullptr: positions
+  long long k_stride = 0, v_stride = 0;      // elements from one token to the next
 };
 
 // The append half of kvq_append_decode: one new token per sequence.
@@ -110,6 +122,13 @@ struct StepArgs {
 // ---- launchers (defined in the .cu files) --------------------------------
 cudaError_t launch_append_int2(const AppendArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_append_bf16(const AppendArgs& a, cudaStream_t st);
+cudaError_t launch_append_int2_rope(const AppendArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_append_bf16_rope(const AppendArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_rope(const uint16_t* x, long long x_stride, uint16_t* y, long long y_stride,
+                        int heads, const int32_t* positions, int n, const RopeArgs& r, bool inverse,
+                        uint32_t* status, cudaStream_t st);
+cudaError_t launch_rope_table(float* table, int table_len, int rot_dim, const uint64_t* turns,
+                              float amplitude, cudaStream_t st);
 cudaError_t launch_qprep(const DecodeArgs& a, const float* RK, const float* mu, float sm_scale,
                          cudaStream_t st);
 cudaError_t launch_step_prep(const DecodeArgs& a, const StepArgs& sa, cudaStream_t st);
@@ -283,6 +302,14 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// One pair of a rotation by the angle with cosine c and sine s: every product
+// is rounded to fp32, then their difference or sum, so that the result is the
+// same wherever it is computed (no contraction to fused multiply-adds).
+__device__ __forceinline__ void rope_pair(float a, float b, float c, float s, float& p, float& q) {
+  p = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  q = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
 }
 
 // 2^x via the SFU (ex2.approx.ftz): 2^-inf = 0, 2^0 = 1.

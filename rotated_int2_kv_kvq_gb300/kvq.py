@@ -23,11 +23,15 @@ KVQ_STATUS_BAD_SEQ = 8
 KVQ_STATUS_TIMEOUT = 16
 KVQ_OUT_ROTATED = 1
 KVQ_Q_ROTATED = 2
+KVQ_ROPE_HALF, KVQ_ROPE_INTERLEAVED = 0, 1
+(KVQ_ROPE_SCALE_NONE, KVQ_ROPE_SCALE_LINEAR, KVQ_ROPE_SCALE_NTK, KVQ_ROPE_SCALE_YARN,
+ KVQ_ROPE_SCALE_BANDED) = range(5)
 INT2_RECORD_BYTES = 1152
 BF16_RECORD_BYTES = 8192
 
 # Every entry point of include/kvq.h, with its ctypes signature.
 _P, _I, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+_LL = ctypes.c_longlong
 SIGNATURES = {
     "kvq_create": ([_P, _P], _I),
     "kvq_destroy": ([_P], _I),
@@ -52,6 +56,11 @@ SIGNATURES = {
                            _P], _I),
     "kvq_append_decode_window": ([_P, _P, _I, _P, _I, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _P,
                                   _P, _SZ, _I, _P], _I),
+    "kvq_rope_table": ([_P, _I, _I, _P, _P], _I),
+    "kvq_rope": ([_P, _P, _LL, _P, _LL, _I, _P, _I, _P, _I, _P], _I),
+    "kvq_append_rope": ([_P, _P, _I, _P, _LL, _P, _LL, _P, _P, _I, _P, _I, _I, _P, _P, _P], _I),
+    "kvq_bf16_append_rope": ([_P, _P, _I, _P, _LL, _P, _LL, _P, _P, _I, _P, _I, _I, _P, _P, _P],
+                             _I),
     "kvq_get_status": ([_P, _P, _P], _I),
     "kvq_selftest_wait_timeout": ([_P, _I, _P], _I),
     "kvq_auto_splits": ([_P, _I, _I], _I),
@@ -67,6 +76,18 @@ class KvqLayout(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("clip_k", ctypes.c_float),
                 ("clip_v", ctypes.c_float), ("sm_scale", ctypes.c_float),
                 ("flags", ctypes.c_uint32)]
+
+
+class KvqRopeSpec(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("table_len", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("style", ctypes.c_int32)]
+
+
+class KvqRopeScaling(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("orig_len", ctypes.c_double), ("low_turns", ctypes.c_double),
+                ("high_turns", ctypes.c_double), ("amplitude", ctypes.c_double),
+                ("kind", ctypes.c_int32)]
 
 
 class KvqError(RuntimeError):
@@ -161,7 +182,9 @@ def make_layout(num_heads, num_kv_heads, clip_k=0.96, clip_v=0.92, sm_scale=0.0,
 def kvq_create(layout: KvqLayout) -> Handle:
     out = ctypes.c_void_p()
     _check("kvq_create", load_library().kvq_create(ctypes.byref(layout), ctypes.byref(out)))
-    return Handle(out.value, layout)
+    h = Handle(out.value, layout)
+    h.device = torch.cuda.current_device()
+    return h
 
 
 def kvq_destroy(h: Handle) -> None:
@@ -294,6 +317,137 @@ def kvq_append_decode_window(h, pool, num_pool_pages, bf16_pool, bf16_num_pool_p
         _ptr(page_table, _I32, "page_table"), max_pages, _ptr(seq_lens, _I32, "seq_lens"), batch,
         int(sink), int(recent), _ptr(out, _F32, "out"), _ptr(workspace, _U8, "workspace"),
         int(workspace.numel()), int(num_splits), _stream(stream)))
+
+
+# ---- rotary positions ---------------------------------------------------------
+
+_ROPE_STYLES = {"half": KVQ_ROPE_HALF, "interleaved": KVQ_ROPE_INTERLEAVED}
+_ROPE_KINDS = {"none": KVQ_ROPE_SCALE_NONE, "linear": KVQ_ROPE_SCALE_LINEAR,
+               "ntk": KVQ_ROPE_SCALE_NTK, "yarn": KVQ_ROPE_SCALE_YARN,
+               "banded": KVQ_ROPE_SCALE_BANDED}
+
+
+def make_rope_scaling(kind="none", base=10000.0, factor=1.0, orig_len=0.0, low_turns=1.0,
+                      high_turns=None, amplitude=0.0) -> KvqRopeScaling:
+    """Frequencies of a table (kvq_rope_scaling).  high_turns defaults to 32 (yarn), 4 (banded)."""
+    if high_turns is None:
+        high_turns = 32.0 if kind == "yarn" else 4.0
+    return KvqRopeScaling(float(base), float(factor), float(orig_len), float(low_turns),
+                          float(high_turns), float(amplitude), _ROPE_KINDS[kind])
+
+
+class Rope:
+    """A rotary-position table and how its pairs lie in a head; keeps the table alive."""
+
+    def __init__(self, table: torch.Tensor, style: str):
+        if table.dim() != 2:
+            raise ValueError("table must be [table_len, rot_dim]")
+        self.table, self.style = table, style
+        self.spec = KvqRopeSpec(_ptr(table, _F32, "table"), int(table.shape[0]),
+                                int(table.shape[1]), _ROPE_STYLES[style])
+
+
+def make_rope(table: torch.Tensor, style: str = "half") -> Rope:
+    """table: fp32 [table_len, rot_dim] (kvq_rope_table); style: "half" or "interleaved"."""
+    return Rope(table, style)
+
+
+def kvq_rope_table(table: torch.Tensor, scaling: KvqRopeScaling, stream=None) -> None:
+    """Fill table (fp32 [table_len, rot_dim]) with cos and sin of every position."""
+    if table.dim() != 2:
+        raise ValueError("table must be [table_len, rot_dim]")
+    with torch.cuda.device(table.device):
+        _check("kvq_rope_table", load_library().kvq_rope_table(
+            _ptr(table, _F32, "table"), int(table.shape[0]), int(table.shape[1]),
+            ctypes.byref(scaling), _stream(stream)))
+
+
+def _rows(t, name, heads=None):
+    """Device pointer and token stride of bf16 rows [n, heads, 128]; only the tokens may be strided."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    if t.dtype not in _BF16:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {_BF16}")
+    if t.dim() != 3 or t.shape[2] != 128 or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name}: expected [n, {heads or 'heads'}, 128], got {tuple(t.shape)}")
+    n, hh = int(t.shape[0]), int(t.shape[1])
+    if n and (t.stride(2) != 1 or (hh > 1 and t.stride(1) != 128)):
+        raise ValueError(f"{name}: the heads of a token must be adjacent and contiguous")
+    return ctypes.c_void_p(t.data_ptr()), int(t.stride(0)) if n > 1 else hh * 128
+
+
+def _same_device(h, *named):
+    """The CUDA device of the handle and of every tensor (entries may be None)."""
+    for name, t in named:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name}: expected a CUDA tensor")
+        if t.device.index != h.device:
+            raise ValueError(f"{name} is on {t.device}, the handle on cuda:{h.device}")
+    return torch.device("cuda", h.device)
+
+
+def _stream_of(stream, device):
+    """`stream`, or the current stream of the device the tensors are on."""
+    if stream is None:
+        return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    return _stream(stream)
+
+
+def _vec(t, n, name):
+    if t.dim() != 1 or int(t.shape[0]) != n:
+        raise ValueError(f"{name}: expected [{n}], got {tuple(t.shape)}")
+    return _ptr(t, _I32, name)
+
+
+def kvq_rope(h, x, y, positions, rope: Rope, inverse=False, stream=None):
+    """y = x rotated by positions; x, y: bf16 [n, heads, 128] (tokens may be strided), y may be x;
+    positions: int32 [n]."""
+    n, heads = int(x.shape[0]), int(x.shape[1])
+    if tuple(y.shape) != tuple(x.shape):
+        raise ValueError("y must have the shape of x")
+    dev = _same_device(h, ("x", x), ("y", y), ("positions", positions), ("table", rope.table))
+    px, sx = _rows(x, "x")
+    py, sy = _rows(y, "y")
+    _check("kvq_rope", load_library().kvq_rope(
+        h.ptr, px, sx, py, sy, heads, _vec(positions, n, "positions"), n,
+        ctypes.byref(rope.spec), 1 if inverse else 0, _stream_of(stream, dev)))
+
+
+def _append_rope(fn, h, pool, num_pool_pages, K, V, seq_idx, positions, page_table, rope,
+                 rope_positions, stream):
+    n, hkv = int(K.shape[0]), int(h.layout.num_kv_heads)
+    batch, max_pages = int(page_table.shape[0]), int(page_table.shape[1])
+    dev = _same_device(h, ("pool", pool), ("K", K), ("V", V), ("seq_idx", seq_idx),
+                       ("positions", positions), ("page_table", page_table),
+                       ("table", rope.table), ("rope_positions", rope_positions))
+    pk, sk = _rows(K, "K", hkv)
+    pv, sv = _rows(V, "V", hkv)
+    if int(V.shape[0]) != n:
+        raise ValueError("K and V must have the same number of tokens")
+    _check(fn, getattr(load_library(), fn)(
+        h.ptr, _ptr(pool, _U8, "pool"), int(num_pool_pages), pk, sk, pv, sv,
+        _vec(seq_idx, n, "seq_idx"), _vec(positions, n, "positions"), n,
+        _ptr(page_table, _I32, "page_table"), batch, max_pages, ctypes.byref(rope.spec),
+        None if rope_positions is None else _vec(rope_positions, n, "rope_positions"),
+        _stream_of(stream, dev)))
+
+
+def kvq_append_rope(h, pool, num_pool_pages, K, V, seq_idx, positions, page_table, rope: Rope,
+                    rope_positions=None, stream=None):
+    """kvq_append with the keys rotated on the way.  K, V: bf16 [n, Hkv, 128], tokens may be
+    strided (slices of a fused projection); rope_positions: int32 [n] if the angles' positions
+    are not the cache's."""
+    _append_rope("kvq_append_rope", h, pool, num_pool_pages, K, V, seq_idx, positions, page_table,
+                 rope, rope_positions, stream)
+
+
+def kvq_bf16_append_rope(h, pool, num_pool_pages, K, V, seq_idx, positions, page_table,
+                         rope: Rope, rope_positions=None, stream=None):
+    """kvq_bf16_append with the keys rotated on the way (arguments as kvq_append_rope)."""
+    _append_rope("kvq_bf16_append_rope", h, pool, num_pool_pages, K, V, seq_idx, positions,
+                 page_table, rope, rope_positions, stream)
 
 
 def kvq_dequant(h, pool, num_pool_pages, page_table, seq, start, length, K_out=None, V_out=None,
