@@ -411,6 +411,48 @@ int kvq_append_decode_window(kvq_handle* h, void* pool, int num_pool_pages, void
                              int batch, int sink, int recent, float* out, void* workspace,
                              size_t ws_bytes, int num_splits, void* stream);
 
+/* ---- attention of a chunk of new tokens ------------------------------------------
+ * The many-token form of kvq_decode, for prompts, prompt chunks, drafts to verify
+ * and mixed batches: every sequence b has n_b = cu_q[b + 1] - cu_q[b] new tokens,
+ * already appended, whose query rows are cu_q[b] .. cu_q[b + 1] - 1.  The i-th of
+ * them sits at position p = seq_lens[b] - n_b + i and attends to [0, p] (causal):
+ *     out[row] = softmax(sm_scale * q_rot . k~_t, t <= p) . v~_t, rotated back by
+ *     R_V(kv)^T,
+ * which is what kvq_decode gives for q[row] and length p + 1.  KVQ_Q_ROTATED and
+ * KVQ_OUT_ROTATED apply as in kvq_decode.  Cache entries and rotated queries are
+ * rounded to fp16 for the tensor cores and the weights too; sums are fp32.
+ *   q          : device bf16, row i at q + i * q_stride (elements), heads adjacent;
+ *                16-byte aligned, q_stride a multiple of 8 and >= H * 128.
+ *   cu_q       : device int32 [batch + 1], non-decreasing, within [0, n].  Rows that
+ *                belong to no sequence are left as they were; a sequence may have none.
+ *   n          : rows of q and out.  0 is a no-op.
+ *   page_table : device int32 [batch][max_pages];  seq_lens: device int32 [batch],
+ *                the context after the append.
+ *   out        : device bf16 [n][H][D], 16-byte aligned.
+ *   workspace  : device, >= kvq_prefill_workspace_bytes(h, batch, n) bytes, 256-byte
+ *                aligned; contents on entry do not matter.
+ * Rows of a sequence with seq_lens[b] < n_b or beyond the page table are set to 0
+ * (KVQ_STATUS_BAD_SEQLEN); one whose rows are no range in [0, n] is skipped
+ * (KVQ_STATUS_BAD_SEQ).  A page id out of range sets KVQ_STATUS_BAD_PAGE and its
+ * tokens are left out.  A value vector that holds a NaN or an infinity makes NaN
+ * the whole output of each row that sees it, and leaves the others alone.
+ * Returns KVQ_ENOSPACE if ws_bytes is too small, KVQ_ENOTREADY before
+ * kvq_set_rotation.  The result does not depend on how the work is divided beyond
+ * fp32 rounding, and is the same on every call. */
+size_t kvq_prefill_workspace_bytes(const kvq_handle* h, int batch, int n);
+int kvq_prefill(kvq_handle* h, const void* pool, int num_pool_pages, const uint16_t* q,
+                long long q_stride, const int32_t* cu_q, int n, const int32_t* page_table,
+                int max_pages, const int32_t* seq_lens, int batch, uint16_t* out, void* workspace,
+                size_t ws_bytes, void* stream);
+
+/* The same over the BF16 cache: plain attention with the unrotated query (no
+ * rotation bank, flags ignored); operands stay bf16. */
+size_t kvq_bf16_prefill_workspace_bytes(const kvq_handle* h, int batch, int n);
+int kvq_bf16_prefill(kvq_handle* h, const void* pool, int num_pool_pages, const uint16_t* q,
+                     long long q_stride, const int32_t* cu_q, int n, const int32_t* page_table,
+                     int max_pages, const int32_t* seq_lens, int batch, uint16_t* out,
+                     void* workspace, size_t ws_bytes, void* stream);
+
 /* ---- test export -----------------------------------------------------------
  * Dequantise positions [start, start+len) of sequence `seq` to fp32 in the
  * rotated (and, for keys, centred) basis: K_out[i][kv][d] = fmaf(code, s, z),

@@ -18,7 +18,9 @@ struct kvq_handle {
   int ctas_int2 = 1, ctas_bf16 = 1;
   int ctas_prep[4] = {1, 1, 1, 1};  // step-preparation CTAs per SM, 1/2/4/8 sequences each
   uint32_t* status = nullptr;      // device
-  float* bank = nullptr;           // device: R [2][Hkv][D][D], RVt [Hkv][D][D], mu [Hkv][D]
+  // device: R [2][Hkv][D][D], RVt [Hkv][D][D], mu [Hkv][D]; then 16-bit operands of the
+  // prefill's rotations, [Hkv][D][D] each: R_K^T high and low parts, R_V
+  float* bank = nullptr;
   bool ready = false;
   // kernel timing
   bool prof = false;
@@ -55,6 +57,15 @@ cudaStream_t S(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 size_t rot_floats(int Hkv) {
   return static_cast<size_t>(3) * Hkv * kDim * kDim + static_cast<size_t>(Hkv) * kDim;
+}
+
+// The prefill's rotation operand `which` (0, 1: R_K^T high and low, 2: R_V) in the bank.
+uint16_t* rot_operand(float* bank, int Hkv, int which) {
+  return reinterpret_cast<uint16_t*>(bank + rot_floats(Hkv)) +
+         static_cast<size_t>(which) * Hkv * kDim * kDim;
+}
+size_t rot_bytes(int Hkv) {
+  return rot_floats(Hkv) * sizeof(float) + static_cast<size_t>(3) * Hkv * kDim * kDim * 2;
 }
 
 // KV heads served by one INT2 decode CTA: the largest of 8, 4, 2, 1 dividing Hkv.
@@ -389,6 +400,58 @@ int append_common(kvq_handle* h, bool int2, void* pool, int num_pool_pages, cons
   return cuda_rc(e);
 }
 
+size_t prefill_bytes(const kvq_handle* h, int batch, int n) {
+  if (!h || batch < 1 || batch > 65535 || n < 0) return 0;
+  return kvq::prefill_ws_layout(batch, h->num_sms).total;
+}
+
+int prefill_common(kvq_handle* h, bool int2, const void* pool, int num_pool_pages,
+                   const uint16_t* q, long long q_stride, const int32_t* cu_q, int n,
+                   const int32_t* page_table, int max_pages, const int32_t* seq_lens, int batch,
+                   uint16_t* out, void* workspace, size_t ws_bytes, void* stream) {
+  if (!h || n < 0 || batch < 1 || batch > 65535) return KVQ_EINVAL;
+  if (int2 && !h->ready) return KVQ_ENOTREADY;
+  if (n == 0) return KVQ_OK;
+  if (!pool || !cu_q || !page_table || !seq_lens || !out || !workspace) return KVQ_EINVAL;
+  if (num_pool_pages < 1 || max_pages < 1 || max_pages > (1 << 26)) return KVQ_EINVAL;
+  if (!rows_ok(q, q_stride, h->L.num_heads)) return KVQ_EINVAL;
+  if (reinterpret_cast<uintptr_t>(pool) % 16 || reinterpret_cast<uintptr_t>(out) % 16 ||
+      reinterpret_cast<uintptr_t>(workspace) % 256)
+    return KVQ_EINVAL;
+  const bool rotate = int2 && !(h->L.flags & KVQ_OUT_ROTATED);
+  const kvq::PrefillWs w = kvq::prefill_ws_layout(batch, h->num_sms);
+  if (ws_bytes < w.total) return KVQ_ENOSPACE;
+  kvq::DeviceGuard dev_guard(h->device);
+  if (!dev_guard.ok()) return KVQ_ECUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const int Hkv = h->L.num_kv_heads;
+  kvq::PrefillArgs a;
+  a.pool = static_cast<const uint8_t*>(pool);
+  a.num_pool_pages = num_pool_pages;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.cu_q = cu_q;
+  a.n = n;
+  a.page_table = page_table;
+  a.max_pages = max_pages;
+  a.seq_lens = seq_lens;
+  a.batch = batch;
+  a.H = h->L.num_heads;
+  a.Hkv = h->L.num_kv_heads;
+  a.G = h->G;
+  a.out = out;
+  a.RVt = rotate ? h->bank + static_cast<size_t>(2) * Hkv * kDim * kDim : nullptr;
+  a.rk_hi = int2 ? rot_operand(h->bank, Hkv, 0) : nullptr;
+  a.rk_lo = int2 ? rot_operand(h->bank, Hkv, 1) : nullptr;
+  a.rv_tile = rotate ? rot_operand(h->bank, Hkv, 2) : nullptr;
+  a.log2_scale = h->sm_scale * 1.4426950408889634f;
+  a.status = h->status;
+  a.prefix = reinterpret_cast<long long*>(ws + w.prefix_off);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.ml_off);
+  a.part = reinterpret_cast<float*>(ws + w.part_off);
+  return cuda_rc(kvq::launch_prefill(a, int2, h->num_sms, S(stream)));
+}
+
 // Each pair's turns per position as a 64-bit fraction, from the base and the
 // scaling (include/kvq.h); false for parameters outside their ranges.
 bool rope_turns(int rot_dim, const kvq_rope_scaling* sc, uint64_t* turns, float* amplitude) {
@@ -516,7 +579,7 @@ int kvq_set_rotation(kvq_handle* h, const float* R, const float* mu, void* strea
   kvq::DeviceGuard dev_guard(h->device);
   if (!dev_guard.ok()) return KVQ_ECUDA;
   const int Hkv = h->L.num_kv_heads;
-  if (!h->bank && cudaMalloc(&h->bank, rot_floats(Hkv) * sizeof(float)) != cudaSuccess) {
+  if (!h->bank && cudaMalloc(&h->bank, rot_bytes(Hkv)) != cudaSuccess) {
     h->bank = nullptr;
     return KVQ_ECUDA;
   }
@@ -530,6 +593,10 @@ int kvq_set_rotation(kvq_handle* h, const float* R, const float* mu, void* strea
                       cudaMemcpyDeviceToDevice, st) != cudaSuccess)
     return KVQ_ECUDA;
   if (kvq::launch_transpose(h->bank + Hkv * mat, RVt, Hkv, st) != cudaSuccess) return KVQ_ECUDA;
+  if (kvq::launch_prefill_bank(h->bank, Hkv, (h->L.flags & KVQ_Q_ROTATED) != 0,
+                               rot_operand(h->bank, Hkv, 0), rot_operand(h->bank, Hkv, 1),
+                               rot_operand(h->bank, Hkv, 2), st) != cudaSuccess)
+    return KVQ_ECUDA;
   h->ready = true;
   return KVQ_OK;
 }
@@ -683,6 +750,30 @@ int kvq_bf16_decode(kvq_handle* h, const void* pool, int num_pool_pages, const u
   if (h && num_splits == 0) num_splits = choose_splits(h, batch, max_pages, false);
   return decode_common(h, false, pool, num_pool_pages, q, page_table, max_pages, seq_lens, batch,
                        out, workspace, ws_bytes, num_splits, stream);
+}
+
+size_t kvq_prefill_workspace_bytes(const kvq_handle* h, int batch, int n) {
+  return prefill_bytes(h, batch, n);
+}
+
+size_t kvq_bf16_prefill_workspace_bytes(const kvq_handle* h, int batch, int n) {
+  return prefill_bytes(h, batch, n);
+}
+
+int kvq_prefill(kvq_handle* h, const void* pool, int num_pool_pages, const uint16_t* q,
+                long long q_stride, const int32_t* cu_q, int n, const int32_t* page_table,
+                int max_pages, const int32_t* seq_lens, int batch, uint16_t* out, void* workspace,
+                size_t ws_bytes, void* stream) {
+  return prefill_common(h, true, pool, num_pool_pages, q, q_stride, cu_q, n, page_table, max_pages,
+                        seq_lens, batch, out, workspace, ws_bytes, stream);
+}
+
+int kvq_bf16_prefill(kvq_handle* h, const void* pool, int num_pool_pages, const uint16_t* q,
+                     long long q_stride, const int32_t* cu_q, int n, const int32_t* page_table,
+                     int max_pages, const int32_t* seq_lens, int batch, uint16_t* out,
+                     void* workspace, size_t ws_bytes, void* stream) {
+  return prefill_common(h, false, pool, num_pool_pages, q, q_stride, cu_q, n, page_table,
+                        max_pages, seq_lens, batch, out, workspace, ws_bytes, stream);
 }
 
 int kvq_dequant(kvq_handle* h, const void* pool, int num_pool_pages, const int32_t* page_table,

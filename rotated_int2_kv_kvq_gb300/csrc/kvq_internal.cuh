@@ -119,6 +119,42 @@ struct StepArgs {
   const int32_t* bf16_page_table = nullptr;
 };
 
+// One kvq_prefill / kvq_bf16_prefill call.
+struct PrefillArgs {
+  const uint8_t* pool;
+  int num_pool_pages;
+  const uint16_t* q;         // rows of [H][128], q_stride elements apart
+  long long q_stride;
+  const int32_t* cu_q;       // [batch + 1]
+  int n;                     // rows (tokens) of q and out
+  const int32_t* page_table;
+  int max_pages;
+  const int32_t* seq_lens;
+  int batch, H, Hkv, G;
+  uint16_t* out;             // [n][H][128] bf16
+  const float* RVt;          // [Hkv][D][D] transposed, nullptr: the output stays in the cache's basis
+  // the rotations as operands, [Hkv][128 x 128] each (INT2): R_K^T in two bf16
+  // parts, R_V in fp16 (nullptr with RVt)
+  const uint16_t* rk_hi;
+  const uint16_t* rk_lo;
+  const uint16_t* rv_tile;
+  float log2_scale;
+  uint32_t* status;
+  // workspace
+  long long* prefix;         // [batch + 1] units before each sequence
+  float2* part_ml;           // [2 * CTAs][256] (max, sum) of partial items
+  float* part;               // [2 * CTAs][256][128]
+};
+struct PrefillWs {
+  size_t prefix_off, ml_off, part_off, total;
+};
+PrefillWs prefill_ws_layout(int batch, int num_sms);
+cudaError_t launch_prefill(const PrefillArgs& a, bool int2, int num_sms, cudaStream_t st);
+// The operands of the prefill's rotations from R [2][Hkv][D][D]; identity_q: the
+// identity in R_K's place (the caller's queries are rotated already).
+cudaError_t launch_prefill_bank(const float* R, int Hkv, bool identity_q, uint16_t* hi, uint16_t* lo,
+                                uint16_t* rv, cudaStream_t st);
+
 // ---- launchers (defined in the .cu files) --------------------------------
 cudaError_t launch_append_int2(const AppendArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_append_bf16(const AppendArgs& a, cudaStream_t st);

@@ -1,0 +1,1376 @@
+// kvq_prefill.cu — causal attention of each sequence's new tokens over its paged
+// cache (INT2 or BF16), on the fifth-generation tensor cores.
+//
+// Row r of sequence b (len = seq_lens[b], n_b new tokens) sits at position
+// p = len - n_b + r and attends to positions [0, p]:
+//   out = softmax(sm_scale * q . k_t, t <= p) . v_t
+// with k_t, v_t the cache's entries; for the INT2 cache the query is first
+// rotated by R_K and the output rotated back by R_V^T, as kvq_decode does.
+//
+// One CTA per SM works through (sequence, KV head, row tile) items.  A row tile
+// is 256 rows (token, query head of the KV head's group): two MMA tiles of 128
+// that share each key tile of 128 positions (8 pages).  Roles:
+//   warps 0-3, 4-7 : softmax of the first and second 128 rows, a thread a row;
+//   warps 8-11     : page producers: codes (or bf16 fragments) -> fp16 (bf16)
+//                    operands in shared memory, two pages a warp, two stages;
+//   warp 12        : one thread issues every tcgen05.mma;
+//   warp 13        : one thread finds the next item while this one is worked on.
+// Scores S = Q K^T and the output O live in TMEM (2 x 128 + 2 x 128 columns);
+// the weights P overwrite S's columns and feed the second product from TMEM.
+// While one row tile's softmax runs, the tensor core works on the other's.
+//
+// INT2: the two rotations are tensor-core steps of the same pipeline, with the
+// rotation matrices (laid out once by kvq_set_rotation) in a stage's place of
+// the pages: first S = q R_K, which the softmax threads turn into the fp16
+// operand Q, and at an item's end out = o R_V^T from the normalised o.
+//
+// All key tiles of all items form one line of work, cut into equal ranges, one
+// per CTA: ragged batches, a single long chunk and a few decode tokens all fill
+// the GPU without a choice of split counts.  An item that a range border cuts
+// leaves partial (max, sum, O) states, joined by the combine kernel.
+#include "kvq_internal.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kTileKeys = 128;             // key positions per tile
+constexpr int kTilePages = kTileKeys / kPage;
+constexpr int kRows = 256;                 // rows per item: two MMA tiles
+constexpr int kThreads = 512;
+constexpr int kProdWarp0 = 8, kMmaWarp = 12, kSchedWarp = 13;
+// Registers a thread after the roles part, of the 128 that each is launched with:
+// 2 x 176 + 104 + 56 = 4 x 128
+constexpr int kRegSoftmax = 176, kRegProducer = 104, kRegIssue = 56;
+constexpr int kStages = 2;
+constexpr int kTileBytes = 128 * 128 * 2;  // one 128 x 128 16-bit operand
+constexpr float kLazy = 8.0f;              // log2 growth of a row maximum before O is rescaled
+
+struct Smem {
+  static constexpr int kQ = 0;                              // [2][32 KB]
+  static constexpr int kK = kQ + 2 * kTileBytes;            // [stages][32 KB]
+  static constexpr int kV = kK + kStages * kTileBytes;      // [stages][32 KB]
+  static constexpr int kBar = kV + kStages * kTileBytes;    // mbarriers
+  static constexpr int kBad = kBar + 128;                   // u32 [stages][4] tokens without a valid page
+  static constexpr int kPoison = kBad + 64;                 // u32 [stages][4] tokens with NaN / Inf values
+  static constexpr int kItem = kPoison + 64;                // Item [2]
+  static constexpr int kScan = kItem + 128;                 // long long [16]
+  static constexpr int kTmem = kScan + 128;
+  static constexpr int kBytes = kTmem + 16;
+  static constexpr int kAlloc = kBytes + 1024;              // base rounded up to 1024
+};
+
+// barrier indices
+enum { kFull = 0, kEmpty = kFull + kStages, kSFull = kEmpty + kStages, kPFull = kSFull + 2,
+       kDrain = kPFull + 2, kNumBars };
+
+struct Item {
+  int b, kv;                // sequence, KV head
+  int row0;                 // first token row (in q / out) of the tile
+  int tokens;               // tokens in the tile
+  int pos0;                 // position of its first token
+  int key_end;              // positions the tile sees: last token's position + 1 (0: none)
+  int tile_begin, tiles;    // key tiles of this CTA's part
+  int part;                 // partial slot, or -1 when this CTA has the whole item
+  int done;                 // no item left
+};
+static_assert(sizeof(Item) <= 64, "two items");
+
+// ---- tcgen05 ---------------------------------------------------------------------
+
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+#define KVQ_R32(v)                                                                              \
+  v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], v[8], v[9], v[10], v[11], v[12], v[13], v[14], \
+      v[15], v[16], v[17], v[18], v[19], v[20], v[21], v[22], v[23], v[24], v[25], v[26], v[27], \
+      v[28], v[29], v[30], v[31]
+__device__ __forceinline__ void tc_ld32(uint32_t (&v)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
+      "%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]),
+        "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
+        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(addr));
+}
+// Orders the loads' registers: nothing that uses them is scheduled before the wait.
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
+                 "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]),
+                 "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]),
+                 "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
+                 "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]),
+                 "+r"(v[31])::"memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,"
+      "%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
+      "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
+      "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tc_ld16(uint32_t (&v)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// 128 columns of this thread's row.
+__device__ __forceinline__ void tc_ld_row(uint32_t (&v)[4][32], uint32_t addr) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tc_ld32(v[c], addr + 32 * c);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tc_wait_ld(v[c]);
+}
+
+// Shared-memory operand of 128 rows x 128 columns of 16 bits, K-major, as two
+// 64-column halves of 128-byte rows with the 128-byte swizzle (16-byte chunk c of
+// row r at chunk c ^ (r & 7)); 8-row groups 1024 bytes apart.  `k` is the
+// 16-column step.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t base, int k) {
+  const uint32_t addr = base + (k >> 2) * (kTileBytes / 2) + (k & 3) * 32;
+  return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+// fp32 accumulate, M = N = 128, both operands fp16 (0) or bf16 (1), K-major
+constexpr uint32_t idesc_f16(int bf16) {
+  return (1u << 4) | (static_cast<uint32_t>(bf16) << 7) | (static_cast<uint32_t>(bf16) << 10) |
+         ((128u >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// ---- element orders ---------------------------------------------------------------
+// S = sum_d q_d k_d and O = sum_t p_t v_t do not depend on the order of d and t, so
+// both follow the page record's: a producer lane's codes become whole 16-byte
+// chunks, and its stores are free of bank conflicts.
+//   d = 16w + 8h + 2t + e : half t >> 1, chunk 4 (t & 1) + ((2h + (w >> 2)) ^ (2 (t >> 1))),
+//                           element 2 (w & 3) + e of the chunk;
+//   position in the tile = 64 g + 32 pp + 16 pi + 8 th + 2t + e : row (column of S,
+//                           K index of V) 64 g + 16 t + 8 pp + 4 pi + 2 th + e.
+__device__ __forceinline__ constexpr int col_pos(int c) {
+  return (c & 64) | ((c >> 3) & 1) << 5 | ((c >> 2) & 1) << 4 | ((c >> 1) & 1) << 3 |
+         ((c >> 4) & 3) << 1 | (c & 1);
+}
+
+// ---- the line of work ---------------------------------------------------------------
+// Row tiles of a sequence with n new tokens behind p0 old ones, TR tokens a tile
+// (TR = 256 / G): tile k sees ceil((p0 + min((k + 1) TR, n)) / 128) key tiles.
+struct Seq {
+  int row0, n, p0;       // first row, new tokens, position of the first
+  bool ok;               // false: invalid lengths; its rows get zeros
+  uint32_t bad;          // status bit of an invalid sequence, or 0
+  int rts;               // row tiles
+  long long units;       // key tiles of one KV head (invalid: one per row tile)
+};
+
+__device__ __forceinline__ long long half_sum(long long m) {   // sum of ceil(i / 2), i = 1 .. m
+  return ((m + 1) * (m + 1)) >> 2;
+}
+// key tiles of row tiles 0 .. k-1, all of them full
+__device__ __forceinline__ long long tiles_before(const Seq& s, int k, int TR) {
+  if (!s.ok) return k;
+  if (TR == 64) {
+    const long long a = (s.p0 + 63) >> 6;
+    return half_sum(a + k) - half_sum(a);
+  }
+  const long long a = (s.p0 + 127) >> 7, kk = k;
+  return a * kk + (TR >> 7) * (kk * (kk + 1) >> 1);
+}
+__device__ __forceinline__ Seq load_seq(const PrefillArgs& a, int b, int TR) {
+  Seq s;
+  const int r0 = a.cu_q[b], r1 = a.cu_q[b + 1];
+  const int len = a.seq_lens[b];
+  s.row0 = r0;
+  s.n = r1 - r0;
+  s.ok = true;
+  s.bad = 0;
+  if (r0 < 0 || r1 < r0 || r1 > a.n) {     // not a range of rows: nothing to write
+    s.n = 0;
+    s.ok = false;
+    s.bad = KVQ_STATUS_BAD_SEQ;
+  } else if (len < s.n || len > a.max_pages * kPage) {
+    s.ok = false;
+    s.bad = KVQ_STATUS_BAD_SEQLEN;
+  }
+  s.p0 = s.ok ? len - s.n : 0;
+  s.rts = (s.n + TR - 1) / TR;
+  s.units = s.rts == 0 ? 0
+            : s.ok     ? tiles_before(s, s.rts - 1, TR) + ((len + kTileKeys - 1) / kTileKeys)
+                       : s.rts;
+  return s;
+}
+
+// Exclusive prefix of v over the block's threads; *total = the sum.
+__device__ __forceinline__ long long block_prefix(long long v, long long* red, long long* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) red[w] = x;
+  __syncthreads();
+  long long before = 0, sum = 0;
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < w) before += red[i];
+    sum += red[i];
+  }
+  __syncthreads();
+  *total = sum;
+  return before + x - v;
+}
+
+// ---- producers -----------------------------------------------------------------------
+
+// The raw bytes of two pages that one lane turns into operands.
+struct RawInt2 {
+  uint4 k[2], v[2];
+  uint2 km[2];          // {s, z} of key tokens L >> 2 and (L >> 2) + 8
+  uint2 vm[2][2];       // {s, z} of value tokens 2t + i and 2t + i + 8
+};
+
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// Codes of both 16-bit halves of `w` at bits [2i, 2i + 2), i <= 4, as exact fp16
+// values: 1024 + code * 4^i in the mantissa, then * 4^-i - 1024 * 4^-i.
+template <int I>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+  constexpr uint32_t mask = 0x00030003u << (2 * I);
+  const uint32_t x = (w & mask) | 0x64006400u;
+  constexpr uint32_t mul = (0x3c00u - (I << 11)) * 0x10001u;             // 2^-2I
+  constexpr uint32_t sub = (0x8000u | (0x6400u - (I << 11))) * 0x10001u;  // -2^(10-2I)
+  return hfma2(x, mul, sub);
+}
+template <int W>
+__device__ __forceinline__ uint32_t dequant(uint32_t w, uint32_t s2, uint32_t z2) {
+  const uint32_t c = W < 5 ? code_pair<W < 5 ? W : 0>(w) : code_pair<W >= 5 ? W - 5 : 0>(w >> 10);
+  return hfma2(c, s2, z2);
+}
+__device__ __forceinline__ uint32_t dup_lo(uint32_t x) { return __byte_perm(x, x, 0x1010); }
+__device__ __forceinline__ uint32_t dup_hi(uint32_t x) { return __byte_perm(x, x, 0x3232); }
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// Nonzero bits where a half of x is infinite or NaN (fp16 / bf16).
+__device__ __forceinline__ uint32_t nonfinite_f16(uint32_t x) {
+  return ((x & 0x7c00u) == 0x7c00u ? 1u : 0u) | ((x & 0x7c000000u) == 0x7c000000u ? 2u : 0u);
+}
+
+__device__ __forceinline__ void int2_load(RawInt2& r, int i, const uint8_t* rec, int lane) {
+  if (!rec) {
+    r.k[i] = r.v[i] = make_uint4(0, 0, 0, 0);
+    r.km[i] = r.vm[i][0] = r.vm[i][1] = make_uint2(0, 0);
+    return;
+  }
+  r.k[i] = *reinterpret_cast<const uint4*>(rec + 16 * lane);
+  r.v[i] = *reinterpret_cast<const uint4*>(rec + 512 + 16 * lane);
+  r.km[i] = *reinterpret_cast<const uint2*>(rec + 1024 + 16 * (lane >> 2));
+  r.vm[i][0] = *reinterpret_cast<const uint2*>(rec + 1024 + 32 * (lane & 3) + 8);
+  r.vm[i][1] = *reinterpret_cast<const uint2*>(rec + 1024 + 32 * (lane & 3) + 16 + 8);
+}
+
+// Values at positions >= key_end (p = the page's first position) become zeros:
+// their slots may hold anything.
+__device__ __forceinline__ void int2_clip(RawInt2& r, int i, int p, int key_end, int lane) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int tau = 2 * (lane & 3) + e;
+    if (p + tau >= key_end) r.vm[i][e].x = 0;
+    if (p + tau + 8 >= key_end) r.vm[i][e].y = 0;
+  }
+}
+
+// Two pages (pair `pw` of the tile) into the stage's K and V operands.  Returns
+// the lane's bits of tokens (16 pi + tau) whose values are not all finite; those
+// tokens' values are stored as zeros.
+__device__ __forceinline__ uint32_t int2_store(RawInt2& r, uint32_t ks, uint32_t vs, int pw, int lane) {
+  const int g64 = pw >> 1, pp = pw & 1;
+  {
+    const int tau7 = lane >> 2, t = lane & 3;
+    const int prow = g64 * 64 + 16 * (tau7 >> 1) + 8 * pp + (tau7 & 1);
+    const uint32_t base = ks + (t >> 1) * (kTileBytes / 2) + prow * 128;
+#pragma unroll
+    for (int pi = 0; pi < 2; ++pi) {
+      const uint32_t w[4] = {r.k[pi].x, r.k[pi].y, r.k[pi].z, r.k[pi].w};
+      const uint32_t m[2] = {r.km[pi].x, r.km[pi].y};
+#pragma unroll
+      for (int th = 0; th < 2; ++th) {
+        const uint32_t s2 = dup_lo(m[th]), z2 = dup_hi(m[th]);
+        const uint32_t row = base + (4 * pi + 2 * th) * 128;
+        const int r7 = 4 * pi + 2 * th + (tau7 & 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t x = w[2 * th + h];
+          const int c0 = 4 * (t & 1) + ((2 * h) ^ (2 * (t >> 1)));
+          sts128(row + ((c0 ^ r7) << 4), dequant<0>(x, s2, z2), dequant<1>(x, s2, z2),
+                 dequant<2>(x, s2, z2), dequant<3>(x, s2, z2));
+          sts128(row + (((c0 + 1) ^ r7) << 4), dequant<4>(x, s2, z2), dequant<5>(x, s2, z2),
+                 dequant<6>(x, s2, z2), dequant<7>(x, s2, z2));
+        }
+      }
+    }
+  }
+  uint32_t poison = 0;
+  {
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t s2[4], z2[4];          // token pairs (pi, th)
+#pragma unroll
+    for (int pi = 0; pi < 2; ++pi)
+#pragma unroll
+      for (int th = 0; th < 2; ++th) {
+        const uint32_t m0 = th ? r.vm[pi][0].y : r.vm[pi][0].x;
+        const uint32_t m1 = th ? r.vm[pi][1].y : r.vm[pi][1].x;
+        uint32_t s = __byte_perm(m0, m1, 0x5410), z = __byte_perm(m0, m1, 0x7632);
+        // the largest |value| of a token is that of code 0 or 3
+        const uint32_t bad = nonfinite_f16(z) | nonfinite_f16(hfma2(s, 0x42004200u, z));
+        if (bad) {
+          const uint32_t keep = ((bad & 1) ? 0u : 0xffffu) | ((bad & 2) ? 0u : 0xffff0000u);
+          s &= keep;
+          z &= keep;
+          poison |= bad << (16 * pi + 8 * th + 2 * t);
+        }
+        s2[2 * pi + th] = s;
+        z2[2 * pi + th] = z;
+      }
+    const uint32_t row = vs + g64 * (kTileBytes / 2) + g * 128 + (((2 * t + pp) ^ g) << 4);
+#define KVQ_V(M)                                                                                  \
+  sts128(row + (16 * M) * 128, dequant<M>(r.v[0].x, s2[0], z2[0]), dequant<M>(r.v[0].z, s2[1], z2[1]), \
+         dequant<M>(r.v[1].x, s2[2], z2[2]), dequant<M>(r.v[1].z, s2[3], z2[3]));                 \
+  sts128(row + (16 * M + 8) * 128, dequant<M>(r.v[0].y, s2[0], z2[0]),                            \
+         dequant<M>(r.v[0].w, s2[1], z2[1]), dequant<M>(r.v[1].y, s2[2], z2[2]),                  \
+         dequant<M>(r.v[1].w, s2[3], z2[3]));
+    KVQ_V(0) KVQ_V(1) KVQ_V(2) KVQ_V(3) KVQ_V(4) KVQ_V(5) KVQ_V(6) KVQ_V(7)
+#undef KVQ_V
+  }
+  return poison;
+}
+
+// BF16 pages: the record's 4-byte pairs are moved, not converted.  Keys: chunk
+// (th, h, w >> 2) of a token takes one word of each of four 16-byte loads.
+__device__ __forceinline__ uint32_t bf16_store(const uint8_t* const (&rec)[2], int p0, int key_end,
+                                               uint32_t ks, uint32_t vs, int pw, int lane) {
+  const int g64 = pw >> 1, pp = pw & 1;
+  uint32_t poison = 0;
+  uint4 x[2][8];
+  // values first: both pages' eight words m are in flight together
+#pragma unroll
+  for (int pi = 0; pi < 2; ++pi)
+#pragma unroll
+    for (int m = 0; m < 8; ++m)
+      x[pi][m] = rec[pi] ? *reinterpret_cast<const uint4*>(rec[pi] + 4096 + 512 * m + 16 * lane)
+                         : make_uint4(0, 0, 0, 0);
+  {
+    const int g = lane >> 2, t = lane & 3;
+    // positions >= key_end: zeros
+    uint32_t keep[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = p0 + 16 * (i >> 1) + 8 * (i & 1) + 2 * t;
+      keep[i] = (p < key_end ? 0xffffu : 0u) | (p + 1 < key_end ? 0xffff0000u : 0u);
+    }
+    // largest |value| of each token pair (NaN counts as larger)
+    uint32_t big[4] = {0, 0, 0, 0};
+    auto maxabs = [](uint32_t a, uint32_t b) {
+      uint32_t d;
+      b &= 0x7fff7fffu;
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+      return d;
+    };
+#pragma unroll
+    for (int pi = 0; pi < 2; ++pi)
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        x[pi][m].x &= keep[2 * pi];
+        x[pi][m].y &= keep[2 * pi];
+        x[pi][m].z &= keep[2 * pi + 1];
+        x[pi][m].w &= keep[2 * pi + 1];
+        big[2 * pi] = maxabs(maxabs(big[2 * pi], x[pi][m].x), x[pi][m].y);
+        big[2 * pi + 1] = maxabs(maxabs(big[2 * pi + 1], x[pi][m].z), x[pi][m].w);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t bad = ((big[i] & 0x7f80u) == 0x7f80u ? 1u : 0u) |
+                     ((big[i] & 0x7f800000u) == 0x7f800000u ? 2u : 0u);
+      // a token is dropped as a whole: by every lane if any lane saw it
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+      if (bad) {
+        const uint32_t k2 = ((bad & 1) ? 0u : 0xffffu) | ((bad & 2) ? 0u : 0xffff0000u);
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          if (i & 1) {
+            x[i >> 1][m].z &= k2;
+            x[i >> 1][m].w &= k2;
+          } else {
+            x[i >> 1][m].x &= k2;
+            x[i >> 1][m].y &= k2;
+          }
+        }
+        poison |= bad << (16 * (i >> 1) + 8 * (i & 1) + 2 * t);
+      }
+    }
+    const uint32_t row = vs + g64 * (kTileBytes / 2) + g * 128 + (((2 * t + pp) ^ g) << 4);
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      sts128(row + (16 * m) * 128, x[0][m].x, x[0][m].z, x[1][m].x, x[1][m].z);
+      sts128(row + (16 * m + 8) * 128, x[0][m].y, x[0][m].w, x[1][m].y, x[1][m].w);
+    }
+  }
+#pragma unroll
+  for (int pi = 0; pi < 2; ++pi)
+#pragma unroll
+    for (int w = 0; w < 8; ++w)
+      x[pi][w] = rec[pi] ? *reinterpret_cast<const uint4*>(rec[pi] + 512 * w + 16 * lane)
+                         : make_uint4(0, 0, 0, 0);
+  {
+    const int tau7 = lane >> 2, t = lane & 3;
+    const int prow = g64 * 64 + 16 * (tau7 >> 1) + 8 * pp + (tau7 & 1);
+    const uint32_t base = ks + (t >> 1) * (kTileBytes / 2) + prow * 128;
+#pragma unroll
+    for (int pi = 0; pi < 2; ++pi)
+#pragma unroll
+      for (int th = 0; th < 2; ++th) {
+        const uint32_t row = base + (4 * pi + 2 * th) * 128;
+        const int r7 = 4 * pi + 2 * th + (tau7 & 1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {           // j = 2h + (w >> 2)
+          const int c = 4 * (t & 1) + (j ^ (2 * (t >> 1)));
+          auto word = [&](int w) {
+            const uint4& q = x[pi][4 * (j & 1) + w];
+            return (j >> 1) ? (th ? q.w : q.z) : (th ? q.y : q.x);
+          };
+          sts128(row + ((c ^ r7) << 4), word(0), word(1), word(2), word(3));
+        }
+      }
+  }
+  return poison;
+}
+
+// A warp's bounded wait: all lanes have seen the phase complete, or none goes on
+// (the tcgen05 loads and stores that follow are warp-wide).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+}
+
+// ---- fp32 pairs ---------------------------------------------------------------------
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// The power of two that brings a row's largest |x| into [1, 2), and its inverse:
+// the row's fp16 operand then neither overflows nor loses bits, whatever its size.
+__device__ __forceinline__ void row_scale(const uint32_t (&v)[4][32], float& down, float& up) {
+  float mx = 0.0f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+      mx = max3(mx, fabsf(__uint_as_float(v[c][i])), fabsf(__uint_as_float(v[c][i + 1])));
+  const uint32_t ex = min((__float_as_uint(mx) >> 23) & 255u, 253u);
+  down = __uint_as_float((254u - ex) << 23);
+  up = __uint_as_float(ex << 23);
+}
+
+template <int N>
+__device__ __forceinline__ void reg_grow() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_shrink() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// All of the CTA's threads, from whichever role's code.
+__device__ __forceinline__ void sync_cta() { asm volatile("barrier.sync 0;" ::: "memory"); }
+
+// ---- the attention kernel ------------------------------------------------------------
+//
+// Steps of an item on the stages' line: [INT2: R_K] key tiles [INT2, whole item,
+// rotated output: R_V].  Row tile t's S_full completes once per step (scores or a
+// rotation's product) and once when O is complete; P_full once per product's
+// operand from the softmax threads (Q, P of each tile, o).
+
+template <bool INT2>
+struct Steps {
+  int pre, tiles, post;
+  __device__ __forceinline__ Steps(const Item& w, const PrefillArgs& a)
+      : pre(INT2 && w.tiles > 0 ? 1 : 0),
+        tiles(w.tiles),
+        post(INT2 && w.tiles > 0 && w.part < 0 && a.rv_tile ? 1 : 0) {}
+  __device__ __forceinline__ int all() const { return pre + tiles + post; }
+};
+
+// A wait gave up somewhere in the CTA: every role leaves after the same item.
+__device__ __forceinline__ bool item_end(bool alive, const PrefillArgs& a, volatile uint32_t* abort) {
+  if (!alive) {
+    atomicOr(a.status, KVQ_STATUS_TIMEOUT);
+    *abort = 1;
+  }
+  sync_cta();
+  return *abort == 0;
+}
+
+// The item's query rows into the Q operands, by the first 384 threads.
+template <bool INT2>
+__device__ __forceinline__ void load_q(const PrefillArgs& a, const Item& w, uint8_t* smem) {
+  const int G = a.G, rows = w.tokens * G;
+  for (int idx = threadIdx.x; idx < (rows > 128 ? 256 : 128) * 16; idx += kMmaWarp * 32) {
+    const int row = idx >> 4, c = idx & 15;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (row < rows) {
+      const int tok = row / G, g = row - tok * G;
+      v = *reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(w.row0 + tok) * a.q_stride +
+                                          (w.kv * G + g) * kDim + 8 * c);
+    }
+    uint8_t* base = smem + Smem::kQ + (row >> 7) * kTileBytes + (row & 127) * 128;
+    if constexpr (INT2) {         // d in order: the left operand of q R_K
+      *reinterpret_cast<uint4*>(base + (c >> 3) * (kTileBytes / 2) + (((c & 7) ^ (row & 7)) << 4)) = v;
+    } else {                      // the 16-byte piece holds the pairs t = 0 .. 3 of one (w, h)
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      const int wq = c >> 1, h = c & 1;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int ch = 4 * (t & 1) + ((2 * h + (wq >> 2)) ^ (2 * (t >> 1)));
+        *reinterpret_cast<uint32_t*>(base + (t >> 1) * (kTileBytes / 2) + ((ch ^ (row & 7)) << 4) +
+                                     4 * (wq & 3)) = x[t];
+      }
+    }
+  }
+  fence_proxy_async();
+}
+
+// One tile's scores (this thread's row, all 128 in registers) into weights: the
+// running maximum, the weights as 16-bit pairs into TMEM, their sum.
+template <bool INT2>
+__device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float scale, bool first,
+                                             int limit, const uint32_t* bw, const uint32_t* pz,
+                                             float& mref, float& l) {
+  uint32_t v[4][32];
+  tc_ld_row(v, ts);
+  const uint4 fb = *reinterpret_cast<const uint4*>(bw), fp = *reinterpret_cast<const uint4*>(pz);
+  const uint32_t flags = fb.x | fb.y | fb.z | fb.w | fp.x | fp.y | fp.z | fp.w;
+  if (__any_sync(0xffffffffu, limit < kTileKeys - 1) || flags != 0) {
+    const uint32_t b4[4] = {fb.x, fb.y, fb.z, fb.w}, p4[4] = {fp.x, fp.y, fp.z, fp.w};
+    uint32_t hide[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int e = limit - 32 * k;          // last visible bit of word k
+      const uint32_t vis = e >= 31 ? 0xffffffffu : e < 0 ? 0u : (2u << e) - 1u;
+      hide[k] = b4[k] | ~vis;
+      if (p4[k] & ~hide[k]) l = __int_as_float(0x7fffffff);   // sees a NaN / Inf value
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int o = col_pos(32 * c + i);
+        if ((hide[o >> 5] >> (o & 31)) & 1) v[c][i] = 0xff800000u;
+      }
+  }
+  float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      m0 = max3(m0, __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
+      m1 = max3(m1, __uint_as_float(v[c][i + 2]), __uint_as_float(v[c][i + 3]));
+    }
+  const float mnew = fmaxf(mref, fmaxf(m0, m1) * scale);
+  if (first) {
+    mref = mnew;
+  } else {
+    // O is rescaled only when a maximum grew by 2^8 (the weights stay below that, in
+    // range of fp16, and the sums are fp32): a step that most tiles skip
+    const bool grow = mnew > mref + kLazy;
+    if (__any_sync(0xffffffffu, grow)) {
+      const float f = grow ? fast_exp2(mref - mnew) : 1.0f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint32_t o[16];
+        tc_ld16(o, to + 16 * c);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tc_st16(to + 16 * c, o);
+      }
+      l *= f;
+      if (grow) mref = mnew;
+    }
+  }
+  const float neg = mref == -INFINITY ? 0.0f : -mref;
+  const uint64_t sc2 = pair2(scale, scale), ng2 = pair2(neg, neg);
+  uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t pk[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t* x = &v[2 * h + (i >> 4)][2 * (i & 15)];
+      float x0, x1;
+      split2(fma2(pair2(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, ng2), x0, x1);
+      const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+      if (i & 1) s1 = add2(s1, pair2(p0, p1));
+      else s0 = add2(s0, pair2(p0, p1));
+      pk[i] = INT2 ? pack_half2(p0, p1) : pack_bf162(p0, p1);
+    }
+    tc_st32(ts + 32 * h, pk);     // all of S is in registers: P may overwrite it
+  }
+  float a0, a1;
+  split2(add2(s0, s1), a0, a1);
+  l += a0 + a1;
+  tc_wait_st();
+}
+
+template <bool INT2>
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t sb = smem_u32(smem);
+  const uint32_t bar = sb + Smem::kBar;
+  Item* items = reinterpret_cast<Item*>(smem + Smem::kItem);
+  long long* red = reinterpret_cast<long long*>(smem + Smem::kScan);
+  uint32_t* badw = reinterpret_cast<uint32_t*>(smem + Smem::kBad);
+  uint32_t* poisonw = reinterpret_cast<uint32_t*>(smem + Smem::kPoison);
+  volatile uint32_t* abort = reinterpret_cast<volatile uint32_t*>(smem + Smem::kTmem + 4);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  auto B = [&](int i) { return bar + 8 * i; };
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(B(kFull + i), 4);
+      mbar_init(B(kEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(B(kSFull + i), 1);
+      mbar_init(B(kPFull + i), 4);
+    }
+    mbar_init(B(kDrain), 1);
+    fence_mbar_init();
+    *abort = 0;
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     sb + Smem::kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+
+  // The line of work: thread i sums a run of sequences; the thread whose run holds
+  // this CTA's first unit hands its sequence to the scheduler.
+  {
+    const int TR = kRows / a.G;
+    const int per_thread = (a.batch + kThreads - 1) / kThreads;
+    const int b_lo = min(tid * per_thread, a.batch), b_hi = min(b_lo + per_thread, a.batch);
+    long long mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const Seq s = load_seq(a, b, TR);
+      if (s.bad && blockIdx.x == 0) atomicOr(a.status, s.bad);
+      mine += s.units * a.Hkv;
+    }
+    long long total;
+    const long long before = block_prefix(mine, red, &total);
+    const long long per = (total + gridDim.x - 1) / gridDim.x;
+    const long long u0 = min(per * blockIdx.x, total), u1 = min(u0 + per, total);
+    const bool here = u0 < u1 && before <= u0 && u0 < before + mine;
+    if (tid == 0) {
+      red[0] = u0;
+      red[1] = u1;
+    }
+    if (blockIdx.x == 0 || here) {
+      long long u = before;
+      bool found = false;
+      for (int b = b_lo; b < b_hi; ++b) {
+        if (blockIdx.x == 0) a.prefix[b] = u;
+        const long long su = load_seq(a, b, TR).units * a.Hkv;
+        if (here && !found && u0 < u + su) {
+          found = true;
+          red[2] = b;
+          red[3] = u;
+        }
+        u += su;
+      }
+    }
+    if (blockIdx.x == 0 && tid == 0) a.prefix[a.batch] = total;
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Smem::kTmem);
+
+  bool alive = true;                // false after a wait gave up
+  uint32_t it = 0;                  // steps so far on the stages' line (stage and phase)
+
+  if (warp < kProdWarp0) {
+    // ======================= softmax: a thread a row =======================
+    reg_grow<kRegSoftmax>();
+    const int t = warp >> 2, row = tid;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+    uint8_t* qrow = smem + Smem::kQ + t * kTileBytes + (row & 127) * 128;
+    const int r7 = row & 7;
+    uint32_t ns = 0;                // S_full phases
+    for (uint32_t i = 0;; ++i) {
+      sync_cta();                   // the item is there
+      const Item w = items[i & 1];
+      if (w.done) break;
+      load_q<INT2>(a, w, smem);
+      sync_cta();                   // Q is there
+      const Steps<INT2> st(w, a);
+      const int rows = w.tokens * a.G;
+      const int tok = row / a.G, g = row - tok * a.G;
+      const bool valid = row < rows, some = warp * 32 < rows;
+      const bool active = t == 0 || rows > 128;
+      float mref = -INFINITY, l = 0.0f, scale = a.log2_scale;
+      auto wait_s = [&]() {
+        alive = warp_wait(B(kSFull + t), ns & 1);
+        ++ns;
+        tc_fence_after();
+        return alive;
+      };
+      auto give = [&]() {           // an operand of this row tile is ready
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(B(kPFull + t));
+      };
+      if (active && st.tiles > 0) {
+        if (INT2 && wait_s()) {
+          if (some) {
+            // q R_K -> fp16 Q, a power of two a row apart, in the pages' order of d
+            uint32_t v[4][32];
+            tc_ld_row(v, ts);
+            float down, up;
+            row_scale(v, down, up);
+            scale *= up;
+            auto h2 = [&](int d) {
+              return pack_half2(__uint_as_float(v[d >> 5][d & 31]) * down,
+                                __uint_as_float(v[d >> 5][(d & 31) + 1]) * down);
+            };
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int wq = 0; wq < 2; ++wq) {
+                  const int ch = 4 * (tt & 1) + ((2 * h + wq) ^ (2 * (tt >> 1)));
+                  const int d = 64 * wq + 8 * h + 2 * tt;
+                  *reinterpret_cast<uint4*>(qrow + (tt >> 1) * (kTileBytes / 2) + ((ch ^ r7) << 4)) =
+                      make_uint4(h2(d), h2(d + 16), h2(d + 32), h2(d + 48));
+                }
+            fence_proxy_async();
+          }
+          give();
+        }
+        const int pos = w.pos0 + tok;
+        for (int j = 0; j < st.tiles && alive; ++j) {
+          const uint32_t k = it + st.pre + j;
+          const int sg = k % kStages;
+          if (!wait_s()) break;
+          // returns at once (the scores were made from that stage): it orders this thread's
+          // reads of the stage's flags behind the producers' writes
+          if (!(alive = warp_wait(B(kFull + sg), (k / kStages) & 1))) break;
+          if (some)
+            softmax_tile<INT2>(ts, to, scale, j == 0,
+                               valid ? pos - (w.tile_begin + j) * kTileKeys : kTileKeys,
+                               badw + 4 * sg, poisonw + 4 * sg, mref, l);
+          give();
+        }
+        if (alive) wait_s();        // O is complete
+      }
+      // ---- this part's result ----
+      const size_t orow = static_cast<size_t>(w.row0 + tok) * a.H + w.kv * a.G + g;
+      if (active && alive && w.part >= 0) {
+        if (some) {
+          float* po = a.part + (static_cast<size_t>(w.part) * kRows + row) * kDim;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            tc_ld32(v, to + 32 * c);
+            tc_wait_ld(v);
+            if (valid) {
+              uint4* dst = reinterpret_cast<uint4*>(po + 32 * c);
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                dst[x] = make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+            }
+            __syncwarp();
+          }
+          if (valid)
+            a.part_ml[static_cast<size_t>(w.part) * kRows + row] =
+                make_float2(l == 0.0f ? -INFINITY : mref, l);
+        }
+      } else if (active && alive) {
+        float f = l == 0.0f ? 0.0f : 1.0f / l;
+        uint4* dst = reinterpret_cast<uint4*>(a.out + orow * kDim);
+        if (st.post) {
+          if (some) {
+            // o / l -> fp16, a power of two a row apart: the left operand of o R_V^T
+            uint32_t v[4][32];
+            tc_ld_row(v, to);
+            float down, up;
+            row_scale(v, down, up);
+            auto h2 = [&](int d) {
+              return pack_half2(__uint_as_float(v[d >> 5][d & 31]) * down,
+                                __uint_as_float(v[d >> 5][(d & 31) + 1]) * down);
+            };
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              *reinterpret_cast<uint4*>(qrow + (c >> 3) * (kTileBytes / 2) + (((c & 7) ^ r7) << 4)) =
+                  make_uint4(h2(8 * c), h2(8 * c + 2), h2(8 * c + 4), h2(8 * c + 6));
+            f *= up;
+            fence_proxy_async();
+          }
+          give();
+          wait_s();
+        }
+        if (alive && st.tiles == 0) {
+          if (valid)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) dst[x] = make_uint4(0, 0, 0, 0);
+        } else if (alive && some) {
+          const uint32_t src = st.post ? ts : to;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            tc_ld32(v, src + 32 * c);
+            tc_wait_ld(v);
+            if (valid) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  o[e] = pack_bf162(__uint_as_float(v[8 * x + 2 * e]) * f,
+                                    __uint_as_float(v[8 * x + 2 * e + 1]) * f);
+                dst[4 * c + x] = make_uint4(o[0], o[1], o[2], o[3]);
+              }
+            }
+            __syncwarp();
+          }
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      it += st.all();
+      if (!item_end(alive, a, abort)) break;
+    }
+  } else if (warp < kMmaWarp) {
+    // ======================= producers =======================
+    reg_shrink<kRegProducer>();
+    const int pw = warp - kProdWarp0;
+    const size_t page_stride = static_cast<size_t>(a.Hkv) * (INT2 ? kInt2Rec : kBf16Rec);
+    for (uint32_t i = 0;; ++i) {
+      sync_cta();
+      const Item w = items[i & 1];
+      if (w.done) break;
+      load_q<INT2>(a, w, smem);
+      const Steps<INT2> st(w, a);
+      const int pages = (w.key_end + kPage - 1) / kPage;
+      const int32_t* ptab = a.page_table + static_cast<size_t>(w.b) * a.max_pages;
+      const uint8_t* pool = a.pool + static_cast<size_t>(w.kv) * (INT2 ? kInt2Rec : kBf16Rec);
+      // page ids of a tile's pair: -1 behind the last page
+      auto ids = [&](int j, int (&id)[2]) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int p = (w.tile_begin + j) * kTilePages + 2 * pw + x;
+          id[x] = j < st.tiles && p < pages ? ptab[p] : -1;
+        }
+      };
+      auto address = [&](int id) -> const uint8_t* {
+        return id >= 0 && id < a.num_pool_pages ? pool + static_cast<size_t>(id) * page_stride : nullptr;
+      };
+      auto wait_empty = [&](uint32_t k) {
+        alive = warp_wait(B(kEmpty + k % kStages), ((k / kStages) & 1) ^ 1);
+        return alive;
+      };
+      auto give = [&](uint32_t k) {
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(B(kFull + k % kStages));
+      };
+      // 32 KB of a rotation's operand, already in the operand's layout
+      auto copy_tile = [&](uint32_t dst, const uint16_t* src) {
+        const uint4* s4 = reinterpret_cast<const uint4*>(src) + pw * 32 + lane;
+        dst += (pw * 32 + lane) * 16;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint4 v[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) v[y] = s4[(8 * x + y) * 128];
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            sts128(dst + (8 * x + y) * 2048, v[y].x, v[y].y, v[y].z, v[y].w);
+        }
+      };
+      int id0[2], id1[2];
+      RawInt2 raw;
+      ids(0, id0);
+      ids(1, id1);
+      if constexpr (INT2) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) int2_load(raw, x, address(id0[x]), lane);
+      }
+      sync_cta();                   // Q is there
+      const size_t mat = static_cast<size_t>(w.kv) * kDim * kDim;
+      if (st.pre && wait_empty(it)) {
+        const int sg = it % kStages;
+        copy_tile(sb + Smem::kK + sg * kTileBytes, a.rk_hi + mat);
+        copy_tile(sb + Smem::kV + sg * kTileBytes, a.rk_lo + mat);
+        give(it);
+      }
+      for (int j = 0; j < st.tiles && alive; ++j) {
+        const uint32_t k = it + st.pre + j;
+        const int sg = k % kStages;
+        if (!wait_empty(k)) break;
+        const int p0 = ((w.tile_begin + j) * kTilePages + 2 * pw) * kPage;
+        uint32_t bad = 0;
+        const uint8_t* rec[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          rec[x] = address(id0[x]);
+          if (!rec[x] && p0 + kPage * x < w.key_end) bad |= 0xffffu << (16 * x);
+        }
+        const uint32_t ks = sb + Smem::kK + sg * kTileBytes, vs = sb + Smem::kV + sg * kTileBytes;
+        uint32_t poison;
+        if constexpr (INT2) {
+          if (p0 + 2 * kPage > w.key_end) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) int2_clip(raw, x, p0 + kPage * x, w.key_end, lane);
+          }
+          RawInt2 now = raw;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) int2_load(raw, x, address(id1[x]), lane);
+          poison = int2_store(now, ks, vs, pw, lane);
+        } else {
+          poison = bf16_store(rec, p0, w.key_end, ks, vs, pw, lane);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) id0[x] = id1[x];
+        ids(j + 2, id1);
+        poison = __reduce_or_sync(0xffffffffu, poison);
+        if (lane == 0) {
+          badw[4 * sg + pw] = bad;
+          poisonw[4 * sg + pw] = poison;
+          if (bad) atomicOr(a.status, KVQ_STATUS_BAD_PAGE);
+        }
+        give(k);
+      }
+      if (st.post && alive && wait_empty(it + st.pre + st.tiles)) {
+        const uint32_t k = it + st.pre + st.tiles;
+        copy_tile(sb + Smem::kK + (k % kStages) * kTileBytes, a.rv_tile + mat);
+        give(k);
+      }
+      it += st.all();
+      if (!item_end(alive, a, abort)) break;
+    }
+  } else {
+    // ======================= tensor-core issue, schedule =======================
+    reg_shrink<kRegIssue>();
+    uint32_t np0 = 0, np1 = 0;      // P_full phases
+    long long cur = red[0], u_end = red[1], cur_b0 = red[3];
+    int cur_b = static_cast<int>(red[2]);
+    auto schedule = [&](Item& w) {
+      const int TR = kRows / a.G;
+      w.done = 1;
+      if (cur >= u_end) return;
+      Seq s = load_seq(a, cur_b, TR);
+      while (cur >= cur_b0 + s.units * a.Hkv) {       // ends: cur < total
+        cur_b0 += s.units * a.Hkv;
+        s = load_seq(a, ++cur_b, TR);
+      }
+      const long long local = cur - cur_b0;
+      const int kv = static_cast<int>(local / s.units);
+      const long long r = local - kv * s.units;
+      int lo = 0, hi = s.rts - 1;                     // last row tile that starts at or before r
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tiles_before(s, mid, TR) <= r) lo = mid;
+        else hi = mid - 1;
+      }
+      const int tok0 = lo * TR;
+      w.b = cur_b;
+      w.kv = kv;
+      w.row0 = s.row0 + tok0;
+      w.tokens = min(TR, s.n - tok0);
+      w.pos0 = s.p0 + tok0;
+      w.key_end = s.ok ? w.pos0 + w.tokens : 0;
+      const int all = s.ok ? (w.key_end + kTileKeys - 1) / kTileKeys : 1;
+      const int t0 = static_cast<int>(r - tiles_before(s, lo, TR));
+      const int t1 = static_cast<int>(min(static_cast<long long>(all), t0 + (u_end - cur)));
+      w.tile_begin = t0;
+      w.tiles = s.ok ? t1 - t0 : 0;
+      w.part = (t0 == 0 && t1 == all) ? -1 : static_cast<int>(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0);
+      w.done = 0;
+      cur += t1 - t0;
+    };
+    if (warp == kSchedWarp && lane == 0) schedule(items[0]);
+    __syncwarp();
+    for (uint32_t i = 0;; ++i) {
+      sync_cta();
+      const Item w = items[i & 1];
+      if (w.done) break;
+      if (warp == kSchedWarp && lane == 0) schedule(items[(i + 1) & 1]);
+      __syncwarp();
+      sync_cta();                   // Q is there
+      const Steps<INT2> st(w, a);
+      if (warp == kMmaWarp && lane == 0 && st.tiles > 0) {
+        constexpr uint32_t idesc = idesc_f16(INT2 ? 0 : 1), idesc_bf = idesc_f16(1);
+        const int nt = w.tokens * a.G > 128 ? 2 : 1;
+        auto full = [&](uint32_t k) {
+          alive = alive && mbar_wait_bounded(B(kFull + k % kStages), (k / kStages) & 1);
+          tc_fence_after();
+          return alive;
+        };
+        auto operand = [&](int t) {      // Q, P or o of row tile t
+          uint32_t& n = t ? np1 : np0;
+          alive = alive && mbar_wait_bounded(B(kPFull + t), n & 1);
+          ++n;
+          tc_fence_after();
+          return alive;
+        };
+        // S_t = Q_t X^T, X a stage's K (or V) operand
+        auto product = [&](int t, uint32_t xb, uint32_t id, bool add) {
+          const uint32_t qb = sb + Smem::kQ + t * kTileBytes;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_ss(tmem + t * 128, tile_desc(qb, k), tile_desc(xb, k), id, add || k != 0);
+        };
+        auto kbuf = [&](uint32_t k) { return sb + Smem::kK + (k % kStages) * kTileBytes; };
+        auto vbuf = [&](uint32_t k) { return sb + Smem::kV + (k % kStages) * kTileBytes; };
+        uint32_t k = it;
+        if (st.pre && full(k)) {
+          for (int t = 0; t < nt; ++t) {
+            product(t, kbuf(k), idesc_bf, false);
+            product(t, vbuf(k), idesc_bf, true);
+            tc_commit(B(kSFull + t));
+          }
+          tc_commit(B(kEmpty + k % kStages));
+          ++k;
+        }
+        if (full(k))
+          for (int t = 0; t < nt; ++t) {
+            if (st.pre && !operand(t)) break;
+            product(t, kbuf(k), idesc, false);
+            tc_commit(B(kSFull + t));
+          }
+        for (int j = 0; j < st.tiles && alive; ++j, ++k) {
+          for (int t = 0; t < nt && alive; ++t) {
+            if (!operand(t)) break;
+            const uint32_t vb = vbuf(k);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * x, tile_desc(vb, x), idesc,
+                        (j | x) != 0);
+            if (t == nt - 1) tc_commit(B(kEmpty + k % kStages));
+            if (j + 1 < st.tiles) {
+              if (t == 0 && !full(k + 1)) break;
+              product(t, kbuf(k + 1), idesc, false);
+            }
+            tc_commit(B(kSFull + t));   // the next scores, or O
+          }
+        }
+        if (st.post && alive && full(k)) {
+          for (int t = 0; t < nt; ++t) {
+            if (!operand(t)) break;
+            product(t, kbuf(k), idesc, false);
+            tc_commit(B(kSFull + t));
+          }
+          tc_commit(B(kEmpty + k % kStages));
+        }
+      }
+      __syncwarp();
+      it += st.all();
+      if (!item_end(alive, a, abort)) break;
+    }
+  }
+
+  // nothing of this CTA may be in flight when it gives its TMEM back
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      tc_commit(B(kDrain));
+      (void)mbar_wait_bounded(B(kDrain), 0);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  sync_cta();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// ---- the rotations' operands ---------------------------------------------------------
+// R_K^T as two bf16 parts (hi + lo: 16 bits of each entry) and R_V as fp16, each a
+// 128 x 128 K-major operand in the swizzled layout above: row n, column k of head kv.
+__global__ void __launch_bounds__(256) prefill_bank_kernel(const float* R, int Hkv, bool identity_q,
+                                                           uint16_t* hi, uint16_t* lo, uint16_t* rv) {
+  const int kv = blockIdx.x;
+  const float* RK = R + static_cast<size_t>(kv) * kDim * kDim;
+  const float* RV = RK + static_cast<size_t>(Hkv) * kDim * kDim;
+  const size_t mat = static_cast<size_t>(kv) * kDim * kDim;
+  for (int idx = threadIdx.x; idx < kDim * kDim; idx += blockDim.x) {
+    const int n = idx & 127, k = idx >> 7;
+    const size_t at = mat + (k >> 6) * (kTileBytes / 4) + n * 64 + ((((k >> 3) & 7) ^ (n & 7)) << 3) + (k & 7);
+    const float x = identity_q ? (n == k ? 1.0f : 0.0f) : RK[k * kDim + n];
+    const __nv_bfloat16 h = __float2bfloat16_rn(x);
+    hi[at] = __bfloat16_as_ushort(h);
+    lo[at] = __bfloat16_as_ushort(__float2bfloat16_rn(x - __bfloat162float(h)));
+    rv[at] = __half_as_ushort(__float2half_rn(RV[n * kDim + k]));
+  }
+}
+
+// ---- rows times a 128 x 128 matrix -----------------------------------------------------
+// acc[i][c] = sum_j A[4 ty + i][j] * M[j][8 tx + c], A: [64][132] fp32 in shared
+// memory, M: [128][128] fp32 in shared memory; 256 threads = 16 (ty) x 16 (tx).
+constexpr int kGemmRows = 64;
+constexpr int kGemmPitch = kDim + 4;
+constexpr int kGemmSmem = (kGemmRows * kGemmPitch + kDim * kDim) * 4;
+
+__device__ __forceinline__ void rows_times(const float* As, const float* Ms, float (&acc)[4][8]) {
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[i][c] = 0.0f;
+#pragma unroll 8
+  for (int j = 0; j < kDim; ++j) {
+    const float4 m0 = *reinterpret_cast<const float4*>(Ms + j * kDim + 4 * tx);
+    const float4 m1 = *reinterpret_cast<const float4*>(Ms + j * kDim + 64 + 4 * tx);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = As[(4 * ty + i) * kGemmPitch + j];
+      acc[i][0] = fmaf(x, m0.x, acc[i][0]);
+      acc[i][1] = fmaf(x, m0.y, acc[i][1]);
+      acc[i][2] = fmaf(x, m0.z, acc[i][2]);
+      acc[i][3] = fmaf(x, m0.w, acc[i][3]);
+      acc[i][4] = fmaf(x, m1.x, acc[i][4]);
+      acc[i][5] = fmaf(x, m1.y, acc[i][5]);
+      acc[i][6] = fmaf(x, m1.z, acc[i][6]);
+      acc[i][7] = fmaf(x, m1.w, acc[i][7]);
+    }
+  }
+}
+
+// Joins the partial states of the items that range borders cut: CTA x stands for
+// the border between ranges x and x + 1, y for 64 of the item's rows; the item's
+// first border does the work.  Then R_V^T (INT2) in fp32, and bf16.
+__global__ void __launch_bounds__(256) prefill_combine_kernel(const __grid_constant__ PrefillArgs a,
+                                                              int num_ctas) {
+  extern __shared__ __align__(16) float sm[];
+  float* As = sm;
+  float* Ms = sm + kGemmRows * kGemmPitch;
+  const int G = a.G, tid = threadIdx.x, TR = kRows / G;
+  const long long total = a.prefix[a.batch];
+  const long long per = (total + num_ctas - 1) / num_ctas;
+  const long long u = per * (blockIdx.x + 1);            // the border, in units
+  if (u >= total) return;
+  int lo = 0, hi = a.batch - 1;                          // last sequence that starts at or before u
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.prefix[mid] <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  const Seq s = load_seq(a, lo, TR);
+  const long long local = u - a.prefix[lo];
+  const int kv = static_cast<int>(local / s.units);
+  const long long r = local - kv * s.units;
+  int rt = 0, rt_hi = s.rts - 1;
+  while (rt < rt_hi) {
+    const int mid = (rt + rt_hi + 1) >> 1;
+    if (tiles_before(s, mid, TR) <= r) rt = mid;
+    else rt_hi = mid - 1;
+  }
+  const long long first = tiles_before(s, rt, TR);       // the item's first unit, in its head
+  if (first == r || !s.ok) return;                       // the border cuts nothing
+  const long long u0 = u - (r - first);
+  const int c0 = static_cast<int>(u0 / per);
+  if (c0 != static_cast<int>(blockIdx.x)) return;        // an earlier border of the item joins it
+  const int tok0 = rt * TR, tokens = min(TR, s.n - tok0);
+  const int row0 = blockIdx.y * kGemmRows, rows = min(tokens * G - row0, kGemmRows);
+  if (rows <= 0) return;
+  const int all = (s.p0 + tok0 + tokens + kTileKeys - 1) / kTileKeys;
+  const int c1 = static_cast<int>((u0 + all - 1) / per);
+  const bool rotate = a.RVt != nullptr;
+  if (rotate)
+    for (int idx = tid; idx < kDim * kDim / 4; idx += 256)
+      reinterpret_cast<float4*>(Ms)[idx] =
+          reinterpret_cast<const float4*>(a.RVt + static_cast<size_t>(kv) * kDim * kDim)[idx];
+  // a warp a row: lane holds elements 4 lane .. 4 lane + 3
+  const int warp = tid >> 5, lane = tid & 31;
+  auto out_row = [&](int row) {
+    const int tk = (row0 + row) / G, g = (row0 + row) - tk * G;
+    return a.out + (static_cast<size_t>(s.row0 + tok0 + tk) * a.H + kv * G + g) * kDim;
+  };
+  for (int row = warp; row < kGemmRows; row += 8) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row < rows) {
+      auto slot = [&](int c) {
+        return static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * kRows + row0 + row;
+      };
+      float m = -INFINITY;
+      for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, a.part_ml[slot(c)].x);
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+      const float ms = m == -INFINITY ? 0.0f : m;
+      float l = 0.0f;
+#pragma unroll 4
+      for (int c = c0; c <= c1; ++c) {
+        const float2 ml = a.part_ml[slot(c)];
+        const float4 x = *reinterpret_cast<const float4*>(a.part + slot(c) * kDim + 4 * lane);
+        if (ml.y == 0.0f) continue;            // the part saw nothing: its O is not used
+        const float f = fast_exp2(ml.x - ms);
+        l += f * ml.y;
+        o.x = fmaf(f, x.x, o.x);
+        o.y = fmaf(f, x.y, o.y);
+        o.z = fmaf(f, x.z, o.z);
+        o.w = fmaf(f, x.w, o.w);
+      }
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      o.x *= inv;
+      o.y *= inv;
+      o.z *= inv;
+      o.w *= inv;
+    }
+    if (rotate)
+      *reinterpret_cast<float4*>(As + row * kGemmPitch + 4 * lane) = o;
+    else if (row < rows)
+      *reinterpret_cast<uint2*>(out_row(row) + 4 * lane) =
+          make_uint2(pack_bf162(o.x, o.y), pack_bf162(o.z, o.w));
+  }
+  if (!rotate) return;
+  __syncthreads();
+  float acc[4][8];
+  rows_times(As, Ms, acc);
+  const int ty = tid >> 4, tx = tid & 15;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 4 * ty + i;
+    if (row >= rows) continue;
+    uint16_t* dst = out_row(row);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      *reinterpret_cast<uint2*>(dst + 64 * c + 4 * tx) =
+          make_uint2(pack_bf162(acc[i][4 * c], acc[i][4 * c + 1]),
+                     pack_bf162(acc[i][4 * c + 2], acc[i][4 * c + 3]));
+  }
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+template <bool INT2>
+cudaError_t launch(const PrefillArgs& a, int num_sms, cudaStream_t st) {
+  static bool attr_set[64] = {};       // per device: the attributes are per context
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<INT2>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::kAlloc);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(prefill_combine_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kGemmSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  prefill_kernel<INT2><<<num_sms, kThreads, Smem::kAlloc, st>>>(a);
+  if (num_sms > 1)
+    prefill_combine_kernel<<<dim3(num_sms - 1, kRows / kGemmRows), 256, kGemmSmem, st>>>(a, num_sms);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+PrefillWs prefill_ws_layout(int batch, int num_sms) {
+  PrefillWs w;
+  size_t o = 0;
+  w.prefix_off = o;
+  o += up256((static_cast<size_t>(batch) + 1) * 8);
+  w.ml_off = o;
+  o += up256(static_cast<size_t>(num_sms) * 2 * kRows * 8);
+  w.part_off = o;
+  o += up256(static_cast<size_t>(num_sms) * 2 * kRows * kDim * 4);
+  w.total = o;
+  return w;
+}
+
+cudaError_t launch_prefill_bank(const float* R, int Hkv, bool identity_q, uint16_t* hi, uint16_t* lo,
+                                uint16_t* rv, cudaStream_t st) {
+  prefill_bank_kernel<<<Hkv, 256, 0, st>>>(R, Hkv, identity_q, hi, lo, rv);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_prefill(const PrefillArgs& a, bool int2, int num_sms, cudaStream_t st) {
+  return int2 ? launch<true>(a, num_sms, st) : launch<false>(a, num_sms, st);
+}
+
+}  // namespace kvq

@@ -61,6 +61,10 @@ SIGNATURES = {
     "kvq_append_rope": ([_P, _P, _I, _P, _LL, _P, _LL, _P, _P, _I, _P, _I, _I, _P, _P, _P], _I),
     "kvq_bf16_append_rope": ([_P, _P, _I, _P, _LL, _P, _LL, _P, _P, _I, _P, _I, _I, _P, _P, _P],
                              _I),
+    "kvq_prefill_workspace_bytes": ([_P, _I, _I], _SZ),
+    "kvq_prefill": ([_P, _P, _I, _P, _LL, _P, _I, _P, _I, _P, _I, _P, _P, _SZ, _P], _I),
+    "kvq_bf16_prefill_workspace_bytes": ([_P, _I, _I], _SZ),
+    "kvq_bf16_prefill": ([_P, _P, _I, _P, _LL, _P, _I, _P, _I, _P, _I, _P, _P, _SZ, _P], _I),
     "kvq_get_status": ([_P, _P, _P], _I),
     "kvq_selftest_wait_timeout": ([_P, _I, _P], _I),
     "kvq_auto_splits": ([_P, _I, _I], _I),
@@ -448,6 +452,48 @@ def kvq_bf16_append_rope(h, pool, num_pool_pages, K, V, seq_idx, positions, page
     """kvq_bf16_append with the keys rotated on the way (arguments as kvq_append_rope)."""
     _append_rope("kvq_bf16_append_rope", h, pool, num_pool_pages, K, V, seq_idx, positions,
                  page_table, rope, rope_positions, stream)
+
+
+# ---- attention of a chunk of new tokens -----------------------------------------
+
+def kvq_prefill_workspace_bytes(h: Handle, batch: int, n: int) -> int:
+    return int(load_library().kvq_prefill_workspace_bytes(h.ptr, int(batch), int(n)))
+
+
+def kvq_bf16_prefill_workspace_bytes(h: Handle, batch: int, n: int) -> int:
+    return int(load_library().kvq_bf16_prefill_workspace_bytes(h.ptr, int(batch), int(n)))
+
+
+def _prefill(fn, h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace, stream):
+    n, H = int(q.shape[0]), int(h.layout.num_heads)
+    batch, max_pages = int(page_table.shape[0]), int(page_table.shape[1])
+    dev = _same_device(h, ("pool", pool), ("q", q), ("cu_q", cu_q), ("page_table", page_table),
+                       ("seq_lens", seq_lens), ("out", out), ("workspace", workspace))
+    pq, sq = _rows(q, "q", H)
+    if tuple(out.shape) != (n, H, 128):
+        raise ValueError(f"out: expected [{n}, {H}, 128], got {tuple(out.shape)}")
+    _check(fn, getattr(load_library(), fn)(
+        h.ptr, _ptr(pool, _U8, "pool"), int(num_pool_pages), pq, sq,
+        _vec(cu_q, batch + 1, "cu_q"), n, _ptr(page_table, _I32, "page_table"), max_pages,
+        _vec(seq_lens, batch, "seq_lens"), batch, _ptr(out, _BF16, "out"),
+        _ptr(workspace, _U8, "workspace"), int(workspace.numel()), _stream_of(stream, dev)))
+
+
+def kvq_prefill(h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace,
+                stream=None):
+    """Causal attention of each sequence's new tokens over its INT2 cache.  q: bf16 [n, H, 128]
+    (tokens may be strided); cu_q: int32 [B + 1], sequence b's rows are cu_q[b]:cu_q[b + 1], the
+    last of its seq_lens[b] positions; out: bf16 [n, H, 128]; workspace: uint8,
+    >= kvq_prefill_workspace_bytes(h, B, n)."""
+    _prefill("kvq_prefill", h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace,
+             stream)
+
+
+def kvq_bf16_prefill(h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace,
+                     stream=None):
+    """kvq_prefill over the BF16 cache (workspace: kvq_bf16_prefill_workspace_bytes)."""
+    _prefill("kvq_bf16_prefill", h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out,
+             workspace, stream)
 
 
 def kvq_dequant(h, pool, num_pool_pages, page_table, seq, start, length, K_out=None, V_out=None,
