@@ -13,7 +13,7 @@
 //   warps 0-3, 4-7 : softmax of the first and second 128 rows, a thread a row;
 //   warps 8-11     : page producers: codes (or bf16 fragments) -> fp16 (bf16)
 //                    operands in shared memory, two pages a warp, two stages;
-//   warp 12        : one thread issues every tcgen05.mma;
+//   warp 12        : its elected thread issues every tcgen05.mma;
 //   warp 13        : one thread finds the next item while this one is worked on.
 // Scores S = Q K^T and the output O live in TMEM (2 x 128 + 2 x 128 columns);
 // the weights P overwrite S's columns and feed the second product from TMEM.
@@ -83,28 +83,41 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
-}
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The issuing warp runs converged with warp-uniform operands (the tensor core takes
+// its descriptors from uniform registers); `one` is true in its elected lane.
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Operand descriptors differ in their low words only (the address); the high word:
+// 8-row groups 1024 bytes apart, descriptor version 1, 128-byte swizzle.
+constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                          uint32_t acc, uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 x, {%1, %6};\n\tmov.b64 y, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(one), "n"(kDescHi)
       : "memory");
 }
-#define KVQ_R32(v)                                                                              \
-  v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], v[8], v[9], v[10], v[11], v[12], v[13], v[14], \
-      v[15], v[16], v[17], v[18], v[19], v[20], v[21], v[22], v[23], v[24], v[25], v[26], v[27], \
-      v[28], v[29], v[30], v[31]
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                          uint32_t acc, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 y, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(one), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
 __device__ __forceinline__ void tc_ld32(uint32_t (&v)[32], uint32_t addr) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -172,12 +185,11 @@ __device__ __forceinline__ void tc_ld_row(uint32_t (&v)[4][32], uint32_t addr) {
 
 // Shared-memory operand of 128 rows x 128 columns of 16 bits, K-major, as two
 // 64-column halves of 128-byte rows with the 128-byte swizzle (16-byte chunk c of
-// row r at chunk c ^ (r & 7)); 8-row groups 1024 bytes apart.  `k` is the
-// 16-column step.
-__device__ __forceinline__ uint64_t tile_desc(uint32_t base, int k) {
-  const uint32_t addr = base + (k >> 2) * (kTileBytes / 2) + (k & 3) * 32;
-  return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
-         (2ull << 61);
+// row r at chunk c ^ (r & 7)); 8-row groups 1024 bytes apart.  The low word of its
+// descriptor, and what its 16-column step k adds to it.
+__device__ __forceinline__ uint32_t tile_desc(uint32_t base) { return (base >> 4) | (1u << 16); }
+__device__ __forceinline__ constexpr uint32_t desc_step(int k) {
+  return ((k >> 2) * (kTileBytes / 2) + (k & 3) * 32) >> 4;
 }
 // fp32 accumulate, M = N = 128, both operands fp16 (0) or bf16 (1), K-major
 constexpr uint32_t idesc_f16(int bf16) {
@@ -1037,6 +1049,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     // ======================= tensor-core issue, schedule =======================
     reg_shrink<kRegIssue>();
     uint32_t np0 = 0, np1 = 0;      // P_full phases
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), one = elect_one();
     long long cur = red[0], u_end = red[1], cur_b0 = red[3];
     int cur_b = static_cast<int>(red[2]);
     auto schedule = [&](Item& w) {
@@ -1083,69 +1096,83 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       __syncwarp();
       sync_cta();                   // Q is there
       const Steps<INT2> st(w, a);
-      if (warp == kMmaWarp && lane == 0 && st.tiles > 0) {
+      if (warp == kMmaWarp && st.tiles > 0) {
         constexpr uint32_t idesc = idesc_f16(INT2 ? 0 : 1), idesc_bf = idesc_f16(1);
-        const int nt = w.tokens * a.G > 128 ? 2 : 1;
+        const bool both = __shfl_sync(0xffffffffu, w.tokens * a.G > 128 ? 1 : 0, 0) != 0;
+        const int tiles = __shfl_sync(0xffffffffu, st.tiles, 0);
         auto full = [&](uint32_t k) {
-          alive = alive && mbar_wait_bounded(B(kFull + k % kStages), (k / kStages) & 1);
+          alive = alive && warp_wait(B(kFull + k % kStages), (k / kStages) & 1);
           tc_fence_after();
           return alive;
         };
         auto operand = [&](int t) {      // Q, P or o of row tile t
           uint32_t& n = t ? np1 : np0;
-          alive = alive && mbar_wait_bounded(B(kPFull + t), n & 1);
+          alive = alive && warp_wait(B(kPFull + t), n & 1);
           ++n;
           tc_fence_after();
           return alive;
         };
         // S_t = Q_t X^T, X a stage's K (or V) operand
-        auto product = [&](int t, uint32_t xb, uint32_t id, bool add) {
-          const uint32_t qb = sb + Smem::kQ + t * kTileBytes;
+        auto product = [&](int t, uint32_t x, uint32_t id, bool add) {
+          const uint32_t q = tile_desc(sb + Smem::kQ + t * kTileBytes);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            tc_mma_ss(tmem + t * 128, tile_desc(qb, k), tile_desc(xb, k), id, add || k != 0);
+            tc_mma_ss(tm + t * 128, q + desc_step(k), x + desc_step(k), id, add || k != 0, one);
         };
-        auto kbuf = [&](uint32_t k) { return sb + Smem::kK + (k % kStages) * kTileBytes; };
-        auto vbuf = [&](uint32_t k) { return sb + Smem::kV + (k % kStages) * kTileBytes; };
-        uint32_t k = it;
+        auto kdesc = [&](uint32_t k) { return tile_desc(sb + Smem::kK + (k % kStages) * kTileBytes); };
+        auto vdesc = [&](uint32_t k) { return tile_desc(sb + Smem::kV + (k % kStages) * kTileBytes); };
+        auto weighted = [&](int t, uint32_t v, bool add) {     // O_t += P_t V
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * k, v + desc_step(k), idesc,
+                      add || k != 0, one);
+        };
+        uint32_t k = __shfl_sync(0xffffffffu, it, 0);
         if (st.pre && full(k)) {
-          for (int t = 0; t < nt; ++t) {
-            product(t, kbuf(k), idesc_bf, false);
-            product(t, vbuf(k), idesc_bf, true);
-            tc_commit(B(kSFull + t));
-          }
-          tc_commit(B(kEmpty + k % kStages));
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (t == 0 || both) {
+              product(t, kdesc(k), idesc_bf, false);
+              product(t, vdesc(k), idesc_bf, true);
+              tc_commit(B(kSFull + t), one);
+            }
+          tc_commit(B(kEmpty + k % kStages), one);
           ++k;
         }
-        if (full(k))
-          for (int t = 0; t < nt; ++t) {
-            if (st.pre && !operand(t)) break;
-            product(t, kbuf(k), idesc, false);
-            tc_commit(B(kSFull + t));
-          }
-        for (int j = 0; j < st.tiles && alive; ++j, ++k) {
-          for (int t = 0; t < nt && alive; ++t) {
-            if (!operand(t)) break;
-            const uint32_t vb = vbuf(k);
+        if (full(k)) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * x, tile_desc(vb, x), idesc,
-                        (j | x) != 0);
-            if (t == nt - 1) tc_commit(B(kEmpty + k % kStages));
-            if (j + 1 < st.tiles) {
-              if (t == 0 && !full(k + 1)) break;
-              product(t, kbuf(k + 1), idesc, false);
+          for (int t = 0; t < 2; ++t)
+            if ((t == 0 || both) && (!st.pre || operand(t))) {
+              product(t, kdesc(k), idesc, false);
+              tc_commit(B(kSFull + t), one);
             }
-            tc_commit(B(kSFull + t));   // the next scores, or O
+        }
+        for (int j = 0; j < tiles && alive; ++j, ++k) {
+          const bool more = j + 1 < tiles;
+          if (!operand(0)) break;
+          weighted(0, vdesc(k), j != 0);
+          if (!both) tc_commit(B(kEmpty + k % kStages), one);
+          if (more) {
+            if (!full(k + 1)) break;
+            product(0, kdesc(k + 1), idesc, false);
+          }
+          tc_commit(B(kSFull + 0), one);   // the next scores, or O
+          if (both) {
+            if (!operand(1)) break;
+            weighted(1, vdesc(k), j != 0);
+            tc_commit(B(kEmpty + k % kStages), one);
+            if (more) product(1, kdesc(k + 1), idesc, false);
+            tc_commit(B(kSFull + 1), one);
           }
         }
         if (st.post && alive && full(k)) {
-          for (int t = 0; t < nt; ++t) {
-            if (!operand(t)) break;
-            product(t, kbuf(k), idesc, false);
-            tc_commit(B(kSFull + t));
-          }
-          tc_commit(B(kEmpty + k % kStages));
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if ((t == 0 || both) && operand(t)) {
+              product(t, kdesc(k), idesc, false);
+              tc_commit(B(kSFull + t), one);
+            }
+          tc_commit(B(kEmpty + k % kStages), one);
         }
       }
       __syncwarp();
@@ -1156,11 +1183,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 
   // nothing of this CTA may be in flight when it gives its TMEM back
   if (warp == kMmaWarp) {
-    if (lane == 0) {
-      tc_commit(B(kDrain));
-      (void)mbar_wait_bounded(B(kDrain), 0);
-    }
-    __syncwarp();
+    tc_commit(B(kDrain), elect_one());
+    (void)warp_wait(B(kDrain), 0);
   }
   tc_fence_before();
   sync_cta();
