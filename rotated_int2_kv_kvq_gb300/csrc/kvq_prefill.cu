@@ -42,6 +42,7 @@ constexpr int kProdWarp0 = 8, kMmaWarp = 12, kSchedWarp = 13;
 // 2 x 176 + 104 + 56 = 4 x 128
 constexpr int kRegSoftmax = 176, kRegProducer = 104, kRegIssue = 56;
 constexpr int kStages = 2;
+constexpr int kFlags = 4;                  // key tiles whose flags are kept
 constexpr int kTileBytes = 128 * 128 * 2;  // one 128 x 128 16-bit operand
 constexpr float kLazy = 8.0f;              // log2 growth of a row maximum before O is rescaled
 
@@ -50,9 +51,10 @@ struct Smem {
   static constexpr int kK = kQ + 2 * kTileBytes;            // [stages][32 KB]
   static constexpr int kV = kK + kStages * kTileBytes;      // [stages][32 KB]
   static constexpr int kBar = kV + kStages * kTileBytes;    // mbarriers
-  static constexpr int kBad = kBar + 128;                   // u32 [stages][4] tokens without a valid page
-  static constexpr int kPoison = kBad + 64;                 // u32 [stages][4] tokens with NaN / Inf values
-  static constexpr int kItem = kPoison + 64;                // Item [2]
+  static constexpr int kAny = kBar + 128;                   // u8 [2][kFlags][4]: a warp's pages set a bit of
+  static constexpr int kBad = kAny + 32;                    // u32 [kFlags][4] tokens without a valid page
+  static constexpr int kPoison = kBad + 64;                 // u32 [kFlags][4] tokens with NaN / Inf values
+  static constexpr int kItem = kPoison + 64 + 32;               // Item [2]
   static constexpr int kScan = kItem + 128;                 // long long [16]
   static constexpr int kTmem = kScan + 128;
   static constexpr int kBytes = kTmem + 16;
@@ -60,8 +62,9 @@ struct Smem {
 };
 
 // barrier indices
-enum { kFull = 0, kEmpty = kFull + kStages, kSFull = kEmpty + kStages, kPFull = kSFull + 2,
-       kDrain = kPFull + 2, kNumBars };
+enum { kKFull = 0, kKEmpty = kKFull + kStages, kVFull = kKEmpty + kStages, kVEmpty = kVFull + kStages,
+       kSFull = kVEmpty + kStages, kPFull = kSFull + 2, kDrain = kPFull + 2, kNumBars };
+static_assert(kNumBars * 8 <= 128, "barriers");
 
 struct Item {
   int b, kv;                // sequence, KV head
@@ -345,10 +348,8 @@ __device__ __forceinline__ void int2_clip(RawInt2& r, int i, int p, int key_end,
   }
 }
 
-// Two pages (pair `pw` of the tile) into the stage's K and V operands.  Returns
-// the lane's bits of tokens (16 pi + tau) whose values are not all finite; those
-// tokens' values are stored as zeros.
-__device__ __forceinline__ uint32_t int2_store(RawInt2& r, uint32_t ks, uint32_t vs, int pw, int lane) {
+// Two pages (pair `pw` of the tile) into a stage's K operand.
+__device__ __forceinline__ void int2_store_k(const RawInt2& r, uint32_t ks, int pw, int lane) {
   const int g64 = pw >> 1, pp = pw & 1;
   {
     const int tau7 = lane >> 2, t = lane & 3;
@@ -375,6 +376,13 @@ __device__ __forceinline__ uint32_t int2_store(RawInt2& r, uint32_t ks, uint32_t
       }
     }
   }
+}
+
+// The same pages into a stage's V operand.  Returns the lane's bits of tokens
+// (16 pi + tau) whose values are not all finite; those tokens' values are stored
+// as zeros.
+__device__ __forceinline__ uint32_t int2_store_v(const RawInt2& r, uint32_t vs, int pw, int lane) {
+  const int g64 = pw >> 1, pp = pw & 1;
   uint32_t poison = 0;
   {
     const int g = lane >> 2, t = lane & 3;
@@ -412,12 +420,11 @@ __device__ __forceinline__ uint32_t int2_store(RawInt2& r, uint32_t ks, uint32_t
 
 // BF16 pages: the record's 4-byte pairs are moved, not converted.  Keys: chunk
 // (th, h, w >> 2) of a token takes one word of each of four 16-byte loads.
-__device__ __forceinline__ uint32_t bf16_store(const uint8_t* const (&rec)[2], int p0, int key_end,
-                                               uint32_t ks, uint32_t vs, int pw, int lane) {
+__device__ __forceinline__ uint32_t bf16_store_v(const uint8_t* const (&rec)[2], int p0, int key_end,
+                                                 uint32_t vs, int pw, int lane) {
   const int g64 = pw >> 1, pp = pw & 1;
   uint32_t poison = 0;
   uint4 x[2][8];
-  // values first: both pages' eight words m are in flight together
 #pragma unroll
   for (int pi = 0; pi < 2; ++pi)
 #pragma unroll
@@ -481,6 +488,13 @@ __device__ __forceinline__ uint32_t bf16_store(const uint8_t* const (&rec)[2], i
       sts128(row + (16 * m + 8) * 128, x[0][m].y, x[0][m].w, x[1][m].y, x[1][m].w);
     }
   }
+  return poison;
+}
+
+__device__ __forceinline__ void bf16_store_k(const uint8_t* const (&rec)[2], uint32_t ks, int pw,
+                                             int lane) {
+  const int g64 = pw >> 1, pp = pw & 1;
+  uint4 x[2][8];
 #pragma unroll
   for (int pi = 0; pi < 2; ++pi)
 #pragma unroll
@@ -508,7 +522,6 @@ __device__ __forceinline__ uint32_t bf16_store(const uint8_t* const (&rec)[2], i
         }
       }
   }
-  return poison;
 }
 
 // A warp's bounded wait: all lanes have seen the phase complete, or none goes on
@@ -569,9 +582,12 @@ __device__ __forceinline__ void sync_cta() { asm volatile("barrier.sync 0;" ::: 
 
 // ---- the attention kernel ------------------------------------------------------------
 //
-// Steps of an item on the stages' line: [INT2: R_K] key tiles [INT2, whole item,
-// rotated output: R_V].  Row tile t's S_full completes once per step (scores or a
-// rotation's product) and once when O is complete; P_full once per product's
+// Steps of an item: [INT2: R_K] key tiles [INT2, whole item, rotated output: R_V].
+// Keys and values have stages and barriers of their own: K of a tile is free after
+// the second row tile's scores, two products before V, so that each operand's
+// producers have five products' time to refill a stage.  R_K takes a stage of both
+// (its two parts), R_V one of K.  Row tile t's S_full completes once per step
+// (scores or a rotation's product) and once when O is complete; P_full once per
 // operand from the softmax threads (Q, P of each tile, o).
 
 template <bool INT2>
@@ -581,7 +597,8 @@ struct Steps {
       : pre(INT2 && w.tiles > 0 ? 1 : 0),
         tiles(w.tiles),
         post(INT2 && w.tiles > 0 && w.part < 0 && a.rv_tile ? 1 : 0) {}
-  __device__ __forceinline__ int all() const { return pre + tiles + post; }
+  __device__ __forceinline__ int keys() const { return pre + tiles + post; }   // stages of K
+  __device__ __forceinline__ int values() const { return pre + tiles; }        // stages of V
 };
 
 // A wait gave up somewhere in the CTA: every role leaves after the same item.
@@ -623,26 +640,24 @@ __device__ __forceinline__ void load_q(const PrefillArgs& a, const Item& w, uint
   fence_proxy_async();
 }
 
+// Word k of the tile's positions that a row sees whose own position is `limit`.
+__device__ __forceinline__ uint32_t visible(int limit, int k) {
+  const int e = limit - 32 * k;          // last visible bit
+  return e >= 31 ? 0xffffffffu : e < 0 ? 0u : (2u << e) - 1u;
+}
+
 // One tile's scores (this thread's row, all 128 in registers) into weights: the
 // running maximum, the weights as 16-bit pairs into TMEM, their sum.
 template <bool INT2>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float scale, bool first,
-                                             int limit, const uint32_t* bw, const uint32_t* pz,
+                                             int limit, uint32_t any, const volatile uint32_t* bad,
                                              float& mref, float& l) {
   uint32_t v[4][32];
   tc_ld_row(v, ts);
-  const uint4 fb = *reinterpret_cast<const uint4*>(bw), fp = *reinterpret_cast<const uint4*>(pz);
-  const uint32_t flags = fb.x | fb.y | fb.z | fb.w | fp.x | fp.y | fp.z | fp.w;
-  if (__any_sync(0xffffffffu, limit < kTileKeys - 1) || flags != 0) {
-    const uint32_t b4[4] = {fb.x, fb.y, fb.z, fb.w}, p4[4] = {fp.x, fp.y, fp.z, fp.w};
+  if (__any_sync(0xffffffffu, limit < kTileKeys - 1) || any != 0) {
     uint32_t hide[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int e = limit - 32 * k;          // last visible bit of word k
-      const uint32_t vis = e >= 31 ? 0xffffffffu : e < 0 ? 0u : (2u << e) - 1u;
-      hide[k] = b4[k] | ~vis;
-      if (p4[k] & ~hide[k]) l = __int_as_float(0x7fffffff);   // sees a NaN / Inf value
-    }
+    for (int k = 0; k < 4; ++k) hide[k] = bad[k] | ~visible(limit, k);
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -712,19 +727,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const uint32_t bar = sb + Smem::kBar;
   Item* items = reinterpret_cast<Item*>(smem + Smem::kItem);
   long long* red = reinterpret_cast<long long*>(smem + Smem::kScan);
-  uint32_t* badw = reinterpret_cast<uint32_t*>(smem + Smem::kBad);
-  uint32_t* poisonw = reinterpret_cast<uint32_t*>(smem + Smem::kPoison);
+  volatile uint32_t* badw = reinterpret_cast<volatile uint32_t*>(smem + Smem::kBad);
+  volatile uint32_t* poisonw = reinterpret_cast<volatile uint32_t*>(smem + Smem::kPoison);
+  volatile uint32_t* anyw = reinterpret_cast<volatile uint32_t*>(smem + Smem::kAny);
+  volatile uint8_t* any8 = reinterpret_cast<volatile uint8_t*>(smem + Smem::kAny);
   volatile uint32_t* abort = reinterpret_cast<volatile uint32_t*>(smem + Smem::kTmem + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   auto B = [&](int i) { return bar + 8 * i; };
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(B(kFull + i), 4);
-      mbar_init(B(kEmpty + i), 1);
+      mbar_init(B(kKFull + i), 4);
+      mbar_init(B(kKEmpty + i), 1);
+      mbar_init(B(kVFull + i), 4);
+      mbar_init(B(kVEmpty + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(B(kSFull + i), 1);
+      mbar_init(B(kSFull + i), 2);
       mbar_init(B(kPFull + i), 4);
     }
     mbar_init(B(kDrain), 1);
@@ -781,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Smem::kTmem);
 
   bool alive = true;                // false after a wait gave up
-  uint32_t it = 0;                  // steps so far on the stages' line (stage and phase)
+  uint32_t itk = 0, itv = 0, itf = 0;   // K and V stages and flag slots used so far
 
   if (warp < kProdWarp0) {
     // ======================= softmax: a thread a row =======================
@@ -844,20 +863,29 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           give();
         }
         const int pos = w.pos0 + tok;
+        // The tile's flags, written before its operands were handed over: K's with the
+        // scores, V's one step later.  A slot is written again four tiles later, which
+        // this thread's weights of two tiles later precede.
+        auto check_values = [&](int j) {
+          const uint32_t f = (itf + j) % kFlags;
+          if (anyw[kFlags + f] == 0) return;
+          const int limit = pos - (w.tile_begin + j) * kTileKeys;
+          uint32_t seen = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) seen |= poisonw[4 * f + k] & visible(limit, k);
+          if (seen) l = __int_as_float(0x7fffffff);      // the row sees a NaN or an infinity
+        };
         for (int j = 0; j < st.tiles && alive; ++j) {
-          const uint32_t k = it + st.pre + j;
-          const int sg = k % kStages;
           if (!wait_s()) break;
-          // returns at once (the scores were made from that stage): it orders this thread's
-          // reads of the stage's flags behind the producers' writes
-          if (!(alive = warp_wait(B(kFull + sg), (k / kStages) & 1))) break;
+          const uint32_t f = (itf + j) % kFlags;
           if (some)
             softmax_tile<INT2>(ts, to, scale, j == 0,
-                               valid ? pos - (w.tile_begin + j) * kTileKeys : kTileKeys,
-                               badw + 4 * sg, poisonw + 4 * sg, mref, l);
+                               valid ? pos - (w.tile_begin + j) * kTileKeys : kTileKeys, anyw[f],
+                               badw + 4 * f, mref, l);
           give();
+          if (j > 0) check_values(j - 1);
         }
-        if (alive) wait_s();        // O is complete
+        if (alive && wait_s()) check_values(st.tiles - 1);        // O is complete
       }
       // ---- this part's result ----
       const size_t orow = static_cast<size_t>(w.row0 + tok) * a.H + w.kv * a.G + g;
@@ -933,7 +961,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         __syncwarp();
       }
       tc_fence_before();
-      it += st.all();
+      itk += st.keys();
+      itv += st.values();
+      itf += st.tiles;
       if (!item_end(alive, a, abort)) break;
     }
   } else if (warp < kMmaWarp) {
@@ -961,15 +991,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       auto address = [&](int id) -> const uint8_t* {
         return id >= 0 && id < a.num_pool_pages ? pool + static_cast<size_t>(id) * page_stride : nullptr;
       };
-      auto wait_empty = [&](uint32_t k) {
-        alive = warp_wait(B(kEmpty + k % kStages), ((k / kStages) & 1) ^ 1);
+      auto wait_empty = [&](int empty, uint32_t k) {
+        alive = alive && warp_wait(B(empty + k % kStages), ((k / kStages) & 1) ^ 1);
         return alive;
       };
-      auto give = [&](uint32_t k) {
+      auto give = [&](int full, uint32_t k) {
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(B(kFull + k % kStages));
+        if (lane == 0) mbar_arrive(B(full + k % kStages));
       };
+      auto kbuf = [&](uint32_t k) { return sb + Smem::kK + (k % kStages) * kTileBytes; };
+      auto vbuf = [&](uint32_t k) { return sb + Smem::kV + (k % kStages) * kTileBytes; };
       // 32 KB of a rotation's operand, already in the operand's layout
       auto copy_tile = [&](uint32_t dst, const uint16_t* src) {
         const uint4* s4 = reinterpret_cast<const uint4*>(src) + pw * 32 + lane;
@@ -994,16 +1026,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       sync_cta();                   // Q is there
       const size_t mat = static_cast<size_t>(w.kv) * kDim * kDim;
-      if (st.pre && wait_empty(it)) {
-        const int sg = it % kStages;
-        copy_tile(sb + Smem::kK + sg * kTileBytes, a.rk_hi + mat);
-        copy_tile(sb + Smem::kV + sg * kTileBytes, a.rk_lo + mat);
-        give(it);
+      if (st.pre && wait_empty(kKEmpty, itk) && wait_empty(kVEmpty, itv)) {
+        copy_tile(kbuf(itk), a.rk_hi + mat);
+        give(kKFull, itk);
+        copy_tile(vbuf(itv), a.rk_lo + mat);
+        give(kVFull, itv);
       }
       for (int j = 0; j < st.tiles && alive; ++j) {
-        const uint32_t k = it + st.pre + j;
-        const int sg = k % kStages;
-        if (!wait_empty(k)) break;
+        const uint32_t k = itk + st.pre + j, kv = itv + st.pre + j;
         const int p0 = ((w.tile_begin + j) * kTilePages + 2 * pw) * kPage;
         uint32_t bad = 0;
         const uint8_t* rec[2];
@@ -1012,9 +1042,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           rec[x] = address(id0[x]);
           if (!rec[x] && p0 + kPage * x < w.key_end) bad |= 0xffffu << (16 * x);
         }
-        const uint32_t ks = sb + Smem::kK + sg * kTileBytes, vs = sb + Smem::kV + sg * kTileBytes;
+        if (!wait_empty(kKEmpty, k)) break;
+        const uint32_t f = itf + j, slot = f % kFlags;
+        if (lane == 0) {
+          badw[4 * slot + pw] = bad;
+          any8[4 * slot + pw] = bad != 0;
+          if (bad) atomicOr(a.status, KVQ_STATUS_BAD_PAGE);
+        }
         uint32_t poison;
         if constexpr (INT2) {
+          int2_store_k(raw, kbuf(k), pw, lane);
+          give(kKFull, k);
           if (p0 + 2 * kPage > w.key_end) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) int2_clip(raw, x, p0 + kPage * x, w.key_end, lane);
@@ -1022,27 +1060,32 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           RawInt2 now = raw;
 #pragma unroll
           for (int x = 0; x < 2; ++x) int2_load(raw, x, address(id1[x]), lane);
-          poison = int2_store(now, ks, vs, pw, lane);
+          if (!wait_empty(kVEmpty, kv)) break;
+          poison = int2_store_v(now, vbuf(kv), pw, lane);
         } else {
-          poison = bf16_store(rec, p0, w.key_end, ks, vs, pw, lane);
+          bf16_store_k(rec, kbuf(k), pw, lane);
+          give(kKFull, k);
+          if (!wait_empty(kVEmpty, kv)) break;
+          poison = bf16_store_v(rec, p0, w.key_end, vbuf(kv), pw, lane);
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) id0[x] = id1[x];
         ids(j + 2, id1);
         poison = __reduce_or_sync(0xffffffffu, poison);
         if (lane == 0) {
-          badw[4 * sg + pw] = bad;
-          poisonw[4 * sg + pw] = poison;
-          if (bad) atomicOr(a.status, KVQ_STATUS_BAD_PAGE);
+          poisonw[4 * slot + pw] = poison;
+          any8[4 * (kFlags + slot) + pw] = poison != 0;
         }
-        give(k);
+        give(kVFull, kv);
       }
-      if (st.post && alive && wait_empty(it + st.pre + st.tiles)) {
-        const uint32_t k = it + st.pre + st.tiles;
-        copy_tile(sb + Smem::kK + (k % kStages) * kTileBytes, a.rv_tile + mat);
-        give(k);
+      if (st.post && alive && wait_empty(kKEmpty, itk + st.pre + st.tiles)) {
+        const uint32_t k = itk + st.pre + st.tiles;
+        copy_tile(kbuf(k), a.rv_tile + mat);
+        give(kKFull, k);
       }
-      it += st.all();
+      itk += st.keys();
+      itv += st.values();
+      itf += st.tiles;
       if (!item_end(alive, a, abort)) break;
     }
   } else {
@@ -1100,11 +1143,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         constexpr uint32_t idesc = idesc_f16(INT2 ? 0 : 1), idesc_bf = idesc_f16(1);
         const bool both = __shfl_sync(0xffffffffu, w.tokens * a.G > 128 ? 1 : 0, 0) != 0;
         const int tiles = __shfl_sync(0xffffffffu, st.tiles, 0);
-        auto full = [&](uint32_t k) {
-          alive = alive && warp_wait(B(kFull + k % kStages), (k / kStages) & 1);
+        auto full = [&](int bar, uint32_t k) {
+          alive = alive && warp_wait(B(bar + k % kStages), (k / kStages) & 1);
           tc_fence_after();
           return alive;
         };
+        // S_t (or O_t) once the products before are done; the plain arrival passes on what
+        // this warp saw of the producers' flags
+        auto scored = [&](int t) {
+          tc_commit(B(kSFull + t), one);
+          if (one) mbar_arrive(B(kSFull + t));
+        };
+        auto empty = [&](int bar, uint32_t k) { tc_commit(B(bar + k % kStages), one); };
         auto operand = [&](int t) {      // Q, P or o of row tile t
           uint32_t& n = t ? np1 : np0;
           alive = alive && warp_wait(B(kPFull + t), n & 1);
@@ -1127,56 +1177,67 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             tc_mma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * k, v + desc_step(k), idesc,
                       add || k != 0, one);
         };
-        uint32_t k = __shfl_sync(0xffffffffu, it, 0);
-        if (st.pre && full(k)) {
+        uint32_t k = __shfl_sync(0xffffffffu, itk, 0), v = __shfl_sync(0xffffffffu, itv, 0);
+        if (st.pre && full(kKFull, k) && full(kVFull, v)) {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
             if (t == 0 || both) {
               product(t, kdesc(k), idesc_bf, false);
-              product(t, vdesc(k), idesc_bf, true);
-              tc_commit(B(kSFull + t), one);
+              product(t, vdesc(v), idesc_bf, true);
+              scored(t);
             }
-          tc_commit(B(kEmpty + k % kStages), one);
+          empty(kKEmpty, k);
+          empty(kVEmpty, v);
           ++k;
+          ++v;
         }
-        if (full(k)) {
+        if (full(kKFull, k)) {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
             if ((t == 0 || both) && (!st.pre || operand(t))) {
               product(t, kdesc(k), idesc, false);
-              tc_commit(B(kSFull + t), one);
+              scored(t);
             }
+          empty(kKEmpty, k);
+          ++k;
         }
-        for (int j = 0; j < tiles && alive; ++j, ++k) {
+        for (int j = 0; j < tiles && alive; ++j, ++v) {
           const bool more = j + 1 < tiles;
-          if (!operand(0)) break;
-          weighted(0, vdesc(k), j != 0);
-          if (!both) tc_commit(B(kEmpty + k % kStages), one);
+          if (!operand(0) || !full(kVFull, v)) break;
+          weighted(0, vdesc(v), j != 0);
+          if (!both) empty(kVEmpty, v);
           if (more) {
-            if (!full(k + 1)) break;
-            product(0, kdesc(k + 1), idesc, false);
+            if (!full(kKFull, k)) break;
+            product(0, kdesc(k), idesc, false);
+            if (!both) empty(kKEmpty, k);
           }
-          tc_commit(B(kSFull + 0), one);   // the next scores, or O
+          scored(0);   // the next scores, or O
           if (both) {
             if (!operand(1)) break;
-            weighted(1, vdesc(k), j != 0);
-            tc_commit(B(kEmpty + k % kStages), one);
-            if (more) product(1, kdesc(k + 1), idesc, false);
-            tc_commit(B(kSFull + 1), one);
+            weighted(1, vdesc(v), j != 0);
+            empty(kVEmpty, v);
+            if (more) {
+              product(1, kdesc(k), idesc, false);
+              empty(kKEmpty, k);
+            }
+            scored(1);
           }
+          if (more) ++k;
         }
-        if (st.post && alive && full(k)) {
+        if (st.post && alive && full(kKFull, k)) {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
             if ((t == 0 || both) && operand(t)) {
               product(t, kdesc(k), idesc, false);
-              tc_commit(B(kSFull + t), one);
+              scored(t);
             }
-          tc_commit(B(kEmpty + k % kStages), one);
+          empty(kKEmpty, k);
         }
       }
       __syncwarp();
-      it += st.all();
+      itk += st.keys();
+      itv += st.values();
+      itf += st.tiles;
       if (!item_end(alive, a, abort)) break;
     }
   }
