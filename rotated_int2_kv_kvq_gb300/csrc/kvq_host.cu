@@ -402,7 +402,7 @@ int append_common(kvq_handle* h, bool int2, void* pool, int num_pool_pages, cons
 
 size_t prefill_bytes(const kvq_handle* h, int batch, int n) {
   if (!h || batch < 1 || batch > 65535 || n < 0) return 0;
-  return kvq::prefill_ws_layout(batch, h->num_sms).total;
+  return kvq::prefill_ws_layout(h->num_sms).total;
 }
 
 int prefill_common(kvq_handle* h, bool int2, const void* pool, int num_pool_pages,
@@ -419,7 +419,7 @@ int prefill_common(kvq_handle* h, bool int2, const void* pool, int num_pool_page
       reinterpret_cast<uintptr_t>(workspace) % 256)
     return KVQ_EINVAL;
   const bool rotate = int2 && !(h->L.flags & KVQ_OUT_ROTATED);
-  const kvq::PrefillWs w = kvq::prefill_ws_layout(batch, h->num_sms);
+  const kvq::PrefillWs w = kvq::prefill_ws_layout(h->num_sms);
   if (ws_bytes < w.total) return KVQ_ENOSPACE;
   kvq::DeviceGuard dev_guard(h->device);
   if (!dev_guard.ok()) return KVQ_ECUDA;
@@ -440,13 +440,12 @@ int prefill_common(kvq_handle* h, bool int2, const void* pool, int num_pool_page
   a.Hkv = h->L.num_kv_heads;
   a.G = h->G;
   a.out = out;
-  a.RVt = rotate ? h->bank + static_cast<size_t>(2) * Hkv * kDim * kDim : nullptr;
   a.rk_hi = int2 ? rot_operand(h->bank, Hkv, 0) : nullptr;
   a.rk_lo = int2 ? rot_operand(h->bank, Hkv, 1) : nullptr;
   a.rv_tile = rotate ? rot_operand(h->bank, Hkv, 2) : nullptr;
   a.log2_scale = h->sm_scale * 1.4426950408889634f;
   a.status = h->status;
-  a.prefix = reinterpret_cast<long long*>(ws + w.prefix_off);
+  a.cuts = reinterpret_cast<kvq::PrefillArgs::Cut*>(ws + w.cuts_off);
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml_off);
   a.part = reinterpret_cast<float*>(ws + w.part_off);
   return cuda_rc(kvq::launch_prefill(a, int2, h->num_sms, S(stream)));

@@ -132,23 +132,26 @@ struct PrefillArgs {
   const int32_t* seq_lens;
   int batch, H, Hkv, G;
   uint16_t* out;             // [n][H][128] bf16
-  const float* RVt;          // [Hkv][D][D] transposed, nullptr: the output stays in the cache's basis
   // the rotations as operands, [Hkv][128 x 128] each (INT2): R_K^T in two bf16
-  // parts, R_V in fp16 (nullptr with RVt)
+  // parts, R_V in fp16 (nullptr: the output stays in the cache's basis)
   const uint16_t* rk_hi;
   const uint16_t* rk_lo;
   const uint16_t* rv_tile;
   float log2_scale;
   uint32_t* status;
   // workspace
-  long long* prefix;         // [batch + 1] units before each sequence
+  struct Cut {               // the item that the border before a CTA's range cuts
+    int row0, rows, kv;      // first row of q / out; rows (token, head), 0: none; KV head
+    int first, last;         // the CTAs that have parts of it
+  };
+  Cut* cuts;                 // [CTAs]
   float2* part_ml;           // [2 * CTAs][256] (max, sum) of partial items
   float* part;               // [2 * CTAs][256][128]
 };
 struct PrefillWs {
-  size_t prefix_off, ml_off, part_off, total;
+  size_t cuts_off, ml_off, part_off, total;
 };
-PrefillWs prefill_ws_layout(int batch, int num_sms);
+PrefillWs prefill_ws_layout(int num_sms);
 cudaError_t launch_prefill(const PrefillArgs& a, bool int2, int num_sms, cudaStream_t st);
 // The operands of the prefill's rotations from R [2][Hkv][D][D]; identity_q: the
 // identity in R_K's place (the caller's queries are rotated already).

@@ -41,6 +41,7 @@ constexpr int kProdWarp0 = 8, kMmaWarp = 12, kSchedWarp = 13;
 // Registers a thread after the roles part, of the 128 that each is launched with:
 // 2 x 176 + 104 + 56 = 4 x 128
 constexpr int kRegSoftmax = 176, kRegProducer = 104, kRegIssue = 56;
+static_assert(2 * kRegSoftmax + kRegProducer + kRegIssue <= 4 * 128, "register split");
 constexpr int kStages = 2;
 constexpr int kFlags = 4;                  // key tiles whose flags are kept
 constexpr int kTileBytes = 128 * 128 * 2;  // one 128 x 128 16-bit operand
@@ -65,6 +66,8 @@ struct Smem {
 enum { kKFull = 0, kKEmpty = kKFull + kStages, kVFull = kKEmpty + kStages, kVEmpty = kVFull + kStages,
        kSFull = kVEmpty + kStages, kPFull = kSFull + 2, kDrain = kPFull + 2, kNumBars };
 static_assert(kNumBars * 8 <= 128, "barriers");
+
+using Cut = PrefillArgs::Cut;
 
 struct Item {
   int b, kv;                // sequence, KV head
@@ -355,10 +358,12 @@ __device__ __forceinline__ void int2_store_k(const RawInt2& r, uint32_t ks, int 
     const int tau7 = lane >> 2, t = lane & 3;
     const int prow = g64 * 64 + 16 * (tau7 >> 1) + 8 * pp + (tau7 & 1);
     const uint32_t base = ks + (t >> 1) * (kTileBytes / 2) + prow * 128;
+    uint4 kw = r.k[0];
+    uint2 km = r.km[0];
 #pragma unroll
     for (int pi = 0; pi < 2; ++pi) {
-      const uint32_t w[4] = {r.k[pi].x, r.k[pi].y, r.k[pi].z, r.k[pi].w};
-      const uint32_t m[2] = {r.km[pi].x, r.km[pi].y};
+      const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+      const uint32_t m[2] = {km.x, km.y};
 #pragma unroll
       for (int th = 0; th < 2; ++th) {
         const uint32_t s2 = dup_lo(m[th]), z2 = dup_hi(m[th]);
@@ -374,6 +379,8 @@ __device__ __forceinline__ void int2_store_k(const RawInt2& r, uint32_t ks, int 
                  dequant<6>(x, s2, z2), dequant<7>(x, s2, z2));
         }
       }
+      kw = r.k[1];
+      km = r.km[1];
     }
   }
 }
@@ -405,14 +412,20 @@ __device__ __forceinline__ uint32_t int2_store_v(const RawInt2& r, uint32_t vs, 
         s2[2 * pi + th] = s;
         z2[2 * pi + th] = z;
       }
-    const uint32_t row = vs + g64 * (kTileBytes / 2) + g * 128 + (((2 * t + pp) ^ g) << 4);
-#define KVQ_V(M)                                                                                  \
-  sts128(row + (16 * M) * 128, dequant<M>(r.v[0].x, s2[0], z2[0]), dequant<M>(r.v[0].z, s2[1], z2[1]), \
-         dequant<M>(r.v[1].x, s2[2], z2[2]), dequant<M>(r.v[1].z, s2[3], z2[3]));                 \
-  sts128(row + (16 * M + 8) * 128, dequant<M>(r.v[0].y, s2[0], z2[0]),                            \
-         dequant<M>(r.v[0].w, s2[1], z2[1]), dequant<M>(r.v[1].y, s2[2], z2[2]),                  \
-         dequant<M>(r.v[1].w, s2[3], z2[3]));
-    KVQ_V(0) KVQ_V(1) KVQ_V(2) KVQ_V(3) KVQ_V(4) KVQ_V(5) KVQ_V(6) KVQ_V(7)
+    uint32_t row = vs + g64 * (kTileBytes / 2) + g * 128 + (((2 * t + pp) ^ g) << 4);
+    uint32_t w0 = r.v[0].x, w1 = r.v[0].z, w2 = r.v[1].x, w3 = r.v[1].z;
+#define KVQ_V(M)                                                                        \
+  sts128(row + (16 * M) * 128, dequant<M>(w0, s2[0], z2[0]), dequant<M>(w1, s2[1], z2[1]), \
+         dequant<M>(w2, s2[2], z2[2]), dequant<M>(w3, s2[3], z2[3]));
+#pragma unroll
+    for (int dh = 0; dh < 2; ++dh) {
+      KVQ_V(0) KVQ_V(1) KVQ_V(2) KVQ_V(3) KVQ_V(4) KVQ_V(5) KVQ_V(6) KVQ_V(7)
+      row += 8 * 128;
+      w0 = r.v[0].y;
+      w1 = r.v[0].w;
+      w2 = r.v[1].y;
+      w3 = r.v[1].w;
+    }
 #undef KVQ_V
   }
   return poison;
@@ -524,10 +537,23 @@ __device__ __forceinline__ void bf16_store_k(const uint8_t* const (&rec)[2], uin
   }
 }
 
-// A warp's bounded wait: all lanes have seen the phase complete, or none goes on
-// (the tcgen05 loads and stores that follow are warp-wide).
+// A warp's wait for a phase, given up after two seconds of the global timer (its low
+// word wraps after 4.3): all lanes have seen the phase complete, or none goes on (the
+// tcgen05 loads and stores that follow are warp-wide).  Kept short: some twenty of
+// these lie between the roles' unrolled loops, which share the instruction cache.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+  bool ok = mbar_try_wait(bar, parity);
+  if (!__all_sync(0xffffffffu, ok)) {
+    uint32_t t0, t1;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t0));
+#pragma unroll 1
+    do {
+      ok = mbar_try_wait_sleep(bar, parity, 100000u);
+      asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t1));
+    } while (!__all_sync(0xffffffffu, ok) && t1 - t0 < 2000000000u);
+    ok = __all_sync(0xffffffffu, ok);
+  }
+  return ok;
 }
 
 // ---- fp32 pairs ---------------------------------------------------------------------
@@ -569,13 +595,11 @@ __device__ __forceinline__ void row_scale(const uint32_t (&v)[4][32], float& dow
   up = __uint_as_float(ex << 23);
 }
 
+// N registers a thread for the calling warpgroup, which was launched with 128.
 template <int N>
-__device__ __forceinline__ void reg_grow() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void reg_shrink() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+__device__ __forceinline__ void reg_set() {
+  if constexpr (N >= 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 // All of the CTA's threads, from whichever role's code.
 __device__ __forceinline__ void sync_cta() { asm volatile("barrier.sync 0;" ::: "memory"); }
@@ -650,11 +674,11 @@ __device__ __forceinline__ uint32_t visible(int limit, int k) {
 // running maximum, the weights as 16-bit pairs into TMEM, their sum.
 template <bool INT2>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float scale, bool first,
-                                             int limit, uint32_t any, const volatile uint32_t* bad,
+                                             int limit, bool edge, uint32_t any, const volatile uint32_t* bad,
                                              float& mref, float& l) {
   uint32_t v[4][32];
   tc_ld_row(v, ts);
-  if (__any_sync(0xffffffffu, limit < kTileKeys - 1) || any != 0) {
+  if (edge || any != 0) {
     uint32_t hide[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) hide[k] = bad[k] | ~visible(limit, k);
@@ -666,15 +690,15 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sca
         if ((hide[o >> 5] >> (o & 31)) & 1) v[c][i] = 0xff800000u;
       }
   }
-  float m0 = -INFINITY, m1 = -INFINITY;
+  float m[4];                    // four chains, a quarter of the columns each
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
+  for (int c = 0; c < 4; ++c) m[c] = fmaxf(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]));
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      m0 = max3(m0, __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
-      m1 = max3(m1, __uint_as_float(v[c][i + 2]), __uint_as_float(v[c][i + 3]));
-    }
-  const float mnew = fmaxf(mref, fmaxf(m0, m1) * scale);
+  for (int i = 2; i < 32; i += 2)
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      m[c] = max3(m[c], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
+  const float mnew = fmaxf(mref, fmaxf(max3(m[0], m[1], m[2]), m[3]) * scale);
   if (first) {
     mref = mnew;
   } else {
@@ -778,22 +802,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     if (tid == 0) {
       red[0] = u0;
       red[1] = u1;
+      red[4] = per;
     }
-    if (blockIdx.x == 0 || here) {
+    if (here) {
       long long u = before;
-      bool found = false;
       for (int b = b_lo; b < b_hi; ++b) {
-        if (blockIdx.x == 0) a.prefix[b] = u;
         const long long su = load_seq(a, b, TR).units * a.Hkv;
-        if (here && !found && u0 < u + su) {
-          found = true;
+        if (u0 < u + su) {
           red[2] = b;
           red[3] = u;
+          break;
         }
         u += su;
       }
     }
-    if (blockIdx.x == 0 && tid == 0) a.prefix[a.batch] = total;
   }
   __syncthreads();
   tc_fence_after();
@@ -804,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 
   if (warp < kProdWarp0) {
     // ======================= softmax: a thread a row =======================
-    reg_grow<kRegSoftmax>();
+    reg_set<kRegSoftmax>();
     const int t = warp >> 2, row = tid;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
@@ -876,12 +898,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           if (seen) l = __int_as_float(0x7fffffff);      // the row sees a NaN or an infinity
         };
         for (int j = 0; j < st.tiles && alive; ++j) {
+          const int limit = valid ? pos - (w.tile_begin + j) * kTileKeys : kTileKeys;
+          const bool edge = __any_sync(0xffffffffu, limit < kTileKeys - 1);
           if (!wait_s()) break;
           const uint32_t f = (itf + j) % kFlags;
           if (some)
-            softmax_tile<INT2>(ts, to, scale, j == 0,
-                               valid ? pos - (w.tile_begin + j) * kTileKeys : kTileKeys, anyw[f],
-                               badw + 4 * f, mref, l);
+            softmax_tile<INT2>(ts, to, scale, j == 0, limit, edge, anyw[f], badw + 4 * f, mref, l);
           give();
           if (j > 0) check_values(j - 1);
         }
@@ -968,7 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
   } else if (warp < kMmaWarp) {
     // ======================= producers =======================
-    reg_shrink<kRegProducer>();
+    reg_set<kRegProducer>();
     const int pw = warp - kProdWarp0;
     const size_t page_stride = static_cast<size_t>(a.Hkv) * (INT2 ? kInt2Rec : kBf16Rec);
     for (uint32_t i = 0;; ++i) {
@@ -1090,10 +1112,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
   } else {
     // ======================= tensor-core issue, schedule =======================
-    reg_shrink<kRegIssue>();
+    reg_set<kRegIssue>();
     uint32_t np0 = 0, np1 = 0;      // P_full phases
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), one = elect_one();
     long long cur = red[0], u_end = red[1], cur_b0 = red[3];
+    const long long per = red[4];
     int cur_b = static_cast<int>(red[2]);
     auto schedule = [&](Item& w) {
       const int TR = kRows / a.G;
@@ -1127,9 +1150,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       w.tiles = s.ok ? t1 - t0 : 0;
       w.part = (t0 == 0 && t1 == all) ? -1 : static_cast<int>(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0);
       w.done = 0;
+      if (t0 > 0) {       // an item that ranges before this one began: what joining it takes
+        Cut c;
+        c.row0 = w.row0;
+        c.rows = w.tokens * a.G;
+        c.kv = kv;
+        c.first = static_cast<int>((cur - t0) / per);
+        c.last = static_cast<int>((cur - t0 + all - 1) / per);
+        a.cuts[blockIdx.x] = c;
+      }
       cur += t1 - t0;
     };
-    if (warp == kSchedWarp && lane == 0) schedule(items[0]);
+    if (warp == kSchedWarp && lane == 0) {
+      a.cuts[blockIdx.x].rows = 0;
+      schedule(items[0]);
+    }
     __syncwarp();
     for (uint32_t i = 0;; ++i) {
       sync_cta();
@@ -1179,7 +1214,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         };
         uint32_t k = __shfl_sync(0xffffffffu, itk, 0), v = __shfl_sync(0xffffffffu, itv, 0);
         if (st.pre && full(kKFull, k) && full(kVFull, v)) {
-#pragma unroll
+#pragma unroll 1
           for (int t = 0; t < 2; ++t)
             if (t == 0 || both) {
               product(t, kdesc(k), idesc_bf, false);
@@ -1192,7 +1227,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           ++v;
         }
         if (full(kKFull, k)) {
-#pragma unroll
+#pragma unroll 1
           for (int t = 0; t < 2; ++t)
             if ((t == 0 || both) && (!st.pre || operand(t))) {
               product(t, kdesc(k), idesc, false);
@@ -1203,7 +1238,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
         for (int j = 0; j < tiles && alive; ++j, ++v) {
           const bool more = j + 1 < tiles;
-          if (!operand(0) || !full(kVFull, v)) break;
+          if (!full(kVFull, v) || !operand(0)) break;
           weighted(0, vdesc(v), j != 0);
           if (!both) empty(kVEmpty, v);
           if (more) {
@@ -1225,7 +1260,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           if (more) ++k;
         }
         if (st.post && alive && full(kKFull, k)) {
-#pragma unroll
+#pragma unroll 1
           for (int t = 0; t < 2; ++t)
             if ((t == 0 || both) && operand(t)) {
               product(t, kdesc(k), idesc, false);
@@ -1275,111 +1310,55 @@ __global__ void __launch_bounds__(256) prefill_bank_kernel(const float* R, int H
   }
 }
 
-// ---- rows times a 128 x 128 matrix -----------------------------------------------------
-// acc[i][c] = sum_j A[4 ty + i][j] * M[j][8 tx + c], A: [64][132] fp32 in shared
-// memory, M: [128][128] fp32 in shared memory; 256 threads = 16 (ty) x 16 (tx).
-constexpr int kGemmRows = 64;
-constexpr int kGemmPitch = kDim + 4;
-constexpr int kGemmSmem = (kGemmRows * kGemmPitch + kDim * kDim) * 4;
+// Joins the partial states of the items that range borders cut, rotates by R_V^T
+// (INT2) and writes bf16.  CTA x stands for the border before range x + 1, y for 16 of
+// the item's rows; the item's first border does the work.  A warp joins four rows
+// (lane: elements 4 lane .. + 3; the parts' loads are independent), then the 16 rows
+// go through mma.sync, 32 output columns a warp, as fp16 with a power of two a row
+// apart: a product of 16 x 128 x 128 is too small for tcgen05's 128 rows.
+constexpr int kJoinRows = 16;
+constexpr int kJoinPitch = kDim + 8;      // halves: rows 4 banks apart
 
-__device__ __forceinline__ void rows_times(const float* As, const float* Ms, float (&acc)[4][8]) {
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int c = 0; c < 8; ++c) acc[i][c] = 0.0f;
-#pragma unroll 8
-  for (int j = 0; j < kDim; ++j) {
-    const float4 m0 = *reinterpret_cast<const float4*>(Ms + j * kDim + 4 * tx);
-    const float4 m1 = *reinterpret_cast<const float4*>(Ms + j * kDim + 64 + 4 * tx);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = As[(4 * ty + i) * kGemmPitch + j];
-      acc[i][0] = fmaf(x, m0.x, acc[i][0]);
-      acc[i][1] = fmaf(x, m0.y, acc[i][1]);
-      acc[i][2] = fmaf(x, m0.z, acc[i][2]);
-      acc[i][3] = fmaf(x, m0.w, acc[i][3]);
-      acc[i][4] = fmaf(x, m1.x, acc[i][4]);
-      acc[i][5] = fmaf(x, m1.y, acc[i][5]);
-      acc[i][6] = fmaf(x, m1.z, acc[i][6]);
-      acc[i][7] = fmaf(x, m1.w, acc[i][7]);
-    }
-  }
-}
-
-// Joins the partial states of the items that range borders cut: CTA x stands for
-// the border between ranges x and x + 1, y for 64 of the item's rows; the item's
-// first border does the work.  Then R_V^T (INT2) in fp32, and bf16.
-__global__ void __launch_bounds__(256) prefill_combine_kernel(const __grid_constant__ PrefillArgs a,
-                                                              int num_ctas) {
-  extern __shared__ __align__(16) float sm[];
-  float* As = sm;
-  float* Ms = sm + kGemmRows * kGemmPitch;
-  const int G = a.G, tid = threadIdx.x, TR = kRows / G;
-  const long long total = a.prefix[a.batch];
-  const long long per = (total + num_ctas - 1) / num_ctas;
-  const long long u = per * (blockIdx.x + 1);            // the border, in units
-  if (u >= total) return;
-  int lo = 0, hi = a.batch - 1;                          // last sequence that starts at or before u
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.prefix[mid] <= u) lo = mid;
-    else hi = mid - 1;
-  }
-  const Seq s = load_seq(a, lo, TR);
-  const long long local = u - a.prefix[lo];
-  const int kv = static_cast<int>(local / s.units);
-  const long long r = local - kv * s.units;
-  int rt = 0, rt_hi = s.rts - 1;
-  while (rt < rt_hi) {
-    const int mid = (rt + rt_hi + 1) >> 1;
-    if (tiles_before(s, mid, TR) <= r) rt = mid;
-    else rt_hi = mid - 1;
-  }
-  const long long first = tiles_before(s, rt, TR);       // the item's first unit, in its head
-  if (first == r || !s.ok) return;                       // the border cuts nothing
-  const long long u0 = u - (r - first);
-  const int c0 = static_cast<int>(u0 / per);
-  if (c0 != static_cast<int>(blockIdx.x)) return;        // an earlier border of the item joins it
-  const int tok0 = rt * TR, tokens = min(TR, s.n - tok0);
-  const int row0 = blockIdx.y * kGemmRows, rows = min(tokens * G - row0, kGemmRows);
-  if (rows <= 0) return;
-  const int all = (s.p0 + tok0 + tokens + kTileKeys - 1) / kTileKeys;
-  const int c1 = static_cast<int>((u0 + all - 1) / per);
-  const bool rotate = a.RVt != nullptr;
-  if (rotate)
-    for (int idx = tid; idx < kDim * kDim / 4; idx += 256)
-      reinterpret_cast<float4*>(Ms)[idx] =
-          reinterpret_cast<const float4*>(a.RVt + static_cast<size_t>(kv) * kDim * kDim)[idx];
-  // a warp a row: lane holds elements 4 lane .. 4 lane + 3
-  const int warp = tid >> 5, lane = tid & 31;
+__global__ void __launch_bounds__(128) prefill_combine_kernel(const __grid_constant__ PrefillArgs a) {
+  __shared__ __align__(16) uint16_t os[kJoinRows * kJoinPitch];
+  __shared__ float ups[kJoinRows];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Cut c = a.cuts[blockIdx.x + 1];
+  const int row0 = blockIdx.y * kJoinRows;
+  if (c.rows <= row0 || c.first != static_cast<int>(blockIdx.x)) return;
+  const int rows = min(c.rows - row0, kJoinRows);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.G;
+  const bool rotate = a.rv_tile != nullptr;
+  auto slot = [&](int i, int row) {
+    return static_cast<size_t>(2 * i + (i == c.first ? 1 : 0)) * kRows + row0 + row;
+  };
   auto out_row = [&](int row) {
     const int tk = (row0 + row) / G, g = (row0 + row) - tk * G;
-    return a.out + (static_cast<size_t>(s.row0 + tok0 + tk) * a.H + kv * G + g) * kDim;
+    return a.out + (static_cast<size_t>(c.row0 + tk) * a.H + c.kv * G + g) * kDim;
   };
-  for (int row = warp; row < kGemmRows; row += 8) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int row = 4 * warp + x;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row < rows) {
-      auto slot = [&](int c) {
-        return static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * kRows + row0 + row;
-      };
       float m = -INFINITY;
-      for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, a.part_ml[slot(c)].x);
+      for (int i = c.first + lane; i <= c.last; i += 32) m = fmaxf(m, a.part_ml[slot(i, row)].x);
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+      for (int y = 16; y > 0; y >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
       const float ms = m == -INFINITY ? 0.0f : m;
       float l = 0.0f;
 #pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
-        const float2 ml = a.part_ml[slot(c)];
-        const float4 x = *reinterpret_cast<const float4*>(a.part + slot(c) * kDim + 4 * lane);
-        if (ml.y == 0.0f) continue;            // the part saw nothing: its O is not used
+      for (int i = c.first; i <= c.last; ++i) {
+        const float2 ml = a.part_ml[slot(i, row)];
+        const float4 v = *reinterpret_cast<const float4*>(a.part + slot(i, row) * kDim + 4 * lane);
         const float f = fast_exp2(ml.x - ms);
-        l += f * ml.y;
-        o.x = fmaf(f, x.x, o.x);
-        o.y = fmaf(f, x.y, o.y);
-        o.z = fmaf(f, x.z, o.z);
-        o.w = fmaf(f, x.w, o.w);
+        if (ml.y != 0.0f) {                    // else the part saw nothing: its O is not used
+          l += f * ml.y;
+          o.x = fmaf(f, v.x, o.x);
+          o.y = fmaf(f, v.y, o.y);
+          o.z = fmaf(f, v.z, o.z);
+          o.w = fmaf(f, v.w, o.w);
+        }
       }
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       o.x *= inv;
@@ -1387,27 +1366,52 @@ __global__ void __launch_bounds__(256) prefill_combine_kernel(const __grid_const
       o.z *= inv;
       o.w *= inv;
     }
-    if (rotate)
-      *reinterpret_cast<float4*>(As + row * kGemmPitch + 4 * lane) = o;
-    else if (row < rows)
+    if (rotate) {
+      float mx = fmaxf(fmaxf(fabsf(o.x), fabsf(o.y)), fmaxf(fabsf(o.z), fabsf(o.w)));
+#pragma unroll
+      for (int y = 16; y > 0; y >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+      const uint32_t ex = min((__float_as_uint(mx) >> 23) & 255u, 253u);
+      const float down = __uint_as_float((254u - ex) << 23);
+      *reinterpret_cast<uint2*>(os + row * kJoinPitch + 4 * lane) =
+          make_uint2(pack_half2(o.x * down, o.y * down), pack_half2(o.z * down, o.w * down));
+      if (lane == 0) ups[row] = __uint_as_float(ex << 23);
+    } else if (row < rows) {
       *reinterpret_cast<uint2*>(out_row(row) + 4 * lane) =
           make_uint2(pack_bf162(o.x, o.y), pack_bf162(o.z, o.w));
+    }
   }
   if (!rotate) return;
   __syncthreads();
-  float acc[4][8];
-  rows_times(As, Ms, acc);
-  const int ty = tid >> 4, tx = tid & 15;
+  // out[row][n] = sum_k o[row][k] R_V[n][k]: A from os, B straight from the operand tile
+  const int g = lane >> 2, t = lane & 3;
+  const uint16_t* rv = a.rv_tile + static_cast<size_t>(c.kv) * kDim * kDim;
+  float acc[4][4] = {};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = 4 * ty + i;
+  for (int k = 0; k < 8; ++k) {
+    const uint16_t* ar = os + g * kJoinPitch + 16 * k + 2 * t;
+    const uint32_t a0 = *reinterpret_cast<const uint32_t*>(ar);
+    const uint32_t a1 = *reinterpret_cast<const uint32_t*>(ar + 8 * kJoinPitch);
+    const uint32_t a2 = *reinterpret_cast<const uint32_t*>(ar + 8);
+    const uint32_t a3 = *reinterpret_cast<const uint32_t*>(ar + 8 * kJoinPitch + 8);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int row = 32 * warp + 8 * n + g;
+      const uint16_t* br = rv + (k >> 2) * (kTileBytes / 4) + row * 64 + 2 * t;
+      const int c0 = 2 * (k & 3);
+      const uint32_t b0 = *reinterpret_cast<const uint32_t*>(br + ((c0 ^ g) << 3));
+      const uint32_t b1 = *reinterpret_cast<const uint32_t*>(br + (((c0 + 1) ^ g) << 3));
+      mma_f16(acc[n], a0, a1, a2, a3, b0, b1);
+    }
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int row = g + 8 * half;
     if (row >= rows) continue;
-    uint16_t* dst = out_row(row);
+    const float up = ups[row];
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-      *reinterpret_cast<uint2*>(dst + 64 * c + 4 * tx) =
-          make_uint2(pack_bf162(acc[i][4 * c], acc[i][4 * c + 1]),
-                     pack_bf162(acc[i][4 * c + 2], acc[i][4 * c + 3]));
+    for (int n = 0; n < 4; ++n)
+      *reinterpret_cast<uint32_t*>(out_row(row) + 32 * warp + 8 * n + 2 * t) =
+          pack_bf162(acc[n][2 * half] * up, acc[n][2 * half + 1] * up);
   }
 }
 
@@ -1421,25 +1425,34 @@ cudaError_t launch(const PrefillArgs& a, int num_sms, cudaStream_t st) {
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
     cudaError_t e = cudaFuncSetAttribute(prefill_kernel<INT2>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::kAlloc);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(prefill_combine_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kGemmSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   prefill_kernel<INT2><<<num_sms, kThreads, Smem::kAlloc, st>>>(a);
-  if (num_sms > 1)
-    prefill_combine_kernel<<<dim3(num_sms - 1, kRows / kGemmRows), 256, kGemmSmem, st>>>(a, num_sms);
+  if (num_sms > 1) {
+    // a programmatic dependent: it is launched while the first kernel ends
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms - 1, kRows / kJoinRows);
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_combine_kernel, a);
+    if (e != cudaSuccess) return e;
+  }
   return cudaGetLastError();
 }
 
 }  // namespace
 
-PrefillWs prefill_ws_layout(int batch, int num_sms) {
+PrefillWs prefill_ws_layout(int num_sms) {
   PrefillWs w;
   size_t o = 0;
-  w.prefix_off = o;
-  o += up256((static_cast<size_t>(batch) + 1) * 8);
+  w.cuts_off = o;
+  o += up256(static_cast<size_t>(num_sms) * sizeof(PrefillArgs::Cut));
   w.ml_off = o;
   o += up256(static_cast<size_t>(num_sms) * 2 * kRows * 8);
   w.part_off = o;
