@@ -17,7 +17,9 @@
 //   warp 13        : one thread finds the next item while this one is worked on.
 // Scores S = Q K^T and the output O live in TMEM (2 x 128 + 2 x 128 columns);
 // the weights P overwrite S's columns and feed the second product from TMEM.
-// While one row tile's softmax runs, the tensor core works on the other's.
+// While one row tile's softmax runs, the tensor core works on the other's.  An item
+// of at most 128 rows has one row tile only: there both softmax groups take it, the
+// even and the odd key tiles, with an O each, joined at the item's end.
 //
 // INT2: the two rotations are tensor-core steps of the same pipeline, with the
 // rotation matrices (laid out once by kvq_set_rotation) in a stage's place of
@@ -58,7 +60,8 @@ struct Smem {
   static constexpr int kItem = kPoison + 64 + 32;               // Item [2]
   static constexpr int kScan = kItem + 128;                 // long long [16]
   static constexpr int kTmem = kScan + 128;
-  static constexpr int kBytes = kTmem + 16;
+  static constexpr int kPair = kTmem + 16;                  // float2 [128]: a split row's scale, then (max, sum) of its odd tiles
+  static constexpr int kBytes = kPair + 1024;
   static constexpr int kAlloc = kBytes + 1024;              // base rounded up to 1024
 };
 
@@ -620,7 +623,9 @@ struct Steps {
   __device__ __forceinline__ Steps(const Item& w, const PrefillArgs& a)
       : pre(INT2 && w.tiles > 0 ? 1 : 0),
         tiles(w.tiles),
-        post(INT2 && w.tiles > 0 && w.part < 0 && a.rv_tile ? 1 : 0) {}
+        post(INT2 && w.tiles > 0 && w.part < 0 && a.rv_tile ? 1 : 0),
+        split(w.tokens * a.G <= 128) {}
+  bool split;       // one row tile: its even and odd key tiles go to the two softmax groups
   __device__ __forceinline__ int keys() const { return pre + tiles + post; }   // stages of K
   __device__ __forceinline__ int values() const { return pre + tiles; }        // stages of V
 };
@@ -827,11 +832,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   if (warp < kProdWarp0) {
     // ======================= softmax: a thread a row =======================
     reg_set<kRegSoftmax>();
-    const int t = warp >> 2, row = tid;
+    const int t = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
-    uint8_t* qrow = smem + Smem::kQ + t * kTileBytes + (row & 127) * 128;
-    const int r7 = row & 7;
+    uint8_t* qrow = smem + Smem::kQ + t * kTileBytes + (tid & 127) * 128;
+    const int r7 = tid & 7;
+    float2* pair = reinterpret_cast<float2*>(smem + Smem::kPair) + (tid & 127);
     uint32_t ns = 0;                // S_full phases
     for (uint32_t i = 0;; ++i) {
       sync_cta();                   // the item is there
@@ -841,9 +847,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       sync_cta();                   // Q is there
       const Steps<INT2> st(w, a);
       const int rows = w.tokens * a.G;
+      const int row = st.split ? (tid & 127) : tid;
       const int tok = row / a.G, g = row - tok * a.G;
-      const bool valid = row < rows, some = warp * 32 < rows;
-      const bool active = t == 0 || rows > 128;
+      const bool valid = row < rows, some = (row & ~31) < rows;
+      const int first = st.split ? t : 0, step = st.split ? 2 : 1;    // this group's key tiles
       float mref = -INFINITY, l = 0.0f, scale = a.log2_scale;
       auto wait_s = [&]() {
         alive = warp_wait(B(kSFull + t), ns & 1);
@@ -856,8 +863,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         __syncwarp();
         if (lane == 0) mbar_arrive(B(kPFull + t));
       };
-      if (active && st.tiles > 0) {
-        if (INT2 && wait_s()) {
+      if (first < st.tiles) {
+        if (INT2 && (t == 0 || !st.split) && wait_s()) {
           if (some) {
             // q R_K -> fp16 Q, a power of two a row apart, in the pages' order of d
             uint32_t v[4][32];
@@ -865,6 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             float down, up;
             row_scale(v, down, up);
             scale *= up;
+            pair->x = scale;        // for the group of the odd tiles
             auto h2 = [&](int d) {
               return pack_half2(__uint_as_float(v[d >> 5][d & 31]) * down,
                                 __uint_as_float(v[d >> 5][(d & 31) + 1]) * down);
@@ -897,18 +905,47 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           for (int k = 0; k < 4; ++k) seen |= poisonw[4 * f + k] & visible(limit, k);
           if (seen) l = __int_as_float(0x7fffffff);      // the row sees a NaN or an infinity
         };
-        for (int j = 0; j < st.tiles && alive; ++j) {
+        for (int j = first; j < st.tiles && alive; j += step) {
           const int limit = valid ? pos - (w.tile_begin + j) * kTileKeys : kTileKeys;
           const bool edge = __any_sync(0xffffffffu, limit < kTileKeys - 1);
           if (!wait_s()) break;
+          if (INT2 && st.split && j == 1) scale = pair->x;
           const uint32_t f = (itf + j) % kFlags;
+          if (st.split && j > first) check_values(j - step);
           if (some)
-            softmax_tile<INT2>(ts, to, scale, j == 0, limit, edge, anyw[f], badw + 4 * f, mref, l);
+            softmax_tile<INT2>(ts, to, scale, j == first, limit, edge, anyw[f], badw + 4 * f, mref, l);
           give();
-          if (j > 0) check_values(j - 1);
+          if (!st.split && j > first) check_values(j - step);
         }
-        if (alive && wait_s()) check_values(st.tiles - 1);        // O is complete
+        // O is complete; the last of this group's tiles
+        if (alive && wait_s()) check_values(st.tiles - 1 - (st.tiles - 1 - first) % step);
       }
+      if (st.split && st.tiles > 1) {
+        // the odd tiles' state to the even tiles' thread of the same row (same TMEM lane)
+        if (t == 1) *pair = make_float2(l == 0.0f ? -INFINITY : mref, l);
+        tc_fence_before();
+        asm volatile("barrier.sync 1, 256;" ::: "memory");
+        tc_fence_after();
+        if (t == 0 && alive && some) {
+          const float2 o = *pair;
+          const float mx = fmaxf(mref, o.x), ms = mx == -INFINITY ? 0.0f : mx;
+          const float f0 = fast_exp2(mref - ms), f1 = fast_exp2(o.x - ms);
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t x[16], y[16];
+            tc_ld16(x, to + 16 * c);
+            tc_ld16(y, to + 128 + 16 * c);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              x[e] = __float_as_uint(__uint_as_float(x[e]) * f0 + __uint_as_float(y[e]) * f1);
+            tc_st16(to + 16 * c, x);
+          }
+          tc_wait_st();
+          l = l * f0 + o.y * f1;
+          mref = mx;
+        }
+      }
+      const bool active = t == 0 || !st.split;
       // ---- this part's result ----
       const size_t orow = static_cast<size_t>(w.row0 + tok) * a.H + w.kv * a.G + g;
       if (active && alive && w.part >= 0) {
@@ -1176,7 +1213,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const Steps<INT2> st(w, a);
       if (warp == kMmaWarp && st.tiles > 0) {
         constexpr uint32_t idesc = idesc_f16(INT2 ? 0 : 1), idesc_bf = idesc_f16(1);
-        const bool both = __shfl_sync(0xffffffffu, w.tokens * a.G > 128 ? 1 : 0, 0) != 0;
+        const bool both = __shfl_sync(0xffffffffu, st.split ? 0 : 1, 0) != 0;
         const int tiles = __shfl_sync(0xffffffffu, st.tiles, 0);
         auto full = [&](int bar, uint32_t k) {
           alive = alive && warp_wait(B(bar + k % kStages), (k / kStages) & 1);
@@ -1199,7 +1236,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         };
         // S_t = Q_t X^T, X a stage's K (or V) operand
         auto product = [&](int t, uint32_t x, uint32_t id, bool add) {
-          const uint32_t q = tile_desc(sb + Smem::kQ + t * kTileBytes);
+          const uint32_t q = tile_desc(sb + Smem::kQ + (both ? t : 0) * kTileBytes);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             tc_mma_ss(tm + t * 128, q + desc_step(k), x + desc_step(k), id, add || k != 0, one);
@@ -1226,38 +1263,55 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           ++k;
           ++v;
         }
-        if (full(kKFull, k)) {
-#pragma unroll 1
-          for (int t = 0; t < 2; ++t)
-            if ((t == 0 || both) && (!st.pre || operand(t))) {
-              product(t, kdesc(k), idesc, false);
-              scored(t);
+        if (!both) {
+          // tile j to group j % 2; two tiles' scores ahead of their weights
+          if (st.pre) operand(0);
+          for (int j = -2; j < tiles && alive; ++j) {
+            const int t = j & 1;
+            if (j >= 0) {
+              if (!full(kVFull, v) || !operand(t)) break;
+              weighted(t, vdesc(v), j > 1);
+              empty(kVEmpty, v);
+              ++v;
             }
-          empty(kKEmpty, k);
-          ++k;
-        }
-        for (int j = 0; j < tiles && alive; ++j, ++v) {
-          const bool more = j + 1 < tiles;
-          if (!full(kVFull, v) || !operand(0)) break;
-          weighted(0, vdesc(v), j != 0);
-          if (!both) empty(kVEmpty, v);
-          if (more) {
-            if (!full(kKFull, k)) break;
-            product(0, kdesc(k), idesc, false);
-            if (!both) empty(kKEmpty, k);
+            if (j + 2 < tiles) {
+              if (!full(kKFull, k)) break;
+              product(t, kdesc(k), idesc, false);
+              empty(kKEmpty, k);
+              ++k;
+            }
+            if (j >= 0 || j + 2 < tiles) scored(t);     // the next scores, or O
           }
-          scored(0);   // the next scores, or O
-          if (both) {
+        } else {
+          if (full(kKFull, k)) {
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t)
+              if (!st.pre || operand(t)) {
+                product(t, kdesc(k), idesc, false);
+                scored(t);
+              }
+            empty(kKEmpty, k);
+            ++k;
+          }
+          for (int j = 0; j < tiles && alive; ++j, ++v) {
+            const bool more = j + 1 < tiles;
+            if (!full(kVFull, v) || !operand(0)) break;
+            weighted(0, vdesc(v), j != 0);
+            if (more) {
+              if (!full(kKFull, k)) break;
+              product(0, kdesc(k), idesc, false);
+            }
+            scored(0);   // the next scores, or O
             if (!operand(1)) break;
             weighted(1, vdesc(v), j != 0);
             empty(kVEmpty, v);
             if (more) {
               product(1, kdesc(k), idesc, false);
               empty(kKEmpty, k);
+              ++k;
             }
             scored(1);
           }
-          if (more) ++k;
         }
         if (st.post && alive && full(kKFull, k)) {
 #pragma unroll 1
