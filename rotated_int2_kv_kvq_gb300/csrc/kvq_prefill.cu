@@ -54,12 +54,13 @@ struct Smem {
   static constexpr int kK = kQ + 2 * kTileBytes;            // [stages][32 KB]
   static constexpr int kV = kK + kStages * kTileBytes;      // [stages][32 KB]
   static constexpr int kBar = kV + kStages * kTileBytes;    // mbarriers
-  static constexpr int kAny = kBar + 128;                   // u8 [2][kFlags][4]: a warp's pages set a bit of
+  static constexpr int kAny = kBar + 160;                   // u8 [2][kFlags][4]: a warp's pages set a bit of
   static constexpr int kBad = kAny + 32;                    // u32 [kFlags][4] tokens without a valid page
   static constexpr int kPoison = kBad + 64;                 // u32 [kFlags][4] tokens with NaN / Inf values
   static constexpr int kItem = kPoison + 64 + 32;               // Item [2]
   static constexpr int kScan = kItem + 128;                 // long long [16]
-  static constexpr int kTmem = kScan + 128;
+  static constexpr int kLine = kScan + 128;                 // Line
+  static constexpr int kTmem = kLine + 48;
   static constexpr int kPair = kTmem + 16;                  // float2 [128]: a split row's scale, then (max, sum) of its odd tiles
   static constexpr int kBytes = kPair + 1024;
   static constexpr int kAlloc = kBytes + 1024;              // base rounded up to 1024
@@ -68,9 +69,17 @@ struct Smem {
 // barrier indices
 enum { kKFull = 0, kKEmpty = kKFull + kStages, kVFull = kKEmpty + kStages, kVEmpty = kVFull + kStages,
        kSFull = kVEmpty + kStages, kPFull = kSFull + 2, kDrain = kPFull + 2, kNumBars };
-static_assert(kNumBars * 8 <= 128, "barriers");
+static_assert(kNumBars * 8 <= 160, "barriers");
 
 using Cut = PrefillArgs::Cut;
+
+struct Line {               // a CTA's range of the line of work
+  long long cur, end;       // its next unit, its end
+  long long per;            // units per range
+  long long b_first;        // first unit of sequence b
+  int b;                    // the sequence of `cur` (or one before it)
+};
+static_assert(sizeof(Line) <= 48, "Line");
 
 struct Item {
   int b, kv;                // sequence, KV head
@@ -243,7 +252,7 @@ __device__ __forceinline__ long long tiles_before(const Seq& s, int k, int TR) {
   const long long a = (s.p0 + 127) >> 7, kk = k;
   return a * kk + (TR >> 7) * (kk * (kk + 1) >> 1);
 }
-__device__ __forceinline__ Seq load_seq(const PrefillArgs& a, int b, int TR) {
+__device__ __noinline__ Seq load_seq(const PrefillArgs& a, int b, int TR) {
   Seq s;
   const int r0 = a.cu_q[b], r1 = a.cu_q[b + 1];
   const int len = a.seq_lens[b];
@@ -279,6 +288,7 @@ __device__ __forceinline__ long long block_prefix(long long v, long long* red, l
   if (lane == 31) red[w] = x;
   __syncthreads();
   long long before = 0, sum = 0;
+#pragma unroll 1
   for (int i = 0; i < kThreads / 32; ++i) {
     if (i < w) before += red[i];
     sum += red[i];
@@ -354,36 +364,37 @@ __device__ __forceinline__ void int2_clip(RawInt2& r, int i, int p, int key_end,
   }
 }
 
+// Where this lane's part of a key page's tokens goes: chunk j of the token pair (pi, th)
+// at key_at(base, j, 4 pi + 2 th).  The swizzle is an exclusive or, so the lane's part
+// of it is in the base and the rest is a constant.
+__device__ __forceinline__ uint32_t key_base(uint32_t ks, int pair, int lane) {
+  const int tau7 = lane >> 2, t = lane & 3;
+  const int row = 64 * (pair >> 1) + 16 * (tau7 >> 1) + 8 * (pair & 1) + (tau7 & 1);
+  return ks + (t >> 1) * (kTileBytes / 2) + row * 128 +
+         (((4 * (t & 1)) ^ (2 * (t >> 1)) ^ (tau7 & 1)) << 4);
+}
+__device__ __forceinline__ uint32_t key_at(uint32_t base, int j, int r) {
+  return (base ^ ((j ^ r) << 4)) + r * 128;
+}
+
 // Two pages (pair `pw` of the tile) into a stage's K operand.
 __device__ __forceinline__ void int2_store_k(const RawInt2& r, uint32_t ks, int pw, int lane) {
-  const int g64 = pw >> 1, pp = pw & 1;
-  {
-    const int tau7 = lane >> 2, t = lane & 3;
-    const int prow = g64 * 64 + 16 * (tau7 >> 1) + 8 * pp + (tau7 & 1);
-    const uint32_t base = ks + (t >> 1) * (kTileBytes / 2) + prow * 128;
-    uint4 kw = r.k[0];
-    uint2 km = r.km[0];
+  const uint32_t base = key_base(ks, pw, lane);
 #pragma unroll
-    for (int pi = 0; pi < 2; ++pi) {
-      const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
-      const uint32_t m[2] = {km.x, km.y};
+  for (int pi = 0; pi < 2; ++pi) {
+    const uint32_t w[4] = {r.k[pi].x, r.k[pi].y, r.k[pi].z, r.k[pi].w};
+    const uint32_t m[2] = {r.km[pi].x, r.km[pi].y};
 #pragma unroll
-      for (int th = 0; th < 2; ++th) {
-        const uint32_t s2 = dup_lo(m[th]), z2 = dup_hi(m[th]);
-        const uint32_t row = base + (4 * pi + 2 * th) * 128;
-        const int r7 = 4 * pi + 2 * th + (tau7 & 1);
+    for (int th = 0; th < 2; ++th) {
+      const uint32_t s2 = dup_lo(m[th]), z2 = dup_hi(m[th]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t x = w[2 * th + h];
-          const int c0 = 4 * (t & 1) + ((2 * h) ^ (2 * (t >> 1)));
-          sts128(row + ((c0 ^ r7) << 4), dequant<0>(x, s2, z2), dequant<1>(x, s2, z2),
-                 dequant<2>(x, s2, z2), dequant<3>(x, s2, z2));
-          sts128(row + (((c0 + 1) ^ r7) << 4), dequant<4>(x, s2, z2), dequant<5>(x, s2, z2),
-                 dequant<6>(x, s2, z2), dequant<7>(x, s2, z2));
-        }
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t x = w[2 * th + h];
+        sts128(key_at(base, 2 * h, 4 * pi + 2 * th), dequant<0>(x, s2, z2), dequant<1>(x, s2, z2),
+               dequant<2>(x, s2, z2), dequant<3>(x, s2, z2));
+        sts128(key_at(base, 2 * h + 1, 4 * pi + 2 * th), dequant<4>(x, s2, z2),
+               dequant<5>(x, s2, z2), dequant<6>(x, s2, z2), dequant<7>(x, s2, z2));
       }
-      kw = r.k[1];
-      km = r.km[1];
     }
   }
 }
@@ -434,116 +445,101 @@ __device__ __forceinline__ uint32_t int2_store_v(const RawInt2& r, uint32_t vs, 
   return poison;
 }
 
-// BF16 pages: the record's 4-byte pairs are moved, not converted.  Keys: chunk
-// (th, h, w >> 2) of a token takes one word of each of four 16-byte loads.
-__device__ __forceinline__ uint32_t bf16_store_v(const uint8_t* const (&rec)[2], int p0, int key_end,
-                                                 uint32_t vs, int pw, int lane) {
-  const int g64 = pw >> 1, pp = pw & 1;
-  uint32_t poison = 0;
-  uint4 x[2][8];
+// BF16 pages: the record's 4-byte pairs are moved, not converted.  A lane's eight
+// loads of a page's keys (or of half a page pair's values) are in flight while the
+// eight before are stored.
+__device__ __forceinline__ void bf16_load_key(uint4 (&x)[8], const uint8_t* rec, int lane) {
 #pragma unroll
-  for (int pi = 0; pi < 2; ++pi)
-#pragma unroll
-    for (int m = 0; m < 8; ++m)
-      x[pi][m] = rec[pi] ? *reinterpret_cast<const uint4*>(rec[pi] + 4096 + 512 * m + 16 * lane)
-                         : make_uint4(0, 0, 0, 0);
-  {
-    const int g = lane >> 2, t = lane & 3;
-    // positions >= key_end: zeros
-    uint32_t keep[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int p = p0 + 16 * (i >> 1) + 8 * (i & 1) + 2 * t;
-      keep[i] = (p < key_end ? 0xffffu : 0u) | (p + 1 < key_end ? 0xffff0000u : 0u);
-    }
-    // largest |value| of each token pair (NaN counts as larger)
-    uint32_t big[4] = {0, 0, 0, 0};
-    auto maxabs = [](uint32_t a, uint32_t b) {
-      uint32_t d;
-      b &= 0x7fff7fffu;
-      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-      return d;
-    };
-#pragma unroll
-    for (int pi = 0; pi < 2; ++pi)
-#pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        x[pi][m].x &= keep[2 * pi];
-        x[pi][m].y &= keep[2 * pi];
-        x[pi][m].z &= keep[2 * pi + 1];
-        x[pi][m].w &= keep[2 * pi + 1];
-        big[2 * pi] = maxabs(maxabs(big[2 * pi], x[pi][m].x), x[pi][m].y);
-        big[2 * pi + 1] = maxabs(maxabs(big[2 * pi + 1], x[pi][m].z), x[pi][m].w);
-      }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t bad = ((big[i] & 0x7f80u) == 0x7f80u ? 1u : 0u) |
-                     ((big[i] & 0x7f800000u) == 0x7f800000u ? 2u : 0u);
-      // a token is dropped as a whole: by every lane if any lane saw it
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-      if (bad) {
-        const uint32_t k2 = ((bad & 1) ? 0u : 0xffffu) | ((bad & 2) ? 0u : 0xffff0000u);
-#pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          if (i & 1) {
-            x[i >> 1][m].z &= k2;
-            x[i >> 1][m].w &= k2;
-          } else {
-            x[i >> 1][m].x &= k2;
-            x[i >> 1][m].y &= k2;
-          }
-        }
-        poison |= bad << (16 * (i >> 1) + 8 * (i & 1) + 2 * t);
-      }
-    }
-    const uint32_t row = vs + g64 * (kTileBytes / 2) + g * 128 + (((2 * t + pp) ^ g) << 4);
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      sts128(row + (16 * m) * 128, x[0][m].x, x[0][m].z, x[1][m].x, x[1][m].z);
-      sts128(row + (16 * m + 8) * 128, x[0][m].y, x[0][m].w, x[1][m].y, x[1][m].w);
-    }
-  }
-  return poison;
+  for (int w = 0; w < 8; ++w)
+    x[w] = rec ? *reinterpret_cast<const uint4*>(rec + 512 * w + 16 * lane) : make_uint4(0, 0, 0, 0);
 }
 
-__device__ __forceinline__ void bf16_store_k(const uint8_t* const (&rec)[2], uint32_t ks, int pw,
-                                             int lane) {
-  const int g64 = pw >> 1, pp = pw & 1;
-  uint4 x[2][8];
+// A key page: chunk (th, h, w >> 2) of a token takes one word of each of four loads.
+__device__ __forceinline__ void bf16_store_key(const uint4 (&x)[8], uint32_t base, int pi) {
 #pragma unroll
-  for (int pi = 0; pi < 2; ++pi)
+  for (int th = 0; th < 2; ++th)
 #pragma unroll
-    for (int w = 0; w < 8; ++w)
-      x[pi][w] = rec[pi] ? *reinterpret_cast<const uint4*>(rec[pi] + 512 * w + 16 * lane)
-                         : make_uint4(0, 0, 0, 0);
-  {
-    const int tau7 = lane >> 2, t = lane & 3;
-    const int prow = g64 * 64 + 16 * (tau7 >> 1) + 8 * pp + (tau7 & 1);
-    const uint32_t base = ks + (t >> 1) * (kTileBytes / 2) + prow * 128;
+    for (int j = 0; j < 4; ++j) {           // j = 2h + (w >> 2)
+      auto word = [&](int w) {
+        const uint4& q = x[4 * (j & 1) + w];
+        return (j >> 1) ? (th ? q.w : q.z) : (th ? q.y : q.x);
+      };
+      sts128(key_at(base, j, 4 * pi + 2 * th), word(0), word(1), word(2), word(3));
+    }
+}
+
+// Elements 64 hf .. 64 hf + 63 of two pages' values.
+__device__ __forceinline__ void bf16_load_value(uint4 (&x)[8], const uint8_t* const (&rec)[2], int hf,
+                                                int lane) {
 #pragma unroll
-    for (int pi = 0; pi < 2; ++pi)
+  for (int i = 0; i < 8; ++i)             // page i & 1, m = 4 hf + (i >> 1)
+    x[i] = rec[i & 1] ? *reinterpret_cast<const uint4*>(rec[i & 1] + 4096 + 512 * (4 * hf + (i >> 1)) +
+                                                        16 * lane)
+                      : make_uint4(0, 0, 0, 0);
+}
+
+// NaN and infinite elements of a word become zeros; bits of the halves that had one.
+__device__ __forceinline__ uint32_t bf16_clean(uint32_t& x) {
+  const uint32_t bad = ((x & 0x7f80u) == 0x7f80u ? 1u : 0u) | ((x & 0x7f800000u) == 0x7f800000u ? 2u : 0u);
+  x &= ((bad & 1) ? 0u : 0xffffu) | ((bad & 2) ? 0u : 0xffff0000u);
+  return bad;
+}
+
+// Returns the lane's bits of tokens (16 pi + tau) that have a NaN or an infinity here.
+__device__ __forceinline__ uint32_t bf16_store_value(uint4 (&x)[8], int p0, int key_end, uint32_t vs,
+                                                     int pw, int hf, int lane) {
+  const int g64 = pw >> 1, pp = pw & 1, g = lane >> 2, t = lane & 3;
+  if (p0 + 2 * kPage > key_end) {           // positions >= key_end: zeros
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int th = 0; th < 2; ++th) {
-        const uint32_t row = base + (4 * pi + 2 * th) * 128;
-        const int r7 = 4 * pi + 2 * th + (tau7 & 1);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {           // j = 2h + (w >> 2)
-          const int c = 4 * (t & 1) + (j ^ (2 * (t >> 1)));
-          auto word = [&](int w) {
-            const uint4& q = x[pi][4 * (j & 1) + w];
-            return (j >> 1) ? (th ? q.w : q.z) : (th ? q.y : q.x);
-          };
-          sts128(row + ((c ^ r7) << 4), word(0), word(1), word(2), word(3));
+        const int p = p0 + 16 * (i & 1) + 8 * th + 2 * t;
+        const uint32_t keep = (p < key_end ? 0xffffu : 0u) | (p + 1 < key_end ? 0xffff0000u : 0u);
+        if (th) {
+          x[i].z &= keep;
+          x[i].w &= keep;
+        } else {
+          x[i].x &= keep;
+          x[i].y &= keep;
         }
       }
   }
+  // largest |value| (NaN counts as larger)
+  uint32_t big = 0;
+  auto maxabs = [&](uint32_t b) {
+    b &= 0x7fff7fffu;
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(big) : "r"(b));
+  };
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    maxabs(x[i].x);
+    maxabs(x[i].y);
+    maxabs(x[i].z);
+    maxabs(x[i].w);
+  }
+  uint32_t poison = 0;
+  if ((big & 0x7f80u) == 0x7f80u || (big & 0x7f800000u) == 0x7f800000u) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      poison |= (bf16_clean(x[i].x) | bf16_clean(x[i].y)) << (16 * (i & 1) + 2 * t);
+      poison |= (bf16_clean(x[i].z) | bf16_clean(x[i].w)) << (16 * (i & 1) + 8 + 2 * t);
+    }
+  }
+  const uint32_t row = vs + g64 * (kTileBytes / 2) + (64 * hf + g) * 128 + (((2 * t + pp) ^ g) << 4);
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const uint4 &u = x[2 * m], &v = x[2 * m + 1];
+    sts128(row + (16 * m) * 128, u.x, u.z, v.x, v.z);
+    sts128(row + (16 * m + 8) * 128, u.y, u.w, v.y, v.w);
+  }
+  return poison;
 }
 
 // A warp's wait for a phase, given up after two seconds of the global timer (its low
 // word wraps after 4.3): all lanes have seen the phase complete, or none goes on (the
 // tcgen05 loads and stores that follow are warp-wide).  Kept short: some twenty of
-// these lie between the roles' unrolled loops, which share the instruction cache.
+// these lie between the roles' loops, which share the instruction cache.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   bool ok = mbar_try_wait(bar, parity);
   if (!__all_sync(0xffffffffu, ok)) {
@@ -584,15 +580,20 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// The power of two that brings a row's largest |x| into [1, 2), and its inverse:
-// the row's fp16 operand then neither overflows nor loses bits, whatever its size.
-__device__ __forceinline__ void row_scale(const uint32_t (&v)[4][32], float& down, float& up) {
+// The power of two that brings the largest |x| of this thread's 128 columns into
+// [1, 2), and its inverse: the row's fp16 operand then neither overflows nor loses
+// bits, whatever its size.
+__device__ __forceinline__ void row_scale(uint32_t addr, float& down, float& up) {
   float mx = 0.0f;
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t v[32];
+    tc_ld32(v, addr + 32 * c);
+    tc_wait_ld(v);
 #pragma unroll
     for (int i = 0; i < 32; i += 2)
-      mx = max3(mx, fabsf(__uint_as_float(v[c][i])), fabsf(__uint_as_float(v[c][i + 1])));
+      mx = max3(mx, fabsf(__uint_as_float(v[i])), fabsf(__uint_as_float(v[i + 1])));
+  }
   const uint32_t ex = min((__float_as_uint(mx) >> 23) & 255u, 253u);
   down = __uint_as_float((254u - ex) << 23);
   up = __uint_as_float(ex << 23);
@@ -629,6 +630,39 @@ struct Steps {
   __device__ __forceinline__ int keys() const { return pre + tiles + post; }   // stages of K
   __device__ __forceinline__ int values() const { return pre + tiles; }        // stages of V
 };
+
+// The pages of an item's sequence and KV head.
+template <bool INT2>
+struct Pages {
+  const int32_t* table;
+  const uint8_t* pool;
+  size_t stride;
+  int count, ids;
+  __device__ __forceinline__ Pages(const PrefillArgs& a, const Item& w)
+      : table(a.page_table + static_cast<size_t>(w.b) * a.max_pages),
+        pool(a.pool + static_cast<size_t>(w.kv) * (INT2 ? kInt2Rec : kBf16Rec)),
+        stride(static_cast<size_t>(a.Hkv) * (INT2 ? kInt2Rec : kBf16Rec)),
+        count((w.key_end + kPage - 1) / kPage),
+        ids(a.num_pool_pages) {}
+  // id of the sequence's page p; -1 behind its last page, or where `wanted` is false
+  __device__ __forceinline__ int id(int p, bool wanted) const {
+    return wanted && p < count ? table[p] : -1;
+  }
+  __device__ __forceinline__ const uint8_t* record(int i) const {
+    return i >= 0 && i < ids ? pool + static_cast<size_t>(i) * stride : nullptr;
+  }
+};
+
+// 32 KB of a rotation's operand, already in the operand's layout, by WARPS warps.
+template <int WARPS>
+__device__ __forceinline__ void copy_tile(uint32_t dst, const uint16_t* src, int warp, int lane) {
+  const uint4* s4 = reinterpret_cast<const uint4*>(src);
+#pragma unroll 4
+  for (int at = warp * 32 + lane; at < kTileBytes / 16; at += WARPS * 32) {
+    const uint4 v = s4[at];
+    sts128(dst + at * 16, v.x, v.y, v.z, v.w);
+  }
+}
 
 // A wait gave up somewhere in the CTA: every role leaves after the same item.
 __device__ __forceinline__ bool item_end(bool alive, const PrefillArgs& a, volatile uint32_t* abort) {
@@ -712,7 +746,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sca
     const bool grow = mnew > mref + kLazy;
     if (__any_sync(0xffffffffu, grow)) {
       const float f = grow ? fast_exp2(mref - mnew) : 1.0f;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < 8; ++c) {
         uint32_t o[16];
         tc_ld16(o, to + 16 * c);
@@ -748,6 +782,90 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sca
   tc_wait_st();
 }
 
+// The CTA's next item from its range of the line of work (not inlined: it runs once an
+// item, and the roles' code shares the instruction cache).
+__device__ __noinline__ void next_item(const PrefillArgs& a, Line& line, Item& w) {
+  const int TR = kRows / a.G;
+  const long long cur = line.cur;
+  w.done = 1;
+  if (cur >= line.end) return;
+  Seq s = load_seq(a, line.b, TR);
+  while (cur >= line.b_first + s.units * a.Hkv) {       // ends: cur < total
+    line.b_first += s.units * a.Hkv;
+    s = load_seq(a, ++line.b, TR);
+  }
+  const long long local = cur - line.b_first;
+  const int kv = static_cast<int>(local / s.units);
+  const long long r = local - kv * s.units;
+  int lo = 0, hi = s.rts - 1;                     // last row tile that starts at or before r
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tiles_before(s, mid, TR) <= r) lo = mid;
+    else hi = mid - 1;
+  }
+  const int tok0 = lo * TR;
+  w.b = line.b;
+  w.kv = kv;
+  w.row0 = s.row0 + tok0;
+  w.tokens = min(TR, s.n - tok0);
+  w.pos0 = s.p0 + tok0;
+  w.key_end = s.ok ? w.pos0 + w.tokens : 0;
+  const int all = s.ok ? (w.key_end + kTileKeys - 1) / kTileKeys : 1;
+  const int t0 = static_cast<int>(r - tiles_before(s, lo, TR));
+  const int t1 = static_cast<int>(min(static_cast<long long>(all), t0 + (line.end - cur)));
+  w.tile_begin = t0;
+  w.tiles = s.ok ? t1 - t0 : 0;
+  w.part = (t0 == 0 && t1 == all) ? -1 : static_cast<int>(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0);
+  w.done = 0;
+  if (t0 > 0) {       // an item that ranges before this one began: what joining it takes
+    Cut c;
+    c.row0 = w.row0;
+    c.rows = w.tokens * a.G;
+    c.kv = kv;
+    c.first = static_cast<int>((cur - t0) / line.per);
+    c.last = static_cast<int>((cur - t0 + all - 1) / line.per);
+    a.cuts[blockIdx.x] = c;
+  }
+  line.cur = cur + (t1 - t0);
+}
+
+// This CTA's range of the line: thread i sums a run of sequences; the thread whose run
+// holds the range's first unit knows its sequence.
+__device__ __noinline__ void start_line(const PrefillArgs& a, Line* line, long long* red) {
+  const int tid = threadIdx.x, TR = kRows / a.G;
+  const int per_thread = (a.batch + kThreads - 1) / kThreads;
+  const int b_lo = min(tid * per_thread, a.batch), b_hi = min(b_lo + per_thread, a.batch);
+  long long mine = 0;
+#pragma unroll 1
+  for (int b = b_lo; b < b_hi; ++b) {
+    const Seq s = load_seq(a, b, TR);
+    if (s.bad && blockIdx.x == 0) atomicOr(a.status, s.bad);
+    mine += s.units * a.Hkv;
+  }
+  long long total;
+  const long long before = block_prefix(mine, red, &total);
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long u0 = min(per * blockIdx.x, total), u1 = min(u0 + per, total);
+  if (tid == 0) {
+    line->cur = u0;
+    line->end = u1;
+    line->per = per;
+  }
+  if (u0 < u1 && before <= u0 && u0 < before + mine) {
+    long long u = before;
+#pragma unroll 1
+    for (int b = b_lo; b < b_hi; ++b) {
+      const long long su = load_seq(a, b, TR).units * a.Hkv;
+      if (u0 < u + su) {
+        line->b = b;
+        line->b_first = u;
+        break;
+      }
+      u += su;
+    }
+  }
+}
+
 template <bool INT2>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -756,6 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const uint32_t bar = sb + Smem::kBar;
   Item* items = reinterpret_cast<Item*>(smem + Smem::kItem);
   long long* red = reinterpret_cast<long long*>(smem + Smem::kScan);
+  Line* line = reinterpret_cast<Line*>(smem + Smem::kLine);
   volatile uint32_t* badw = reinterpret_cast<volatile uint32_t*>(smem + Smem::kBad);
   volatile uint32_t* poisonw = reinterpret_cast<volatile uint32_t*>(smem + Smem::kPoison);
   volatile uint32_t* anyw = reinterpret_cast<volatile uint32_t*>(smem + Smem::kAny);
@@ -787,47 +906,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   }
   tc_fence_before();
 
-  // The line of work: thread i sums a run of sequences; the thread whose run holds
-  // this CTA's first unit hands its sequence to the scheduler.
-  {
-    const int TR = kRows / a.G;
-    const int per_thread = (a.batch + kThreads - 1) / kThreads;
-    const int b_lo = min(tid * per_thread, a.batch), b_hi = min(b_lo + per_thread, a.batch);
-    long long mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) {
-      const Seq s = load_seq(a, b, TR);
-      if (s.bad && blockIdx.x == 0) atomicOr(a.status, s.bad);
-      mine += s.units * a.Hkv;
-    }
-    long long total;
-    const long long before = block_prefix(mine, red, &total);
-    const long long per = (total + gridDim.x - 1) / gridDim.x;
-    const long long u0 = min(per * blockIdx.x, total), u1 = min(u0 + per, total);
-    const bool here = u0 < u1 && before <= u0 && u0 < before + mine;
-    if (tid == 0) {
-      red[0] = u0;
-      red[1] = u1;
-      red[4] = per;
-    }
-    if (here) {
-      long long u = before;
-      for (int b = b_lo; b < b_hi; ++b) {
-        const long long su = load_seq(a, b, TR).units * a.Hkv;
-        if (u0 < u + su) {
-          red[2] = b;
-          red[3] = u;
-          break;
-        }
-        u += su;
-      }
-    }
-  }
+  start_line(a, line, red);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Smem::kTmem);
 
   bool alive = true;                // false after a wait gave up
-  uint32_t itk = 0, itv = 0, itf = 0;   // K and V stages and flag slots used so far
+  uint32_t itk = 0, itv = 0, itf = 0;   // K and V stages and key tiles so far
 
   if (warp < kProdWarp0) {
     // ======================= softmax: a thread a row =======================
@@ -867,27 +952,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (INT2 && (t == 0 || !st.split) && wait_s()) {
           if (some) {
             // q R_K -> fp16 Q, a power of two a row apart, in the pages' order of d
-            uint32_t v[4][32];
-            tc_ld_row(v, ts);
             float down, up;
-            row_scale(v, down, up);
+            row_scale(ts, down, up);
             scale *= up;
             pair->x = scale;        // for the group of the odd tiles
-            auto h2 = [&](int d) {
-              return pack_half2(__uint_as_float(v[d >> 5][d & 31]) * down,
-                                __uint_as_float(v[d >> 5][(d & 31) + 1]) * down);
-            };
+#pragma unroll 1
+            for (int wq = 0; wq < 2; ++wq) {
+              uint32_t v[2][32];
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt)
+              for (int c = 0; c < 2; ++c) tc_ld32(v[c], ts + 64 * wq + 32 * c);
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
+              for (int c = 0; c < 2; ++c) tc_wait_ld(v[c]);
+              auto h2 = [&](int d) {
+                return pack_half2(__uint_as_float(v[d >> 5][d & 31]) * down,
+                                  __uint_as_float(v[d >> 5][(d & 31) + 1]) * down);
+              };
 #pragma unroll
-                for (int wq = 0; wq < 2; ++wq) {
-                  const int ch = 4 * (tt & 1) + ((2 * h + wq) ^ (2 * (tt >> 1)));
-                  const int d = 64 * wq + 8 * h + 2 * tt;
+              for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int ch = 4 * (tt & 1) + ((2 * h + wq) ^ (2 * (tt >> 1))), d = 8 * h + 2 * tt;
                   *reinterpret_cast<uint4*>(qrow + (tt >> 1) * (kTileBytes / 2) + ((ch ^ r7) << 4)) =
                       make_uint4(h2(d), h2(d + 16), h2(d + 32), h2(d + 48));
                 }
+            }
             fence_proxy_async();
           }
           give();
@@ -951,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (active && alive && w.part >= 0) {
         if (some) {
           float* po = a.part + (static_cast<size_t>(w.part) * kRows + row) * kDim;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t v[32];
             tc_ld32(v, to + 32 * c);
@@ -974,18 +1062,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (st.post) {
           if (some) {
             // o / l -> fp16, a power of two a row apart: the left operand of o R_V^T
-            uint32_t v[4][32];
-            tc_ld_row(v, to);
             float down, up;
-            row_scale(v, down, up);
-            auto h2 = [&](int d) {
-              return pack_half2(__uint_as_float(v[d >> 5][d & 31]) * down,
-                                __uint_as_float(v[d >> 5][(d & 31) + 1]) * down);
-            };
+            row_scale(to, down, up);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t v[32];
+              tc_ld32(v, to + 32 * c);
+              tc_wait_ld(v);
+              auto h2 = [&](int d) {
+                return pack_half2(__uint_as_float(v[d]) * down, __uint_as_float(v[d + 1]) * down);
+              };
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-              *reinterpret_cast<uint4*>(qrow + (c >> 3) * (kTileBytes / 2) + (((c & 7) ^ r7) << 4)) =
-                  make_uint4(h2(8 * c), h2(8 * c + 2), h2(8 * c + 4), h2(8 * c + 6));
+              for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<uint4*>(qrow + (c >> 1) * (kTileBytes / 2) +
+                                          (((4 * (c & 1) + x) ^ r7) << 4)) =
+                    make_uint4(h2(8 * x), h2(8 * x + 2), h2(8 * x + 4), h2(8 * x + 6));
+            }
             f *= up;
             fence_proxy_async();
           }
@@ -998,7 +1090,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             for (int x = 0; x < 16; ++x) dst[x] = make_uint4(0, 0, 0, 0);
         } else if (alive && some) {
           const uint32_t src = st.post ? ts : to;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t v[32];
             tc_ld32(v, src + 32 * c);
@@ -1029,27 +1121,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     // ======================= producers =======================
     reg_set<kRegProducer>();
     const int pw = warp - kProdWarp0;
-    const size_t page_stride = static_cast<size_t>(a.Hkv) * (INT2 ? kInt2Rec : kBf16Rec);
     for (uint32_t i = 0;; ++i) {
       sync_cta();
       const Item w = items[i & 1];
       if (w.done) break;
       load_q<INT2>(a, w, smem);
       const Steps<INT2> st(w, a);
-      const int pages = (w.key_end + kPage - 1) / kPage;
-      const int32_t* ptab = a.page_table + static_cast<size_t>(w.b) * a.max_pages;
-      const uint8_t* pool = a.pool + static_cast<size_t>(w.kv) * (INT2 ? kInt2Rec : kBf16Rec);
-      // page ids of a tile's pair: -1 behind the last page
-      auto ids = [&](int j, int (&id)[2]) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int p = (w.tile_begin + j) * kTilePages + 2 * pw + x;
-          id[x] = j < st.tiles && p < pages ? ptab[p] : -1;
-        }
-      };
-      auto address = [&](int id) -> const uint8_t* {
-        return id >= 0 && id < a.num_pool_pages ? pool + static_cast<size_t>(id) * page_stride : nullptr;
-      };
+      const Pages<INT2> pages(a, w);
+      const int first = w.tile_begin * kTilePages + 2 * pw;       // the pair: first + 8 j, + 1
       auto wait_empty = [&](int empty, uint32_t k) {
         alive = alive && warp_wait(B(empty + k % kStages), ((k / kStages) & 1) ^ 1);
         return alive;
@@ -1061,75 +1140,80 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       };
       auto kbuf = [&](uint32_t k) { return sb + Smem::kK + (k % kStages) * kTileBytes; };
       auto vbuf = [&](uint32_t k) { return sb + Smem::kV + (k % kStages) * kTileBytes; };
-      // 32 KB of a rotation's operand, already in the operand's layout
-      auto copy_tile = [&](uint32_t dst, const uint16_t* src) {
-        const uint4* s4 = reinterpret_cast<const uint4*>(src) + pw * 32 + lane;
-        dst += (pw * 32 + lane) * 16;
+      // the pair's records (of the tile that is loaded next) and the ids behind them
+      const uint8_t* rec[2];
+      RawInt2 raw;
+      int id[2];
+      uint4 x[8];
+      auto records = [&](int j) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint4 v[8];
-#pragma unroll
-          for (int y = 0; y < 8; ++y) v[y] = s4[(8 * x + y) * 128];
-#pragma unroll
-          for (int y = 0; y < 8; ++y)
-            sts128(dst + (8 * x + y) * 2048, v[y].x, v[y].y, v[y].z, v[y].w);
+        for (int y = 0; y < 2; ++y) {
+          rec[y] = pages.record(id[y]);
+          id[y] = pages.id(first + kTilePages * (j + 1) + y, j + 1 < st.tiles);
         }
       };
-      int id0[2], id1[2];
-      RawInt2 raw;
-      ids(0, id0);
-      ids(1, id1);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) id[y] = pages.id(first + y, st.tiles > 0);
+      records(0);
       if constexpr (INT2) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) int2_load(raw, x, address(id0[x]), lane);
+        for (int y = 0; y < 2; ++y) int2_load(raw, y, rec[y], lane);
+      } else {
+        bf16_load_key(x, rec[0], lane);
       }
       sync_cta();                   // Q is there
       const size_t mat = static_cast<size_t>(w.kv) * kDim * kDim;
       if (st.pre && wait_empty(kKEmpty, itk) && wait_empty(kVEmpty, itv)) {
-        copy_tile(kbuf(itk), a.rk_hi + mat);
+        copy_tile<4>(kbuf(itk), a.rk_hi + mat, pw, lane);
         give(kKFull, itk);
-        copy_tile(vbuf(itv), a.rk_lo + mat);
+        copy_tile<4>(vbuf(itv), a.rk_lo + mat, pw, lane);
         give(kVFull, itv);
       }
       for (int j = 0; j < st.tiles && alive; ++j) {
         const uint32_t k = itk + st.pre + j, kv = itv + st.pre + j;
-        const int p0 = ((w.tile_begin + j) * kTilePages + 2 * pw) * kPage;
-        uint32_t bad = 0;
-        const uint8_t* rec[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          rec[x] = address(id0[x]);
-          if (!rec[x] && p0 + kPage * x < w.key_end) bad |= 0xffffu << (16 * x);
-        }
-        if (!wait_empty(kKEmpty, k)) break;
         const uint32_t f = itf + j, slot = f % kFlags;
-        if (lane == 0) {
-          badw[4 * slot + pw] = bad;
-          any8[4 * slot + pw] = bad != 0;
-          if (bad) atomicOr(a.status, KVQ_STATUS_BAD_PAGE);
-        }
-        uint32_t poison;
+        const int p0 = (first + kTilePages * j) * kPage;
+        uint32_t bad = 0, poison;
+        auto key_flags = [&]() {
+          if (lane == 0) {
+            badw[4 * slot + pw] = bad;
+            any8[4 * slot + pw] = bad != 0;
+            if (bad) atomicOr(a.status, KVQ_STATUS_BAD_PAGE);
+          }
+        };
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          if (!rec[y] && p0 + kPage * y < w.key_end) bad |= 0xffffu << (16 * y);
+        if (!wait_empty(kKEmpty, k)) break;
+        key_flags();
         if constexpr (INT2) {
           int2_store_k(raw, kbuf(k), pw, lane);
           give(kKFull, k);
           if (p0 + 2 * kPage > w.key_end) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) int2_clip(raw, x, p0 + kPage * x, w.key_end, lane);
+            for (int y = 0; y < 2; ++y) int2_clip(raw, y, p0 + kPage * y, w.key_end, lane);
           }
-          RawInt2 now = raw;
+          const RawInt2 now = raw;
+          records(j + 1);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) int2_load(raw, x, address(id1[x]), lane);
+          for (int y = 0; y < 2; ++y) int2_load(raw, y, rec[y], lane);
           if (!wait_empty(kVEmpty, kv)) break;
           poison = int2_store_v(now, vbuf(kv), pw, lane);
         } else {
-          bf16_store_k(rec, kbuf(k), pw, lane);
+          uint4 ahead[8];
+          bf16_load_key(ahead, rec[1], lane);
+          const uint32_t base = key_base(kbuf(k), pw, lane);
+          bf16_store_key(x, base, 0);
+          bf16_load_value(x, rec, 0, lane);
+          bf16_store_key(ahead, base, 1);
           give(kKFull, k);
+          bf16_load_value(ahead, rec, 1, lane);
           if (!wait_empty(kVEmpty, kv)) break;
-          poison = bf16_store_v(rec, p0, w.key_end, vbuf(kv), pw, lane);
+          poison = bf16_store_value(x, p0, w.key_end, vbuf(kv), pw, 0, lane);
+          records(j + 1);
+          bf16_load_key(x, rec[0], lane);
+          poison |= bf16_store_value(ahead, p0, w.key_end, vbuf(kv), pw, 1, lane);
         }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) id0[x] = id1[x];
-        ids(j + 2, id1);
         poison = __reduce_or_sync(0xffffffffu, poison);
         if (lane == 0) {
           poisonw[4 * slot + pw] = poison;
@@ -1139,7 +1223,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       if (st.post && alive && wait_empty(kKEmpty, itk + st.pre + st.tiles)) {
         const uint32_t k = itk + st.pre + st.tiles;
-        copy_tile(kbuf(k), a.rv_tile + mat);
+        copy_tile<4>(kbuf(k), a.rv_tile + mat, pw, lane);
         give(kKFull, k);
       }
       itk += st.keys();
@@ -1152,65 +1236,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     reg_set<kRegIssue>();
     uint32_t np0 = 0, np1 = 0;      // P_full phases
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), one = elect_one();
-    long long cur = red[0], u_end = red[1], cur_b0 = red[3];
-    const long long per = red[4];
-    int cur_b = static_cast<int>(red[2]);
-    auto schedule = [&](Item& w) {
-      const int TR = kRows / a.G;
-      w.done = 1;
-      if (cur >= u_end) return;
-      Seq s = load_seq(a, cur_b, TR);
-      while (cur >= cur_b0 + s.units * a.Hkv) {       // ends: cur < total
-        cur_b0 += s.units * a.Hkv;
-        s = load_seq(a, ++cur_b, TR);
-      }
-      const long long local = cur - cur_b0;
-      const int kv = static_cast<int>(local / s.units);
-      const long long r = local - kv * s.units;
-      int lo = 0, hi = s.rts - 1;                     // last row tile that starts at or before r
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (tiles_before(s, mid, TR) <= r) lo = mid;
-        else hi = mid - 1;
-      }
-      const int tok0 = lo * TR;
-      w.b = cur_b;
-      w.kv = kv;
-      w.row0 = s.row0 + tok0;
-      w.tokens = min(TR, s.n - tok0);
-      w.pos0 = s.p0 + tok0;
-      w.key_end = s.ok ? w.pos0 + w.tokens : 0;
-      const int all = s.ok ? (w.key_end + kTileKeys - 1) / kTileKeys : 1;
-      const int t0 = static_cast<int>(r - tiles_before(s, lo, TR));
-      const int t1 = static_cast<int>(min(static_cast<long long>(all), t0 + (u_end - cur)));
-      w.tile_begin = t0;
-      w.tiles = s.ok ? t1 - t0 : 0;
-      w.part = (t0 == 0 && t1 == all) ? -1 : static_cast<int>(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0);
-      w.done = 0;
-      if (t0 > 0) {       // an item that ranges before this one began: what joining it takes
-        Cut c;
-        c.row0 = w.row0;
-        c.rows = w.tokens * a.G;
-        c.kv = kv;
-        c.first = static_cast<int>((cur - t0) / per);
-        c.last = static_cast<int>((cur - t0 + all - 1) / per);
-        a.cuts[blockIdx.x] = c;
-      }
-      cur += t1 - t0;
-    };
     if (warp == kSchedWarp && lane == 0) {
       a.cuts[blockIdx.x].rows = 0;
-      schedule(items[0]);
+      next_item(a, *line, items[0]);
     }
     __syncwarp();
     for (uint32_t i = 0;; ++i) {
       sync_cta();
       const Item w = items[i & 1];
       if (w.done) break;
-      if (warp == kSchedWarp && lane == 0) schedule(items[(i + 1) & 1]);
+      if (warp == kSchedWarp && lane == 0) next_item(a, *line, items[(i + 1) & 1]);
       __syncwarp();
-      sync_cta();                   // Q is there
       const Steps<INT2> st(w, a);
+      sync_cta();                   // Q is there
       if (warp == kMmaWarp && st.tiles > 0) {
         constexpr uint32_t idesc = idesc_f16(INT2 ? 0 : 1), idesc_bf = idesc_f16(1);
         const bool both = __shfl_sync(0xffffffffu, st.split ? 0 : 1, 0) != 0;
@@ -1263,54 +1301,31 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           ++k;
           ++v;
         }
-        if (!both) {
-          // tile j to group j % 2; two tiles' scores ahead of their weights
-          if (st.pre) operand(0);
-          for (int j = -2; j < tiles && alive; ++j) {
-            const int t = j & 1;
-            if (j >= 0) {
+        if (st.pre) {
+          operand(0);
+          if (both) operand(1);
+        }
+        // Step s: O_t += P_t V, then row tile t's next scores, t = s % 2.  Both row tiles:
+        // tile s / 2 each; one row tile: tile s, to group t.  Two scores ahead.
+        const int total = both ? 2 * tiles : tiles;
+        for (int s0 = -2; s0 < total && alive; s0 += 2) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int s = s0 + t;
+            if (s >= total) break;
+            const bool last = t == 1 || !both;       // of the stages' users
+            if (s0 >= 0) {
               if (!full(kVFull, v) || !operand(t)) break;
-              weighted(t, vdesc(v), j > 1);
-              empty(kVEmpty, v);
-              ++v;
+              weighted(t, vdesc(v), s0 != 0);
+              if (last) empty(kVEmpty, v++);
             }
-            if (j + 2 < tiles) {
+            const bool more = s + 2 < total;
+            if (more) {
               if (!full(kKFull, k)) break;
               product(t, kdesc(k), idesc, false);
-              empty(kKEmpty, k);
-              ++k;
+              if (last) empty(kKEmpty, k++);
             }
-            if (j >= 0 || j + 2 < tiles) scored(t);     // the next scores, or O
-          }
-        } else {
-          if (full(kKFull, k)) {
-#pragma unroll 1
-            for (int t = 0; t < 2; ++t)
-              if (!st.pre || operand(t)) {
-                product(t, kdesc(k), idesc, false);
-                scored(t);
-              }
-            empty(kKEmpty, k);
-            ++k;
-          }
-          for (int j = 0; j < tiles && alive; ++j, ++v) {
-            const bool more = j + 1 < tiles;
-            if (!full(kVFull, v) || !operand(0)) break;
-            weighted(0, vdesc(v), j != 0);
-            if (more) {
-              if (!full(kKFull, k)) break;
-              product(0, kdesc(k), idesc, false);
-            }
-            scored(0);   // the next scores, or O
-            if (!operand(1)) break;
-            weighted(1, vdesc(v), j != 0);
-            empty(kVEmpty, v);
-            if (more) {
-              product(1, kdesc(k), idesc, false);
-              empty(kKEmpty, k);
-              ++k;
-            }
-            scored(1);
+            if (s0 >= 0 || more) scored(t);          // the next scores, or O
           }
         }
         if (st.post && alive && full(kKFull, k)) {
