@@ -653,17 +653,6 @@ struct Pages {
   }
 };
 
-// 32 KB of a rotation's operand, already in the operand's layout, by WARPS warps.
-template <int WARPS>
-__device__ __forceinline__ void copy_tile(uint32_t dst, const uint16_t* src, int warp, int lane) {
-  const uint4* s4 = reinterpret_cast<const uint4*>(src);
-#pragma unroll 4
-  for (int at = warp * 32 + lane; at < kTileBytes / 16; at += WARPS * 32) {
-    const uint4 v = s4[at];
-    sts128(dst + at * 16, v.x, v.y, v.z, v.w);
-  }
-}
-
 // A wait gave up somewhere in the CTA: every role leaves after the same item.
 __device__ __forceinline__ bool item_end(bool alive, const PrefillArgs& a, volatile uint32_t* abort) {
   if (!alive) {
@@ -1121,11 +1110,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     // ======================= producers =======================
     reg_set<kRegProducer>();
     const int pw = warp - kProdWarp0;
+    uint32_t copy_k = 0, copy_v = 0;       // stages of the last bulk copies
     for (uint32_t i = 0;; ++i) {
       sync_cta();
       const Item w = items[i & 1];
       if (w.done) break;
-      load_q<INT2>(a, w, smem);
       const Steps<INT2> st(w, a);
       const Pages<INT2> pages(a, w);
       const int first = w.tile_begin * kTilePages + 2 * pw;       // the pair: first + 8 j, + 1
@@ -1143,6 +1132,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       // the pair's records (of the tile that is loaded next) and the ids behind them
       const uint8_t* rec[2];
       RawInt2 raw;
+      // a rotation's operand (32 KB, already in the operand's layout) into a stage by one
+      // bulk copy, whose bytes complete the stage's phase with the warps' arrivals
+      auto give_copy = [&](int full, uint32_t k, uint32_t dst, const uint16_t* src) {
+        if (lane == 0) {
+          const uint32_t bar = B(full + k % kStages);
+          if (pw == 0) {
+            mbar_arrive_expect_tx(bar, kTileBytes);
+            bulk_g2s(dst, src, kTileBytes, bar);
+          } else {
+            mbar_arrive(bar);
+          }
+        }
+        __syncwarp();
+      };
+      const size_t mat = static_cast<size_t>(w.kv) * kDim * kDim;
+      if (st.pre && wait_empty(kKEmpty, itk) && wait_empty(kVEmpty, itv)) {
+        give_copy(kKFull, itk, kbuf(itk), a.rk_hi + mat);
+        give_copy(kVFull, itv, vbuf(itv), a.rk_lo + mat);
+        copy_k = itk;
+        copy_v = itv;
+      }
       int id[2];
       uint4 x[8];
       auto records = [&](int j) {
@@ -1161,14 +1171,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       } else {
         bf16_load_key(x, rec[0], lane);
       }
+      load_q<INT2>(a, w, smem);
       sync_cta();                   // Q is there
-      const size_t mat = static_cast<size_t>(w.kv) * kDim * kDim;
-      if (st.pre && wait_empty(kKEmpty, itk) && wait_empty(kVEmpty, itv)) {
-        copy_tile<4>(kbuf(itk), a.rk_hi + mat, pw, lane);
-        give(kKFull, itk);
-        copy_tile<4>(vbuf(itv), a.rk_lo + mat, pw, lane);
-        give(kVFull, itv);
-      }
       for (int j = 0; j < st.tiles && alive; ++j) {
         const uint32_t k = itk + st.pre + j, kv = itv + st.pre + j;
         const uint32_t f = itf + j, slot = f % kFlags;
@@ -1223,13 +1227,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       if (st.post && alive && wait_empty(kKEmpty, itk + st.pre + st.tiles)) {
         const uint32_t k = itk + st.pre + st.tiles;
-        copy_tile<4>(kbuf(k), a.rv_tile + mat, pw, lane);
-        give(kKFull, k);
+        give_copy(kKFull, k, kbuf(k), a.rv_tile + mat);
+        copy_k = k;
       }
       itk += st.keys();
       itv += st.values();
       itf += st.tiles;
       if (!item_end(alive, a, abort)) break;
+    }
+    // after a wait gave up: a copy may still be under way that nobody waited for
+    if (INT2 && *abort) {
+      (void)warp_wait(B(kKFull + copy_k % kStages), (copy_k / kStages) & 1);
+      (void)warp_wait(B(kVFull + copy_v % kStages), (copy_v / kStages) & 1);
     }
   } else {
     // ======================= tensor-core issue, schedule =======================
