@@ -349,6 +349,8 @@ class Rope:
         self.table, self.style = table, style
         self.spec = KvqRopeSpec(_ptr(table, _F32, "table"), int(table.shape[0]),
                                 int(table.shape[1]), _ROPE_STYLES[style])
+        self.device = table.get_device()
+        self._as_parameter_ = ctypes.byref(self.spec)
 
 
 def make_rope(table: torch.Tensor, style: str = "half") -> Rope:
@@ -360,82 +362,119 @@ def kvq_rope_table(table: torch.Tensor, scaling: KvqRopeScaling, stream=None) ->
     """Fill table (fp32 [table_len, rot_dim]) with cos and sin of every position."""
     if table.dim() != 2:
         raise ValueError("table must be [table_len, rot_dim]")
-    with torch.cuda.device(table.device):
-        _check("kvq_rope_table", load_library().kvq_rope_table(
-            _ptr(table, _F32, "table"), int(table.shape[0]), int(table.shape[1]),
-            ctypes.byref(scaling), _stream(stream)))
+    p, dev, call = _ptr(table, _F32, "table"), table.get_device(), load_library().kvq_rope_table
+    n, rot = table.shape
+    if dev == torch.cuda.current_device():
+        rc = call(p, n, rot, ctypes.byref(scaling), _raw_stream(stream, dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = call(p, n, rot, ctypes.byref(scaling), _raw_stream(stream, dev))
+    _check("kvq_rope_table", rc)
 
 
-def _rows(t, name, heads=None):
-    """Device pointer and token stride of bf16 rows [n, heads, 128]; only the tokens may be strided."""
+# The calls of a decode step are bound by this module's own time, so the functions
+# below look at each tensor once and hand plain integers to ctypes.
+
+def _raw_stream(stream, device: int) -> int:
+    """`stream`, or the current stream of the device the tensors are on."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _at(t, dtypes, device, name):
+    """Address of a contiguous tensor of one of `dtypes` on CUDA device `device`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the handle on cuda:{device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _vec(t, n, device, name):
+    """Address of an int32 [n] tensor."""
+    at = _at(t, _I32, device, name)
+    if t.dim() != 1 or t.numel() != n:
+        raise ValueError(f"{name}: expected [{n}], got {tuple(t.shape)}")
+    return at
+
+
+def _table2(t, device):
+    """Address, batch and pages per sequence of a page table."""
+    at = _at(t, _I32, device, "page_table")
+    if t.dim() != 2:
+        raise ValueError(f"page_table: expected [batch, max_pages], got {tuple(t.shape)}")
+    batch, max_pages = t.shape
+    return at, batch, max_pages
+
+
+def _rows(t, device, name, heads=None):
+    """(address, token stride, n, heads) of bf16 rows [n, heads, 128]; only the tokens may be
+    strided."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor")
     if t.dtype not in _BF16:
         raise TypeError(f"{name}: dtype {t.dtype} not in {_BF16}")
-    if t.dim() != 3 or t.shape[2] != 128 or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name}: expected [n, {heads or 'heads'}, 128], got {tuple(t.shape)}")
-    n, hh = int(t.shape[0]), int(t.shape[1])
-    if n and (t.stride(2) != 1 or (hh > 1 and t.stride(1) != 128)):
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the handle on cuda:{device}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != 128 or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name}: expected [n, {heads or 'heads'}, 128], got {tuple(shape)}")
+    n, hh = shape[0], shape[1]
+    s0, s1, s2 = t.stride()
+    if n and (s2 != 1 or (hh > 1 and s1 != 128)):
         raise ValueError(f"{name}: the heads of a token must be adjacent and contiguous")
-    return ctypes.c_void_p(t.data_ptr()), int(t.stride(0)) if n > 1 else hh * 128
+    return t.data_ptr(), s0 if n > 1 else hh * 128, n, hh
 
 
-def _same_device(h, *named):
-    """The CUDA device of the handle and of every tensor (entries may be None)."""
-    for name, t in named:
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name}: expected a CUDA tensor")
-        if t.device.index != h.device:
-            raise ValueError(f"{name} is on {t.device}, the handle on cuda:{h.device}")
-    return torch.device("cuda", h.device)
+def _pool(t, pages, page_bytes, device):
+    """Address of a pool that holds `pages` pages."""
+    at = _at(t, _U8, device, "pool")
+    if t.numel() < pages * page_bytes:
+        raise ValueError(f"pool: {t.numel()} bytes hold fewer than {pages} pages")
+    return at
 
 
-def _stream_of(stream, device):
-    """`stream`, or the current stream of the device the tensors are on."""
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-    return _stream(stream)
-
-
-def _vec(t, n, name):
-    if t.dim() != 1 or int(t.shape[0]) != n:
-        raise ValueError(f"{name}: expected [{n}], got {tuple(t.shape)}")
-    return _ptr(t, _I32, name)
+def _rope_on(rope, device):
+    if rope.device != device:
+        raise ValueError(f"the rotary-position table is on cuda:{rope.device}, the handle on "
+                         f"cuda:{device}")
+    return rope
 
 
 def kvq_rope(h, x, y, positions, rope: Rope, inverse=False, stream=None):
     """y = x rotated by positions; x, y: bf16 [n, heads, 128] (tokens may be strided), y may be x;
     positions: int32 [n]."""
-    n, heads = int(x.shape[0]), int(x.shape[1])
-    if tuple(y.shape) != tuple(x.shape):
+    dev = h.device
+    px, sx, n, heads = _rows(x, dev, "x")
+    py, sy, ny, hy = _rows(y, dev, "y")
+    if ny != n or hy != heads:
         raise ValueError("y must have the shape of x")
-    dev = _same_device(h, ("x", x), ("y", y), ("positions", positions), ("table", rope.table))
-    px, sx = _rows(x, "x")
-    py, sy = _rows(y, "y")
     _check("kvq_rope", load_library().kvq_rope(
-        h.ptr, px, sx, py, sy, heads, _vec(positions, n, "positions"), n,
-        ctypes.byref(rope.spec), 1 if inverse else 0, _stream_of(stream, dev)))
+        h.ptr, px, sx, py, sy, heads, _vec(positions, n, dev, "positions"), n, _rope_on(rope, dev),
+        1 if inverse else 0, _raw_stream(stream, dev)))
 
 
-def _append_rope(fn, h, pool, num_pool_pages, K, V, seq_idx, positions, page_table, rope,
+def _append_rope(int2, h, pool, num_pool_pages, K, V, seq_idx, positions, page_table, rope,
                  rope_positions, stream):
-    n, hkv = int(K.shape[0]), int(h.layout.num_kv_heads)
-    batch, max_pages = int(page_table.shape[0]), int(page_table.shape[1])
-    dev = _same_device(h, ("pool", pool), ("K", K), ("V", V), ("seq_idx", seq_idx),
-                       ("positions", positions), ("page_table", page_table),
-                       ("table", rope.table), ("rope_positions", rope_positions))
-    pk, sk = _rows(K, "K", hkv)
-    pv, sv = _rows(V, "V", hkv)
-    if int(V.shape[0]) != n:
+    dev, hkv = h.device, h.layout.num_kv_heads
+    pk, sk, n, _ = _rows(K, dev, "K", hkv)
+    pv, sv, nv, _ = _rows(V, dev, "V", hkv)
+    if nv != n:
         raise ValueError("K and V must have the same number of tokens")
+    pt, batch, max_pages = _table2(page_table, dev)
+    pages, record = int(num_pool_pages), INT2_RECORD_BYTES if int2 else BF16_RECORD_BYTES
+    fn = "kvq_append_rope" if int2 else "kvq_bf16_append_rope"
     _check(fn, getattr(load_library(), fn)(
-        h.ptr, _ptr(pool, _U8, "pool"), int(num_pool_pages), pk, sk, pv, sv,
-        _vec(seq_idx, n, "seq_idx"), _vec(positions, n, "positions"), n,
-        _ptr(page_table, _I32, "page_table"), batch, max_pages, ctypes.byref(rope.spec),
-        None if rope_positions is None else _vec(rope_positions, n, "rope_positions"),
-        _stream_of(stream, dev)))
+        h.ptr, _pool(pool, pages, hkv * record, dev), pages, pk, sk, pv, sv,
+        _vec(seq_idx, n, dev, "seq_idx"), _vec(positions, n, dev, "positions"), n, pt, batch,
+        max_pages, _rope_on(rope, dev),
+        None if rope_positions is None else _vec(rope_positions, n, dev, "rope_positions"),
+        _raw_stream(stream, dev)))
 
 
 def kvq_append_rope(h, pool, num_pool_pages, K, V, seq_idx, positions, page_table, rope: Rope,
@@ -443,14 +482,14 @@ def kvq_append_rope(h, pool, num_pool_pages, K, V, seq_idx, positions, page_tabl
     """kvq_append with the keys rotated on the way.  K, V: bf16 [n, Hkv, 128], tokens may be
     strided (slices of a fused projection); rope_positions: int32 [n] if the angles' positions
     are not the cache's."""
-    _append_rope("kvq_append_rope", h, pool, num_pool_pages, K, V, seq_idx, positions, page_table,
+    _append_rope(True, h, pool, num_pool_pages, K, V, seq_idx, positions, page_table,
                  rope, rope_positions, stream)
 
 
 def kvq_bf16_append_rope(h, pool, num_pool_pages, K, V, seq_idx, positions, page_table,
                          rope: Rope, rope_positions=None, stream=None):
     """kvq_bf16_append with the keys rotated on the way (arguments as kvq_append_rope)."""
-    _append_rope("kvq_bf16_append_rope", h, pool, num_pool_pages, K, V, seq_idx, positions,
+    _append_rope(False, h, pool, num_pool_pages, K, V, seq_idx, positions,
                  page_table, rope, rope_positions, stream)
 
 
@@ -464,19 +503,20 @@ def kvq_bf16_prefill_workspace_bytes(h: Handle, batch: int, n: int) -> int:
     return int(load_library().kvq_bf16_prefill_workspace_bytes(h.ptr, int(batch), int(n)))
 
 
-def _prefill(fn, h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace, stream):
-    n, H = int(q.shape[0]), int(h.layout.num_heads)
-    batch, max_pages = int(page_table.shape[0]), int(page_table.shape[1])
-    dev = _same_device(h, ("pool", pool), ("q", q), ("cu_q", cu_q), ("page_table", page_table),
-                       ("seq_lens", seq_lens), ("out", out), ("workspace", workspace))
-    pq, sq = _rows(q, "q", H)
+def _prefill(int2, h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace, stream):
+    dev, H = h.device, h.layout.num_heads
+    pq, sq, n, _ = _rows(q, dev, "q", H)
+    pt, batch, max_pages = _table2(page_table, dev)
+    po = _at(out, _BF16, dev, "out")
     if tuple(out.shape) != (n, H, 128):
         raise ValueError(f"out: expected [{n}, {H}, 128], got {tuple(out.shape)}")
+    pages, record = int(num_pool_pages), INT2_RECORD_BYTES if int2 else BF16_RECORD_BYTES
+    fn = "kvq_prefill" if int2 else "kvq_bf16_prefill"
     _check(fn, getattr(load_library(), fn)(
-        h.ptr, _ptr(pool, _U8, "pool"), int(num_pool_pages), pq, sq,
-        _vec(cu_q, batch + 1, "cu_q"), n, _ptr(page_table, _I32, "page_table"), max_pages,
-        _vec(seq_lens, batch, "seq_lens"), batch, _ptr(out, _BF16, "out"),
-        _ptr(workspace, _U8, "workspace"), int(workspace.numel()), _stream_of(stream, dev)))
+        h.ptr, _pool(pool, pages, h.layout.num_kv_heads * record, dev), pages, pq, sq,
+        _vec(cu_q, batch + 1, dev, "cu_q"), n, pt, max_pages,
+        _vec(seq_lens, batch, dev, "seq_lens"), batch, po, _at(workspace, _U8, dev, "workspace"),
+        workspace.numel(), _raw_stream(stream, dev)))
 
 
 def kvq_prefill(h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace,
@@ -485,15 +525,13 @@ def kvq_prefill(h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, wor
     (tokens may be strided); cu_q: int32 [B + 1], sequence b's rows are cu_q[b]:cu_q[b + 1], the
     last of its seq_lens[b] positions; out: bf16 [n, H, 128]; workspace: uint8,
     >= kvq_prefill_workspace_bytes(h, B, n)."""
-    _prefill("kvq_prefill", h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace,
-             stream)
+    _prefill(True, h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace, stream)
 
 
 def kvq_bf16_prefill(h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace,
                      stream=None):
     """kvq_prefill over the BF16 cache (workspace: kvq_bf16_prefill_workspace_bytes)."""
-    _prefill("kvq_bf16_prefill", h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out,
-             workspace, stream)
+    _prefill(False, h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace, stream)
 
 
 def kvq_dequant(h, pool, num_pool_pages, page_table, seq, start, length, K_out=None, V_out=None,
