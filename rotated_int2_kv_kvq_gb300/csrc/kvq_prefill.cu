@@ -230,27 +230,31 @@ __device__ __forceinline__ constexpr int col_pos(int c) {
 
 // ---- the line of work ---------------------------------------------------------------
 // Row tiles of a sequence with n new tokens behind p0 old ones, TR tokens a tile
-// (TR = 256 / G): tile k sees ceil((p0 + min((k + 1) TR, n)) / 128) key tiles.
+// (TR = 256 / G): tile k sees ceil((p0 + min((k + 1) TR, n)) / 128) key tiles, and
+// counts for kItemCost units more (its queries, rotations and results: 8 us beside
+// 1.4 to 1.9 us a key tile), so that ranges of many short items are not the longest.
+constexpr int kItemCost = 4;
 struct Seq {
   int row0, n, p0;       // first row, new tokens, position of the first
   bool ok;               // false: invalid lengths; its rows get zeros
   uint32_t bad;          // status bit of an invalid sequence, or 0
   int rts;               // row tiles
-  long long units;       // key tiles of one KV head (invalid: one per row tile)
+  long long units;       // of one KV head (invalid: one per row tile)
 };
 
 __device__ __forceinline__ long long half_sum(long long m) {   // sum of ceil(i / 2), i = 1 .. m
   return ((m + 1) * (m + 1)) >> 2;
 }
-// key tiles of row tiles 0 .. k-1, all of them full
-__device__ __forceinline__ long long tiles_before(const Seq& s, int k, int TR) {
+// units of row tiles 0 .. k-1, all of them full
+__device__ __forceinline__ long long units_before(const Seq& s, int k, int TR) {
   if (!s.ok) return k;
+  const long long cost = static_cast<long long>(k) * kItemCost;
   if (TR == 64) {
     const long long a = (s.p0 + 63) >> 6;
-    return half_sum(a + k) - half_sum(a);
+    return half_sum(a + k) - half_sum(a) + cost;
   }
   const long long a = (s.p0 + 127) >> 7, kk = k;
-  return a * kk + (TR >> 7) * (kk * (kk + 1) >> 1);
+  return a * kk + (TR >> 7) * (kk * (kk + 1) >> 1) + cost;
 }
 __device__ __noinline__ Seq load_seq(const PrefillArgs& a, int b, int TR) {
   Seq s;
@@ -271,7 +275,7 @@ __device__ __noinline__ Seq load_seq(const PrefillArgs& a, int b, int TR) {
   s.p0 = s.ok ? len - s.n : 0;
   s.rts = (s.n + TR - 1) / TR;
   s.units = s.rts == 0 ? 0
-            : s.ok     ? tiles_before(s, s.rts - 1, TR) + ((len + kTileKeys - 1) / kTileKeys)
+            : s.ok     ? units_before(s, s.rts - 1, TR) + kItemCost + (len + kTileKeys - 1) / kTileKeys
                        : s.rts;
   return s;
 }
@@ -666,26 +670,37 @@ __device__ __forceinline__ bool item_end(bool alive, const PrefillArgs& a, volat
 // The item's query rows into the Q operands, by the first 384 threads.
 template <bool INT2>
 __device__ __forceinline__ void load_q(const PrefillArgs& a, const Item& w, uint8_t* smem) {
-  const int G = a.G, rows = w.tokens * G;
-  for (int idx = threadIdx.x; idx < (rows > 128 ? 256 : 128) * 16; idx += kMmaWarp * 32) {
-    const int row = idx >> 4, c = idx & 15;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (row < rows) {
-      const int tok = row / G, g = row - tok * G;
-      v = *reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(w.row0 + tok) * a.q_stride +
-                                          (w.kv * G + g) * kDim + 8 * c);
-    }
-    uint8_t* base = smem + Smem::kQ + (row >> 7) * kTileBytes + (row & 127) * 128;
-    if constexpr (INT2) {         // d in order: the left operand of q R_K
-      *reinterpret_cast<uint4*>(base + (c >> 3) * (kTileBytes / 2) + (((c & 7) ^ (row & 7)) << 4)) = v;
-    } else {                      // the 16-byte piece holds the pairs t = 0 .. 3 of one (w, h)
-      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-      const int wq = c >> 1, h = c & 1;
+  const int lg = a.G >> 1, rows = w.tokens << lg;         // log2 of 1, 2, 4
+  const int pieces = (rows > 128 ? 256 : 128) * 16;
+  constexpr int kStep = kMmaWarp * 32, kBatch = 6;        // loads in flight a thread
+#pragma unroll 1
+  for (int base = threadIdx.x; base < pieces; base += kBatch * kStep) {
+    uint4 v[kBatch];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int ch = 4 * (t & 1) + ((2 * h + (wq >> 2)) ^ (2 * (t >> 1)));
-        *reinterpret_cast<uint32_t*>(base + (t >> 1) * (kTileBytes / 2) + ((ch ^ (row & 7)) << 4) +
-                                     4 * (wq & 3)) = x[t];
+    for (int y = 0; y < kBatch; ++y) {
+      const int idx = base + y * kStep, row = idx >> 4;
+      v[y] = make_uint4(0, 0, 0, 0);
+      if (row < rows)
+        v[y] = *reinterpret_cast<const uint4*>(
+            a.q + static_cast<size_t>(w.row0 + (row >> lg)) * a.q_stride +
+            ((w.kv << lg) + (row & (a.G - 1))) * kDim + 8 * (idx & 15));
+    }
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      const int idx = base + y * kStep, row = idx >> 4, c = idx & 15;
+      if (idx >= pieces) break;
+      uint8_t* at = smem + Smem::kQ + (row >> 7) * kTileBytes + (row & 127) * 128;
+      if constexpr (INT2) {         // d in order: the left operand of q R_K
+        *reinterpret_cast<uint4*>(at + (c >> 3) * (kTileBytes / 2) + (((c & 7) ^ (row & 7)) << 4)) = v[y];
+      } else {                      // the 16-byte piece holds the pairs t = 0 .. 3 of one (w, h)
+        const uint32_t x[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+        const int wq = c >> 1, h = c & 1;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int ch = 4 * (t & 1) + ((2 * h + (wq >> 2)) ^ (2 * (t >> 1)));
+          *reinterpret_cast<uint32_t*>(at + (t >> 1) * (kTileBytes / 2) + ((ch ^ (row & 7)) << 4) +
+                                       4 * (wq & 3)) = x[t];
+        }
       }
     }
   }
@@ -789,10 +804,12 @@ __device__ __noinline__ void next_item(const PrefillArgs& a, Line& line, Item& w
   int lo = 0, hi = s.rts - 1;                     // last row tile that starts at or before r
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (tiles_before(s, mid, TR) <= r) lo = mid;
+    if (units_before(s, mid, TR) <= r) lo = mid;
     else hi = mid - 1;
   }
-  const int tok0 = lo * TR;
+  // the item's first units are its cost, one per key tile follows: unit `tile0` is tile 0
+  const int tok0 = lo * TR, cost = s.ok ? kItemCost : 0;
+  const long long tile0 = cur - (r - units_before(s, lo, TR)) + cost;
   w.b = line.b;
   w.kv = kv;
   w.row0 = s.row0 + tok0;
@@ -800,8 +817,9 @@ __device__ __noinline__ void next_item(const PrefillArgs& a, Line& line, Item& w
   w.pos0 = s.p0 + tok0;
   w.key_end = s.ok ? w.pos0 + w.tokens : 0;
   const int all = s.ok ? (w.key_end + kTileKeys - 1) / kTileKeys : 1;
-  const int t0 = static_cast<int>(r - tiles_before(s, lo, TR));
-  const int t1 = static_cast<int>(min(static_cast<long long>(all), t0 + (line.end - cur)));
+  const int t0 = static_cast<int>(max(cur - tile0, 0ll));
+  const int t1 = static_cast<int>(min(static_cast<long long>(all), line.end - tile0));
+  if (t1 <= t0) return;               // the range ends before the item's first tile
   w.tile_begin = t0;
   w.tiles = s.ok ? t1 - t0 : 0;
   w.part = (t0 == 0 && t1 == all) ? -1 : static_cast<int>(blockIdx.x) * 2 + (t0 == 0 ? 1 : 0);
@@ -811,11 +829,11 @@ __device__ __noinline__ void next_item(const PrefillArgs& a, Line& line, Item& w
     c.row0 = w.row0;
     c.rows = w.tokens * a.G;
     c.kv = kv;
-    c.first = static_cast<int>((cur - t0) / line.per);
-    c.last = static_cast<int>((cur - t0 + all - 1) / line.per);
+    c.first = static_cast<int>(tile0 / line.per);
+    c.last = static_cast<int>((tile0 + all - 1) / line.per);
     a.cuts[blockIdx.x] = c;
   }
-  line.cur = cur + (t1 - t0);
+  line.cur = tile0 + t1;
 }
 
 // This CTA's range of the line: thread i sums a run of sequences; the thread whose run
