@@ -40,10 +40,12 @@ constexpr int kTilePages = kTileKeys / kPage;
 constexpr int kRows = 256;                 // rows per item: two MMA tiles
 constexpr int kThreads = 512;
 constexpr int kProdWarp0 = 8, kMmaWarp = 12, kSchedWarp = 13;
-// Registers a thread after the roles part, of the 128 that each is launched with:
-// 2 x 176 + 104 + 56 = 4 x 128
+// Registers a thread: at launch, and after the roles part (warpgroups: two softmax,
+// producers, one for issue and schedule).  The parts come out of the launch's, so
+// they must not add up to more, or a role would wait for ever.
+constexpr int kRegLaunch = 128;
 constexpr int kRegSoftmax = 176, kRegProducer = 104, kRegIssue = 56;
-static_assert(2 * kRegSoftmax + kRegProducer + kRegIssue <= 4 * 128, "register split");
+static_assert(2 * kRegSoftmax + kRegProducer + kRegIssue <= 4 * kRegLaunch, "register split");
 constexpr int kStages = 2;
 constexpr int kFlags = 4;                  // key tiles whose flags are kept
 constexpr int kTileBytes = 128 * 128 * 2;  // one 128 x 128 16-bit operand
@@ -603,10 +605,10 @@ __device__ __forceinline__ void row_scale(uint32_t addr, float& down, float& up)
   up = __uint_as_float(ex << 23);
 }
 
-// N registers a thread for the calling warpgroup, which was launched with 128.
+// N registers a thread for the calling warpgroup.
 template <int N>
 __device__ __forceinline__ void reg_set() {
-  if constexpr (N >= 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  if constexpr (N >= kRegLaunch) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 // All of the CTA's threads, from whichever role's code.
@@ -1522,6 +1524,10 @@ cudaError_t launch(const PrefillArgs& a, int num_sms, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(prefill_kernel<INT2>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::kAlloc);
     if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, prefill_kernel<INT2>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != kRegLaunch) return cudaErrorInvalidConfiguration;   // see kRegLaunch
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   prefill_kernel<INT2><<<num_sms, kThreads, Smem::kAlloc, st>>>(a);

@@ -20,7 +20,8 @@ namespace {
 // F_i = f_i / (2 pi) * 2^64 (made on the host in fp64): the integer product
 // wraps exactly, so the reduction by full turns costs no fp64 and the error is
 // that of F_i, p * 2^-53 of a turn at most.  The top two bits (rounded) are the
-// quadrant; the rest, at most 1/8 turn, goes through sincospif.
+// quadrant; of the rest, y = at most pi / 4, the Taylor series up to y^9 (sine) and
+// y^10 (cosine) leave less than 2e-9.
 // Writes are the bound: 4 * table_len * rot_dim bytes.
 // ---------------------------------------------------------------------------
 struct TableArgs {
@@ -43,8 +44,11 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_
     const uint32_t hi = static_cast<uint32_t>((static_cast<uint64_t>(p) * f) >> 32);
     const uint32_t quad = (hi + 0x20000000u) >> 30;      // nearest quarter turn (mod 4)
     const int rest = static_cast<int>(hi - (quad << 30));  // in [-2^29, 2^29)
-    float s, c;
-    sincospif(static_cast<float>(rest) * 0x1p-31f, &s, &c);
+    const float y = static_cast<float>(rest) * 1.46291807926715968e-9f;   // pi / 2^31
+    const float z = y * y;
+    const float s = fmaf(y * z, fmaf(z, fmaf(z, fmaf(z, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), y);
+    const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720),
+                                         1.0f / 24), -0.5f), 1.0f);
     const float cs = (quad & 1u) ? s : c, sn = (quad & 1u) ? c : s;
     float* t = a.table + static_cast<size_t>(p) * (2 * a.half) + i;
     t[0] = a.amplitude * ((quad == 1u || quad == 2u) ? -cs : cs);
@@ -53,13 +57,16 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_
 }
 
 // ---------------------------------------------------------------------------
-// Rotation of rows x[n][heads][128] -> y.  One CTA per token (looping when the
-// grid is capped), so the token's cos / sin row is read from DRAM once and from
-// L1 by its other heads; a thread owns one unit of one head:
+// Rotation of rows x[n][heads][128] -> y.  One CTA per token, so the token's cos / sin
+// row is read from DRAM once and from L1 by its other heads; a thread owns units of
+// its heads, one or two at a time (eight CTAs per SM are worth more than more loads a
+// thread: 8191 x 32 heads took 27.5 us with 8 CTAs of 32 registers, 39.2 with 4 of 54):
 //   kHalfVec  : 8 elements of the first half and their 8 partners (2 x 16 B);
 //   kInterVec : 8 adjacent elements, four pairs (16 B);
 //   kScalar   : one pair (any even rot_dim),
-// and, behind the rotated part, 16 B (kScalar: two elements) copied unchanged.
+// and, behind the rotated part, 16 B (kScalar: two elements) copied unchanged.  The
+// units' elements are loaded before the position is looked at, so that its two
+// dependent loads (position, table row) overlap them.
 // HBM bound at 2 * 2 bytes per element.
 // ---------------------------------------------------------------------------
 enum RopeMode { kHalfVec, kInterVec, kScalar };
@@ -78,82 +85,110 @@ struct RopeRowArgs {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// Eight elements of each half (kHalfVec) of a pair group, rotated.
+__device__ __forceinline__ void rotate_halves(uint4& va, uint4& vb, const float* cosp, const float* sinp,
+                                              float sign) {
+  const float4 c0 = *reinterpret_cast<const float4*>(cosp);
+  const float4 c1 = *reinterpret_cast<const float4*>(cosp + 4);
+  const float4 s0 = *reinterpret_cast<const float4*>(sinp);
+  const float4 s1 = *reinterpret_cast<const float4*>(sinp + 4);
+  uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+  const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+  const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float p0, q0, p1, q1;
+    rope_pair(lo_f(wa[e]), lo_f(wb[e]), c[2 * e], sign * s[2 * e], p0, q0);
+    rope_pair(hi_f(wa[e]), hi_f(wb[e]), c[2 * e + 1], sign * s[2 * e + 1], p1, q1);
+    wa[e] = pack_bf162(p0, p1);
+    wb[e] = pack_bf162(q0, q1);
+  }
+  va = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+  vb = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+}
+
+// Four adjacent pairs (kInterVec), rotated.
+__device__ __forceinline__ void rotate_pairs(uint4& v, const float* cosp, const float* sinp, float sign) {
+  const float4 c4 = *reinterpret_cast<const float4*>(cosp);
+  const float4 s4 = *reinterpret_cast<const float4*>(sinp);
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float p, q;
+    rope_pair(lo_f(w[e]), hi_f(w[e]), c[e], sign * s[e], p, q);
+    w[e] = pack_bf162(p, q);
+  }
+  v = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 template <int MODE>
-__global__ void __launch_bounds__(256) rope_kernel(RopeRowArgs a) {
+__global__ void __launch_bounds__(256, 8) rope_kernel(RopeRowArgs a) {
   const int rot = a.r.rot_dim, half = rot >> 1;
   // units per head: rotated ones, then copied ones
   const int rot_units = MODE == kHalfVec ? rot / 16 : MODE == kInterVec ? rot / 8 : half;
   const int units = rot_units + (MODE == kScalar ? (kDim - rot) / 2 : (kDim - rot) / 8);
   const int total = a.heads * units;
-  for (int tok = blockIdx.x; tok < a.n; tok += gridDim.x) {
-    const int pos = a.positions[tok];
+  const int tok = blockIdx.x;
+  const uint16_t* xr = a.x + static_cast<size_t>(tok) * a.x_stride;
+  uint16_t* yr = a.y + static_cast<size_t>(tok) * a.y_stride;
+  const int pos = a.positions[tok];
+  constexpr int kU = MODE == kHalfVec ? 1 : 2;      // units in flight a thread
+  for (int base = threadIdx.x; base < total; base += kU * 256) {
+    uint4 va[kU], vb[kU];
+    int at[kU], u[kU];                               // first element of the unit's head; unit
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int idx = base + i * 256, head = idx / units;
+      u[i] = idx - head * units;
+      at[i] = head * kDim;
+      if (idx >= total) continue;
+      const uint16_t* xh = xr + at[i];
+      if constexpr (MODE == kScalar) {
+        const bool inter = a.r.style == KVQ_ROPE_INTERLEAVED, turn = u[i] < rot_units;
+        const int d0 = !turn ? rot + 2 * (u[i] - rot_units) : inter ? 2 * u[i] : u[i];
+        va[i].x = xh[d0];
+        va[i].y = xh[turn && !inter ? u[i] + half : d0 + 1];
+      } else if (u[i] >= rot_units) {
+        va[i] = *reinterpret_cast<const uint4*>(xh + rot + 8 * (u[i] - rot_units));
+      } else {
+        va[i] = *reinterpret_cast<const uint4*>(xh + 8 * u[i]);
+        if (MODE == kHalfVec) vb[i] = *reinterpret_cast<const uint4*>(xh + half + 8 * u[i]);
+      }
+    }
     if (pos < 0 || pos >= a.r.table_len) {
       if (threadIdx.x == 0) atomicOr(a.status, KVQ_STATUS_BAD_POS);
-      continue;
+      return;
     }
     const float* cosp = a.r.table + static_cast<size_t>(pos) * rot;
     const float* sinp = cosp + half;
-    const uint16_t* xr = a.x + static_cast<size_t>(tok) * a.x_stride;
-    uint16_t* yr = a.y + static_cast<size_t>(tok) * a.y_stride;
-    for (int idx = threadIdx.x; idx < total; idx += blockDim.x) {
-      const int head = idx / units, u = idx - head * units;
-      const uint16_t* xh = xr + head * kDim;
-      uint16_t* yh = yr + head * kDim;
-      if (u >= rot_units) {
-        if (MODE == kScalar) {
-          const int d = rot + 2 * (u - rot_units);
-          *reinterpret_cast<uint32_t*>(yh + d) = *reinterpret_cast<const uint32_t*>(xh + d);
-        } else {
-          const int d = rot + 8 * (u - rot_units);
-          *reinterpret_cast<uint4*>(yh + d) = *reinterpret_cast<const uint4*>(xh + d);
-        }
-        continue;
-      }
-      if constexpr (MODE == kHalfVec) {
-        const int d = 8 * u;
-        const uint4 va = *reinterpret_cast<const uint4*>(xh + d);
-        const uint4 vb = *reinterpret_cast<const uint4*>(xh + half + d);
-        const float4 c0 = *reinterpret_cast<const float4*>(cosp + d);
-        const float4 c1 = *reinterpret_cast<const float4*>(cosp + d + 4);
-        const float4 s0 = *reinterpret_cast<const float4*>(sinp + d);
-        const float4 s1 = *reinterpret_cast<const float4*>(sinp + d + 4);
-        const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
-        const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-        const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-        uint32_t oa[4], ob[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float p0, q0, p1, q1;
-          rope_pair(lo_f(wa[e]), lo_f(wb[e]), c[2 * e], a.sign * s[2 * e], p0, q0);
-          rope_pair(hi_f(wa[e]), hi_f(wb[e]), c[2 * e + 1], a.sign * s[2 * e + 1], p1, q1);
-          oa[e] = pack_bf162(p0, p1);
-          ob[e] = pack_bf162(q0, q1);
-        }
-        *reinterpret_cast<uint4*>(yh + d) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
-        *reinterpret_cast<uint4*>(yh + half + d) = make_uint4(ob[0], ob[1], ob[2], ob[3]);
-      } else if constexpr (MODE == kInterVec) {
-        const uint4 v = *reinterpret_cast<const uint4*>(xh + 8 * u);
-        const float4 c4 = *reinterpret_cast<const float4*>(cosp + 4 * u);
-        const float4 s4 = *reinterpret_cast<const float4*>(sinp + 4 * u);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float p, q;
-          rope_pair(lo_f(w[e]), hi_f(w[e]), c[e], a.sign * s[e], p, q);
-          o[e] = pack_bf162(p, q);
-        }
-        *reinterpret_cast<uint4*>(yh + 8 * u) = make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
+    for (int i = 0; i < kU; ++i) {
+      if (base + i * 256 >= total) break;
+      uint16_t* yh = yr + at[i];
+      const bool turn = u[i] < rot_units;
+      if constexpr (MODE == kScalar) {
         const bool inter = a.r.style == KVQ_ROPE_INTERLEAVED;
-        const int d0 = inter ? 2 * u : u, d1 = inter ? 2 * u + 1 : u + half;
-        const float x0 = __uint_as_float(static_cast<uint32_t>(xh[d0]) << 16);
-        const float x1 = __uint_as_float(static_cast<uint32_t>(xh[d1]) << 16);
-        float p, q;
-        rope_pair(x0, x1, cosp[u], a.sign * sinp[u], p, q);
-        yh[d0] = __bfloat16_as_ushort(__float2bfloat16_rn(p));
-        yh[d1] = __bfloat16_as_ushort(__float2bfloat16_rn(q));
+        const int d0 = !turn ? rot + 2 * (u[i] - rot_units) : inter ? 2 * u[i] : u[i];
+        const int d1 = turn && !inter ? u[i] + half : d0 + 1;
+        if (turn) {
+          float p, q;
+          rope_pair(__uint_as_float(va[i].x << 16), __uint_as_float(va[i].y << 16), cosp[u[i]],
+                    a.sign * sinp[u[i]], p, q);
+          va[i].x = __bfloat16_as_ushort(__float2bfloat16_rn(p));
+          va[i].y = __bfloat16_as_ushort(__float2bfloat16_rn(q));
+        }
+        yh[d0] = static_cast<uint16_t>(va[i].x);
+        yh[d1] = static_cast<uint16_t>(va[i].y);
+      } else if (!turn) {
+        *reinterpret_cast<uint4*>(yh + rot + 8 * (u[i] - rot_units)) = va[i];
+      } else if constexpr (MODE == kHalfVec) {
+        rotate_halves(va[i], vb[i], cosp + 8 * u[i], sinp + 8 * u[i], a.sign);
+        *reinterpret_cast<uint4*>(yh + 8 * u[i]) = va[i];
+        *reinterpret_cast<uint4*>(yh + half + 8 * u[i]) = vb[i];
+      } else {
+        rotate_pairs(va[i], cosp + 4 * u[i], sinp + 4 * u[i], a.sign);
+        *reinterpret_cast<uint4*>(yh + 8 * u[i]) = va[i];
       }
     }
   }
@@ -180,6 +215,7 @@ constexpr int kMaxTok = kSpan + kPage - 1;
 // the 4 row pairs x 8 elements of a value piece are in different banks
 constexpr int kRowB = 2 * kDim + 16;
 constexpr int kBfThreads = 256;
+constexpr int kLoads = 2;      // 16-byte pieces in flight a thread (4: fewer CTAs per SM, 96 against 86 us)
 
 struct BfSmem {
   static constexpr int kK = 0;
@@ -198,6 +234,9 @@ __device__ __forceinline__ long long span_start(const AppendArgs& a, int k, int 
   return s < a.n ? s : a.n;
 }
 
+// MODE: how the keys are rotated: in registers between their load and the staging
+// (kHalfVec, kInterVec), or pair by pair in shared memory (kScalar).
+template <int MODE>
 __global__ void __launch_bounds__(kBfThreads) append_bf16_rope_kernel(AppendArgs a, int span) {
   extern __shared__ __align__(16) uint8_t sm[];
   long long* rec = reinterpret_cast<long long*>(sm + BfSmem::kRec);
@@ -211,13 +250,60 @@ __global__ void __launch_bounds__(kBfThreads) append_bf16_rope_kernel(AppendArgs
   const int cnt = static_cast<int>(span_start(a, blockIdx.x + 1, span) - t0);   // <= kMaxTok
   if (cnt <= 0) return;
 
-  // the tokens' rows, 16 bytes a thread, keys then values
-  for (int idx = tid; idx < 2 * cnt * 16; idx += kBfThreads) {
-    const int ch = idx & 15, k = (idx >> 4) % cnt, which = (idx >> 4) / cnt;
-    const uint16_t* src = which ? a.V + static_cast<size_t>(t0 + k) * a.v_stride
-                                : a.K + static_cast<size_t>(t0 + k) * a.k_stride;
-    *reinterpret_cast<uint4*>(sm + (which ? BfSmem::kV : BfSmem::kK) + k * kRowB + 16 * ch) =
-        *reinterpret_cast<const uint4*>(src + kv * kDim + 8 * ch);
+  // The tokens' rows.  Keys: units as in rope_kernel (a piece of each half, or four
+  // pairs, or a copied piece); kScalar: plain pieces.  Then values, a piece a unit.
+  const int rot_units = MODE == kHalfVec ? rot / 16 : MODE == kInterVec ? rot / 8 : 0;
+  const int units = rot_units + (MODE == kScalar ? 16 : (kDim - rot) / 8);
+  const int kpieces = cnt * units, pieces = kpieces + cnt * 16;
+  const int32_t* ang_pos = a.rope_positions ? a.rope_positions : a.positions;
+#pragma unroll 1
+  for (int base = tid; base < pieces; base += kLoads * kBfThreads) {
+    uint4 va[kLoads], vb[kLoads];
+    int w[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int idx = base + i * kBfThreads;
+      w[i] = -1;
+      if (idx >= pieces) continue;
+      if (idx >= kpieces) {
+        const int k = (idx - kpieces) >> 4, ch = (idx - kpieces) & 15;
+        va[i] = *reinterpret_cast<const uint4*>(a.V + static_cast<size_t>(t0 + k) * a.v_stride +
+                                                kv * kDim + 8 * ch);
+        continue;
+      }
+      const int k = idx / units, u = idx - k * units;
+      const uint16_t* src = a.K + static_cast<size_t>(t0 + k) * a.k_stride + kv * kDim;
+      if (u < rot_units) {
+        va[i] = *reinterpret_cast<const uint4*>(src + 8 * u);
+        if (MODE == kHalfVec) vb[i] = *reinterpret_cast<const uint4*>(src + half + 8 * u);
+        w[i] = ang_pos[t0 + k];
+      } else {
+        va[i] = *reinterpret_cast<const uint4*>(src + (MODE == kScalar ? 0 : rot) + 8 * (u - rot_units));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int idx = base + i * kBfThreads;
+      if (idx >= pieces) break;
+      if (idx >= kpieces) {
+        const int k = (idx - kpieces) >> 4, ch = (idx - kpieces) & 15;
+        *reinterpret_cast<uint4*>(sm + BfSmem::kV + k * kRowB + 16 * ch) = va[i];
+        continue;
+      }
+      const int k = idx / units, u = idx - k * units;
+      uint8_t* dst = sm + BfSmem::kK + k * kRowB;
+      if (u >= rot_units) {
+        *reinterpret_cast<uint4*>(dst + 2 * ((MODE == kScalar ? 0 : rot) + 8 * (u - rot_units))) = va[i];
+        continue;
+      }
+      if (w[i] >= 0 && w[i] < a.rope.table_len) {     // else the token is skipped below
+        const float* t = a.rope.table + static_cast<size_t>(w[i]) * rot;
+        if constexpr (MODE == kHalfVec) rotate_halves(va[i], vb[i], t + 8 * u, t + half + 8 * u, 1.0f);
+        if constexpr (MODE == kInterVec) rotate_pairs(va[i], t + 4 * u, t + half + 4 * u, 1.0f);
+      }
+      *reinterpret_cast<uint4*>(dst + 16 * u) = va[i];
+      if (MODE == kHalfVec) *reinterpret_cast<uint4*>(dst + 2 * half + 16 * u) = vb[i];
+    }
   }
   if (tid < cnt) {
     const long long tok = t0 + tid;
@@ -250,7 +336,7 @@ __global__ void __launch_bounds__(kBfThreads) append_bf16_rope_kernel(AppendArgs
     if (full) lead[tid] = 1;
   }
   // rotate the keys in place: thread -> (token, pair)
-  for (int idx = tid; idx < cnt * (kDim / 2); idx += kBfThreads) {
+  for (int idx = tid; MODE == kScalar && idx < cnt * (kDim / 2); idx += kBfThreads) {
     const int k = idx / (kDim / 2), i = idx % (kDim / 2);
     if (i >= half || ang[k] < 0) continue;
     const float* t = a.rope.table + static_cast<size_t>(ang[k]) * rot + i;
@@ -273,25 +359,30 @@ __global__ void __launch_bounds__(kBfThreads) append_bf16_rope_kernel(AppendArgs
   for (int k = 0; k < cnt; ++k) {
     if (lead[k] != 1) continue;
     uint8_t* base = a.pool + (rec[k] / kPage) * kBf16Rec;
-    for (int u = tid; u < 512; u += kBfThreads) {
-      const int L = u & 31, w = (u >> 5) & 7;
-      uint4 o;
-      if (u < 256) {           // keys: tokens L/4 and L/4 + 8, elements 16w + 2t (+8)
-        const uint8_t* r0 = sm + BfSmem::kK + (k + (L >> 2)) * kRowB + 2 * (16 * w + 2 * (L & 3));
-        const uint8_t* r1 = r0 + 8 * kRowB;
-        o = make_uint4(*reinterpret_cast<const uint32_t*>(r0),
-                       *reinterpret_cast<const uint32_t*>(r1),
-                       *reinterpret_cast<const uint32_t*>(r0 + 16),
-                       *reinterpret_cast<const uint32_t*>(r1 + 16));
-      } else {                 // values: tokens 2t, 2t + 1 (+8), elements 16w + g (+8)
-        const uint8_t* r0 = sm + BfSmem::kV + (k + 2 * (L & 3)) * kRowB + 2 * (16 * w + (L >> 2));
-        auto pair = [&](const uint8_t* p) {
-          return static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p)) |
-                 (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p + kRowB)) << 16);
-        };
-        o = make_uint4(pair(r0), pair(r0 + 16), pair(r0 + 8 * kRowB), pair(r0 + 8 * kRowB + 16));
+    {                          // keys: tokens L/4 and L/4 + 8, elements 16w + 2t (+8)
+      const int L = tid & 31, w = tid >> 5;
+      const uint8_t* r0 = sm + BfSmem::kK + (k + (L >> 2)) * kRowB + 2 * (16 * w + 2 * (L & 3));
+      const uint8_t* r1 = r0 + 8 * kRowB;
+      *reinterpret_cast<uint4*>(base + 512 * w + 16 * L) =
+          make_uint4(*reinterpret_cast<const uint32_t*>(r0), *reinterpret_cast<const uint32_t*>(r1),
+                     *reinterpret_cast<const uint32_t*>(r0 + 16),
+                     *reinterpret_cast<const uint32_t*>(r1 + 16));
+    }
+    if (tid < 128) {           // values: tokens 2t, 2t + 1 (+8), elements 16w + g, g + 1 (+8), g even
+      const int t = tid & 3, g = 2 * ((tid >> 2) & 3), w = tid >> 4;
+      const uint8_t* r0 = sm + BfSmem::kV + (k + 2 * t) * kRowB + 2 * (16 * w + g);
+      uint32_t lo[4], hi[4];   // th, dh
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* r = r0 + 8 * (i >> 1) * kRowB + 16 * (i & 1);
+        const uint32_t e0 = *reinterpret_cast<const uint32_t*>(r);
+        const uint32_t e1 = *reinterpret_cast<const uint32_t*>(r + kRowB);
+        lo[i] = __byte_perm(e0, e1, 0x5410);
+        hi[i] = __byte_perm(e0, e1, 0x7632);
       }
-      *reinterpret_cast<uint4*>(base + (u < 256 ? 0 : 4096) + 512 * w + 16 * L) = o;
+      uint4* dst = reinterpret_cast<uint4*>(base + 4096 + 512 * w + 16 * (4 * g + t));
+      dst[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      dst[4] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     }
   }
   for (int idx = tid; idx < cnt * kDim; idx += kBfThreads) {
@@ -358,7 +449,13 @@ cudaError_t launch_append_bf16_rope(const AppendArgs& a, int num_sms, cudaStream
   int span = kSpan;
   while (span > 4 && (static_cast<long long>(a.n) + span - 1) / span * a.Hkv < num_sms) span /= 4;
   dim3 grid((static_cast<unsigned>(a.n) + span - 1) / span, a.Hkv);
-  append_bf16_rope_kernel<<<grid, kBfThreads, BfSmem::kBytes, st>>>(a, span);
+  const bool inter = a.rope.style == KVQ_ROPE_INTERLEAVED;
+  if (!inter && a.rope.rot_dim % 16 == 0)
+    append_bf16_rope_kernel<kHalfVec><<<grid, kBfThreads, BfSmem::kBytes, st>>>(a, span);
+  else if (inter && a.rope.rot_dim % 8 == 0)
+    append_bf16_rope_kernel<kInterVec><<<grid, kBfThreads, BfSmem::kBytes, st>>>(a, span);
+  else
+    append_bf16_rope_kernel<kScalar><<<grid, kBfThreads, BfSmem::kBytes, st>>>(a, span);
   return cudaGetLastError();
 }
 

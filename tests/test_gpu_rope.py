@@ -5,8 +5,8 @@ Tolerances.  The rotation rounds two products and their sum to fp32 and the resu
 |y - exact| <= 2^-8 |exact| + 3 * 2^-24 (|a c| + |b s|) (a half step of bf16; the second term also
 covers the half step of a result that the fp32 errors moved).  The table: reducing the angle leaves
 2^-32 of a turn and float64's own p f 2^-52 in the reference, converting the rest of the angle (at
-most pi/4) to fp32 pi/4 2^-24, sincospif at most 2 units in the last place of a value below 1
-(2^-23), the amplitude's product 2^-24: below 3e-7 times the amplitude together.  The appends must
+most pi/4) to fp32 pi/4 2^-24, the sine and cosine of it at most 2 units in the last place of a
+value below 1 (2^-23), the amplitude's product 2^-24: below 3e-7 times the amplitude together.  The appends must
 equal the unfused calls byte for byte.
 """
 import math
