@@ -217,6 +217,16 @@ constexpr uint32_t idesc_f16(int bf16) {
          ((128u >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+// One lane's arrival, as a predicated instruction: no branch for the warp to diverge at
+// (the tcgen05 loads that follow are warp-wide).
+__device__ __forceinline__ void arrive_if(uint32_t bar, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+      "r"(static_cast<uint32_t>(on))
+      : "memory");
+}
+
 // ---- element orders ---------------------------------------------------------------
 // S = sum_d q_d k_d and O = sum_t p_t v_t do not depend on the order of d and t, so
 // both follow the page record's: a producer lane's codes become whole 16-byte
@@ -955,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       auto give = [&]() {           // an operand of this row tile is ready
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(B(kPFull + t));
+        arrive_if(B(kPFull + t), lane == 0);
       };
       if (first < st.tiles) {
         if (INT2 && (t == 0 || !st.split) && wait_s()) {
@@ -1145,7 +1155,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       auto give = [&](int full, uint32_t k) {
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(B(full + k % kStages));
+        arrive_if(B(full + k % kStages), lane == 0);
       };
       auto kbuf = [&](uint32_t k) { return sb + Smem::kK + (k % kStages) * kTileBytes; };
       auto vbuf = [&](uint32_t k) { return sb + Smem::kV + (k % kStages) * kTileBytes; };
@@ -1291,7 +1301,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         // this warp saw of the producers' flags
         auto scored = [&](int t) {
           tc_commit(B(kSFull + t), one);
-          if (one) mbar_arrive(B(kSFull + t));
+          arrive_if(B(kSFull + t), one);
         };
         auto empty = [&](int bar, uint32_t k) { tc_commit(B(bar + k % kStages), one); };
         auto operand = [&](int t) {      // Q, P or o of row tile t
@@ -1410,10 +1420,11 @@ __global__ void __launch_bounds__(256) prefill_bank_kernel(const float* R, int H
 
 // Joins the partial states of the items that range borders cut, rotates by R_V^T
 // (INT2) and writes bf16.  CTA x stands for the border before range x + 1, y for 16 of
-// the item's rows; the item's first border does the work.  A warp joins four rows
-// (lane: elements 4 lane .. + 3; the parts' loads are independent), then the 16 rows
-// go through mma.sync, 32 output columns a warp, as fp16 with a power of two a row
-// apart: a product of 16 x 128 x 128 is too small for tcgen05's 128 rows.
+// the item's rows; the item's first border does the work.  A warp joins four rows side
+// by side (their loads are independent: two round trips to L2 in all), a lane holding
+// elements 4 lane .. + 3; then the 16 rows go through mma.sync, 32 output columns a
+// warp, as fp16 with a power of two a row apart: a product of 16 x 128 x 128 is too
+// small for tcgen05's 128 rows.  Bound by those round trips and the launch.
 constexpr int kJoinRows = 16;
 constexpr int kJoinPitch = kDim + 8;      // halves: rows 4 banks apart
 
@@ -1424,83 +1435,112 @@ __global__ void __launch_bounds__(128) prefill_combine_kernel(const __grid_const
   const Cut c = a.cuts[blockIdx.x + 1];
   const int row0 = blockIdx.y * kJoinRows;
   if (c.rows <= row0 || c.first != static_cast<int>(blockIdx.x)) return;
-  const int rows = min(c.rows - row0, kJoinRows);
+  const int rows = min(c.rows - row0, kJoinRows), parts = c.last - c.first + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.G;
+  const int g = lane >> 2, t = lane & 3;
   const bool rotate = a.rv_tile != nullptr;
+  // part i of row `row`: CTA first + i left it, the first one in its second slot
   auto slot = [&](int i, int row) {
-    return static_cast<size_t>(2 * i + (i == c.first ? 1 : 0)) * kRows + row0 + row;
+    return static_cast<size_t>(2 * (c.first + i) + (i == 0 ? 1 : 0)) * kRows + row0 + row;
   };
   auto out_row = [&](int row) {
-    const int tk = (row0 + row) / G, g = (row0 + row) - tk * G;
-    return a.out + (static_cast<size_t>(c.row0 + tk) * a.H + c.kv * G + g) * kDim;
+    const int tk = (row0 + row) / G, gg = (row0 + row) - tk * G;
+    return a.out + (static_cast<size_t>(c.row0 + tk) * a.H + c.kv * G + gg) * kDim;
   };
+  // R_V's rows n = 32 warp + 8i + g, chunks 4q + t: asked for first, used last
+  uint4 b[4][4];
+  if (rotate) {
+    const uint16_t* rv = a.rv_tile + static_cast<size_t>(c.kv) * kDim * kDim;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int ch = 4 * q + t;
+        b[i][q] = *reinterpret_cast<const uint4*>(rv + (ch >> 3) * (kTileBytes / 4) +
+                                                  (32 * warp + 8 * i + g) * 64 + (((ch & 7) ^ g) << 3));
+      }
+  }
+  float m[4], l[4];
+  float4 o[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    m[x] = -INFINITY;
+    l[x] = 0.0f;
+    o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  // rows behind the last read row 0's parts and are not written
+  auto row_of = [&](int x) { return 4 * warp + x < rows ? 4 * warp + x : 0; };
+  for (int i = lane; i < parts; i += 32)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) m[x] = fmaxf(m[x], a.part_ml[slot(i, row_of(x))].x);
+#pragma unroll
+  for (int y = 16; y > 0; y >>= 1)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) m[x] = fmaxf(m[x], __shfl_xor_sync(0xffffffffu, m[x], y));
+  for (int base = 0; base < parts; base += 32) {
+    float f[4] = {0.f, 0.f, 0.f, 0.f}, fl[4] = {0.f, 0.f, 0.f, 0.f};
+    if (base + lane < parts) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float2 ml = a.part_ml[slot(base + lane, row_of(x))];
+        f[x] = ml.y == 0.0f ? 0.0f : fast_exp2(ml.x - (m[x] == -INFINITY ? 0.0f : m[x]));
+        fl[x] = f[x] * ml.y;
+      }
+    }
+#pragma unroll
+    for (int y = 16; y > 0; y >>= 1)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) fl[x] += __shfl_xor_sync(0xffffffffu, fl[x], y);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) l[x] += fl[x];
+    const int count = min(32, parts - base);
+#pragma unroll 2
+    for (int i = 0; i < count; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float fi = __shfl_sync(0xffffffffu, f[x], i);
+        const float4 v = *reinterpret_cast<const float4*>(a.part + slot(base + i, row_of(x)) * kDim + 4 * lane);
+        o[x].x = fmaf(fi, v.x, o[x].x);
+        o[x].y = fmaf(fi, v.y, o[x].y);
+        o[x].z = fmaf(fi, v.z, o[x].z);
+        o[x].w = fmaf(fi, v.w, o[x].w);
+      }
+  }
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
     const int row = 4 * warp + x;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row < rows) {
-      float m = -INFINITY;
-      for (int i = c.first + lane; i <= c.last; i += 32) m = fmaxf(m, a.part_ml[slot(i, row)].x);
-#pragma unroll
-      for (int y = 16; y > 0; y >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
-      const float ms = m == -INFINITY ? 0.0f : m;
-      float l = 0.0f;
-#pragma unroll 4
-      for (int i = c.first; i <= c.last; ++i) {
-        const float2 ml = a.part_ml[slot(i, row)];
-        const float4 v = *reinterpret_cast<const float4*>(a.part + slot(i, row) * kDim + 4 * lane);
-        const float f = fast_exp2(ml.x - ms);
-        if (ml.y != 0.0f) {                    // else the part saw nothing: its O is not used
-          l += f * ml.y;
-          o.x = fmaf(f, v.x, o.x);
-          o.y = fmaf(f, v.y, o.y);
-          o.z = fmaf(f, v.z, o.z);
-          o.w = fmaf(f, v.w, o.w);
-        }
-      }
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      o.x *= inv;
-      o.y *= inv;
-      o.z *= inv;
-      o.w *= inv;
-    }
+    const float inv = l[x] == 0.0f ? 0.0f : 1.0f / l[x];
+    o[x] = make_float4(o[x].x * inv, o[x].y * inv, o[x].z * inv, o[x].w * inv);
     if (rotate) {
-      float mx = fmaxf(fmaxf(fabsf(o.x), fabsf(o.y)), fmaxf(fabsf(o.z), fabsf(o.w)));
+      float mx = fmaxf(fmaxf(fabsf(o[x].x), fabsf(o[x].y)), fmaxf(fabsf(o[x].z), fabsf(o[x].w)));
 #pragma unroll
       for (int y = 16; y > 0; y >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
       const uint32_t ex = min((__float_as_uint(mx) >> 23) & 255u, 253u);
       const float down = __uint_as_float((254u - ex) << 23);
       *reinterpret_cast<uint2*>(os + row * kJoinPitch + 4 * lane) =
-          make_uint2(pack_half2(o.x * down, o.y * down), pack_half2(o.z * down, o.w * down));
+          make_uint2(pack_half2(o[x].x * down, o[x].y * down), pack_half2(o[x].z * down, o[x].w * down));
       if (lane == 0) ups[row] = __uint_as_float(ex << 23);
     } else if (row < rows) {
       *reinterpret_cast<uint2*>(out_row(row) + 4 * lane) =
-          make_uint2(pack_bf162(o.x, o.y), pack_bf162(o.z, o.w));
+          make_uint2(pack_bf162(o[x].x, o[x].y), pack_bf162(o[x].z, o[x].w));
     }
   }
   if (!rotate) return;
   __syncthreads();
-  // out[row][n] = sum_k o[row][k] R_V[n][k]: A from os, B straight from the operand tile
-  const int g = lane >> 2, t = lane & 3;
-  const uint16_t* rv = a.rv_tile + static_cast<size_t>(c.kv) * kDim * kDim;
+  // out[row][n] = sum_k o[row][k] R_V[n][k], the k of a step in the order of the lanes'
+  // 16-byte chunks: 8 (4q + t) + 4i + {0, 1} and {2, 3}
   float acc[4][4] = {};
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint16_t* ar = os + g * kJoinPitch + 16 * k + 2 * t;
-    const uint32_t a0 = *reinterpret_cast<const uint32_t*>(ar);
-    const uint32_t a1 = *reinterpret_cast<const uint32_t*>(ar + 8 * kJoinPitch);
-    const uint32_t a2 = *reinterpret_cast<const uint32_t*>(ar + 8);
-    const uint32_t a3 = *reinterpret_cast<const uint32_t*>(ar + 8 * kJoinPitch + 8);
+  for (int q = 0; q < 4; ++q)
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const int row = 32 * warp + 8 * n + g;
-      const uint16_t* br = rv + (k >> 2) * (kTileBytes / 4) + row * 64 + 2 * t;
-      const int c0 = 2 * (k & 3);
-      const uint32_t b0 = *reinterpret_cast<const uint32_t*>(br + ((c0 ^ g) << 3));
-      const uint32_t b1 = *reinterpret_cast<const uint32_t*>(br + (((c0 + 1) ^ g) << 3));
-      mma_f16(acc[n], a0, a1, a2, a3, b0, b1);
+    for (int i = 0; i < 2; ++i) {
+      const uint16_t* ar = os + g * kJoinPitch + 8 * (4 * q + t) + 4 * i;
+      const uint2 lo = *reinterpret_cast<const uint2*>(ar);
+      const uint2 hi = *reinterpret_cast<const uint2*>(ar + 8 * kJoinPitch);
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        mma_f16(acc[n], lo.x, hi.x, lo.y, hi.y, i ? b[n][q].z : b[n][q].x, i ? b[n][q].w : b[n][q].y);
     }
-  }
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int row = g + 8 * half;
