@@ -44,8 +44,11 @@ constexpr int kProdWarp0 = 8, kMmaWarp = 12, kSchedWarp = 13;
 // producers, one for issue and schedule).  The parts come out of the launch's, so
 // they must not add up to more, or a role would wait for ever.
 constexpr int kRegLaunch = 128;
-constexpr int kRegSoftmax = 176, kRegProducer = 104, kRegIssue = 56;
-static_assert(2 * kRegSoftmax + kRegProducer + kRegIssue <= 4 * kRegLaunch, "register split");
+template <bool INT2>
+struct Regs {
+  static constexpr int kSoftmax = INT2 ? 184 : 176, kProducer = INT2 ? 96 : 112, kIssue = 48;
+  static_assert(2 * kSoftmax + kProducer + kIssue <= 4 * kRegLaunch, "register split");
+};
 constexpr int kStages = 2;
 constexpr int kFlags = 4;                  // key tiles whose flags are kept
 constexpr int kTileBytes = 128 * 128 * 2;  // one 128 x 128 16-bit operand
@@ -935,7 +938,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 
   if (warp < kProdWarp0) {
     // ======================= softmax: a thread a row =======================
-    reg_set<kRegSoftmax>();
+    reg_set<Regs<INT2>::kSoftmax>();
     const int t = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
@@ -1138,7 +1141,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
   } else if (warp < kMmaWarp) {
     // ======================= producers =======================
-    reg_set<kRegProducer>();
+    reg_set<Regs<INT2>::kProducer>();
     const int pw = warp - kProdWarp0;
     uint32_t copy_k = 0, copy_v = 0;       // stages of the last bulk copies
     for (uint32_t i = 0;; ++i) {
@@ -1272,7 +1275,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
   } else {
     // ======================= tensor-core issue, schedule =======================
-    reg_set<kRegIssue>();
+    reg_set<Regs<INT2>::kIssue>();
     uint32_t np0 = 0, np1 = 0;      // P_full phases
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), one = elect_one();
     if (warp == kSchedWarp && lane == 0) {
