@@ -50,7 +50,7 @@ struct Regs {
   static_assert(2 * kSoftmax + kProducer + kIssue <= 4 * kRegLaunch, "register split");
 };
 constexpr int kStages = 2;
-constexpr int kFlags = 4;                  // key tiles whose flags are kept
+constexpr int kFlags = 4;                  // key tiles whose missing pages are kept
 constexpr int kTileBytes = 128 * 128 * 2;  // one 128 x 128 16-bit operand
 constexpr float kLazy = 8.0f;              // log2 growth of a row maximum before O is rescaled
 
@@ -59,10 +59,10 @@ struct Smem {
   static constexpr int kK = kQ + 2 * kTileBytes;            // [stages][32 KB]
   static constexpr int kV = kK + kStages * kTileBytes;      // [stages][32 KB]
   static constexpr int kBar = kV + kStages * kTileBytes;    // mbarriers
-  static constexpr int kAny = kBar + 160;                   // u8 [2][kFlags][4]: a warp's pages set a bit of
-  static constexpr int kBad = kAny + 32;                    // u32 [kFlags][4] tokens without a valid page
-  static constexpr int kPoison = kBad + 64;                 // u32 [kFlags][4] tokens with NaN / Inf values
-  static constexpr int kItem = kPoison + 64 + 32;               // Item [2]
+  static constexpr int kAny = kBar + 160;                   // u8 [kFlags][4]: a producer warp has set a bit of
+  static constexpr int kBad = kAny + 16;                    // u32 [kFlags][4] tokens without a valid page
+  static constexpr int kPoison = kBad + 64;                 // u32 [2] first position with a NaN / Inf value
+  static constexpr int kItem = kPoison + 16;                // Item [2]
   static constexpr int kScan = kItem + 128;                 // long long [16]
   static constexpr int kLine = kScan + 128;                 // Line
   static constexpr int kTmem = kLine + 48;
@@ -734,20 +734,31 @@ template <bool INT2>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float scale, bool first,
                                              int limit, bool edge, uint32_t any, const volatile uint32_t* bad,
                                              float& mref, float& l) {
-  uint32_t v[4][32];
-  tc_ld_row(v, ts);
   if (edge || any != 0) {
-    uint32_t hide[4];
+    // Hidden scores become -inf in TMEM first, 32 columns a step: rolled and apart from
+    // the tiles' common path, whose code it would double.  Column 32c + i stands for
+    // position 64 (c >> 1) + 4 (c & 1) + col_pos(i).
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t hide[2], x[32];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) hide[k] = bad[k] | ~visible(limit, k);
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
+      for (int k = 0; k < 2; ++k) {
+        const int w = (c & 2) + k;
+        hide[k] = (bad[w] | ~visible(limit, w)) >> (4 * (c & 1));
+      }
+      tc_ld32(x, ts + 32 * c);
+      tc_wait_ld(x);
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const int o = col_pos(32 * c + i);
-        if ((hide[o >> 5] >> (o & 31)) & 1) v[c][i] = 0xff800000u;
+        const int o = col_pos(i);
+        if ((hide[o >> 5] >> (o & 31)) & 1) x[i] = 0xff800000u;
       }
+      tc_st32(ts + 32 * c, x);
+    }
+    tc_wait_st();
   }
+  uint32_t v[4][32];
+  tc_ld_row(v, ts);
   float m[4];                    // four chains, a quarter of the columns each
 #pragma unroll
   for (int c = 0; c < 4; ++c) m[c] = fmaxf(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]));
@@ -898,7 +909,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   long long* red = reinterpret_cast<long long*>(smem + Smem::kScan);
   Line* line = reinterpret_cast<Line*>(smem + Smem::kLine);
   volatile uint32_t* badw = reinterpret_cast<volatile uint32_t*>(smem + Smem::kBad);
-  volatile uint32_t* poisonw = reinterpret_cast<volatile uint32_t*>(smem + Smem::kPoison);
+  uint32_t* first_bad = reinterpret_cast<uint32_t*>(smem + Smem::kPoison);
+  volatile uint32_t* poison = first_bad;
   volatile uint32_t* anyw = reinterpret_cast<volatile uint32_t*>(smem + Smem::kAny);
   volatile uint8_t* any8 = reinterpret_cast<volatile uint8_t*>(smem + Smem::kAny);
   volatile uint32_t* abort = reinterpret_cast<volatile uint32_t*>(smem + Smem::kTmem + 4);
@@ -919,6 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     mbar_init(B(kDrain), 1);
     fence_mbar_init();
     *abort = 0;
+    first_bad[0] = 0xffffffffu;
   }
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -1003,32 +1016,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           give();
         }
         const int pos = w.pos0 + tok;
-        // The tile's flags, written before its operands were handed over: K's with the
-        // scores, V's one step later.  A slot is written again four tiles later, which
-        // this thread's weights of two tiles later precede.
-        auto check_values = [&](int j) {
-          const uint32_t f = (itf + j) % kFlags;
-          if (anyw[kFlags + f] == 0) return;
-          const int limit = pos - (w.tile_begin + j) * kTileKeys;
-          uint32_t seen = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) seen |= poisonw[4 * f + k] & visible(limit, k);
-          if (seen) l = __int_as_float(0x7fffffff);      // the row sees a NaN or an infinity
-        };
         for (int j = first; j < st.tiles && alive; j += step) {
           const int limit = valid ? pos - (w.tile_begin + j) * kTileKeys : kTileKeys;
           const bool edge = __any_sync(0xffffffffu, limit < kTileKeys - 1);
           if (!wait_s()) break;
           if (INT2 && st.split && j == 1) scale = pair->x;
+          // the tile's missing pages, written before its operands were handed over; the slot
+          // is written again four tiles later, which weights of two tiles later precede
           const uint32_t f = (itf + j) % kFlags;
-          if (st.split && j > first) check_values(j - step);
           if (some)
             softmax_tile<INT2>(ts, to, scale, j == first, limit, edge, anyw[f], badw + 4 * f, mref, l);
           give();
-          if (!st.split && j > first) check_values(j - step);
         }
-        // O is complete; the last of this group's tiles
-        if (alive && wait_s()) check_values(st.tiles - 1 - (st.tiles - 1 - first) % step);
+        // O is complete.  A row sees all positions up to its own, so it sees a NaN or an
+        // infinity if the first one is there (the producers stored zeros in their place).
+        if (alive && wait_s() && poison[i & 1] <= static_cast<uint32_t>(pos))
+          l = __int_as_float(0x7fffffff);
       }
       if (st.split && st.tiles > 1) {
         // the odd tiles' state to the even tiles' thread of the same row (same TMEM lane)
@@ -1251,11 +1254,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           bf16_load_key(x, rec[0], lane);
           poison |= bf16_store_value(ahead, p0, w.key_end, vbuf(kv), pw, 1, lane);
         }
-        poison = __reduce_or_sync(0xffffffffu, poison);
-        if (lane == 0) {
-          poisonw[4 * slot + pw] = poison;
-          any8[4 * (kFlags + slot) + pw] = poison != 0;
-        }
+        if (poison) atomicMin(first_bad + (i & 1), p0 + __ffs(poison) - 1);
         give(kVFull, kv);
       }
       if (st.post && alive && wait_empty(kKEmpty, itk + st.pre + st.tiles)) {
@@ -1287,7 +1286,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       sync_cta();
       const Item w = items[i & 1];
       if (w.done) break;
-      if (warp == kSchedWarp && lane == 0) next_item(a, *line, items[(i + 1) & 1]);
+      if (warp == kSchedWarp && lane == 0) {
+        first_bad[(i + 1) & 1] = 0xffffffffu;
+        next_item(a, *line, items[(i + 1) & 1]);
+      }
       __syncwarp();
       const Steps<INT2> st(w, a);
       sync_cta();                   // Q is there
