@@ -989,7 +989,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             // q R_K -> fp16 Q, a power of two a row apart, in the pages' order of d
             float down, up;
             row_scale(ts, down, up);
-            scale *= up;
+            scale = fmaxf(scale * up, 1.17549435e-38f);  // a row of zeros: 0 * -inf would be NaN
             pair->x = scale;        // for the group of the odd tiles
 #pragma unroll 1
             for (int wq = 0; wq < 2; ++wq) {

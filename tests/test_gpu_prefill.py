@@ -181,6 +181,63 @@ def test_tiny_and_large_values():
         c.check(c.prefill(q, [0, 100]), q, [100])
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("size", [0.0, 1e-38, 1e-30])
+def test_queries_near_zero(kind, size):
+    """Rows of zeros (padding) and of next to nothing weigh what they see alike; what lies behind
+    their position stays hidden, and other rows of the tile are as ever."""
+    c = Paged(kind, 4, 2, [300, 70], seed=6)
+    q = c.queries(130)
+    q[::2] = (q[::2].float() * size).bfloat16()
+    c.check(c.prefill(q, [0, 90, 130]), q, [90, 40])
+    q = c.queries(5, scale=size)               # one row tile, several of the keys' tiles
+    c.check(c.prefill(q, [0, 5, 5]), q, [5, 0])
+
+
+@pytest.mark.parametrize("kind,extra", [("int2", 500_000), ("bf16", 80_000)])
+def test_pool_past_32_bits(kind, extra):
+    """Records beyond 4 GB, and appends to them."""
+    c = Paged(kind, 16, 8, [400], seed=7, extra=extra)
+    assert int(c.pt.max()) * (c.pool.numel() // c.pages) > 2 ** 32
+    q = c.queries(33)
+    c.check(c.prefill(q, [0, 33]), q, [33])
+    rope, pos = K.make_rope(torch.ones(1, 2, device="cuda"), "half"), torch.zeros(1, dtype=torch.int32,
+                                                                                  device="cuda")
+    app = K.kvq_append_rope if kind == "int2" else K.kvq_bf16_append_rope
+    plain = K.kvq_append if kind == "int2" else K.kvq_bf16_append
+    last, seq = pos + 399, torch.zeros_like(pos)
+    turned = torch.empty_like(c.k[:1])
+    K.kvq_rope(c.h, c.k[:1], turned, pos, rope)
+    plain(c.h, c.pool, c.pages, turned, c.v[:1], seq, last, c.pt)
+    want = c.prefill(q, [0, 33])
+    c.append(c.k, c.v)
+    app(c.h, c.pool, c.pages, c.k[:1], c.v[:1], seq, last, c.pt, rope, rope_positions=pos)
+    assert torch.equal(c.prefill(q, [0, 33]), want)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_two_streams(kind):
+    """Calls that overlap on two streams, each with its own workspace, and a call whose tensors
+    were made on another stream."""
+    c = Paged(kind, 8, 2, [3000, 40], seed=8)
+    q = [c.queries(n) for n in (140, 60)]
+    cu = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 120, 140], [0, 60, 60])]
+    want = [c.prefill(*a) for a in zip(q, cu)]
+    size = (K.kvq_prefill_workspace_bytes if kind == "int2" else K.kvq_bf16_prefill_workspace_bytes)
+    ws = [torch.empty(size(c.h, 2, 140), dtype=torch.uint8, device="cuda") for _ in q]
+    streams = [torch.cuda.Stream() for _ in q]
+    outs = [[torch.empty_like(w) for _ in range(4)] for w in want]
+    torch.cuda.synchronize()
+    for r in range(4):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                c.prefill(q[i], cu[i], out=outs[i][r], ws=ws[i])
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, x) for x in o)
+    assert K.kvq_get_status(c.h) == 0
+
+
 @pytest.mark.parametrize("out_rotated,q_rotated", [(True, False), (False, True), (True, True)])
 def test_folded_rotations(out_rotated, q_rotated):
     c = Paged("int2", 8, 2, [500, 90], out_rotated=out_rotated, q_rotated=q_rotated)
