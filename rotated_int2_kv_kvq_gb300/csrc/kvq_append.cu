@@ -210,17 +210,37 @@ __global__ void __launch_bounds__(NW * 32) append_int2_kernel(AppendArgs a) {
       if (which == 0) {
         __syncthreads();
         const int half = a.rope.rot_dim >> 1;
-        for (int idx = tid; idx < half * kTile; idx += kAppThreads) {
-          const int k = idx % kTile, i = idx / kTile;
-          const int w = ang[k];
-          if (w < 0) continue;
-          const float* t = a.rope.table + static_cast<size_t>(w) * a.rope.rot_dim + i;
-          const bool inter = a.rope.style == KVQ_ROPE_INTERLEAVED;
+        const bool inter = a.rope.style == KVQ_ROPE_INTERLEAVED;
+        auto turn = [&](int k, int i, float c, float s) {      // pair i of token k
           const int d0 = inter ? 2 * i : i, d1 = inter ? 2 * i + 1 : i + half;
           float p, q;
-          rope_pair(Cs[d0 * kTile + k], Cs[d1 * kTile + k], t[0], t[half], p, q);
+          rope_pair(Cs[d0 * kTile + k], Cs[d1 * kTile + k], c, s, p, q);
           Cs[d0 * kTile + k] = __fsub_rn(__bfloat162float(__float2bfloat16_rn(p)), mus[d0]);
           Cs[d1 * kTile + k] = __fsub_rn(__bfloat162float(__float2bfloat16_rn(q)), mus[d1]);
+        };
+        // Lanes are tokens (Cs is read and written without bank conflicts), so a load of
+        // the table touches 32 rows: eight pairs at a time use whole sectors of them.
+        if (half % 8 == 0) {
+          for (int idx = tid; idx < half / 8 * kTile; idx += kAppThreads) {
+            const int k = idx % kTile, i = idx / kTile * 8;
+            const int w = ang[k];
+            if (w < 0) continue;
+            const float4* t = reinterpret_cast<const float4*>(
+                a.rope.table + static_cast<size_t>(w) * a.rope.rot_dim + i);
+            const float4 c0 = t[0], c1 = t[1], s0 = t[half / 4], s1 = t[half / 4 + 1];
+            const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+            const float sn[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) turn(k, i + e, c[e], sn[e]);
+          }
+        } else {
+          for (int idx = tid; idx < half * kTile; idx += kAppThreads) {
+            const int k = idx % kTile, i = idx / kTile;
+            const int w = ang[k];
+            if (w < 0) continue;
+            const float* t = a.rope.table + static_cast<size_t>(w) * a.rope.rot_dim + i;
+            turn(k, i, t[0], t[half]);
+          }
         }
       }
     }

@@ -194,6 +194,20 @@ def test_queries_near_zero(kind, size):
     c.check(c.prefill(q, [0, 5, 5]), q, [5, 0])
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [9, 200])
+def test_nonfinite_queries(kind, n):
+    """A query with a NaN or an infinity spoils its own row and head, and no other."""
+    c = Paged(kind, 4, 2, [300])
+    q = c.queries(n)
+    want = c.prefill(q, [0, n])
+    q[3, 1, 5], q[n - 1, 2, 77] = float("nan"), float("inf")
+    out = c.prefill(q, [0, n])
+    bad = torch.zeros(n, 4, dtype=torch.bool, device="cuda")
+    bad[3, 1] = bad[n - 1, 2] = True
+    assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], want[~bad])
+
+
 @pytest.mark.parametrize("kind,extra", [("int2", 500_000), ("bf16", 80_000)])
 def test_pool_past_32_bits(kind, extra):
     """Records beyond 4 GB, and appends to them."""
