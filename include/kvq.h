@@ -81,7 +81,8 @@ extern "C" {
 #define KVQ_STATUS_BAD_POS     2u  /* position < 0 or >= max_pages*page_size      */
 #define KVQ_STATUS_BAD_SEQLEN  4u  /* seq_len < 0 or > max_pages*page_size        */
 #define KVQ_STATUS_BAD_SEQ     8u  /* seq_idx < 0 or >= batch                     */
-#define KVQ_STATUS_TIMEOUT    16u  /* a bounded wait on a page copy gave up (2 s)  */
+#define KVQ_STATUS_TIMEOUT    16u  /* a bounded wait inside a kernel gave up (2 s):
+                                     the call's output is incomplete           */
 
 /* ---- layout flags -------------------------------------------------------- */
 /* Decode returns the output in the rotated value basis (o_rot) instead of
@@ -291,8 +292,9 @@ int kvq_rope(kvq_handle* h, const uint16_t* x, long long x_stride, uint16_t* y, 
  *   positions : the tokens' places in the cache, and their angles unless
  *   rope_positions (device int32 [n], may be NULL) gives other ones.
  * A rotation position outside the table sets KVQ_STATUS_BAD_POS and the token is
- * skipped (key and value).  Other arguments, errors and status bits as for
- * kvq_append. */
+ * skipped (key and value).  Two tokens of one call must not share (seq, position):
+ * what that position then holds is undefined (parts of both, even); the others are
+ * as ever.  Other arguments, errors and status bits as for kvq_append. */
 int kvq_append_rope(kvq_handle* h, void* pool, int num_pool_pages, const uint16_t* K,
                     long long k_stride, const uint16_t* V, long long v_stride,
                     const int32_t* seq_idx, const int32_t* positions, int n,
@@ -426,11 +428,12 @@ int kvq_append_decode_window(kvq_handle* h, void* pool, int num_pool_pages, void
  *   cu_q       : device int32 [batch + 1], non-decreasing, within [0, n].  Rows that
  *                belong to no sequence are left as they were; a sequence may have none.
  *   n          : rows of q and out.  0 is a no-op.
- *   page_table : device int32 [batch][max_pages];  seq_lens: device int32 [batch],
- *                the context after the append.
- *   out        : device bf16 [n][H][D], 16-byte aligned.
+ *   page_table : device int32 [batch][max_pages], max_pages <= 2^26, batch <= 65535;
+ *                seq_lens: device int32 [batch], the context after the append.
+ *   out        : device bf16 [n][H][D], 16-byte aligned; must not overlap q.
  *   workspace  : device, >= kvq_prefill_workspace_bytes(h, batch, n) bytes, 256-byte
- *                aligned; contents on entry do not matter.
+ *                aligned; contents on entry do not matter.  Calls (and captured
+ *                graphs) that can run at the same time need one each.
  * Rows of a sequence with seq_lens[b] < n_b or beyond the page table are set to 0
  * (KVQ_STATUS_BAD_SEQLEN); one whose rows are no range in [0, n] is skipped
  * (KVQ_STATUS_BAD_SEQ).  A page id out of range sets KVQ_STATUS_BAD_PAGE and its

@@ -81,7 +81,8 @@ __device__ __forceinline__ float bf16_to_f32(uint32_t bits16) {
 // ROPE: keys are first rotated by their position (rope_pair, rounded to bf16 as
 // the rotated key that kvq_rope writes), in the staged tile between its load and
 // the centring: 64 pairs per token beside the 16,384 products of the rotation
-// into the cache's basis, so it is not worth a pass of its own over HBM.  K and
+// into the cache's basis, so it is not worth a pass of its own over HBM: 4,099 x 8
+// heads take 75 us, 66 without turning the keys; a 16-token step 8.5 and 7.3.  K and
 // V rows may be strided (slices of a fused projection).
 template <int TPW, int NW, bool ROPE>
 __global__ void __launch_bounds__(NW * 32) append_int2_kernel(AppendArgs a) {
@@ -219,7 +220,8 @@ __global__ void __launch_bounds__(NW * 32) append_int2_kernel(AppendArgs a) {
           Cs[d1 * kTile + k] = __fsub_rn(__bfloat162float(__float2bfloat16_rn(q)), mus[d1]);
         };
         // Lanes are tokens (Cs is read and written without bank conflicts), so a load of
-        // the table touches 32 rows: eight pairs at a time use whole sectors of them.
+        // the table touches 32 rows: eight pairs at a time use whole sectors of them
+        // (4,099 tokens: 75 us against 92 pair by pair).
         if (half % 8 == 0) {
           for (int idx = tid; idx < half / 8 * kTile; idx += kAppThreads) {
             const int k = idx % kTile, i = idx / kTile * 8;
