@@ -31,17 +31,18 @@
 // the GPU without a choice of split counts.  An item that a range border cuts
 // leaves partial (max, sum, O) states, joined by the combine kernel.
 //
-// Measured (32 query, 8 KV heads): 4096 new tokens at 32K, INT2: 1421 us, 1456 TFLOP/s,
-// 78 % of the bf16 rate of a large library product on the same GPU (1865); the products
+// Measured (32 query, 8 KV heads): 4096 new tokens at 32K, INT2: 1435 us, 1440 TFLOP/s,
+// 77 % of the bf16 rate of a large library product on the same GPU (1865); the products
 // alone, with the softmax and the unpacking left out, take 1091 us at the power limit.
-// What is left is the softmax's instructions (128 threads' exponentials, sums and packing
-// beside each product; issue slots 54 % busy) and the waits of a step's chain
-// S -> P -> O.  Two prompts of 4093, BF16: 290 us.  Sixteen decode tokens beside a
-// 1021-token chunk: 176 us.  Eight drafts of five tokens at up to 8K: 50 us, of which the
-// launches, the line's setup, the rotations and the join take about half.
+// What is left is the chain S -> softmax -> P -> O of a row tile, of which two fit TMEM:
+// tensor pipe 59 % and issue slots 58 % busy, the exponentials' unit 29 %.  Two prompts
+// of 4093, BF16: 290 us.  Sixteen decode tokens beside a 1021-token chunk: 177 us.
+// Eight drafts of five tokens at up to 8K: 51 us, of which the launches, the line's
+// setup, the rotations and the join take about half.
 // Tried and slower: half tiles of 64 columns (2045 us: such a product runs at half rate),
 // producer warps for keys and values apart (1759), eight producer warps (1844), a ring of
-// raw records in shared memory (1745), no CTA-wide barrier between items (1524: spills).
+// raw records in shared memory (1745), no CTA-wide barrier between items (1524: spills),
+// part of the exponentials as polynomials (an eighth of them: 1494).
 #include "kvq_internal.cuh"
 
 namespace kvq {
