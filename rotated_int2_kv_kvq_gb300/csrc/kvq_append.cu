@@ -81,9 +81,8 @@ __device__ __forceinline__ float bf16_to_f32(uint32_t bits16) {
 // ROPE: keys are first rotated by their position (rope_pair, rounded to bf16 as
 // the rotated key that kvq_rope writes), in the staged tile between its load and
 // the centring: 64 pairs per token beside the 16,384 products of the rotation
-// into the cache's basis, so it is not worth a pass of its own over HBM: 4,099 x 8
-// heads take 75 us, 66 without turning the keys; a 16-token step 8.5 and 7.3.  K and
-// V rows may be strided (slices of a fused projection).
+// into the cache's basis, so it is not worth a pass of its own over HBM: 9 of the
+// 69 us that 4,099 x 8 heads take, 1.2 of a 16-token step's 8.5.  K and V rows may be strided (slices of a fused projection).
 template <int TPW, int NW, bool ROPE>
 __global__ void __launch_bounds__(NW * 32) append_int2_kernel(AppendArgs a) {
   constexpr int kAppThreads = NW * 32;
@@ -127,33 +126,53 @@ __global__ void __launch_bounds__(NW * 32) append_int2_kernel(AppendArgs a) {
   }
   bool r_ready = false;
 
+  // Tiles are dealt in turn while every CTA gets one; what is left is shared out in
+  // steps of what a warp takes, so that the last round is as short for all (idle warps
+  // leave the ALUs to the SM's other CTA).  Rotary keys, 8 heads: 1,300 tokens 31 us
+  // against 37 with whole tiles only, 4,099 tokens 69 against 75, 32,767 tokens 493 against
+  // 490; equal contiguous shares from the start 31, 68, 502.
+  constexpr int kShare = TPW == 1 ? kTile : TPW;
+  const int rounds = a.n / static_cast<int>(kTile * gridDim.x);
+  const int rest = rounds * static_cast<int>(kTile * gridDim.x);
+  const int shares = (a.n - rest + kShare - 1) / kShare;      // < gridDim.x * kTile / kShare
+  const int gx = static_cast<int>(gridDim.x), x = static_cast<int>(blockIdx.x);
+  auto tile_begin = [&](int round) {
+    return round < rounds ? (round * gx + x) * kTile : rest + shares * x / gx * kShare;
+  };
+  auto tile_end = [&](int round) {
+    return round < rounds ? tile_begin(round) + kTile
+                          : min(rest + shares * (x + 1) / gx * kShare, a.n);
+  };
+
   // The tile's tokens: 16-byte pieces (8 bf16) of [kTile][128], loaded one tile
   // ahead into registers so that the loads of tile i+1 are in flight while the
   // rotation of tile i runs.
   constexpr int kPieces = kTile * (kDim / 8);
   constexpr int kPre = (kPieces + kAppThreads - 1) / kAppThreads;
   uint4 pre[kPre];
-  auto load_tile = [&](int t0) {
+  auto load_tile = [&](int round) {
+    const int t0 = tile_begin(round), end = tile_end(round);
 #pragma unroll
     for (int r = 0; r < kPre; ++r) {
       const int idx = tid + r * kAppThreads;
       const int k = idx % kTile, ch = idx / kTile;
       const int tok = t0 + k;
       pre[r] = make_uint4(0u, 0u, 0u, 0u);
-      if (idx < kPieces && tok < a.n)
+      if (idx < kPieces && tok < end)
         pre[r] = *reinterpret_cast<const uint4*>(X + static_cast<size_t>(tok) * row + kv * kDim +
                                                  ch * 8);
     }
   };
-  if (static_cast<long long>(blockIdx.x) * kTile < a.n) load_tile(blockIdx.x * kTile);
+  load_tile(0);
 
-  for (int tile = blockIdx.x; tile * kTile < a.n; tile += gridDim.x) {
-    const int tok0 = tile * kTile;
+  for (int round = 0; round <= rounds; ++round) {
+    const int tok0 = tile_begin(round), end = tile_end(round);
+    if (tok0 >= end) break;            // nothing is left
     // (1) record address of each token of the tile (or -1 if it is skipped)
     if (tid < kTile) {
       const int tok = tok0 + tid;
       long long r = -1;
-      if (tok < a.n) {
+      if (tok < end) {
         const int b = a.seq_idx[tok];
         const int p = a.positions[tok];
         if (b < 0 || b >= a.batch) {
@@ -195,7 +214,7 @@ __global__ void __launch_bounds__(NW * 32) append_int2_kernel(AppendArgs a) {
           v[2 * e] = bf16_to_f32(w4[e] & 0xffffu);
           v[2 * e + 1] = bf16_to_f32(w4[e] >> 16);
         }
-        if (mu && tok0 + k < a.n) {
+        if (mu && tok0 + k < end) {
           const float4 m0 = *reinterpret_cast<const float4*>(mus + ch * 8);
           const float4 m1 = *reinterpret_cast<const float4*>(mus + ch * 8 + 4);
           const float mv[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
@@ -221,7 +240,7 @@ __global__ void __launch_bounds__(NW * 32) append_int2_kernel(AppendArgs a) {
         };
         // Lanes are tokens (Cs is read and written without bank conflicts), so a load of
         // the table touches 32 rows: eight pairs at a time use whole sectors of them
-        // (4,099 tokens: 75 us against 92 pair by pair).
+        // (17 us less for 4,099 tokens than pair by pair).
         if (half % 8 == 0) {
           for (int idx = tid; idx < half / 8 * kTile; idx += kAppThreads) {
             const int k = idx % kTile, i = idx / kTile * 8;
@@ -260,86 +279,88 @@ __global__ void __launch_bounds__(NW * 32) append_int2_kernel(AppendArgs a) {
     }
     __syncthreads();
     // the next tile's tokens, in flight during this tile's rotation
-    if (static_cast<long long>(tile + gridDim.x) * kTile < a.n) load_tile((tile + gridDim.x) * kTile);
+    if (round < rounds) load_tile(round + 1);
 
-    // (3) rotate: r_i = fmaf chain over j = 0..127 in order, for TPW tokens x 4 outputs
-    float acc[TPW][4];
+    if (tok0 + warp * TPW < end) {       // the warp has tokens
+      // (3) rotate: r_i = fmaf chain over j = 0..127 in order, for TPW tokens x 4 outputs
+      float acc[TPW][4];
 #pragma unroll
-    for (int t = 0; t < TPW; ++t)
+      for (int t = 0; t < TPW; ++t)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[t][c] = 0.0f;
-    const float4* R4 = reinterpret_cast<const float4*>(Rs);
-    const float* cw = Cs + warp * TPW;
-    // operands of step j + 1 are loaded while step j's products run
-    float4 rn = R4[lane];
-    float cn[TPW];
-    auto load_c = [&](int j, float (&c)[TPW]) {
-      const float* cj = cw + j * kTile;
-      if constexpr (TPW % 4 == 0) {
+        for (int c = 0; c < 4; ++c) acc[t][c] = 0.0f;
+      const float4* R4 = reinterpret_cast<const float4*>(Rs);
+      const float* cw = Cs + warp * TPW;
+      // operands of step j + 1 are loaded while step j's products run
+      float4 rn = R4[lane];
+      float cn[TPW];
+      auto load_c = [&](int j, float (&c)[TPW]) {
+        const float* cj = cw + j * kTile;
+        if constexpr (TPW % 4 == 0) {
 #pragma unroll
-        for (int t = 0; t < TPW; t += 4) {
-          const float4 c4 = *reinterpret_cast<const float4*>(cj + t);
-          c[t] = c4.x; c[t + 1] = c4.y; c[t + 2] = c4.z; c[t + 3] = c4.w;
+          for (int t = 0; t < TPW; t += 4) {
+            const float4 c4 = *reinterpret_cast<const float4*>(cj + t);
+            c[t] = c4.x; c[t + 1] = c4.y; c[t + 2] = c4.z; c[t + 3] = c4.w;
+          }
+        } else {
+#pragma unroll
+          for (int t = 0; t < TPW; ++t) c[t] = cj[t];
         }
-      } else {
-#pragma unroll
-        for (int t = 0; t < TPW; ++t) c[t] = cj[t];
-      }
-    };
-    load_c(0, cn);
+      };
+      load_c(0, cn);
 #pragma unroll kAUnroll
-    for (int j = 0; j < kDim; ++j) {
-      const float4 r = rn;
-      float c[TPW];
+      for (int j = 0; j < kDim; ++j) {
+        const float4 r = rn;
+        float c[TPW];
 #pragma unroll
-      for (int t = 0; t < TPW; ++t) c[t] = cn[t];
-      if (j + 1 < kDim) {
-        rn = R4[(j + 1) * (kDim / 4) + lane];
-        load_c(j + 1, cn);
+        for (int t = 0; t < TPW; ++t) c[t] = cn[t];
+        if (j + 1 < kDim) {
+          rn = R4[(j + 1) * (kDim / 4) + lane];
+          load_c(j + 1, cn);
+        }
+#pragma unroll
+        for (int t = 0; t < TPW; ++t) {
+          acc[t][0] = fmaf(c[t], r.x, acc[t][0]);
+          acc[t][1] = fmaf(c[t], r.y, acc[t][1]);
+          acc[t][2] = fmaf(c[t], r.z, acc[t][2]);
+          acc[t][3] = fmaf(c[t], r.w, acc[t][3]);
+        }
       }
+
+      // (4) group max/min (whole vector), clip, fp16 scale/zero, codes
 #pragma unroll
       for (int t = 0; t < TPW; ++t) {
-        acc[t][0] = fmaf(c[t], r.x, acc[t][0]);
-        acc[t][1] = fmaf(c[t], r.y, acc[t][1]);
-        acc[t][2] = fmaf(c[t], r.z, acc[t][2]);
-        acc[t][3] = fmaf(c[t], r.w, acc[t][3]);
-      }
-    }
-
-    // (4) group max/min (whole vector), clip, fp16 scale/zero, codes
+        const float mx = warp_max(fmaxf(fmaxf(acc[t][0], acc[t][1]), fmaxf(acc[t][2], acc[t][3])));
+        const float mn = warp_min(fminf(fminf(acc[t][0], acc[t][1]), fminf(acc[t][2], acc[t][3])));
+        const float mxc = __fmul_rn(clip, mx);
+        const float mnc = __fmul_rn(clip, mn);
+        const float s32 = __fdiv_rn(__fsub_rn(mxc, mnc), 3.0f);
+        const __half sh = __float2half_rn(s32);
+        const __half zh = __float2half_rn(mnc);
+        const float s = __half2float(sh), z = __half2float(zh);
+        uint32_t packed = 0;
+        if (s != 0.0f) {
+          const float rs = rcp_approx(s);
+          float d[4], q[4];
+          bool near = false;
 #pragma unroll
-    for (int t = 0; t < TPW; ++t) {
-      const float mx = warp_max(fmaxf(fmaxf(acc[t][0], acc[t][1]), fmaxf(acc[t][2], acc[t][3])));
-      const float mn = warp_min(fminf(fminf(acc[t][0], acc[t][1]), fminf(acc[t][2], acc[t][3])));
-      const float mxc = __fmul_rn(clip, mx);
-      const float mnc = __fmul_rn(clip, mn);
-      const float s32 = __fdiv_rn(__fsub_rn(mxc, mnc), 3.0f);
-      const __half sh = __float2half_rn(s32);
-      const __half zh = __float2half_rn(mnc);
-      const float s = __half2float(sh), z = __half2float(zh);
-      uint32_t packed = 0;
-      if (s != 0.0f) {
-        const float rs = rcp_approx(s);
-        float d[4], q[4];
-        bool near = false;
+          for (int c = 0; c < 4; ++c) {
+            d[c] = __fsub_rn(acc[t][c], z);
+            q[c] = __fmul_rn(d[c], rs);
+            near = near || near_half(q[c]);
+          }
+          if (near) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          d[c] = __fsub_rn(acc[t][c], z);
-          q[c] = __fmul_rn(d[c], rs);
-          near = near || near_half(q[c]);
+            for (int c = 0; c < 4; ++c) q[c] = __fdiv_rn(d[c], s);
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) packed |= clamp_code(q[c]) << (8 * c);
         }
-        if (near) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) q[c] = __fdiv_rn(d[c], s);
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) packed |= clamp_code(q[c]) << (8 * c);
+        const int k = warp * TPW + t;
+        reinterpret_cast<uint32_t*>(codes)[k * (kCodeRow / 4) + lane] = packed;
+        if (lane == 0)
+          sz[k] = static_cast<uint32_t>(__half_as_ushort(sh)) |
+                  (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
       }
-      const int k = warp * TPW + t;
-      reinterpret_cast<uint32_t*>(codes)[k * (kCodeRow / 4) + lane] = packed;
-      if (lane == 0)
-        sz[k] = static_cast<uint32_t>(__half_as_ushort(sh)) |
-                (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
     }
     __syncthreads();
 
@@ -455,14 +476,15 @@ cudaError_t launch_tpw(const AppendArgs& a, int num_sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  const int tiles = (a.n + S::kTile - 1) / S::kTile;
+  const int share = TPW == 1 ? S::kTile : TPW;       // kShare
+  const int shares = (a.n + share - 1) / share;
   // One wave of CTAs (two per SM, the shared-memory limit); each CTA loops
   // over tiles so the rotation matrix is staged once per CTA, not once per
   // tile (measured: 408 us per 32,767-token prefill against 419 us with two
   // waves).
   const int per_head = a.Hkv * 2;
   int gx = (2 * num_sms + per_head - 1) / per_head;
-  if (gx > tiles) gx = tiles;
+  if (gx > shares) gx = shares;
   if (gx < 1) gx = 1;
   dim3 grid(gx, a.Hkv, 2);
   append_int2_kernel<TPW, NW, ROPE>
