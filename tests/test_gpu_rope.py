@@ -260,6 +260,23 @@ def test_append_equals_rope_then_append(kind, style, rot, Hkv, new, lens):
     assert K.kvq_get_status(h) == 0
 
 
+@pytest.mark.parametrize("Hkv", [8, 1])
+@pytest.mark.parametrize("n", [151, 153, 161, 290, 304, 305, 620, 1215, 1217, 1300, 2431, 2433])
+def test_int2_append_sizes(Hkv, n):
+    """Token counts at which the tokens a warp takes, or the tiles a CTA takes, change."""
+    g = _gen(n)
+    h = _handle(Hkv, Hkv, seed=8)
+    rope = K.make_rope(_table(128, n), "half")
+    pt, pages = _paged([n])
+    seq, pos = _tokens([n], [n])
+    k, v = (torch.randn(n, Hkv, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    pool = torch.zeros(pages * K.kvq_page_bytes(h), device="cuda", dtype=torch.uint8)
+    want = pool.clone()
+    K.kvq_append_rope(h, pool, pages, k, v, seq, pos, pt, rope)
+    _unfused("int2", h, want, pages, k, v, seq, pos, pt, rope)
+    assert torch.equal(pool, want)
+
+
 @pytest.mark.parametrize("kind", ["int2", "bf16"])
 def test_append_skips_bad_tokens(kind):
     """Bad sequence, position, page and angle: the token is skipped (key and value), the bit is
