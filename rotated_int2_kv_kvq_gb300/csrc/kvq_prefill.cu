@@ -66,6 +66,13 @@ constexpr int kStages = 2;
 constexpr int kFlags = 4;                  // key tiles whose missing pages are kept
 constexpr int kTileBytes = 128 * 128 * 2;  // one 128 x 128 16-bit operand
 constexpr float kLazy = 8.0f;              // log2 growth of a row maximum before O is rescaled
+// The INT2 path's weights are 2^(s - reference + kBias), up to 2^15 with a reference that lags by kLazy:
+// fp16 then keeps its 11 bits down to 2^-21 of the reference (14.5 nats below it) and something down to
+// 2^-32, so that a long flat tail behind one dominant key keeps its mass.  O and the sum carry the same
+// factor.  Without it a tail at 2^-22.6 came out 13.7 % too large and one at 2^-25 as zero.  A smaller
+// kLazy would leave more room but rescales O more often (4096 tokens at 32K: 8: 1441 us, 7: 1459,
+// 6: 1487, 4: 1519; without the factor 1442).
+constexpr float kBias = 15.0f - kLazy;
 
 struct Smem {
   static constexpr int kQ = 0;                              // [2][32 KB]
@@ -784,8 +791,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sca
   if (first) {
     mref = mnew;
   } else {
-    // O is rescaled only when a maximum grew by 2^8 (the weights stay below that, in
-    // range of fp16, and the sums are fp32): a step that most tiles skip
+    // O is rescaled only when a maximum grew by 2^8 (the weights stay below that times
+    // kBias's 2^7, in range of fp16, and the sums are fp32): a step that most tiles skip
     const bool grow = mnew > mref + kLazy;
     if (__any_sync(0xffffffffu, grow)) {
       const float f = grow ? fast_exp2(mref - mnew) : 1.0f;
@@ -801,7 +808,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sca
       if (grow) mref = mnew;
     }
   }
-  const float neg = mref == -INFINITY ? 0.0f : -mref;
+  const float neg = mref == -INFINITY ? 0.0f : (INT2 ? kBias : 0.0f) - mref;
   const uint64_t sc2 = pair2(scale, scale), ng2 = pair2(neg, neg);
   uint64_t s0 = 0, s1 = 0;
 #pragma unroll
