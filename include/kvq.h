@@ -182,7 +182,9 @@ size_t kvq_bf16_page_bytes(const kvq_handle* h);
  *   mu : device fp32 [Hkv][D], the per-channel key mean.
  * The arrays are copied (stream-ordered) into the handle; the caller may free
  * them once the stream has passed this call.  May be called again to replace
- * the bank.  Orthogonality is not checked. */
+ * the bank.  Orthogonality is not checked.  The handle's bank takes 288 KB of
+ * device memory a KV head: R and R_V^T in fp32, and the 16-bit operands of
+ * kvq_prefill. */
 int kvq_set_rotation(kvq_handle* h, const float* R, const float* mu, void* stream);
 
 /* ---- quantise-on-append --------------------------------------------------

@@ -1991,19 +1991,6 @@ __global__ void __launch_bounds__(128) dequant_kernel(const uint8_t* __restrict_
   }
 }
 
-// out[c][j][i] = in[c][i][j] for count 128x128 matrices.
-__global__ void transpose_kernel(const float* __restrict__ in, float* __restrict__ out) {
-  __shared__ float tile[32][33];
-  const float* src = in + static_cast<size_t>(blockIdx.z) * kDim * kDim;
-  float* dst = out + static_cast<size_t>(blockIdx.z) * kDim * kDim;
-  const int bx = blockIdx.x * 32, by = blockIdx.y * 32;
-  for (int k = threadIdx.y; k < 32; k += blockDim.y)
-    tile[k][threadIdx.x] = src[(by + k) * kDim + bx + threadIdx.x];
-  __syncthreads();
-  for (int k = threadIdx.y; k < 32; k += blockDim.y)
-    dst[(bx + k) * kDim + by + threadIdx.x] = tile[threadIdx.x][k];
-}
-
 // Dynamic shared-memory size and carve-out of kernel kKern, set once per
 // device (one flag set per kernel: each instantiation of this template is
 // its own kernel).
@@ -2133,12 +2120,6 @@ cudaError_t launch_dequant(const uint8_t* pool, int num_pool_pages, const int32_
   dim3 grid(len, Hkv);
   dequant_kernel<<<grid, 128, 0, st>>>(pool, num_pool_pages, page_table, max_pages, Hkv, seq,
                                        start, K_out, V_out, status);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_transpose(const float* in, float* out, int count, cudaStream_t st) {
-  dim3 grid(kDim / 32, kDim / 32, count), block(32, 8);
-  transpose_kernel<<<grid, block, 0, st>>>(in, out);
   return cudaGetLastError();
 }
 

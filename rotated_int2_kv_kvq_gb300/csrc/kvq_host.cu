@@ -591,10 +591,9 @@ int kvq_set_rotation(kvq_handle* h, const float* R, const float* mu, void* strea
       cudaMemcpyAsync(mub, mu, static_cast<size_t>(Hkv) * kDim * sizeof(float),
                       cudaMemcpyDeviceToDevice, st) != cudaSuccess)
     return KVQ_ECUDA;
-  if (kvq::launch_transpose(h->bank + Hkv * mat, RVt, Hkv, st) != cudaSuccess) return KVQ_ECUDA;
-  if (kvq::launch_prefill_bank(h->bank, Hkv, (h->L.flags & KVQ_Q_ROTATED) != 0,
-                               rot_operand(h->bank, Hkv, 0), rot_operand(h->bank, Hkv, 1),
-                               rot_operand(h->bank, Hkv, 2), st) != cudaSuccess)
+  if (kvq::launch_rotation_bank(h->bank, Hkv, (h->L.flags & KVQ_Q_ROTATED) != 0, RVt,
+                                rot_operand(h->bank, Hkv, 0), rot_operand(h->bank, Hkv, 1),
+                                rot_operand(h->bank, Hkv, 2), st) != cudaSuccess)
     return KVQ_ECUDA;
   h->ready = true;
   return KVQ_OK;

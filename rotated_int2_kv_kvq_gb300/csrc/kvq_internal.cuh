@@ -153,10 +153,10 @@ struct PrefillWs {
 };
 PrefillWs prefill_ws_layout(int num_sms);
 cudaError_t launch_prefill(const PrefillArgs& a, bool int2, int num_sms, cudaStream_t st);
-// The operands of the prefill's rotations from R [2][Hkv][D][D]; identity_q: the
+// R_V^T and the operands of the prefill's rotations from R [2][Hkv][D][D]; identity_q: the
 // identity in R_K's place (the caller's queries are rotated already).
-cudaError_t launch_prefill_bank(const float* R, int Hkv, bool identity_q, uint16_t* hi, uint16_t* lo,
-                                uint16_t* rv, cudaStream_t st);
+cudaError_t launch_rotation_bank(const float* R, int Hkv, bool identity_q, float* RVt, uint16_t* hi,
+                                 uint16_t* lo, uint16_t* rv, cudaStream_t st);
 
 // ---- launchers (defined in the .cu files) --------------------------------
 cudaError_t launch_append_int2(const AppendArgs& a, int num_sms, cudaStream_t st);
@@ -177,7 +177,6 @@ cudaError_t launch_combine(const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_dequant(const uint8_t* pool, int num_pool_pages, const int32_t* page_table,
                            int max_pages, int Hkv, int seq, int start, int len, float* K_out,
                            float* V_out, uint32_t* status, cudaStream_t st);
-cudaError_t launch_transpose(const float* in, float* out, int count, cudaStream_t st);
 size_t optr_workspace_bytes(int H, int T, int Nq, int G, int Dm);
 int optr_calibrate(int H, int T, int Nq, int G, int Dm, const uint16_t* K, const uint16_t* V,
                    const uint16_t* Q, const float* W, const float* R0, const float* mu,

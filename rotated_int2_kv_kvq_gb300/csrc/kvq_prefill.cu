@@ -1423,23 +1423,41 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   }
 }
 
-// ---- the rotations' operands ---------------------------------------------------------
-// R_K^T as two bf16 parts (hi + lo: 16 bits of each entry) and R_V as fp16, each a
-// 128 x 128 K-major operand in the swizzled layout above: row n, column k of head kv.
-__global__ void __launch_bounds__(256) prefill_bank_kernel(const float* R, int Hkv, bool identity_q,
-                                                           uint16_t* hi, uint16_t* lo, uint16_t* rv) {
-  const int kv = blockIdx.x;
-  const float* RK = R + static_cast<size_t>(kv) * kDim * kDim;
-  const float* RV = RK + static_cast<size_t>(Hkv) * kDim * kDim;
-  const size_t mat = static_cast<size_t>(kv) * kDim * kDim;
-  for (int idx = threadIdx.x; idx < kDim * kDim; idx += blockDim.x) {
-    const int n = idx & 127, k = idx >> 7;
-    const size_t at = mat + (k >> 6) * (kTileBytes / 4) + n * 64 + ((((k >> 3) & 7) ^ (n & 7)) << 3) + (k & 7);
-    const float x = identity_q ? (n == k ? 1.0f : 0.0f) : RK[k * kDim + n];
-    const __nv_bfloat16 h = __float2bfloat16_rn(x);
-    hi[at] = __bfloat16_as_ushort(h);
-    lo[at] = __bfloat16_as_ushort(__float2bfloat16_rn(x - __bfloat162float(h)));
-    rv[at] = __half_as_ushort(__float2half_rn(RV[n * kDim + k]));
+// ---- the rotation bank ---------------------------------------------------------------
+// What kvq_set_rotation derives from R [2][Hkv][D][D]: R_V^T in fp32 (the decode's combine),
+// and the prefill's operands: R_K^T as two bf16 parts (hi + lo: 16 bits of each entry) and R_V
+// as fp16, each a 128 x 128 K-major operand in the swizzled layout above, row n, column k of
+// head kv.  A CTA takes a 32 x 32 tile through shared memory, so that reads and writes are
+// both along rows: one kernel, as many launches as before the operands (a CTA a head that read
+// R_V by columns took 58 us).
+__global__ void __launch_bounds__(256) rotation_bank_kernel(const float* R, int Hkv, bool identity_q,
+                                                            float* RVt, uint16_t* hi, uint16_t* lo,
+                                                            uint16_t* rv) {
+  __shared__ float tile[32][33];
+  const bool value = blockIdx.z >= static_cast<unsigned>(Hkv);
+  const size_t mat = static_cast<size_t>(value ? blockIdx.z - Hkv : blockIdx.z) * kDim * kDim;
+  const float* src = R + static_cast<size_t>(blockIdx.z) * kDim * kDim;
+  const int bx = blockIdx.x * 32, by = blockIdx.y * 32, x = threadIdx.x;
+  auto at = [&](int n, int k) {
+    return mat + (k >> 6) * (kTileBytes / 4) + n * 64 + ((((k >> 3) & 7) ^ (n & 7)) << 3) + (k & 7);
+  };
+  for (int y = threadIdx.y; y < 32; y += 8) {
+    const float e = src[(by + y) * kDim + bx + x];
+    tile[y][x] = e;
+    if (value) rv[at(by + y, bx + x)] = __half_as_ushort(__float2half_rn(e));
+  }
+  __syncthreads();
+  for (int y = threadIdx.y; y < 32; y += 8) {
+    const int n = bx + y, k = by + x;
+    const float e = tile[x][y];                    // R[k][n]
+    if (value) {
+      RVt[mat + n * kDim + k] = e;
+    } else {
+      const float q = identity_q ? (n == k ? 1.0f : 0.0f) : e;
+      const __nv_bfloat16 h = __float2bfloat16_rn(q);
+      hi[at(n, k)] = __bfloat16_as_ushort(h);
+      lo[at(n, k)] = __bfloat16_as_ushort(__float2bfloat16_rn(q - __bfloat162float(h)));
+    }
   }
 }
 
@@ -1628,9 +1646,10 @@ PrefillWs prefill_ws_layout(int num_sms) {
   return w;
 }
 
-cudaError_t launch_prefill_bank(const float* R, int Hkv, bool identity_q, uint16_t* hi, uint16_t* lo,
-                                uint16_t* rv, cudaStream_t st) {
-  prefill_bank_kernel<<<Hkv, 256, 0, st>>>(R, Hkv, identity_q, hi, lo, rv);
+cudaError_t launch_rotation_bank(const float* R, int Hkv, bool identity_q, float* RVt, uint16_t* hi,
+                                 uint16_t* lo, uint16_t* rv, cudaStream_t st) {
+  rotation_bank_kernel<<<dim3(kDim / 32, kDim / 32, 2 * Hkv), dim3(32, 8), 0, st>>>(R, Hkv, identity_q,
+                                                                                   RVt, hi, lo, rv);
   return cudaGetLastError();
 }
 
