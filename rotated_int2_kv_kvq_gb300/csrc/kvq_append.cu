@@ -83,8 +83,10 @@ __device__ __forceinline__ float bf16_to_f32(uint32_t bits16) {
 // the centring: 64 pairs per token beside the 16,384 products of the rotation
 // into the cache's basis, so it is not worth a pass of its own over HBM: 9 of the
 // 69 us that 4,099 x 8 heads take, 1.2 of a 16-token step's 8.5.  K and V rows may be strided (slices of a fused projection).
+// Two CTAs an SM are what shared memory allows; saying so is worth 0.1 us of a step and 1.2 us
+// of 200 rotary tokens x 8 heads, and costs eight-token warps 2 %, so those go without it.
 template <int TPW, int NW, bool ROPE>
-__global__ void __launch_bounds__(NW * 32) append_int2_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(NW * 32, TPW == 8 ? 0 : 2) append_int2_kernel(AppendArgs a) {
   constexpr int kAppThreads = NW * 32;
   using S = AppendSmem<TPW, NW>;
   constexpr int kTile = S::kTile;
@@ -131,18 +133,19 @@ __global__ void __launch_bounds__(NW * 32) append_int2_kernel(AppendArgs a) {
   // leave the ALUs to the SM's other CTA).  Rotary keys, 8 heads: 1,300 tokens 31 us
   // against 37 with whole tiles only, 4,099 tokens 69 against 75, 32,767 tokens 493 against
   // 490; equal contiguous shares from the start 31, 68, 502.
+  // The division into rounds and shares comes from the host (launch_tpw): here it would
+  // stand before the first load (a step of 16 plain tokens 5.8 us against 5.1).
   constexpr int kShare = TPW == 1 ? kTile : TPW;
-  const int rounds = a.n / static_cast<int>(kTile * gridDim.x);
-  const int rest = rounds * static_cast<int>(kTile * gridDim.x);
-  const int shares = (a.n - rest + kShare - 1) / kShare;      // < gridDim.x * kTile / kShare
-  const int gx = static_cast<int>(gridDim.x), x = static_cast<int>(blockIdx.x);
+  const int rounds = a.rounds, gx = static_cast<int>(gridDim.x), x = static_cast<int>(blockIdx.x);
+  const int stride = gx * kTile, rest = rounds * stride;
+  const int begin = rest + (a.share * x + min(x, a.longer)) * kShare;      // this CTA's part of the rest
+  const int finish = min(begin + (a.share + (x < a.longer ? 1 : 0)) * kShare, a.n);
+  // (two ways of writing one product: 32,767 plain tokens 405 us against 412 the other way,
+  // rotary ones 476 against 490)
   auto tile_begin = [&](int round) {
-    return round < rounds ? (round * gx + x) * kTile : rest + shares * x / gx * kShare;
+    return round >= rounds ? begin : ROPE ? (round * gx + x) * kTile : round * stride + x * kTile;
   };
-  auto tile_end = [&](int round) {
-    return round < rounds ? tile_begin(round) + kTile
-                          : min(rest + shares * (x + 1) / gx * kShare, a.n);
-  };
+  auto tile_end = [&](int round) { return round < rounds ? tile_begin(round) + kTile : finish; };
 
   // The tile's tokens: 16-byte pieces (8 bf16) of [kTile][128], loaded one tile
   // ahead into registers so that the loads of tile i+1 are in flight while the
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(128) append_bf16_kernel(AppendArgs a) {
 }
 
 template <int TPW, int NW, bool ROPE>
-cudaError_t launch_tpw(const AppendArgs& a, int num_sms, cudaStream_t st) {
+cudaError_t launch_tpw(AppendArgs a, int num_sms, cudaStream_t st) {
   using S = AppendSmem<TPW, NW>;
   static bool attr_set[64] = {};       // per device: the attribute is per context
   int dev = 0;
@@ -486,6 +489,12 @@ cudaError_t launch_tpw(const AppendArgs& a, int num_sms, cudaStream_t st) {
   int gx = (2 * num_sms + per_head - 1) / per_head;
   if (gx > shares) gx = shares;
   if (gx < 1) gx = 1;
+  // whole tiles while every CTA gets one, then the rest in shares: `share` each, one more
+  // for the first `longer` CTAs
+  a.rounds = a.n / (S::kTile * gx);
+  const int left = (a.n - a.rounds * S::kTile * gx + share - 1) / share;   // < gx * kTile / share
+  a.share = left / gx;
+  a.longer = left % gx;
   dim3 grid(gx, a.Hkv, 2);
   append_int2_kernel<TPW, NW, ROPE>
       <<<grid, NW * 32, ROPE ? S::kBytesRope : S::kBytes, st>>>(a);

@@ -96,6 +96,8 @@ struct AppendArgs {
   const float* mu;           // [Hkv][D]
   float clip_k, clip_v;
   uint32_t* status;
+  // INT2: rounds of whole tiles; then shares of the rest a CTA, and the CTAs with one more
+  int rounds = 0, share = 0, longer = 0;
   // kvq_append_rope and kvq_bf16_append_rope only
   RopeArgs rope;
   const int32_t* rope_positions = nullptr;   // the rotation's positions; nullptr: positions
