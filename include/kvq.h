@@ -422,9 +422,14 @@ int kvq_append_decode_window(kvq_handle* h, void* pool, int num_pool_pages, void
  * them sits at position p = seq_lens[b] - n_b + i and attends to [0, p] (causal):
  *     out[row] = softmax(sm_scale * q_rot . k~_t, t <= p) . v~_t, rotated back by
  *     R_V(kv)^T,
- * which is what kvq_decode gives for q[row] and length p + 1.  KVQ_Q_ROTATED and
- * KVQ_OUT_ROTATED apply as in kvq_decode.  Cache entries and rotated queries are
- * rounded to fp16 for the tensor cores and the weights too; sums are fp32.
+ * which is what kvq_decode computes for q[row] and length p + 1, in fewer bits.
+ * KVQ_Q_ROTATED and KVQ_OUT_ROTATED apply as in kvq_decode.  The tensor cores get
+ * 16-bit operands of one part each, where kvq_decode keeps a low part beside its own:
+ * cache entries code * s + z, rotated queries (times a power of two a row), weights,
+ * the output before R_V^T (likewise scaled) and R_V are rounded to fp16.  Sums and
+ * softmax statistics are fp32, the result is rounded to bf16.  A weight keeps fp16's
+ * 11 bits down to 2^-21 of the row's largest, fewer below that, none below 2^-32.
+ * An entry that fp16 cannot hold (65520 and more) counts as infinite.
  *   q          : device bf16, row i at q + i * q_stride (elements), heads adjacent;
  *                16-byte aligned, q_stride a multiple of 8 and >= H * 128.
  *   cu_q       : device int32 [batch + 1], non-decreasing, within [0, n].  Rows that
@@ -442,8 +447,10 @@ int kvq_append_decode_window(kvq_handle* h, void* pool, int num_pool_pages, void
  * tokens are left out.  A value vector that holds a NaN or an infinity makes NaN
  * the whole output of each row that sees it, and leaves the others alone.
  * Returns KVQ_ENOSPACE if ws_bytes is too small, KVQ_ENOTREADY before
- * kvq_set_rotation.  The result does not depend on how the work is divided beyond
- * fp32 rounding, and is the same on every call. */
+ * kvq_set_rotation.  The same call on the same GPU gives the same bits.  In another
+ * batch, or cut into other chunks, a row's fp32 sums are taken in another order, which
+ * now and then moves one of the 16-bit roundings above or that of the result; its
+ * weights are rounded alike, but for those too small for fp16's 11 bits. */
 size_t kvq_prefill_workspace_bytes(const kvq_handle* h, int batch, int n);
 int kvq_prefill(kvq_handle* h, const void* pool, int num_pool_pages, const uint16_t* q,
                 long long q_stride, const int32_t* cu_q, int n, const int32_t* page_table,
@@ -451,7 +458,8 @@ int kvq_prefill(kvq_handle* h, const void* pool, int num_pool_pages, const uint1
                 size_t ws_bytes, void* stream);
 
 /* The same over the BF16 cache: plain attention with the unrotated query (no
- * rotation bank, flags ignored); operands stay bf16. */
+ * rotation bank, flags ignored).  Entries and queries are taken as they are, weights
+ * are rounded to bf16, sums are fp32. */
 size_t kvq_bf16_prefill_workspace_bytes(const kvq_handle* h, int batch, int n);
 int kvq_bf16_prefill(kvq_handle* h, const void* pool, int num_pool_pages, const uint16_t* q,
                      long long q_stride, const int32_t* cu_q, int n, const int32_t* page_table,

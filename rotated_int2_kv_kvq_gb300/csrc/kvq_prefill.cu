@@ -619,10 +619,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// The power of two that brings the largest |x| of this thread's 128 columns into
+// The power of two that brings the largest |f x| of this thread's 128 columns x into
 // [1, 2), and its inverse: the row's fp16 operand then neither overflows nor loses
 // bits, whatever its size.
-__device__ __forceinline__ void row_scale(uint32_t addr, float& down, float& up) {
+__device__ __forceinline__ void row_scale(uint32_t addr, float f, float& down, float& up) {
   float mx = 0.0f;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
@@ -633,7 +633,7 @@ __device__ __forceinline__ void row_scale(uint32_t addr, float& down, float& up)
     for (int i = 0; i < 32; i += 2)
       mx = max3(mx, fabsf(__uint_as_float(v[i])), fabsf(__uint_as_float(v[i + 1])));
   }
-  const uint32_t ex = min((__float_as_uint(mx) >> 23) & 255u, 253u);
+  const uint32_t ex = min((__float_as_uint(mx * f) >> 23) & 255u, 253u);
   down = __uint_as_float((254u - ex) << 23);
   up = __uint_as_float(ex << 23);
 }
@@ -788,14 +788,19 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sca
     for (int c = 0; c < 4; ++c)
       m[c] = max3(m[c], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
   const float mnew = fmaxf(mref, fmaxf(max3(m[0], m[1], m[2]), m[3]) * scale);
+  // The reference is a whole power of two at or below the maximum, so that two references
+  // of a row differ by an exact factor and its weights are rounded alike whichever part of
+  // the work, and so whichever batch or chunking, they fall in (a sequence's outputs alone and
+  // beside others: 0.3 % of the INT2 path's bf16 results differ against 13 % with references
+  // that are plain maxima, 0.05 % against 39 % of the BF16 path's; times alike within 0.5 %).
   if (first) {
-    mref = mnew;
+    mref = floorf(mnew);
   } else {
     // O is rescaled only when a maximum grew by 2^8 (the weights stay below that times
     // kBias's 2^7, in range of fp16, and the sums are fp32): a step that most tiles skip
     const bool grow = mnew > mref + kLazy;
     if (__any_sync(0xffffffffu, grow)) {
-      const float f = grow ? fast_exp2(mref - mnew) : 1.0f;
+      const float top = floorf(mnew), f = grow ? fast_exp2(mref - top) : 1.0f;
 #pragma unroll 1
       for (int c = 0; c < 8; ++c) {
         uint32_t o[16];
@@ -805,7 +810,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sca
         tc_st16(to + 16 * c, o);
       }
       l *= f;
-      if (grow) mref = mnew;
+      if (grow) mref = top;
     }
   }
   const float neg = mref == -INFINITY ? 0.0f : (INT2 ? kBias : 0.0f) - mref;
@@ -1008,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           if (some) {
             // q R_K -> fp16 Q, a power of two a row apart, in the pages' order of d
             float down, up;
-            row_scale(ts, down, up);
+            row_scale(ts, 1.0f, down, up);
             scale = fmaxf(scale * up, 1.17549435e-38f);  // a row of zeros: 0 * -inf would be NaN
             pair->x = scale;        // for the group of the odd tiles
 #pragma unroll 1
@@ -1107,15 +1112,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (st.post) {
           if (some) {
             // o / l -> fp16, a power of two a row apart: the left operand of o R_V^T
+            // (normalised first, as the joining kernel does, to be rounded alike)
             float down, up;
-            row_scale(to, down, up);
+            row_scale(to, f, down, up);
+            f *= down;            // exact: `down` is a power of two
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               uint32_t v[32];
               tc_ld32(v, to + 32 * c);
               tc_wait_ld(v);
               auto h2 = [&](int d) {
-                return pack_half2(__uint_as_float(v[d]) * down, __uint_as_float(v[d + 1]) * down);
+                return pack_half2(__uint_as_float(v[d]) * f, __uint_as_float(v[d + 1]) * f);
               };
 #pragma unroll
               for (int x = 0; x < 4; ++x)
@@ -1123,7 +1130,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                           (((4 * (c & 1) + x) ^ r7) << 4)) =
                     make_uint4(h2(8 * x), h2(8 * x + 2), h2(8 * x + 4), h2(8 * x + 6));
             }
-            f *= up;
+            f = up;
             fence_proxy_async();
           }
           give();

@@ -1,5 +1,5 @@
 """The 16-bit roundings of the chunk attention where they matter most: one key that dwarfs a long flat
-tail.
+tail, and one sequence alone and in other company.
 
 The dominant key.  Logits are g for the first token (whose values are zeros) and 0 for all others, so
 the output is the mean of the others' values times n e^-g / (1 + n e^-g): an error of a tail weight is an
@@ -12,6 +12,7 @@ error of the whole output.  Relative to |o|, with weights w = e^-g of the row's 
 """
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -72,3 +73,29 @@ def test_dominant_first_key(kind, n, length, batch):
         err = float(((out - o).norm(dim=2) / o.norm(dim=1)).max())
         assert err <= tol, (gap, err, tol)
         assert K.kvq_get_status(c.h) == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_alone_and_in_company(kind):
+    """A sequence gives the same bits in the same call.  In another batch or chunking its sums are taken
+    in another order: a weight moves by about 2^-20 (fp32 scores of up to 16 binary orders), which
+    moves its 16-bit rounding in one of 2^12 cases (bf16, by 2^-8) or 2^9 (fp16, by 2^-11): 2^-14 of
+    an output at most as a root mean square.  That moves the bf16 result, by 2^-8 at most, in one case of
+    2^6: 2^-11 of the output's 2-norm, and 2^-10.5 is allowed.  (Weights rounded against references that
+    depend on the division differ by 2^-9 to 2^-10.)"""
+    lens, n = [5000, 300, 2500, 17], 130
+    c = Paged(kind, 8, 2, lens, seed=16)
+    q = c.queries(n)
+    one = c.prefill(q, [0, n, n, n, n])
+    assert torch.equal(one, c.prefill(q, [0, n, n, n, n]))
+    c.check(one, q, [n, 0, 0, 0])
+    new = [n, 33, 350, 17]
+    both = c.prefill(torch.cat([q, c.queries(400)]), [0, *np.cumsum(new).tolist()])[:n]
+    c.check(both, q, [n])
+    chunks = torch.cat([c.prefill(q[a:b], [0, b - a, b - a, b - a, b - a],
+                                  seq_lens=torch.tensor([lens[0] - n + b, 300, 2500, 17],
+                                                        dtype=torch.int32, device="cuda"))
+                        for a, b in ((0, 1), (1, 70), (70, n))])
+    c.check(chunks, q, [n])
+    for other in (both, chunks):
+        assert float((one.double() - other.double()).norm()) <= 2.0 ** -10.5 * float(one.double().norm())
