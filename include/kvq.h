@@ -43,6 +43,8 @@
  *     griddepcontrol.wait (cudaGridDependencySynchronize) before reading `out`;
  *     ordinary launches, copies and host synchronisation need nothing.
  *   - bf16 tensors are passed as uint16_t bit patterns.
+ *   - max_pages, the pages a row of a page table has, is below 2^27 (positions are
+ *     int32), and at most 2^26 for the prefill calls: KVQ_EINVAL otherwise.
  *   - Return codes: KVQ_OK, or a KVQ_E* code below.  Argument errors are found on
  *     the host before anything is launched.  Data errors that only the device can
  *     see (a page id outside the pool, a position beyond the page table, a

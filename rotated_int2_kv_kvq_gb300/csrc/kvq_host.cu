@@ -179,11 +179,16 @@ void prof_end(kvq_handle* h, cudaStream_t st, int slot) {
   h->launches += 1;
 }
 
+// The kernels compare positions with max_pages * 16 in 32 bits; positions are int32,
+// so no longer table has a use.
+constexpr int kMaxTablePages = (1 << 27) - 1;
+
 int check_decode_args(kvq_handle* h, const void* pool, int num_pool_pages, const uint16_t* q,
                       const int32_t* page_table, int max_pages, const int32_t* seq_lens,
                       int batch, float* out, void* workspace, int num_splits) {
   if (!h || !pool || !q || !page_table || !seq_lens || !out || !workspace) return KVQ_EINVAL;
   if (num_pool_pages < 1 || max_pages < 1 || batch < 1 || batch > 65535) return KVQ_EINVAL;
+  if (max_pages > kMaxTablePages) return KVQ_EINVAL;
   if (num_splits < 0 || num_splits > kvq::kMaxSplits) return KVQ_EINVAL;
   if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return KVQ_EINVAL;
   if (reinterpret_cast<uintptr_t>(pool) % 16 != 0) return KVQ_EINVAL;
@@ -369,7 +374,8 @@ int append_common(kvq_handle* h, bool int2, void* pool, int num_pool_pages, cons
   }
   if (n == 0) return KVQ_OK;
   if (!pool || !K || !V || !seq_idx || !positions || !page_table) return KVQ_EINVAL;
-  if (num_pool_pages < 1 || batch < 1 || max_pages < 1) return KVQ_EINVAL;
+  if (num_pool_pages < 1 || batch < 1 || max_pages < 1 || max_pages > kMaxTablePages)
+    return KVQ_EINVAL;
   if (reinterpret_cast<uintptr_t>(K) % 16 || reinterpret_cast<uintptr_t>(V) % 16 ||
       reinterpret_cast<uintptr_t>(pool) % 16)
     return KVQ_EINVAL;
@@ -778,7 +784,7 @@ int kvq_dequant(kvq_handle* h, const void* pool, int num_pool_pages, const int32
                 int max_pages, int seq, int start, int len, float* K_out, float* V_out,
                 void* stream) {
   if (!h || !pool || !page_table || len < 0 || seq < 0 || start < 0) return KVQ_EINVAL;
-  if (num_pool_pages < 1 || max_pages < 1) return KVQ_EINVAL;
+  if (num_pool_pages < 1 || max_pages < 1 || max_pages > kMaxTablePages) return KVQ_EINVAL;
   if (len == 0 || (!K_out && !V_out)) return KVQ_OK;
   kvq::DeviceGuard dev_guard(h->device);
   if (!dev_guard.ok()) return KVQ_ECUDA;
