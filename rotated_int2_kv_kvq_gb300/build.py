@@ -6,6 +6,7 @@ and rebuilt on every machine (the library is architecture specific)."""
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 from concurrent.futures import ThreadPoolExecutor
@@ -21,6 +22,11 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", INCLUDE, "-I", CSRC]
 
+# Kernels whose launch needs an exact register count: source -> (kernel, registers a thread,
+# instantiations).  prefill_kernel's roles share out what the block was launched with, so with
+# any other count the call would be refused at run time.
+REGISTERS = {"kvq_prefill.cu": ("prefill_kernel", 128, 2)}
+
 
 def nvcc() -> str:
     cand = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
@@ -33,6 +39,19 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
+def check_registers(source: str, ptxas_log: str) -> None:
+    """Raise if the compiler gave a kernel of REGISTERS another register count than it needs."""
+    name, want, count = REGISTERS[os.path.basename(source)]
+    got = []
+    for entry in ptxas_log.split("Compiling entry function")[1:]:
+        used = re.search(r"Used (\d+) registers", entry)
+        if used and re.search(r"\d" + name + r"(?![a-z_])", entry.split("'")[1]):
+            got.append(int(used.group(1)))
+    if got != [want] * count:
+        raise RuntimeError(f"{source}: {name} needs {want} registers a thread in each of {count} "
+                           f"instantiations, the compiler used {got}")
+
+
 def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -41,13 +60,16 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
         cmd = [cc, *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj]
-        if ptxas_verbose:
+        exact = os.path.basename(src) in REGISTERS
+        if ptxas_verbose or exact:
             cmd.insert(1, "-Xptxas=-v")
         if verbose:
             print(" ".join(cmd))
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+        if exact:
+            check_registers(src, r.stderr)
         return obj, r.stderr
 
     with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:

@@ -1617,7 +1617,8 @@ cudaError_t launch(const PrefillArgs& a, int num_sms, cudaStream_t st) {
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, prefill_kernel<INT2>);
     if (e != cudaSuccess) return e;
-    if (fa.numRegs != kRegLaunch) return cudaErrorInvalidConfiguration;   // see kRegLaunch
+    // see kRegLaunch; the build checks it too (build.py, REGISTERS)
+    if (fa.numRegs != kRegLaunch) return cudaErrorInvalidConfiguration;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   prefill_kernel<INT2><<<num_sms, kThreads, Smem::kAlloc, st>>>(a);
