@@ -613,6 +613,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// The two bf16 values of a word.
+__device__ __forceinline__ uint64_t bf16_pair(uint32_t x) {
+  return pair2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -749,7 +753,12 @@ __device__ __forceinline__ uint32_t visible(int limit, int k) {
 }
 
 // One tile's scores (this thread's row, all 128 in registers) into weights: the
-// running maximum, the weights as 16-bit pairs into TMEM, their sum.
+// running maximum, the weights as 16-bit pairs into TMEM, their sum.  BF16: the sum is that of
+// the rounded weights, so that a weight's rounding (2^-8) moves the output by what sets its
+// value apart from the rest only, and a row that sees one token returns it exactly (error
+// against 64 bits on two 4093-token prompts 0.0022 against 0.0023; 279 us against 282).
+// INT2: the fp16 rounding is an eighth of that and the sum of the unrounded ones (the two
+// conversions would cost 5 to 11 % there) as good, 0.0018 either way.
 template <bool INT2>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float scale, bool first,
                                              int limit, bool edge, uint32_t any, const volatile uint32_t* bad,
@@ -825,9 +834,10 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sca
       float x0, x1;
       split2(fma2(pair2(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, ng2), x0, x1);
       const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-      if (i & 1) s1 = add2(s1, pair2(p0, p1));
-      else s0 = add2(s0, pair2(p0, p1));
       pk[i] = INT2 ? pack_half2(p0, p1) : pack_bf162(p0, p1);
+      const uint64_t w = INT2 ? pair2(p0, p1) : bf16_pair(pk[i]);
+      if (i & 1) s1 = add2(s1, w);
+      else s0 = add2(s0, w);
     }
     tc_st32(ts + 32 * h, pk);     // all of S is in registers: P may overwrite it
   }

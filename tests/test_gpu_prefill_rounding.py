@@ -99,3 +99,15 @@ def test_alone_and_in_company(kind):
     c.check(chunks, q, [n])
     for other in (both, chunks):
         assert float((one.double() - other.double()).norm()) <= 2.0 ** -10.5 * float(one.double().norm())
+
+
+@pytest.mark.parametrize("H,Hkv", [(4, 1), (3, 3), (16, 8)])
+def test_one_visible_token_is_returned(H, Hkv):
+    """BF16: rows that see one token give its values bit for bit, whatever the score: first rows of
+    prompts, and single tokens."""
+    new = [1] * 40 + [300, 5, 130]
+    c = Paged("bf16", H, Hkv, new, seed=18)
+    q = c.queries(sum(new), scale=2.0)
+    out = c.prefill(q, [0, *np.cumsum(new).tolist()])
+    first = torch.tensor([0, *np.cumsum(new)[:-1].tolist()], device="cuda")
+    assert torch.equal(out[first], c.v[first].repeat_interleave(H // Hkv, 1))
