@@ -81,8 +81,9 @@ __device__ __forceinline__ float bf16_to_f32(uint32_t bits16) {
 // ROPE: keys are first rotated by their position (rope_pair, rounded to bf16 as
 // the rotated key that kvq_rope writes), in the staged tile between its load and
 // the centring: 64 pairs per token beside the 16,384 products of the rotation
-// into the cache's basis, so it is not worth a pass of its own over HBM: 9 of the
-// 69 us that 4,099 x 8 heads take, 1.2 of a 16-token step's 8.5.  K and V rows may be strided (slices of a fused projection).
+// into the cache's basis, so it is not worth a pass of its own over HBM: 11 of the
+// 67 us that 4,099 x 8 heads take on the GPU, 1.0 of a 16-token step's 6.3.  K and V rows
+// may be strided (slices of a fused projection).
 // Two CTAs an SM are what shared memory allows; saying so is worth 0.1 us of a step and 1.2 us
 // of 200 rotary tokens x 8 heads, and costs eight-token warps 2 %, so those go without it.
 template <int TPW, int NW, bool ROPE>
@@ -130,9 +131,9 @@ __global__ void __launch_bounds__(NW * 32, TPW == 8 ? 0 : 2) append_int2_kernel(
 
   // Tiles are dealt in turn while every CTA gets one; what is left is shared out in
   // steps of what a warp takes, so that the last round is as short for all (idle warps
-  // leave the ALUs to the SM's other CTA).  Rotary keys, 8 heads: 1,300 tokens 31 us
-  // against 37 with whole tiles only, 4,099 tokens 69 against 75, 32,767 tokens 493 against
-  // 490; equal contiguous shares from the start 31, 68, 502.
+  // leave the ALUs to the SM's other CTA).  Plain tokens, 8 heads: 1,300 tokens 23.5 us
+  // against 32.3 with whole tiles only, 4,099 tokens 55.7 against 61.8, 32,767 tokens 406
+  // against 405.
   // The division into rounds and shares comes from the host (launch_tpw): here it would
   // stand before the first load (a step of 16 plain tokens 5.8 us against 5.1).
   constexpr int kShare = TPW == 1 ? kTile : TPW;
@@ -512,9 +513,9 @@ cudaError_t launch_append_int2(const AppendArgs& a, int num_sms, cudaStream_t st
 }
 
 cudaError_t launch_append_int2_rope(const AppendArgs& a, int num_sms, cudaStream_t st) {
-  // Between the two, four tokens per warp: 200 and 300 tokens x 8 heads 11.4 and 12.6 us
-  // against 14.6 with eight and 16.7 and 18.7 with one; at 152 one is as fast (12.3), from
-  // 500 on eight are.
+  // Between the two, four tokens per warp.  One / four / eight of them, 8 heads, us on the
+  // GPU: 152 tokens 9.0 / 7.6 / 9.9, 200 15.6 / 8.2 / 12.5, 300 15.6 / 8.9 / 12.6,
+  // 500 28.3 / 12.5 / 13.4, 620 34.6 / 17.8 / 17.3.
   const int per_head = num_sms / (a.Hkv > 0 ? a.Hkv : 1);
   if (a.n <= 8 * per_head) return launch_tpw<1, 8, true>(a, num_sms, st);
   if (a.n <= 16 * per_head) return launch_tpw<4, 8, true>(a, num_sms, st);

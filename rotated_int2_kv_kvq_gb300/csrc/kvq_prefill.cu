@@ -31,12 +31,15 @@
 // the GPU without a choice of split counts.  An item that a range border cuts
 // leaves partial (max, sum, O) states, joined by the combine kernel.
 //
-// Measured (32 query, 8 KV heads): 4096 new tokens at 32K, INT2: 1435 us, 1440 TFLOP/s,
-// 77 % of the bf16 rate of a large library product on the same GPU (1865); the products
-// alone, with the softmax and the unpacking left out, take 1091 us at the power limit.
+// Measured (32 query, 8 KV heads): 4096 new tokens at 32K, INT2: 1490 us in long runs, at the
+// power limit (1390 TFLOP/s, 75 % of the bf16 rate of a large library product on the same
+// GPU, 1865), 1442 us in short ones; the products alone, with the softmax and the unpacking
+// left out, take 1091 us at the power limit.
 // What is left is the chain S -> softmax -> P -> O of a row tile, of which two fit TMEM:
 // tensor pipe 59 % and issue slots 58 % busy, the exponentials' unit 29 %.  Two prompts
-// of 4093, BF16: 290 us.  Sixteen decode tokens beside a 1021-token chunk: 177 us.
+// of 4093, BF16: 288 us.  Sixteen decode tokens beside a 1021-token chunk: 178 us, of which
+// the uneven line is a part: a key tile counts one unit, though one of a one-row-tile item
+// takes half as long as one of two row tiles, so the CTAs on the chunk end last.
 // Eight drafts of five tokens at up to 8K: 51 us, of which the launches, the line's
 // setup, the rotations and the join take about half.
 // Tried and slower: half tiles of 64 columns (2045 us: such a product runs at half rate),

@@ -18,10 +18,12 @@ namespace {
 // Table.  Entry (p, i) is amplitude * cos / sin of p * f_i.  The angle is kept
 // as a 64-bit fixed-point fraction of a turn, p * F_i mod 2^64 with
 // F_i = f_i / (2 pi) * 2^64 (made on the host in fp64): the integer product
-// wraps exactly, so the reduction by full turns costs no fp64 and the error is
-// that of F_i, p * 2^-53 of a turn at most.  The top two bits (rounded) are the
-// quadrant; of the rest, y = at most pi / 4, the Taylor series up to y^9 (sine) and
-// y^10 (cosine) leave less than 2e-9.
+// wraps exactly, so the reduction by full turns costs no fp64.  The angle is off by
+// F_i's error, some p f_i 2^-53, and by 2^-32 of a turn (1.5e-9 rad) for the product's
+// low half, which is dropped.  The top two bits (rounded) are the quadrant; the rest,
+// y = at most pi / 4, is rounded to fp32 (pi / 4 * 2^-24); the Taylor series up to y^9
+// (sine) and y^10 (cosine) leave less than 2e-9 and their fp32 steps 2^-23.  Below 3e-7
+// together up to 2^20 positions (tested).
 // Writes are the bound: 4 * table_len * rot_dim bytes; 131072 x 128 takes 16.5 us
 // (4.1 TB/s), 8192 x 128 6 us, most of it the launch.
 // ---------------------------------------------------------------------------
@@ -61,7 +63,8 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_
 // Rotation of rows x[n][heads][128] -> y.  One CTA per token, so the token's cos / sin
 // row is read from DRAM once and from L1 by its other heads; a thread owns units of
 // its heads, one or two at a time (eight CTAs per SM are worth more than more loads a
-// thread: 8191 x 32 heads took 27.5 us with 8 CTAs of 32 registers, 39.2 with 4 of 54):
+// thread: 8191 x 32 heads took 27.5 us with 8 CTAs of 32 registers, for which the two
+// vector forms spill 16 bytes, 39.2 with 4 of 54):
 //   kHalfVec  : 8 elements of the first half and their 8 partners (2 x 16 B);
 //   kInterVec : 8 adjacent elements, four pairs (16 B);
 //   kScalar   : one pair (any even rot_dim),
@@ -199,7 +202,7 @@ __global__ void __launch_bounds__(256, 8) rope_kernel(RopeRowArgs a) {
 // Append of rotated keys and plain values into the BF16 cache.
 //
 // A BF16 record (include/kvq.h) interleaves its 16 tokens element by element, so
-// a token alone is written in 4-byte (keys) and 2-byte (values) pieces, while a
+// a token alone is written in 2-byte pieces (a key's pairs would allow 4), while a
 // whole page is 512 16-byte pieces.  A CTA takes about kSpan consecutive tokens
 // of one KV head, stages them in shared memory (rotating the keys there), and
 // writes every page that its tokens fill completely with 16-byte stores; the
@@ -210,7 +213,8 @@ __global__ void __launch_bounds__(256, 8) rope_kernel(RopeRowArgs a) {
 // positions are; only the speed depends on them).
 // HBM bound: 2 * 256 bytes read and 512 written per (token, KV head); 32767 x 8 heads
 // in 86 us (49 % of the copy rate: a CTA's loads, transpose and stores follow one
-// another, five CTAs an SM; spans of 48 and 32 tokens 95 and 103), a 64-token step 6.3.
+// another, five CTAs an SM; spans of 48 and 32 tokens 95 and 103), a 64-token step 6.2
+// on the GPU (the call's host side takes 7.7).
 // ---------------------------------------------------------------------------
 constexpr int kSpan = 64;      // the widest span; 16 and 4 for fewer tokens (launch below)
 constexpr int kMaxTok = kSpan + kPage - 1;
