@@ -155,6 +155,22 @@ typedef struct kvq_handle kvq_handle;
  * ========================================================================== */
 #define KVQ_BF16_RECORD_BYTES 8192
 
+/* ==========================================================================
+ * 8-bit page record: pool[num_pool_pages][num_kv_heads][KVQ_FP8_RECORD_BYTES].
+ * One record holds 16 tokens of one KV head: 8-bit floating-point codes (sign, four
+ * exponent bits, three of mantissa; value m / 8 * 2^-6 for exponent 0, else
+ * (1 + m / 8) * 2^(exponent - 7); 0x7f and 0xff NaN, so the largest is 448) and a
+ * power of two for K and one for V: an entry is code * s.  For (tau, d), with
+ * w = d >> 4, r = d & 15:
+ *   K code at byte 512*(w >> 1) + 16*L + 4*reg + 2*(w & 1) + e with
+ *     t = (r >> 1) & 3, e = r & 1, L = 4*(tau & 7) + t, reg = (tau >> 3) + 2*(r >> 3);
+ *   V code at byte 2048 + 512*(w >> 1) + 16*L + 4*(2*(w & 1) + (r >> 3)) + 2*(tau >> 3) + e
+ *     with t = (tau & 7) >> 1, e = tau & 1, L = 4*(r & 7) + t.
+ * Byte 4096: s of K, 4100: s of V (fp32, powers of two from 2^-100 to 2^120); 4104: uint32,
+ * bit 0 set if a K code may be NaN, bit 1 if a V code may; 4108: unused, 0.
+ * ========================================================================== */
+#define KVQ_FP8_RECORD_BYTES 4112
+
 /* ---- lifetime ------------------------------------------------------------ */
 
 /* Validate `layout` on the host and create a handle.  On success *out owns a
@@ -172,6 +188,9 @@ size_t kvq_page_bytes(const kvq_handle* h);
 
 /* Bytes of one BF16 comparison page of all KV heads: num_kv_heads * 8192. */
 size_t kvq_bf16_page_bytes(const kvq_handle* h);
+
+/* Bytes of one page of the 8-bit cache: num_kv_heads * 4112. */
+size_t kvq_fp8_page_bytes(const kvq_handle* h);
 
 /* ---- rotation bank -------------------------------------------------------
  * Per-head orthogonal rotations and the key mean, the outputs of offline
@@ -287,6 +306,48 @@ int kvq_rope_table(float* table, int table_len, int rot_dim, const kvq_rope_scal
 int kvq_rope(kvq_handle* h, const uint16_t* x, long long x_stride, uint16_t* y, long long y_stride,
              int heads, const int32_t* positions, int n, const kvq_rope_spec* rope, int inverse,
              void* stream);
+
+/* ---- norms of query and key heads, with the rotation in the same pass -------------
+ * Each head's 128 elements are normalised by their root mean square, weighted, and
+ * rotated by the token's position (T, as kvq_rope does):
+ *     r = 1 / sqrt(mean_d x_d^2 + eps),   y = T (x_d r w_d)
+ * in fp32, with one rounding to bf16 (so not the bits of a norm rounded to bf16 and then
+ * kvq_rope).  The heads are the handle's: num_heads queries, num_kv_heads keys a token.
+ *   q, k         : device bf16, token i at q + i * q_stride (elements), heads adjacent;
+ *                  16-byte aligned, strides multiples of 8 and >= heads * 128, so that both
+ *                  may be slices of a fused projection.  Either may be NULL (then its other
+ *                  arguments are ignored), not both.
+ *   q_out, k_out : device bf16, likewise; may be q and k (with the same strides), otherwise
+ *                  nothing may overlap.
+ *   q_weight, k_weight : device fp32 [128], NULL: ones.
+ *   eps          : >= 0, finite.
+ *   positions    : device int32 [n]; a position outside the table sets KVQ_STATUS_BAD_POS
+ *                  and leaves the token's rows of the results as they were.
+ * n == 0 is a no-op.  A row of zeros with eps = 0 gives NaN. */
+int kvq_norm_rope(kvq_handle* h, const uint16_t* q, long long q_stride, const uint16_t* k,
+                  long long k_stride, uint16_t* q_out, long long q_out_stride, uint16_t* k_out,
+                  long long k_out_stride, const float* q_weight, const float* k_weight, float eps,
+                  const int32_t* positions, int n, const kvq_rope_spec* rope, void* stream);
+
+/* Its backward pass: from dy (dq_out, dk_out: the gradients of q_out and k_out) those of q, k
+ * and the weights.  With dn = T^t dy, xh = x r, g = dn w:
+ *     dx = r (g - xh mean_d(g_d xh_d)),   dw_d = sum over tokens and heads of dn_d xh_d.
+ *   dq_out, dk_out, dq, dk : device bf16, as q_out and k_out above; dq may be dq_out (with the
+ *                same stride), dk may be dk_out.
+ *   dq_weight, dk_weight : device fp32 [128], written (not added to); NULL: not wanted.
+ *   workspace  : device, >= kvq_norm_rope_backward_workspace_bytes(h, n) bytes, 256-byte
+ *                aligned; contents on entry do not matter.  Calls (and captured graphs) that can
+ *                run at the same time need one each.
+ * A token whose position is outside the table adds nothing to dw.  n == 0 sets dw to 0.  The same
+ * call on the same GPU gives the same bits.  Returns KVQ_ENOSPACE if ws_bytes is too small. */
+size_t kvq_norm_rope_backward_workspace_bytes(const kvq_handle* h, int n);
+int kvq_norm_rope_backward(kvq_handle* h, const uint16_t* q, long long q_stride, const uint16_t* k,
+                           long long k_stride, const uint16_t* dq_out, long long dq_out_stride,
+                           const uint16_t* dk_out, long long dk_out_stride, uint16_t* dq,
+                           long long dq_stride, uint16_t* dk, long long dk_stride,
+                           const float* q_weight, const float* k_weight, float* dq_weight,
+                           float* dk_weight, float eps, const int32_t* positions, int n,
+                           const kvq_rope_spec* rope, void* workspace, size_t ws_bytes, void* stream);
 
 /* ---- append with rotary positions ----------------------------------------------
  * kvq_append / kvq_bf16_append of keys that still lack their position: equal, byte
@@ -468,6 +529,68 @@ int kvq_bf16_prefill(kvq_handle* h, const void* pool, int num_pool_pages, const 
                      long long q_stride, const int32_t* cu_q, int n, const int32_t* page_table,
                      int max_pages, const int32_t* seq_lens, int batch, uint16_t* out,
                      void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- the 8-bit cache -----------------------------------------------------------
+ * Plain (unrotated, uncentred) keys and values in 8 bits with one scale for each page
+ * of a KV head: half the BF16 cache's bytes, 3.6 times the INT2 cache's.  No rotation
+ * bank is needed and the layout's clip ratios, group and flags are ignored.
+ *
+ * Tokens are given as kvq_prefill takes its queries: sequence b's rows are cu[b] ..
+ * cu[b + 1] - 1, the last of its seq_lens[b] positions.  cu: device int32 [batch + 1],
+ * non-decreasing, within [0, n]; seq_lens: device int32 [batch]; page_table: device int32
+ * [batch][max_pages]; max_pages <= 2^26, batch <= 65535.  A sequence whose rows are no range
+ * in [0, n] is skipped (KVQ_STATUS_BAD_SEQ), as is one with seq_lens[b] < its rows or beyond
+ * the page table (KVQ_STATUS_BAD_SEQLEN) or a page out of range (KVQ_STATUS_BAD_PAGE).
+ *
+ * kvq_fp8_append quantises rows of K and V into the cache.  For K and V of each touched page
+ * and KV head:
+ *     e = max(e of the page, least e >= -100 with |x| <= 448 * 2^e for the new tokens),
+ *     code = x * 2^-e rounded to nearest (ties to even), s = 2^e;
+ * where e grew, the older tokens' codes are rounded again from what they stood for (exact but
+ * for those below 2^-14 of the page's largest).  Elements that are not finite become NaN and do
+ * not count for e.  A call that writes a page's slot 0 begins the page: what it held counts no
+ * more and the slots the call does not write become 0.  So a page serves a new sequence without
+ * being cleared, and a sequence that was cut back goes on where it was cut (tokens behind the
+ * cut may keep e larger than needed).  Two sequences of one call must not share a page that
+ * both write to.
+ *   K, V : device bf16, row i at K + i * k_stride (elements), KV heads adjacent; 16-byte
+ *          aligned, strides multiples of 8 and >= Hkv * 128.
+ *   pool : device, 16-byte aligned.
+ * n == 0 is a no-op.
+ *
+ * kvq_fp8_read gives entries back: the same rows as K_out and V_out (either may be NULL), exactly
+ * as bf16.  Rows of a skipped sequence with valid rows, or of a bad page, are set to 0; rows that
+ * belong to no sequence are left as they were. */
+int kvq_fp8_append(kvq_handle* h, void* pool, int num_pool_pages, const uint16_t* K,
+                   long long k_stride, const uint16_t* V, long long v_stride, const int32_t* cu,
+                   int n, const int32_t* page_table, int max_pages, const int32_t* seq_lens,
+                   int batch, void* stream);
+int kvq_fp8_read(kvq_handle* h, const void* pool, int num_pool_pages, uint16_t* K_out,
+                 long long k_stride, uint16_t* V_out, long long v_stride, const int32_t* cu, int n,
+                 const int32_t* page_table, int max_pages, const int32_t* seq_lens, int batch,
+                 void* stream);
+
+/* One decode step over the 8-bit cache: for every sequence b with len = seq_lens[b],
+ *     out = softmax(sm_scale * q . k_t) . v_t  over the positions t < len with
+ *     t >= len - window  or  t < sinks          (window = 0: all of them)
+ * that is, a sliding window that holds the token itself and the first `sinks` tokens, which stay
+ * visible.  Pages without a visible position are not read, and need not exist.  Products are of
+ * fp32 accuracy, sums and statistics fp32.  A NaN among the visible keys makes a head's output
+ * NaN, one among the values its element.
+ *   q         : device bf16 [batch][H][D], 4-byte aligned.   out : device fp32 [batch][H][D].
+ *   window, sinks : >= 0 (sinks has no effect without a window).
+ *   workspace : device, >= kvq_fp8_workspace_bytes(h, batch) bytes, 256-byte aligned; contents on
+ *               entry do not matter.  Calls (and captured graphs) that can run at the same time
+ *               need one each.
+ * seq_lens[b] == 0 gives out = 0, as does a length out of range (KVQ_STATUS_BAD_SEQLEN); a page
+ * id out of range is skipped (KVQ_STATUS_BAD_PAGE).  Work is shared out over the GPU by pages,
+ * whatever the lengths; the same call on the same GPU gives the same bits.  1 <= batch <= 65535.
+ * Returns KVQ_ENOSPACE if ws_bytes is too small. */
+size_t kvq_fp8_workspace_bytes(const kvq_handle* h, int batch);
+int kvq_fp8_decode(kvq_handle* h, const void* pool, int num_pool_pages, const uint16_t* q,
+                   const int32_t* page_table, int max_pages, const int32_t* seq_lens, int batch,
+                   int window, int sinks, float* out, void* workspace, size_t ws_bytes,
+                   void* stream);
 
 /* ---- test export -----------------------------------------------------------
  * Dequantise positions [start, start+len) of sequence `seq` to fp32 in the

@@ -1,0 +1,474 @@
+// kvq_fp8_decode.cu — attention of one query token a sequence over the 8-bit paged cache, all
+// of it or a sliding window and the first tokens.
+//
+// Entries are code * 2^e with one e for a page's keys and one for its values (include/kvq.h),
+// and a page is the M = 16 tokens of an mma.sync tile, so no entry is ever scaled: codes become
+// fp16 operands by one conversion a pair, and the two factors go into the page's scores,
+//   logit_t = scale 2^ek (q . code_t),
+// and its weights, w_t = 2^(logit_t + ev - mv).  mv is the running maximum of logit + ev, so w
+// fits fp16 whatever the pages' scales; the softmax's own maximum m and sum l are kept apart,
+// and the result is (sum w code) 2^(mv - m) / l.  Query and weights enter as an fp16 part and a
+// residual in a column of its own (times 2^11): products of fp32 accuracy, as kvq_decode's.
+//
+// All visible pages of all (sequence, KV head) items form one line of work, cut into equal
+// ranges, one a CTA; an item that a border cuts leaves partial states for the joining kernel.
+#include "kvq_internal.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 3;
+constexpr int kCtasPerSm = 2;
+constexpr int kMinUnits = kWarps;       // pages of a CTA's range at least: one a warp
+constexpr int kFlush = 16;              // pages of a warp between flushes of the accumulators
+constexpr int kMaxCtas = 1024;          // of the grid: sizes the joining kernel's arrays
+constexpr float kLazy = 8.0f;           // log2 by which a reference may lag behind its maximum
+
+struct __align__(16) Smem {
+  uint8_t ring[kWarps][kStages][kFp8Rec];
+  uint64_t bar[kWarps][kStages];
+  int ids[kWarps][kStages];
+  float m[kWarps][kMaxG], mv[kWarps][kMaxG], l[kWarps][kMaxG];
+  long long red[kWarps];
+};
+
+// What a sequence's query sees: positions [0, lead) and [first, len), in pages 0 .. sp - 1 and
+// sp + skip onwards, `pages` of them.
+struct Seen {
+  int len, first, lead, sp, skip, pages;
+  bool bad;
+};
+__device__ __forceinline__ Seen seen_of(const Fp8DecodeArgs& a, int b) {
+  Seen s;
+  s.len = a.seq_lens[b];
+  s.bad = s.len < 0 || s.len > a.max_pages * kPage;
+  if (s.bad) s.len = 0;
+  s.first = a.window > 0 ? max(0, s.len - a.window) : 0;
+  s.lead = min(a.sinks, s.first);
+  s.sp = (s.lead + kPage - 1) / kPage;
+  s.skip = max(0, s.first / kPage - s.sp);
+  s.pages = (s.len + kPage - 1) / kPage - s.skip;
+  return s;
+}
+
+// Exclusive prefix of v over the block's threads; *total = the sum.
+__device__ __forceinline__ long long block_prefix(long long v, long long* red, long long* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) red[w] = x;
+  __syncthreads();
+  long long before = 0, sum = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < w) before += red[i];
+    sum += red[i];
+  }
+  __syncthreads();
+  *total = sum;
+  return before + x - v;
+}
+
+struct Start {            // a CTA's range of the line of work
+  long long cur, end, per;
+  long long b_first;      // first unit of sequence b
+  int b;
+};
+
+// An item counts its pages, at least one.
+__device__ __forceinline__ void start_line(const Fp8DecodeArgs& a, Start* line, long long* red) {
+  const int tid = threadIdx.x;
+  const int per_thread = (a.batch + kThreads - 1) / kThreads;
+  const int b_lo = min(tid * per_thread, a.batch), b_hi = min(b_lo + per_thread, a.batch);
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const Seen s = seen_of(a, b);
+    if (s.bad && blockIdx.x == 0) atomicOr(a.status, KVQ_STATUS_BAD_SEQLEN);
+    mine += static_cast<long long>(max(s.pages, 1)) * a.Hkv;
+  }
+  long long total;
+  const long long before = block_prefix(mine, red, &total);
+  const long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinUnits));
+  const long long u0 = min(per * blockIdx.x, total), u1 = min(u0 + per, total);
+  if (tid == 0) {
+    line->cur = u0;
+    line->end = u1;
+    line->per = per;
+  }
+  if (u0 < u1 && before <= u0 && u0 < before + mine) {
+    long long u = before;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const long long su = static_cast<long long>(max(seen_of(a, b).pages, 1)) * a.Hkv;
+      if (u0 < u + su) {
+        line->b = b;
+        line->b_first = u;
+        break;
+      }
+      u += su;
+    }
+  }
+  __syncthreads();
+}
+
+// B fragments of the query: column 2h holds q_h * 2^-x (largest element in [1, 2)) as fp16, column
+// 2h + 1 the residual times 2^11.  Returns 2^x of head lane & 3.
+__device__ __forceinline__ float query_frags(const Fp8DecodeArgs& a, int b, int kv, int lane, uint32_t (&qf)[16]) {
+  const int g = lane >> 2, t = lane & 3, head = g >> 1;
+  const bool use = head < a.G;
+  const uint32_t* row = reinterpret_cast<const uint32_t*>(
+      a.q + (static_cast<size_t>(b) * a.H + kv * a.G + (use ? head : 0)) * kDim);
+  float mx = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    qf[i] = use ? row[4 * i + t] : 0u;       // elements 8i + 2t, + 1
+    mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(qf[i] << 16)), fabsf(__uint_as_float(qf[i] & 0xffff0000u))));
+  }
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  const uint32_t ex = min((__float_as_uint(mx) >> 23) & 255u, 253u);
+  const float down = __uint_as_float((254u - ex) << 23), up = __uint_as_float(ex << 23);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float x = __uint_as_float(qf[i] << 16) * down, y = __uint_as_float(qf[i] & 0xffff0000u) * down;
+    const uint32_t hi = pack_half2(x, y);
+    qf[i] = (g & 1) ? pack_half2((x - half_lo(hi)) * 2048.0f, (y - half_hi(hi)) * 2048.0f) : hi;
+  }
+  return __shfl_sync(0xffffffffu, up, 8 * t);
+}
+
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_fp8_kernel(const __grid_constant__ Fp8DecodeArgs a) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  __shared__ Start line;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&sm.bar[warp][s]), 1);
+    fence_mbar_init();
+  }
+  dependency_wait();
+  start_line(a, &line, sm.red);
+  long long cur = line.cur, b_first = line.b_first;
+  const long long end = line.end, per = line.per;
+  int b = line.b;
+  if (tid == 0) a.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  const size_t page_stride = static_cast<size_t>(a.Hkv) * kFp8Rec;
+  uint32_t used = 0;                 // ring stages so far
+  bool alive = true;
+
+  while (cur < end) {
+    Seen s = seen_of(a, b);
+    while (cur >= b_first + static_cast<long long>(max(s.pages, 1)) * a.Hkv) {     // ends: cur < total
+      b_first += static_cast<long long>(max(s.pages, 1)) * a.Hkv;
+      s = seen_of(a, ++b);
+    }
+    const int units = max(s.pages, 1);
+    const long long item = b_first + (cur - b_first) / units * units;       // its first unit
+    const int kv = static_cast<int>((cur - b_first) / units);
+    const int j0 = static_cast<int>(cur - item);
+    const int j1 = static_cast<int>(min(static_cast<long long>(units), end - item));
+    const int jp = min(j1, s.pages);                                        // pages j0 .. jp - 1
+    const int count = jp - j0 > warp ? (jp - j0 - warp + kWarps - 1) / kWarps : 0;
+    const int32_t* ptab = a.page_table + static_cast<size_t>(b) * a.max_pages;
+    const uint8_t* pool_kv = a.pool + static_cast<size_t>(kv) * kFp8Rec;
+    auto page_of = [&](int i) {      // the warp's i-th page
+      const int j = j0 + warp + kWarps * i;
+      return j < s.sp ? j : j + s.skip;
+    };
+    auto load_ids = [&](int blk) {
+      const int i = 32 * blk + lane;
+      return i < count ? ptab[page_of(i)] : -1;
+    };
+    int blk = 0, ids = load_ids(0), ids_next = load_ids(1);
+    auto issue = [&](int i) {
+      if ((i >> 5) != blk) {
+        blk = i >> 5;
+        ids = ids_next;
+        ids_next = load_ids(blk + 1);
+      }
+      const int id = __shfl_sync(0xffffffffu, ids, i & 31);
+      if (lane == 0) {
+        const int slot = (used + i) % kStages;
+        const uint32_t bar = smem_u32(&sm.bar[warp][slot]);
+        const bool ok = id >= 0 && id < a.num_pool_pages;
+        sm.ids[warp][slot] = ok ? id : -1;
+        if (ok) {
+          mbar_arrive_expect_tx(bar, kFp8Rec);
+          bulk_g2s(smem_u32(sm.ring[warp][slot]), pool_kv + static_cast<size_t>(id) * page_stride, kFp8Rec, bar);
+        } else {
+          atomicOr(a.status, KVQ_STATUS_BAD_PAGE);
+          mbar_arrive(bar);
+        }
+      }
+    };
+    if (lane == 0) fence_proxy_async();      // the last item's state was written over the ring
+    __syncwarp();
+    for (int i = 0; i < kStages && i < count; ++i) issue(i);
+    __syncwarp();
+
+    uint32_t qf[16];
+    const float up = query_frags(a, b, kv, lane, qf);
+    const float kq = a.log2_scale * up;
+
+    float acc[8][4], tot[8][2];
+#pragma unroll
+    for (int mb = 0; mb < 8; ++mb) {
+      tot[mb][0] = tot[mb][1] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[mb][k] = 0.0f;
+    }
+    float m = -INFINITY, mv = -INFINITY, l = 0.0f;      // of head t
+    auto flush = [&]() {
+#pragma unroll
+      for (int mb = 0; mb < 8; ++mb) {
+        tot[mb][0] += fmaf(acc[mb][1], 0x1p-11f, acc[mb][0]);
+        tot[mb][1] += fmaf(acc[mb][3], 0x1p-11f, acc[mb][2]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[mb][k] = 0.0f;
+      }
+    };
+
+    int i = 0;
+    for (; i < count; ++i) {
+      const int slot = (used + i) % kStages;
+      if (!mbar_wait_bounded(smem_u32(&sm.bar[warp][slot]), ((used + i) / kStages) & 1)) {
+        if (lane == 0) atomicOr(a.status, KVQ_STATUS_TIMEOUT);
+        alive = false;
+        break;
+      }
+      const bool page_ok = sm.ids[warp][slot] >= 0;
+      const uint8_t* st = sm.ring[warp][slot];
+      const uint4 meta = *reinterpret_cast<const uint4*>(st + 4096);
+      float sa[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sb[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4 w = *reinterpret_cast<const uint4*>(st + 512 * k + 16 * lane);
+        mma_f16(sa, fp8_lo(w.x), fp8_lo(w.y), fp8_lo(w.z), fp8_lo(w.w), qf[4 * k], qf[4 * k + 1]);
+        mma_f16(sb, fp8_hi(w.x), fp8_hi(w.y), fp8_hi(w.z), fp8_hi(w.w), qf[4 * k + 2], qf[4 * k + 3]);
+      }
+      uint4 vw[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) vw[k] = *reinterpret_cast<const uint4*>(st + 2048 + 512 * k + 16 * lane);
+      __syncwarp();
+      if (i + kStages < count) {
+        if (lane == 0) fence_proxy_async();
+        issue(i + kStages);
+      }
+      if (!page_ok) continue;
+      const int pos = page_of(i) * kPage;
+      auto visible = [&](int tau) {
+        const int p = pos + tau;
+        return p < s.len && (p >= s.first || p < s.lead);
+      };
+      const float sk = __uint_as_float(meta.x);
+      const float ev = static_cast<float>(static_cast<int>(meta.y >> 23) - 127);
+      const float l0 = visible(g) ? fmaf(sa[1] + sb[1], 0x1p-11f, sa[0] + sb[0]) * sk * kq : -INFINITY;
+      const float l1 = visible(g + 8) ? fmaf(sa[3] + sb[3], 0x1p-11f, sa[2] + sb[2]) * sk * kq : -INFINITY;
+      float pm = fmaxf(l0, l1);
+      pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 4));
+      pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 8));
+      pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 16));
+      if (__any_sync(0xffffffffu, pm > m + kLazy || pm + ev > mv + kLazy)) {
+        const float mn = fmaxf(m, pm), mvn = fmaxf(mv, pm + ev);
+        l *= m == mn ? 1.0f : fast_exp2(m - mn);
+        const float f = mv == mvn ? 1.0f : fast_exp2(mv - mvn);
+#pragma unroll
+        for (int mb = 0; mb < 8; ++mb) {
+          tot[mb][0] *= f;
+          tot[mb][1] *= f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[mb][k] *= f;
+        }
+        m = mn;
+        mv = mvn;
+      }
+      const float mr = m == -INFINITY ? 0.0f : m, wr = (mv == -INFINITY ? 0.0f : mv) - ev;
+      l += fast_exp2(l0 - mr) + fast_exp2(l1 - mr);
+      const float w0 = fast_exp2(l0 - wr), w1 = fast_exp2(l1 - wr);
+      const uint32_t hi = pack_half2(w0, w1);
+      const uint32_t lo = pack_half2((w0 - half_lo(hi)) * 2048.0f, (w1 - half_hi(hi)) * 2048.0f);
+      const uint32_t p0 = movmatrix_trans(__byte_perm(hi, lo, 0x5410));
+      const uint32_t p1 = movmatrix_trans(__byte_perm(hi, lo, 0x7632));
+      if (meta.z & 2u) {       // NaN codes among the values: hidden tokens' must not reach the sum
+        const uint32_t keep = (visible(2 * t) ? 0xffu : 0u) | (visible(2 * t + 1) ? 0xff00u : 0u) |
+                              (visible(2 * t + 8) ? 0xff0000u : 0u) | (visible(2 * t + 9) ? 0xff000000u : 0u);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          vw[k] = make_uint4(vw[k].x & keep, vw[k].y & keep, vw[k].z & keep, vw[k].w & keep);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        mma_f16(acc[2 * k], fp8_lo(vw[k].x), fp8_lo(vw[k].y), fp8_hi(vw[k].x), fp8_hi(vw[k].y), p0, p1);
+        mma_f16(acc[2 * k + 1], fp8_lo(vw[k].z), fp8_lo(vw[k].w), fp8_hi(vw[k].z), fp8_hi(vw[k].w), p0, p1);
+      }
+      if (i % kFlush == kFlush - 1) flush();
+    }
+    if (i < count) {
+      // stage i gave up; it and the stages issued after it may still be in flight
+      for (int j = i; j < count && j < i + kStages; ++j)
+        mbar_drain(smem_u32(&sm.bar[warp][(used + j) % kStages]), ((used + j) / kStages) & 1);
+    }
+    used += count;
+    flush();
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+
+    // the warps' states, each over its own ring (its copies have landed), then joined
+    float* mine = reinterpret_cast<float*>(sm.ring[warp][0]);
+    if (t < a.G) {
+#pragma unroll
+      for (int mb = 0; mb < 8; ++mb) {
+        mine[t * kDim + 16 * mb + g] = tot[mb][0];
+        mine[t * kDim + 16 * mb + 8 + g] = tot[mb][1];
+      }
+      if (g == 0) {
+        sm.m[warp][t] = m;
+        sm.mv[warp][t] = mv;
+        sm.l[warp][t] = l;
+      }
+    }
+    const bool stop = __syncthreads_or(!alive);
+    const bool whole = j0 == 0 && j1 == units;
+    for (int e = tid; e < a.G * kDim; e += kThreads) {
+      const int h = e / kDim, d = e % kDim;
+      float M = -INFINITY, MV = -INFINITY, L = 0.0f, o = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        M = fmaxf(M, sm.m[w][h]);
+        MV = fmaxf(MV, sm.mv[w][h]);
+      }
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        // a warp without a token has l = 0 (one that met a NaN logit has l = NaN and no maximum)
+        const float x = sm.m[w][h], y = sm.mv[w][h], lw = sm.l[w][h];
+        if (lw == 0.0f) continue;
+        L = fmaf(x == M ? 1.0f : fast_exp2(x - M), lw, L);
+        o = fmaf(y == MV ? 1.0f : fast_exp2(y - MV), reinterpret_cast<const float*>(sm.ring[w][0])[e], o);
+      }
+      if (whole) {
+        a.out[(static_cast<size_t>(b) * a.H + kv * a.G + h) * kDim + d] =
+            L == 0.0f ? 0.0f : o * (MV == M ? 1.0f : fast_exp2(MV - M)) / L;
+      } else {
+        float* p = a.part + (static_cast<size_t>(2 * blockIdx.x + (j0 == 0 ? 1 : 0)) * kMaxG + h) * kPartStride;
+        p[4 + d] = o;
+        if (d == 0) {
+          p[0] = M;
+          p[1] = L;
+          p[2] = MV;
+        }
+      }
+    }
+    if (tid == 0 && j0 > 0)     // an item that CTAs before this one began: what joining it takes
+      a.cuts[blockIdx.x] = make_int4(b, kv, static_cast<int>(item / per), static_cast<int>((item + units - 1) / per));
+    __syncthreads();
+    if (stop) break;
+    cur = item + j1;
+  }
+  dependents_begin();
+}
+
+// Joins the partial states of the items that range borders cut.  CTA (x, h): border behind range
+// x, head h; the item's first border does the work.
+__global__ void __launch_bounds__(kDim) join_fp8_kernel(const __grid_constant__ Fp8DecodeArgs a) {
+  __shared__ float f[kMaxCtas], red[3][4];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
+  dependency_wait();
+  const int4 c = a.cuts[blockIdx.x + 1];
+  if (c.x < 0 || c.z != static_cast<int>(blockIdx.x)) return;
+  const int parts = c.w - c.z + 1;
+  // part i: CTA first + i left it, the first one in its second slot
+  auto part = [&](int i) {
+    return a.part + (static_cast<size_t>(2 * (c.z + i) + (i == 0 ? 1 : 0)) * kMaxG + h) * kPartStride;
+  };
+  float M = -INFINITY, MV = -INFINITY, L = 0.0f;
+  for (int i = tid; i < parts; i += kDim) {
+    M = fmaxf(M, part(i)[0]);
+    MV = fmaxf(MV, part(i)[2]);
+  }
+  auto all = [&](float x, int which, bool sum) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float y = __shfl_xor_sync(0xffffffffu, x, o);
+      x = sum ? x + y : fmaxf(x, y);
+    }
+    if (lane == 0) red[which][warp] = x;
+    __syncthreads();
+    return sum ? (red[which][0] + red[which][1]) + (red[which][2] + red[which][3])
+               : fmaxf(fmaxf(red[which][0], red[which][1]), fmaxf(red[which][2], red[which][3]));
+  };
+  M = all(M, 0, false);
+  MV = all(MV, 1, false);
+  for (int i = tid; i < parts; i += kDim) {
+    const float x = part(i)[0], lw = part(i)[1], y = part(i)[2];
+    L += lw == 0.0f ? 0.0f : (x == M ? 1.0f : fast_exp2(x - M)) * lw;
+    f[i] = lw == 0.0f ? 0.0f : y == MV ? 1.0f : fast_exp2(y - MV);
+  }
+  L = all(L, 2, true);        // its barrier is also that of f
+  float o = 0.0f;
+#pragma unroll 8
+  for (int i = 0; i < parts; ++i) o = fmaf(f[i], part(i)[4 + tid], o);
+  a.out[(static_cast<size_t>(c.x) * a.H + c.y * a.G + h) * kDim + tid] =
+      L == 0.0f ? 0.0f : o * (MV == M ? 1.0f : fast_exp2(MV - M)) / L;
+}
+
+int grid_of(int num_sms) {
+  const int n = num_sms * kCtasPerSm;
+  return n < kMaxCtas ? n : kMaxCtas;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+template <typename... Args>
+cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                             Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+}  // namespace
+
+Fp8DecodeWs fp8_decode_ws_layout(int num_sms) {
+  Fp8DecodeWs w;
+  const size_t ctas = grid_of(num_sms);
+  w.cuts_off = 0;
+  w.part_off = up256(ctas * sizeof(int4));
+  w.total = w.part_off + up256(ctas * 2 * kMaxG * kPartStride * sizeof(float));
+  return w;
+}
+
+cudaError_t launch_fp8_decode(const Fp8DecodeArgs& a, int num_sms, cudaStream_t st) {
+  static bool attr_set[64] = {};       // per device: the attributes are per context
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t e;
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(decode_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(sizeof(Smem)));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(decode_fp8_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               static_cast<int>(cudaSharedmemCarveoutMaxShared));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  const int grid = grid_of(num_sms);
+  e = launch_dependent(decode_fp8_kernel, dim3(grid), dim3(kThreads), sizeof(Smem), st, a);
+  if (e == cudaSuccess && grid > 1)
+    e = launch_dependent(join_fp8_kernel, dim3(grid - 1, a.G), dim3(kDim), 0, st, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace kvq

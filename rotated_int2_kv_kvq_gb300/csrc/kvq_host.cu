@@ -457,6 +457,67 @@ int prefill_common(kvq_handle* h, bool int2, const void* pool, int num_pool_page
   return cuda_rc(kvq::launch_prefill(a, int2, h->num_sms, S(stream)));
 }
 
+// The arguments that the calls over the 8-bit cache share.
+bool fp8_cache_ok(const void* pool, int num_pool_pages, const int32_t* page_table, int max_pages,
+                  const int32_t* seq_lens, int batch) {
+  return pool && reinterpret_cast<uintptr_t>(pool) % 16 == 0 && num_pool_pages >= 1 && page_table &&
+         max_pages >= 1 && max_pages <= (1 << 26) && seq_lens && batch >= 1 && batch <= 65535;
+}
+
+int fp8_rows(kvq_handle* h, bool append, const void* pool, int num_pool_pages, const uint16_t* K,
+             long long k_stride, const uint16_t* V, long long v_stride, const int32_t* cu, int n,
+             const int32_t* page_table, int max_pages, const int32_t* seq_lens, int batch, void* stream) {
+  if (!h || n < 0 || batch < 1 || batch > 65535) return KVQ_EINVAL;
+  if (n == 0) return KVQ_OK;
+  if (!cu || !fp8_cache_ok(pool, num_pool_pages, page_table, max_pages, seq_lens, batch)) return KVQ_EINVAL;
+  const int Hkv = h->L.num_kv_heads;
+  const bool k_ok = rows_ok(K, k_stride, Hkv), v_ok = rows_ok(V, v_stride, Hkv);
+  if (append ? !k_ok || !v_ok : (!K && !V) || (K && !k_ok) || (V && !v_ok)) return KVQ_EINVAL;
+  kvq::DeviceGuard dev_guard(h->device);
+  if (!dev_guard.ok()) return KVQ_ECUDA;
+  kvq::Fp8RowArgs a;
+  a.pool = static_cast<uint8_t*>(const_cast<void*>(pool));     // read: not written
+  a.num_pool_pages = num_pool_pages;
+  a.K = const_cast<uint16_t*>(K);                              // append: not written
+  a.V = const_cast<uint16_t*>(V);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.cu = cu;
+  a.n = n;
+  a.page_table = page_table;
+  a.max_pages = max_pages;
+  a.seq_lens = seq_lens;
+  a.batch = batch;
+  a.Hkv = Hkv;
+  a.status = h->status;
+  return cuda_rc(append ? kvq::launch_fp8_append(a, h->num_sms, S(stream))
+                        : kvq::launch_fp8_read(a, h->num_sms, S(stream)));
+}
+
+// The rows of one of kvq_norm_rope's operands (dy: backward only), or false.
+bool norm_rows(kvq::NormRows* r, const uint16_t* x, long long x_stride, bool backward, const uint16_t* dy,
+               long long dy_stride, uint16_t* y, long long y_stride, int heads, const float* weight, float* dw) {
+  if (!x) return true;
+  if (!rows_ok(x, x_stride, heads) || !rows_ok(y, y_stride, heads)) return false;
+  if (backward && !rows_ok(dy, dy_stride, heads)) return false;
+  if (reinterpret_cast<uintptr_t>(weight) % 4 || reinterpret_cast<uintptr_t>(dw) % 4) return false;
+  r->x = x;
+  r->dy = dy;
+  r->y = y;
+  r->x_stride = x_stride;
+  r->dy_stride = dy_stride;
+  r->y_stride = y_stride;
+  r->heads = heads;
+  r->weight = weight;
+  r->dw = dw;
+  return true;
+}
+
+size_t norm_backward_bytes(const kvq_handle* h, int n) {
+  if (!h || n < 0) return 0;
+  return static_cast<size_t>(2) * kvq::norm_backward_parts(n, h->num_sms) * kDim * sizeof(float);
+}
+
 // Each pair's turns per position as a 64-bit fraction, from the base and the
 // scaling (include/kvq.h); false for parameters outside their ranges.
 bool rope_turns(int rot_dim, const kvq_rope_scaling* sc, uint64_t* turns, float* amplitude) {
@@ -577,6 +638,10 @@ size_t kvq_page_bytes(const kvq_handle* h) {
 
 size_t kvq_bf16_page_bytes(const kvq_handle* h) {
   return h ? static_cast<size_t>(h->L.num_kv_heads) * KVQ_BF16_RECORD_BYTES : 0;
+}
+
+size_t kvq_fp8_page_bytes(const kvq_handle* h) {
+  return h ? static_cast<size_t>(h->L.num_kv_heads) * KVQ_FP8_RECORD_BYTES : 0;
 }
 
 int kvq_set_rotation(kvq_handle* h, const float* R, const float* mu, void* stream) {
@@ -778,6 +843,116 @@ int kvq_bf16_prefill(kvq_handle* h, const void* pool, int num_pool_pages, const 
                      void* workspace, size_t ws_bytes, void* stream) {
   return prefill_common(h, false, pool, num_pool_pages, q, q_stride, cu_q, n, page_table,
                         max_pages, seq_lens, batch, out, workspace, ws_bytes, stream);
+}
+
+int kvq_norm_rope(kvq_handle* h, const uint16_t* q, long long q_stride, const uint16_t* k,
+                  long long k_stride, uint16_t* q_out, long long q_out_stride, uint16_t* k_out,
+                  long long k_out_stride, const float* q_weight, const float* k_weight, float eps,
+                  const int32_t* positions, int n, const kvq_rope_spec* rope, void* stream) {
+  if (!h || n < 0 || !(eps >= 0.0f) || isinf(eps)) return KVQ_EINVAL;
+  kvq::NormArgs a;
+  if (!rope_ok(rope, &a.rope)) return KVQ_EINVAL;
+  if (n == 0) return KVQ_OK;
+  if ((!q && !k) || !positions) return KVQ_EINVAL;
+  if (!norm_rows(&a.q, q, q_stride, false, nullptr, 0, q_out, q_out_stride, h->L.num_heads, q_weight, nullptr) ||
+      !norm_rows(&a.k, k, k_stride, false, nullptr, 0, k_out, k_out_stride, h->L.num_kv_heads, k_weight, nullptr))
+    return KVQ_EINVAL;
+  kvq::DeviceGuard dev_guard(h->device);
+  if (!dev_guard.ok()) return KVQ_ECUDA;
+  a.positions = positions;
+  a.n = n;
+  a.eps = eps;
+  a.status = h->status;
+  return cuda_rc(kvq::launch_norm_rope(a, S(stream)));
+}
+
+size_t kvq_norm_rope_backward_workspace_bytes(const kvq_handle* h, int n) { return norm_backward_bytes(h, n); }
+
+int kvq_norm_rope_backward(kvq_handle* h, const uint16_t* q, long long q_stride, const uint16_t* k,
+                           long long k_stride, const uint16_t* dq_out, long long dq_out_stride,
+                           const uint16_t* dk_out, long long dk_out_stride, uint16_t* dq,
+                           long long dq_stride, uint16_t* dk, long long dk_stride,
+                           const float* q_weight, const float* k_weight, float* dq_weight,
+                           float* dk_weight, float eps, const int32_t* positions, int n,
+                           const kvq_rope_spec* rope, void* workspace, size_t ws_bytes, void* stream) {
+  if (!h || n < 0 || !(eps >= 0.0f) || isinf(eps)) return KVQ_EINVAL;
+  kvq::NormArgs a;
+  if (!rope_ok(rope, &a.rope)) return KVQ_EINVAL;
+  if ((n > 0 && !q && !k) || (n > 0 && !positions)) return KVQ_EINVAL;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return KVQ_EINVAL;
+  if (n > 0 &&
+      (!norm_rows(&a.q, q, q_stride, true, dq_out, dq_out_stride, dq, dq_stride, h->L.num_heads, q_weight,
+                  dq_weight) ||
+       !norm_rows(&a.k, k, k_stride, true, dk_out, dk_out_stride, dk, dk_stride, h->L.num_kv_heads, k_weight,
+                  dk_weight)))
+    return KVQ_EINVAL;
+  if (n == 0) {        // no rows: the sums are zero
+    a.q.dw = dq_weight;
+    a.k.dw = dk_weight;
+  }
+  if (ws_bytes < norm_backward_bytes(h, n)) return KVQ_ENOSPACE;
+  kvq::DeviceGuard dev_guard(h->device);
+  if (!dev_guard.ok()) return KVQ_ECUDA;
+  a.positions = positions;
+  a.n = n;
+  a.eps = eps;
+  a.status = h->status;
+  a.part = static_cast<float*>(workspace);
+  return cuda_rc(kvq::launch_norm_rope_backward(a, h->num_sms, S(stream)));
+}
+
+int kvq_fp8_append(kvq_handle* h, void* pool, int num_pool_pages, const uint16_t* K,
+                   long long k_stride, const uint16_t* V, long long v_stride, const int32_t* cu,
+                   int n, const int32_t* page_table, int max_pages, const int32_t* seq_lens,
+                   int batch, void* stream) {
+  return fp8_rows(h, true, pool, num_pool_pages, K, k_stride, V, v_stride, cu, n, page_table, max_pages,
+                  seq_lens, batch, stream);
+}
+
+int kvq_fp8_read(kvq_handle* h, const void* pool, int num_pool_pages, uint16_t* K_out,
+                 long long k_stride, uint16_t* V_out, long long v_stride, const int32_t* cu, int n,
+                 const int32_t* page_table, int max_pages, const int32_t* seq_lens, int batch,
+                 void* stream) {
+  return fp8_rows(h, false, pool, num_pool_pages, K_out, k_stride, V_out, v_stride, cu, n, page_table,
+                  max_pages, seq_lens, batch, stream);
+}
+
+size_t kvq_fp8_workspace_bytes(const kvq_handle* h, int batch) {
+  if (!h || batch < 1 || batch > 65535) return 0;
+  return kvq::fp8_decode_ws_layout(h->num_sms).total;
+}
+
+int kvq_fp8_decode(kvq_handle* h, const void* pool, int num_pool_pages, const uint16_t* q,
+                   const int32_t* page_table, int max_pages, const int32_t* seq_lens, int batch,
+                   int window, int sinks, float* out, void* workspace, size_t ws_bytes,
+                   void* stream) {
+  if (!h || !fp8_cache_ok(pool, num_pool_pages, page_table, max_pages, seq_lens, batch)) return KVQ_EINVAL;
+  if (!q || !out || !workspace || window < 0 || sinks < 0) return KVQ_EINVAL;
+  if (reinterpret_cast<uintptr_t>(q) % 4 || reinterpret_cast<uintptr_t>(workspace) % 256) return KVQ_EINVAL;
+  const kvq::Fp8DecodeWs w = kvq::fp8_decode_ws_layout(h->num_sms);
+  if (ws_bytes < w.total) return KVQ_ENOSPACE;
+  kvq::DeviceGuard dev_guard(h->device);
+  if (!dev_guard.ok()) return KVQ_ECUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  kvq::Fp8DecodeArgs a;
+  a.pool = static_cast<const uint8_t*>(pool);
+  a.num_pool_pages = num_pool_pages;
+  a.q = q;
+  a.page_table = page_table;
+  a.max_pages = max_pages;
+  a.seq_lens = seq_lens;
+  a.batch = batch;
+  a.H = h->L.num_heads;
+  a.Hkv = h->L.num_kv_heads;
+  a.G = h->G;
+  a.window = window;
+  a.sinks = sinks;
+  a.out = out;
+  a.log2_scale = h->sm_scale * 1.4426950408889634f;
+  a.status = h->status;
+  a.cuts = reinterpret_cast<int4*>(ws + w.cuts_off);
+  a.part = reinterpret_cast<float*>(ws + w.part_off);
+  return cuda_rc(kvq::launch_fp8_decode(a, h->num_sms, S(stream)));
 }
 
 int kvq_dequant(kvq_handle* h, const void* pool, int num_pool_pages, const int32_t* page_table,

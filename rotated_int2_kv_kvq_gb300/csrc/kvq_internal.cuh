@@ -16,6 +16,8 @@ constexpr int kDim = 128;          // head_dim
 constexpr int kPage = 16;          // tokens per page
 constexpr int kInt2Rec = KVQ_INT2_RECORD_BYTES;   // bytes per (page, kv head)
 constexpr int kBf16Rec = KVQ_BF16_RECORD_BYTES;
+constexpr int kFp8Rec = KVQ_FP8_RECORD_BYTES;
+constexpr int kFp8MinExp = -100, kFp8MaxExp = 120;   // of a record's scales
 constexpr int kMaxG = 4;           // query heads per KV head handled per CTA
 constexpr int kPartStride = 132;   // floats per split partial: m, l, 2 pad, o[128]
 constexpr int kQFragWords = 32 * 16;   // uint32 per (b, kv): 32 lanes x 16 B-fragment regs
@@ -159,6 +161,70 @@ cudaError_t launch_prefill(const PrefillArgs& a, bool int2, int num_sms, cudaStr
 // identity in R_K's place (the caller's queries are rotated already).
 cudaError_t launch_rotation_bank(const float* R, int Hkv, bool identity_q, float* RVt, uint16_t* hi,
                                  uint16_t* lo, uint16_t* rv, cudaStream_t st);
+
+// One kvq_norm_rope / kvq_norm_rope_backward call: the queries' rows and the keys'.
+struct NormRows {
+  const uint16_t* x = nullptr;   // nullptr: none
+  const uint16_t* dy = nullptr;  // backward: the gradient of the forward's result
+  uint16_t* y = nullptr;         // the result, or the gradient of x
+  long long x_stride = 0, dy_stride = 0, y_stride = 0;   // elements from one token to the next
+  int heads = 0;
+  const float* weight = nullptr; // [128], nullptr: ones
+  float* dw = nullptr;           // backward: [128], nullptr: not wanted
+};
+struct NormArgs {
+  NormRows q, k;
+  const int32_t* positions;
+  int n;
+  RopeArgs rope;
+  float eps;
+  uint32_t* status;
+  float* part = nullptr;         // backward: [2][CTAs][128]
+};
+int norm_backward_parts(int n, int num_sms);
+cudaError_t launch_norm_rope(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_rope_backward(const NormArgs& a, int num_sms, cudaStream_t st);
+
+// One kvq_fp8_append / kvq_fp8_read call: row i of sequence b is position
+// seq_lens[b] - cu[b + 1] + i.
+struct Fp8RowArgs {
+  uint8_t* pool;
+  int num_pool_pages;
+  uint16_t* K;               // append: read; read: written, nullptr: not wanted
+  uint16_t* V;
+  long long k_stride, v_stride;
+  const int32_t* cu;         // [batch + 1]
+  int n;
+  const int32_t* page_table;
+  int max_pages;
+  const int32_t* seq_lens;
+  int batch, Hkv;
+  uint32_t* status;
+};
+cudaError_t launch_fp8_append(const Fp8RowArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_fp8_read(const Fp8RowArgs& a, int num_sms, cudaStream_t st);
+
+// One kvq_fp8_decode call.
+struct Fp8DecodeArgs {
+  const uint8_t* pool;
+  int num_pool_pages;
+  const uint16_t* q;
+  const int32_t* page_table;
+  int max_pages;
+  const int32_t* seq_lens;
+  int batch, H, Hkv, G;
+  int window, sinks;         // window 0: all positions
+  float* out;
+  float log2_scale;
+  uint32_t* status;
+  int4* cuts;                // [CTAs] {sequence, KV head, first, last CTA}; sequence -1: none
+  float* part;               // [2 * CTAs][kMaxG][kPartStride]: m, l, mv, -, o[128]
+};
+struct Fp8DecodeWs {
+  size_t cuts_off, part_off, total;
+};
+Fp8DecodeWs fp8_decode_ws_layout(int num_sms);
+cudaError_t launch_fp8_decode(const Fp8DecodeArgs& a, int num_sms, cudaStream_t st);
 
 // ---- launchers (defined in the .cu files) --------------------------------
 cudaError_t launch_append_int2(const AppendArgs& a, int num_sms, cudaStream_t st);
@@ -382,6 +448,23 @@ __device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
 }
+
+// Programmatic dependent launch: wait for the work before, let the work behind begin.
+__device__ __forceinline__ void dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void dependents_begin() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Two 8-bit codes (e4m3: the low byte is the first) as two fp16 numbers, exactly.
+__device__ __forceinline__ uint32_t fp8_pair(uint16_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
+  return h;
+}
+__device__ __forceinline__ uint32_t fp8_lo(uint32_t w) { return fp8_pair(static_cast<uint16_t>(w)); }
+__device__ __forceinline__ uint32_t fp8_hi(uint32_t w) { return fp8_pair(static_cast<uint16_t>(w >> 16)); }
 
 #endif  // __CUDACC__
 

@@ -28,6 +28,7 @@ KVQ_ROPE_HALF, KVQ_ROPE_INTERLEAVED = 0, 1
  KVQ_ROPE_SCALE_BANDED) = range(5)
 INT2_RECORD_BYTES = 1152
 BF16_RECORD_BYTES = 8192
+FP8_RECORD_BYTES = 4112
 
 # Every entry point of include/kvq.h, with its ctypes signature.
 _P, _I, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
@@ -65,6 +66,15 @@ SIGNATURES = {
     "kvq_prefill": ([_P, _P, _I, _P, _LL, _P, _I, _P, _I, _P, _I, _P, _P, _SZ, _P], _I),
     "kvq_bf16_prefill_workspace_bytes": ([_P, _I, _I], _SZ),
     "kvq_bf16_prefill": ([_P, _P, _I, _P, _LL, _P, _I, _P, _I, _P, _I, _P, _P, _SZ, _P], _I),
+    "kvq_norm_rope": ([_P, _P, _LL, _P, _LL, _P, _LL, _P, _LL, _P, _P, _F, _P, _I, _P, _P], _I),
+    "kvq_norm_rope_backward_workspace_bytes": ([_P, _I], _SZ),
+    "kvq_norm_rope_backward": ([_P, _P, _LL, _P, _LL, _P, _LL, _P, _LL, _P, _LL, _P, _LL, _P, _P, _P,
+                                _P, _F, _P, _I, _P, _P, _SZ, _P], _I),
+    "kvq_fp8_page_bytes": ([_P], _SZ),
+    "kvq_fp8_append": ([_P, _P, _I, _P, _LL, _P, _LL, _P, _I, _P, _I, _P, _I, _P], _I),
+    "kvq_fp8_read": ([_P, _P, _I, _P, _LL, _P, _LL, _P, _I, _P, _I, _P, _I, _P], _I),
+    "kvq_fp8_workspace_bytes": ([_P, _I], _SZ),
+    "kvq_fp8_decode": ([_P, _P, _I, _P, _P, _I, _P, _I, _I, _I, _P, _P, _SZ, _P], _I),
     "kvq_get_status": ([_P, _P, _P], _I),
     "kvq_selftest_wait_timeout": ([_P, _I, _P], _I),
     "kvq_auto_splits": ([_P, _I, _I], _I),
@@ -202,6 +212,10 @@ def kvq_page_bytes(h: Handle) -> int:
 
 def kvq_bf16_page_bytes(h: Handle) -> int:
     return int(load_library().kvq_bf16_page_bytes(h.ptr))
+
+
+def kvq_fp8_page_bytes(h: Handle) -> int:
+    return int(load_library().kvq_fp8_page_bytes(h.ptr))
 
 
 def kvq_set_rotation(h: Handle, R: torch.Tensor, mu: torch.Tensor, stream=None) -> None:
@@ -459,6 +473,75 @@ def kvq_rope(h, x, y, positions, rope: Rope, inverse=False, stream=None):
         1 if inverse else 0, _raw_stream(stream, dev)))
 
 
+def _norm_rows(x, others, heads, dev, names):
+    """[address, stride] of x and each of `others` (rows of one shape), and n; x may be None."""
+    if x is None:
+        return [None, 0] * (1 + len(others)), None
+    p, s, n, _ = _rows(x, dev, names[0], heads)
+    got = [p, s]
+    for t, name in zip(others, names[1:]):
+        p, s, m, _ = _rows(t, dev, name, heads)
+        if m != n:
+            raise ValueError(f"{name} must have the shape of {names[0]}")
+        got += [p, s]
+    return got, n
+
+
+def _weight(t, device, name):
+    """Address of an fp32 [128] tensor (None: NULL)."""
+    if t is None:
+        return None
+    at = _at(t, _F32, device, name)
+    if t.dim() != 1 or t.numel() != 128:
+        raise ValueError(f"{name}: expected [128], got {tuple(t.shape)}")
+    return at
+
+
+def _one_length(nq, nk):
+    if nq is None and nk is None:
+        raise ValueError("q and k must not both be None")
+    if nq is not None and nk is not None and nq != nk:
+        raise ValueError("q and k must have the same number of tokens")
+    return nk if nq is None else nq
+
+
+def kvq_norm_rope(h, q, k, q_out, k_out, q_weight, k_weight, eps, positions, rope: Rope,
+                  stream=None):
+    """Root-mean-square norm of each query and key head, weighted, then rotated by positions, in
+    one pass.  q, q_out: bf16 [n, H, 128]; k, k_out: bf16 [n, Hkv, 128] (tokens may be strided;
+    q_out may be q, k_out may be k); either pair may be None; weights: fp32 [128] or None (ones);
+    positions: int32 [n]."""
+    dev, lay = h.device, h.layout
+    aq, nq = _norm_rows(q, [q_out], lay.num_heads, dev, ["q", "q_out"])
+    ak, nk = _norm_rows(k, [k_out], lay.num_kv_heads, dev, ["k", "k_out"])
+    n = _one_length(nq, nk)
+    _check("kvq_norm_rope", load_library().kvq_norm_rope(
+        h.ptr, *aq[:2], *ak[:2], *aq[2:], *ak[2:], _weight(q_weight, dev, "q_weight"),
+        _weight(k_weight, dev, "k_weight"), eps, _vec(positions, n, dev, "positions"), n,
+        _rope_on(rope, dev), _raw_stream(stream, dev)))
+
+
+def kvq_norm_rope_backward_workspace_bytes(h: Handle, n: int) -> int:
+    return int(load_library().kvq_norm_rope_backward_workspace_bytes(h.ptr, int(n)))
+
+
+def kvq_norm_rope_backward(h, q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, dq_weight,
+                           dk_weight, eps, positions, rope: Rope, workspace, stream=None):
+    """Gradients of kvq_norm_rope: dq, dk (bf16, as q and k; dq may be dq_out, dk may be dk_out)
+    and dq_weight, dk_weight (fp32 [128], written; None: not wanted) from dq_out, dk_out.
+    workspace: uint8, >= kvq_norm_rope_backward_workspace_bytes(h, n)."""
+    dev, lay = h.device, h.layout
+    aq, nq = _norm_rows(q, [dq_out, dq], lay.num_heads, dev, ["q", "dq_out", "dq"])
+    ak, nk = _norm_rows(k, [dk_out, dk], lay.num_kv_heads, dev, ["k", "dk_out", "dk"])
+    n = _one_length(nq, nk)
+    _check("kvq_norm_rope_backward", load_library().kvq_norm_rope_backward(
+        h.ptr, *aq[:2], *ak[:2], *aq[2:4], *ak[2:4], *aq[4:], *ak[4:],
+        _weight(q_weight, dev, "q_weight"), _weight(k_weight, dev, "k_weight"),
+        _weight(dq_weight, dev, "dq_weight"), _weight(dk_weight, dev, "dk_weight"), eps,
+        _vec(positions, n, dev, "positions"), n, _rope_on(rope, dev),
+        _at(workspace, _U8, dev, "workspace"), workspace.numel(), _raw_stream(stream, dev)))
+
+
 def _append_rope(int2, h, pool, num_pool_pages, K, V, seq_idx, positions, page_table, rope,
                  rope_positions, stream):
     dev, hkv = h.device, h.layout.num_kv_heads
@@ -532,6 +615,66 @@ def kvq_bf16_prefill(h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out
                      stream=None):
     """kvq_prefill over the BF16 cache (workspace: kvq_bf16_prefill_workspace_bytes)."""
     _prefill(False, h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace, stream)
+
+
+# ---- the 8-bit cache --------------------------------------------------------------
+
+def _fp8_rows(fn, h, pool, num_pool_pages, K, V, names, cu, page_table, seq_lens, stream):
+    dev, hkv = h.device, h.layout.num_kv_heads
+    at, n = [], None
+    for t, name in zip((K, V), names):
+        if t is None and fn == "kvq_fp8_read":
+            at += [None, 0]
+            continue
+        p, s, m, _ = _rows(t, dev, name, hkv)
+        if n is not None and m != n:
+            raise ValueError(f"{names[0]} and {names[1]} must have the same number of tokens")
+        n = m
+        at += [p, s]
+    if n is None:
+        raise ValueError(f"{names[0]} and {names[1]} must not both be None")
+    pt, batch, max_pages = _table2(page_table, dev)
+    pages = int(num_pool_pages)
+    _check(fn, getattr(load_library(), fn)(
+        h.ptr, _pool(pool, pages, hkv * FP8_RECORD_BYTES, dev), pages, *at,
+        _vec(cu, batch + 1, dev, "cu"), n, pt, max_pages, _vec(seq_lens, batch, dev, "seq_lens"),
+        batch, _raw_stream(stream, dev)))
+
+
+def kvq_fp8_append(h, pool, num_pool_pages, K, V, cu, page_table, seq_lens, stream=None):
+    """Quantise K, V (bf16 [n, Hkv, 128], tokens may be strided) into the 8-bit cache.  cu: int32
+    [B + 1], sequence b's rows are cu[b]:cu[b + 1], the last of its seq_lens[b] positions."""
+    _fp8_rows("kvq_fp8_append", h, pool, num_pool_pages, K, V, ("K", "V"), cu, page_table,
+              seq_lens, stream)
+
+
+def kvq_fp8_read(h, pool, num_pool_pages, K_out, V_out, cu, page_table, seq_lens, stream=None):
+    """The cache's entries as bf16 rows [n, Hkv, 128] (tokens may be strided; either may be None):
+    rows cu[b]:cu[b + 1] are the last of the positions below seq_lens[b] of sequence b."""
+    _fp8_rows("kvq_fp8_read", h, pool, num_pool_pages, K_out, V_out, ("K_out", "V_out"), cu,
+              page_table, seq_lens, stream)
+
+
+def kvq_fp8_workspace_bytes(h: Handle, batch: int) -> int:
+    return int(load_library().kvq_fp8_workspace_bytes(h.ptr, int(batch)))
+
+
+def kvq_fp8_decode(h, pool, num_pool_pages, q, page_table, seq_lens, out, workspace, window=0,
+                   sinks=0, stream=None):
+    """Attention of each sequence's last token over its 8-bit cache: all positions, or the last
+    `window` and the first `sinks`.  q: bf16 [B, H, 128]; out: fp32 [B, H, 128]; workspace: uint8,
+    >= kvq_fp8_workspace_bytes(h, B)."""
+    dev, lay = h.device, h.layout
+    pt, batch, max_pages = _table2(page_table, dev)
+    pages, shape = int(num_pool_pages), (batch, lay.num_heads, 128)
+    pq, po = _at(q, _BF16, dev, "q"), _at(out, _F32, dev, "out")
+    if tuple(q.shape) != shape or tuple(out.shape) != shape:
+        raise ValueError(f"q and out: expected {list(shape)}, got {tuple(q.shape)} and "
+                         f"{tuple(out.shape)}")
+    _check("kvq_fp8_decode", load_library().kvq_fp8_decode(
+        h.ptr, _pool(pool, pages, lay.num_kv_heads * FP8_RECORD_BYTES, dev), pages, pq, pt,
+        max_pages, _vec(seq_lens, batch, dev, "seq_lens"), batch, int(window), int(sinks), po,
+        _at(workspace, _U8, dev, "workspace"), workspace.numel(), _raw_stream(stream, dev)))
 
 
 def kvq_dequant(h, pool, num_pool_pages, page_table, seq, start, length, K_out=None, V_out=None,
