@@ -592,6 +592,20 @@ int kvq_fp8_decode(kvq_handle* h, const void* pool, int num_pool_pages, const ui
                    int window, int sinks, float* out, void* workspace, size_t ws_bytes,
                    void* stream);
 
+/* The same for chunks of new tokens (prompts, drafts, mixed batches), as kvq_bf16_prefill: row i of
+ * sequence b, at position p = seq_lens[b] - n_b + i, attends to the positions t <= p with
+ *     t > p - window  or  t < sinks          (window = 0: all of them).
+ * Entries and queries enter the products as they are, weights are rounded to bf16, sums are fp32.
+ * Key tiles of 128 positions that no row of a tile of rows sees are not worked on; pages without a
+ * visible position are not read, and need not exist.  A value vector that holds a NaN makes NaN
+ * the whole output of each row that sees it, and leaves the others alone.
+ * Arguments, errors and status bits otherwise as for kvq_prefill. */
+size_t kvq_fp8_prefill_workspace_bytes(const kvq_handle* h, int batch, int n);
+int kvq_fp8_prefill(kvq_handle* h, const void* pool, int num_pool_pages, const uint16_t* q,
+                    long long q_stride, const int32_t* cu_q, int n, const int32_t* page_table,
+                    int max_pages, const int32_t* seq_lens, int batch, int window, int sinks,
+                    uint16_t* out, void* workspace, size_t ws_bytes, void* stream);
+
 /* ---- test export -----------------------------------------------------------
  * Dequantise positions [start, start+len) of sequence `seq` to fp32 in the
  * rotated (and, for keys, centred) basis: K_out[i][kv][d] = fmaf(code, s, z),

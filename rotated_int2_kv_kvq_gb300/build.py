@@ -25,7 +25,8 @@ NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-r
 # Kernels whose launch needs an exact register count: source -> (kernel, registers a thread,
 # instantiations).  prefill_kernel's roles share out what the block was launched with, so with
 # any other count the call would be refused at run time.
-REGISTERS = {"kvq_prefill.cu": ("prefill_kernel", 128, 2)}
+REGISTERS = {"kvq_prefill.cu": ("prefill_kernel", 128, 2),
+             "kvq_fp8_prefill.cu": ("prefill_kernel", 128, 1)}
 
 
 def nvcc() -> str:

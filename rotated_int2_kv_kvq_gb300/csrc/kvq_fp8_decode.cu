@@ -274,7 +274,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_fp8_kernel(const 
       pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 8));
       pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 16));
       if (__any_sync(0xffffffffu, pm > m + kLazy || pm + ev > mv + kLazy)) {
-        const float mn = fmaxf(m, pm), mvn = fmaxf(mv, pm + ev);
+        // whole powers of two: their differences, and ev's, are exact, and a weight is rounded alike
+        // whichever reference it meets
+        const float mn = fmaxf(m, floorf(pm)), mvn = fmaxf(mv, floorf(pm) + ev);
         l *= m == mn ? 1.0f : fast_exp2(m - mn);
         const float f = mv == mvn ? 1.0f : fast_exp2(mv - mvn);
 #pragma unroll

@@ -406,15 +406,33 @@ int append_common(kvq_handle* h, bool int2, void* pool, int num_pool_pages, cons
   return cuda_rc(e);
 }
 
+// The arguments that the calls over the 8-bit cache share.
+bool fp8_cache_ok(const void* pool, int num_pool_pages, const int32_t* page_table, int max_pages,
+                  const int32_t* seq_lens, int batch) {
+  return pool && reinterpret_cast<uintptr_t>(pool) % 16 == 0 && num_pool_pages >= 1 && page_table &&
+         max_pages >= 1 && max_pages <= (1 << 26) && seq_lens && batch >= 1 && batch <= 65535;
+}
+
+// A window that holds every position is none; beyond the positions, more sinks are no more.
+void clip_window(int max_pages, int* window, int* sinks) {
+  const int most = max_pages * kvq::kPage;
+  if (*window >= most) *window = 0;
+  if (*sinks > most) *sinks = most;
+}
+
 size_t prefill_bytes(const kvq_handle* h, int batch, int n) {
   if (!h || batch < 1 || batch > 65535 || n < 0) return 0;
   return kvq::prefill_ws_layout(h->num_sms).total;
 }
 
-int prefill_common(kvq_handle* h, bool int2, const void* pool, int num_pool_pages,
+enum class Cache { kBf16, kInt2, kFp8 };
+
+int prefill_common(kvq_handle* h, Cache cache, const void* pool, int num_pool_pages,
                    const uint16_t* q, long long q_stride, const int32_t* cu_q, int n,
                    const int32_t* page_table, int max_pages, const int32_t* seq_lens, int batch,
-                   uint16_t* out, void* workspace, size_t ws_bytes, void* stream) {
+                   uint16_t* out, void* workspace, size_t ws_bytes, void* stream, int window = 0,
+                   int sinks = 0) {
+  const bool int2 = cache == Cache::kInt2;
   if (!h || n < 0 || batch < 1 || batch > 65535) return KVQ_EINVAL;
   if (int2 && !h->ready) return KVQ_ENOTREADY;
   if (n == 0) return KVQ_OK;
@@ -454,14 +472,11 @@ int prefill_common(kvq_handle* h, bool int2, const void* pool, int num_pool_page
   a.cuts = reinterpret_cast<kvq::PrefillArgs::Cut*>(ws + w.cuts_off);
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml_off);
   a.part = reinterpret_cast<float*>(ws + w.part_off);
-  return cuda_rc(kvq::launch_prefill(a, int2, h->num_sms, S(stream)));
-}
-
-// The arguments that the calls over the 8-bit cache share.
-bool fp8_cache_ok(const void* pool, int num_pool_pages, const int32_t* page_table, int max_pages,
-                  const int32_t* seq_lens, int batch) {
-  return pool && reinterpret_cast<uintptr_t>(pool) % 16 == 0 && num_pool_pages >= 1 && page_table &&
-         max_pages >= 1 && max_pages <= (1 << 26) && seq_lens && batch >= 1 && batch <= 65535;
+  a.window = window;
+  a.sinks = sinks;
+  clip_window(max_pages, &a.window, &a.sinks);
+  return cuda_rc(cache == Cache::kFp8 ? kvq::launch_fp8_prefill(a, h->num_sms, S(stream))
+                                      : kvq::launch_prefill(a, int2, h->num_sms, S(stream)));
 }
 
 int fp8_rows(kvq_handle* h, bool append, const void* pool, int num_pool_pages, const uint16_t* K,
@@ -833,7 +848,7 @@ int kvq_prefill(kvq_handle* h, const void* pool, int num_pool_pages, const uint1
                 long long q_stride, const int32_t* cu_q, int n, const int32_t* page_table,
                 int max_pages, const int32_t* seq_lens, int batch, uint16_t* out, void* workspace,
                 size_t ws_bytes, void* stream) {
-  return prefill_common(h, true, pool, num_pool_pages, q, q_stride, cu_q, n, page_table, max_pages,
+  return prefill_common(h, Cache::kInt2, pool, num_pool_pages, q, q_stride, cu_q, n, page_table, max_pages,
                         seq_lens, batch, out, workspace, ws_bytes, stream);
 }
 
@@ -841,7 +856,7 @@ int kvq_bf16_prefill(kvq_handle* h, const void* pool, int num_pool_pages, const 
                      long long q_stride, const int32_t* cu_q, int n, const int32_t* page_table,
                      int max_pages, const int32_t* seq_lens, int batch, uint16_t* out,
                      void* workspace, size_t ws_bytes, void* stream) {
-  return prefill_common(h, false, pool, num_pool_pages, q, q_stride, cu_q, n, page_table,
+  return prefill_common(h, Cache::kBf16, pool, num_pool_pages, q, q_stride, cu_q, n, page_table,
                         max_pages, seq_lens, batch, out, workspace, ws_bytes, stream);
 }
 
@@ -947,12 +962,26 @@ int kvq_fp8_decode(kvq_handle* h, const void* pool, int num_pool_pages, const ui
   a.G = h->G;
   a.window = window;
   a.sinks = sinks;
+  clip_window(max_pages, &a.window, &a.sinks);
   a.out = out;
   a.log2_scale = h->sm_scale * 1.4426950408889634f;
   a.status = h->status;
   a.cuts = reinterpret_cast<int4*>(ws + w.cuts_off);
   a.part = reinterpret_cast<float*>(ws + w.part_off);
   return cuda_rc(kvq::launch_fp8_decode(a, h->num_sms, S(stream)));
+}
+
+size_t kvq_fp8_prefill_workspace_bytes(const kvq_handle* h, int batch, int n) {
+  return prefill_bytes(h, batch, n);
+}
+
+int kvq_fp8_prefill(kvq_handle* h, const void* pool, int num_pool_pages, const uint16_t* q,
+                    long long q_stride, const int32_t* cu_q, int n, const int32_t* page_table,
+                    int max_pages, const int32_t* seq_lens, int batch, int window, int sinks,
+                    uint16_t* out, void* workspace, size_t ws_bytes, void* stream) {
+  if (window < 0 || sinks < 0) return KVQ_EINVAL;
+  return prefill_common(h, Cache::kFp8, pool, num_pool_pages, q, q_stride, cu_q, n, page_table, max_pages,
+                        seq_lens, batch, out, workspace, ws_bytes, stream, window, sinks);
 }
 
 int kvq_dequant(kvq_handle* h, const void* pool, int num_pool_pages, const int32_t* page_table,

@@ -143,6 +143,7 @@ struct PrefillArgs {
   const uint16_t* rv_tile;
   float log2_scale;
   uint32_t* status;
+  int window = 0, sinks = 0; // 8-bit cache: see kvq_fp8_prefill (window 0: all positions)
   // workspace
   struct Cut {               // the item that the border before a CTA's range cuts
     int row0, rows, kv;      // first row of q / out; rows (token, head), 0: none; KV head
@@ -157,6 +158,7 @@ struct PrefillWs {
 };
 PrefillWs prefill_ws_layout(int num_sms);
 cudaError_t launch_prefill(const PrefillArgs& a, bool int2, int num_sms, cudaStream_t st);
+cudaError_t launch_fp8_prefill(const PrefillArgs& a, int num_sms, cudaStream_t st);
 // R_V^T and the operands of the prefill's rotations from R [2][Hkv][D][D]; identity_q: the
 // identity in R_K's place (the caller's queries are rotated already).
 cudaError_t launch_rotation_bank(const float* R, int Hkv, bool identity_q, float* RVt, uint16_t* hi,

@@ -75,6 +75,8 @@ SIGNATURES = {
     "kvq_fp8_read": ([_P, _P, _I, _P, _LL, _P, _LL, _P, _I, _P, _I, _P, _I, _P], _I),
     "kvq_fp8_workspace_bytes": ([_P, _I], _SZ),
     "kvq_fp8_decode": ([_P, _P, _I, _P, _P, _I, _P, _I, _I, _I, _P, _P, _SZ, _P], _I),
+    "kvq_fp8_prefill_workspace_bytes": ([_P, _I, _I], _SZ),
+    "kvq_fp8_prefill": ([_P, _P, _I, _P, _LL, _P, _I, _P, _I, _P, _I, _I, _I, _P, _P, _SZ, _P], _I),
     "kvq_get_status": ([_P, _P, _P], _I),
     "kvq_selftest_wait_timeout": ([_P, _I, _P], _I),
     "kvq_auto_splits": ([_P, _I, _I], _I),
@@ -586,20 +588,20 @@ def kvq_bf16_prefill_workspace_bytes(h: Handle, batch: int, n: int) -> int:
     return int(load_library().kvq_bf16_prefill_workspace_bytes(h.ptr, int(batch), int(n)))
 
 
-def _prefill(int2, h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace, stream):
+def _prefill(fn, record, h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace, stream,
+             *more):
     dev, H = h.device, h.layout.num_heads
     pq, sq, n, _ = _rows(q, dev, "q", H)
     pt, batch, max_pages = _table2(page_table, dev)
     po = _at(out, _BF16, dev, "out")
     if tuple(out.shape) != (n, H, 128):
         raise ValueError(f"out: expected [{n}, {H}, 128], got {tuple(out.shape)}")
-    pages, record = int(num_pool_pages), INT2_RECORD_BYTES if int2 else BF16_RECORD_BYTES
-    fn = "kvq_prefill" if int2 else "kvq_bf16_prefill"
+    pages = int(num_pool_pages)
     _check(fn, getattr(load_library(), fn)(
         h.ptr, _pool(pool, pages, h.layout.num_kv_heads * record, dev), pages, pq, sq,
         _vec(cu_q, batch + 1, dev, "cu_q"), n, pt, max_pages,
-        _vec(seq_lens, batch, dev, "seq_lens"), batch, po, _at(workspace, _U8, dev, "workspace"),
-        workspace.numel(), _raw_stream(stream, dev)))
+        _vec(seq_lens, batch, dev, "seq_lens"), batch, *more, po,
+        _at(workspace, _U8, dev, "workspace"), workspace.numel(), _raw_stream(stream, dev)))
 
 
 def kvq_prefill(h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace,
@@ -608,13 +610,15 @@ def kvq_prefill(h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, wor
     (tokens may be strided); cu_q: int32 [B + 1], sequence b's rows are cu_q[b]:cu_q[b + 1], the
     last of its seq_lens[b] positions; out: bf16 [n, H, 128]; workspace: uint8,
     >= kvq_prefill_workspace_bytes(h, B, n)."""
-    _prefill(True, h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace, stream)
+    _prefill("kvq_prefill", INT2_RECORD_BYTES, h, pool, num_pool_pages, q, cu_q, page_table, seq_lens,
+             out, workspace, stream)
 
 
 def kvq_bf16_prefill(h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace,
                      stream=None):
     """kvq_prefill over the BF16 cache (workspace: kvq_bf16_prefill_workspace_bytes)."""
-    _prefill(False, h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace, stream)
+    _prefill("kvq_bf16_prefill", BF16_RECORD_BYTES, h, pool, num_pool_pages, q, cu_q, page_table,
+             seq_lens, out, workspace, stream)
 
 
 # ---- the 8-bit cache --------------------------------------------------------------
@@ -675,6 +679,18 @@ def kvq_fp8_decode(h, pool, num_pool_pages, q, page_table, seq_lens, out, worksp
         h.ptr, _pool(pool, pages, lay.num_kv_heads * FP8_RECORD_BYTES, dev), pages, pq, pt,
         max_pages, _vec(seq_lens, batch, dev, "seq_lens"), batch, int(window), int(sinks), po,
         _at(workspace, _U8, dev, "workspace"), workspace.numel(), _raw_stream(stream, dev)))
+
+
+def kvq_fp8_prefill_workspace_bytes(h: Handle, batch: int, n: int) -> int:
+    return int(load_library().kvq_fp8_prefill_workspace_bytes(h.ptr, int(batch), int(n)))
+
+
+def kvq_fp8_prefill(h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out, workspace,
+                    window=0, sinks=0, stream=None):
+    """kvq_prefill over the 8-bit cache (workspace: kvq_fp8_prefill_workspace_bytes): each row sees
+    all positions up to its own, or the last `window` of them and the first `sinks`."""
+    _prefill("kvq_fp8_prefill", FP8_RECORD_BYTES, h, pool, num_pool_pages, q, cu_q, page_table, seq_lens,
+             out, workspace, stream, int(window), int(sinks))
 
 
 def kvq_dequant(h, pool, num_pool_pages, page_table, seq, start, length, K_out=None, V_out=None,
