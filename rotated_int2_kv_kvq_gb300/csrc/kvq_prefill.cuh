@@ -47,7 +47,9 @@ struct Smem {
   static constexpr int kTmem = kLine + 48;
   static constexpr int kPair = kTmem + 16;                  // float2 [128]: a split row's scale, then (max, sum) of its odd tiles
   static constexpr int kLook = kPair + 1024;                // Look [2] (8-bit cache)
-  static constexpr int kBytes = kLook + 128;
+  static constexpr int kTileExp = kLook + 96;               // float [kFlags] 2^e of a tile's keys (8-bit cache)
+  static constexpr int kQScale = kLook + 128;               // float [256] a query row's power of two (8-bit cache)
+  static constexpr int kBytes = kQScale + 1024;
   static constexpr int kAlloc = kBytes + 1024;              // base rounded up to 1024
 };
 
@@ -63,7 +65,7 @@ using Cut = PrefillArgs::Cut;
 struct Look {
   uint32_t first, before, rows[8];
 };
-static_assert(2 * sizeof(Look) <= 128, "Look");
+static_assert(2 * sizeof(Look) <= 96 && 4 * kFlags <= 32, "Look, tile exponents");
 
 struct Line {               // a CTA's range of the line of work
   long long cur, end;       // its next unit, its end
@@ -380,6 +382,12 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
                : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Nonzero bits where a half of x is infinite or NaN (fp16 / bf16).
 __device__ __forceinline__ uint32_t nonfinite_f16(uint32_t x) {
   return ((x & 0x7c00u) == 0x7c00u ? 1u : 0u) | ((x & 0x7c000000u) == 0x7c000000u ? 2u : 0u);
@@ -581,34 +589,43 @@ __device__ __forceinline__ uint32_t bf16_store_value(uint4 (&x)[8], int p0, int 
   return poison;
 }
 
-// 8-bit pages: K or V of two pages (16 codes a load) and what the record says of them.
+// 8-bit pages.  Keys become fp16: code * 2^(e - E) with E the largest e of the tile's eight pages,
+// whose 2^E goes into the scores' scale.  Exact unless a page is 2^15 and more below its tile's
+// largest; what that loses is 2^-24 of the tile's largest entry at most.  Values become bf16,
+// exactly, because their sum spans tiles.
+// What lane l < 8 knows of the tile's page l: bits of the scales, flags.
 struct Fp8Meta {
   uint32_t scale_k, scale_v, flags;
 };
-// Codes at byte `at` of both records; with the keys (at = 0) the scales and flags.
-__device__ __forceinline__ void fp8_load_half(uint4 (&x)[8], Fp8Meta (&m)[2], const uint8_t* const (&rec)[2],
-                                              int at, int lane) {
-#pragma unroll
-  for (int y = 0; y < 2; ++y) {
-    if (at == 0) {
-      const uint4 w = rec[y] ? *reinterpret_cast<const uint4*>(rec[y] + 4096) : make_uint4(0, 0, 0, 0);
-      m[y] = Fp8Meta{w.x, w.y, w.z};
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      x[4 * y + i] = rec[y] ? *reinterpret_cast<const uint4*>(rec[y] + at + 512 * i + 16 * lane)
-                            : make_uint4(0, 0, 0, 0);
-  }
+__device__ __forceinline__ Fp8Meta fp8_meta(const uint8_t* rec) {
+  const uint4 w = rec ? *reinterpret_cast<const uint4*>(rec + 4096) : make_uint4(0, 0, 0, 0);
+  return Fp8Meta{w.x, w.y, w.z};
 }
-// Two codes (bytes 2 HI and 2 HI + 1 of w) as bf16 on the scale s, through fp32.
-template <int HI>
-__device__ __forceinline__ uint32_t fp8_wide(uint32_t w, uint32_t s) {
-  const uint32_t h = HI ? fp8_hi(w) : fp8_lo(w);
-  const float f = __uint_as_float(s);
-  return pack_bf162(half_lo(h) * f, half_hi(h) * f);
+// Codes at byte `at` of two pages.
+__device__ __forceinline__ void fp8_load_half(uint4 (&x)[8], const uint8_t* const (&rec)[2], int at, int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    x[i] = rec[i >> 2] ? *reinterpret_cast<const uint4*>(rec[i >> 2] + at + 512 * (i & 3) + 16 * lane)
+                       : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// 2^-d, d >= 0, as two fp16 numbers (0 below the smallest).
+__device__ __forceinline__ uint32_t half_pow2(int d) {
+  const uint32_t h = d <= 14 ? static_cast<uint32_t>(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
+  return h * 0x10001u;
 }
 
-__device__ __forceinline__ void fp8_store_k(const uint4 (&x)[8], const Fp8Meta (&m)[2], uint32_t base) {
+// The pair's keys, each page times its fp16 factor f.
+__device__ __forceinline__ void fp8_store_k(const uint4 (&x)[8], const uint32_t (&f)[2], uint32_t base) {
 #pragma unroll
   for (int pi = 0; pi < 2; ++pi)
 #pragma unroll
@@ -619,35 +636,67 @@ __device__ __forceinline__ void fp8_store_k(const uint4 (&x)[8], const Fp8Meta (
           const uint4& q = x[4 * pi + i];
           return (j >> 1) ? (th ? q.w : q.z) : (th ? q.y : q.x);
         };
-        const uint32_t a = word(2 * (j & 1)), b = word(2 * (j & 1) + 1), s = m[pi].scale_k;
-        sts128(key_at(base, j, 4 * pi + 2 * th), fp8_wide<0>(a, s), fp8_wide<1>(a, s), fp8_wide<0>(b, s),
-               fp8_wide<1>(b, s));
+        const uint32_t a = word(2 * (j & 1)), b = word(2 * (j & 1) + 1);
+        sts128(key_at(base, j, 4 * pi + 2 * th), hmul2(fp8_lo(a), f[pi]), hmul2(fp8_hi(a), f[pi]),
+               hmul2(fp8_lo(b), f[pi]), hmul2(fp8_hi(b), f[pi]));
       }
 }
 
-// Returns the lane's bits of tokens (16 pi + tau) with a value that is not finite here; zeros are
-// stored in its place.
-__device__ __forceinline__ uint32_t fp8_store_v(const uint4 (&x)[8], const Fp8Meta (&m)[2], uint32_t vs, int pw,
-                                                int lane) {
+// Four codes as bf16: sign, exponent and mantissa bits moved to their places, which is code *
+// 2^-120, then times f = 2^(120 + e) (two bf16 numbers).  NaN codes come out as numbers.
+__device__ __forceinline__ void fp8_wide(uint32_t w, uint32_t f, uint32_t& lo, uint32_t& hi) {
+  const uint32_t h = (w & 0x80808080u) | ((w >> 4) & 0x07070707u), l = (w << 4) & 0xf0f0f0f0u;
+  lo = hmul2_bf16(__byte_perm(l, h, 0x5140), f);
+  hi = hmul2_bf16(__byte_perm(l, h, 0x7362), f);
+}
+// Whether that form holds a page's values, and the factor.
+__device__ __forceinline__ bool fp8_plain(uint32_t scale, uint32_t flags) {
+  return (flags & 2u) == 0 && scale <= 0x43000000u;      // 2^7: f is at most 2^127
+}
+__device__ __forceinline__ uint32_t fp8_factor(uint32_t scale) { return ((scale >> 23) + 120u) * 0x00800080u; }
+
+// Where the value rows of a page pair go.
+__device__ __forceinline__ uint32_t value_base(uint32_t vs, int pw, int lane) {
   const int g64 = pw >> 1, pp = pw & 1, g = lane >> 2, t = lane & 3;
-  const uint32_t row = vs + g64 * (kTileBytes / 2) + g * 128 + (((2 * t + pp) ^ g) << 4);
-  uint32_t poison = 0;
+  return vs + g64 * (kTileBytes / 2) + g * 128 + (((2 * t + pp) ^ g) << 4);
+}
+__device__ __forceinline__ void fp8_store_v(const uint4 (&x)[8], const uint32_t (&f)[2], uint32_t row) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {             // element 16 (2i + (r >> 1)) + 8 (r & 1) + g
+      const uint4 &p = x[i], &q = x[4 + i];
       uint32_t e[4];
-#pragma unroll
-      for (int pi = 0; pi < 2; ++pi) {
-        const uint4& q = x[4 * pi + i];
-        const uint32_t w = r == 0 ? q.x : r == 1 ? q.y : r == 2 ? q.z : q.w;
-        e[2 * pi] = fp8_wide<0>(w, m[pi].scale_v);
-        e[2 * pi + 1] = fp8_wide<1>(w, m[pi].scale_v);
-        poison |= bf16_clean(e[2 * pi]) << (16 * pi + 2 * t);
-        poison |= bf16_clean(e[2 * pi + 1]) << (16 * pi + 8 + 2 * t);
-      }
-      sts128(row + (16 * (2 * i + (r >> 1)) + 8 * (r & 1)) * 128, e[0], e[1], e[2], e[3]);
+      fp8_wide(r == 0 ? p.x : r == 1 ? p.y : r == 2 ? p.z : p.w, f[0], e[0], e[1]);
+      fp8_wide(r == 0 ? q.x : r == 1 ? q.y : r == 2 ? q.z : q.w, f[1], e[2], e[3]);
+      sts128(row + (32 * i + 8 * r) * 128, e[0], e[1], e[2], e[3]);
     }
+}
+// The same from the records, for any scales and codes: through fp32, a word at a time.  Returns
+// the lane's bits of tokens (16 pi + tau) with a value that is not finite; zeros are stored in its
+// place.
+__device__ __noinline__ uint32_t fp8_store_v_any(const uint8_t* rec0, const uint8_t* rec1, uint32_t row, int lane) {
+  uint32_t poison = 0;
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i) {
+    uint32_t e[4];
+#pragma unroll
+    for (int pi = 0; pi < 2; ++pi) {
+      const uint8_t* rec = pi ? rec1 : rec0;
+      uint32_t w = 0;
+      float s = 0.0f;
+      if (rec) {
+        w = *reinterpret_cast<const uint32_t*>(rec + 2048 + 512 * (i >> 2) + 16 * lane + 4 * (i & 3));
+        s = *reinterpret_cast<const float*>(rec + 4100);
+      }
+      const uint32_t lo = fp8_lo(w), hi = fp8_hi(w);
+      e[2 * pi] = pack_bf162(half_lo(lo) * s, half_hi(lo) * s);
+      e[2 * pi + 1] = pack_bf162(half_lo(hi) * s, half_hi(hi) * s);
+      poison |= bf16_clean(e[2 * pi]) << (16 * pi + 2 * (lane & 3));
+      poison |= bf16_clean(e[2 * pi + 1]) << (16 * pi + 8 + 2 * (lane & 3));
+    }
+    sts128(row + (32 * (i >> 2) + 8 * (i & 3)) * 128, e[0], e[1], e[2], e[3]);
+  }
   return poison;
 }
 
@@ -692,11 +741,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // The two bf16 values of a word.
 __device__ __forceinline__ uint64_t bf16_pair(uint32_t x) {
   return pair2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
 }
 
 // The power of two that brings the largest |f x| of this thread's 128 columns x into
@@ -794,7 +838,7 @@ __device__ __forceinline__ bool item_end(bool alive, const PrefillArgs& a, volat
 }
 
 // The item's query rows into the Q operands, by the first 384 threads.
-template <bool INT2>
+template <bool INT2, bool FP8>
 __device__ __forceinline__ void load_q(const PrefillArgs& a, const Item& w, uint8_t* smem) {
   const int lg = a.G >> 1, rows = w.tokens << lg;         // log2 of 1, 2, 4
   const int pieces = (rows > 128 ? 256 : 128) * 16;
@@ -815,6 +859,22 @@ __device__ __forceinline__ void load_q(const PrefillArgs& a, const Item& w, uint
     for (int y = 0; y < kBatch; ++y) {
       const int idx = base + y * kStep, row = idx >> 4, c = idx & 15;
       if (idx >= pieces) break;
+      if constexpr (FP8) {          // to fp16, a power of two a row apart (a row is 16 lanes)
+        uint32_t x[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+        float mx = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          mx = max3(mx, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xffff0000u)));
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const uint32_t ex = min((__float_as_uint(mx) >> 23) & 255u, 253u);
+        const float down = __uint_as_float((254u - ex) << 23);
+        if (c == 0) reinterpret_cast<float*>(smem + Smem::kQScale)[row] = __uint_as_float(ex << 23);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[e] = pack_half2(__uint_as_float(x[e] << 16) * down, __uint_as_float(x[e] & 0xffff0000u) * down);
+        v[y] = make_uint4(x[0], x[1], x[2], x[3]);
+      }
       uint8_t* at = smem + Smem::kQ + (row >> 7) * kTileBytes + (row & 127) * 128;
       if constexpr (INT2) {         // d in order: the left operand of q R_K
         *reinterpret_cast<uint4*>(at + (c >> 3) * (kTileBytes / 2) + (((c & 7) ^ (row & 7)) << 4)) = v[y];
@@ -1096,7 +1156,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       sync_cta();                   // the item is there
       const Item w = items[i & 1];
       if (w.done) break;
-      load_q<INT2>(a, w, smem);
+      load_q<INT2, FP8>(a, w, smem);
       sync_cta();                   // Q is there
       const Steps<INT2> st(w, a);
       const int rows = w.tokens * a.G;
@@ -1105,6 +1165,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const bool valid = row < rows, some = (row & ~31) < rows;
       const int first = st.split ? t : 0, step = st.split ? 2 : 1;    // this group's key tiles
       float mref = -INFINITY, l = 0.0f, scale = a.log2_scale;
+      // (a row of zeros: 0 * -inf would be NaN)
+      if constexpr (FP8)
+        scale = fmaxf(scale * reinterpret_cast<const float*>(smem + Smem::kQScale)[row], 1.17549435e-38f);
       auto wait_s = [&]() {
         alive = warp_wait(B(kSFull + t), ns & 1);
         ++ns;
@@ -1165,8 +1228,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           // the tile's missing pages, written before its operands were handed over; the slot
           // is written again four tiles later, which weights of two tiles later precede
           const uint32_t f = (itf + j) % kFlags;
+          float sc = scale;
+          if constexpr (FP8)
+            sc = fminf(fmaxf(scale * reinterpret_cast<const volatile float*>(smem + Smem::kTileExp)[f], 1.17549435e-38f),
+                       1.7014118e38f);
           if (some)
-            softmax_tile<INT2, FP8>(ts, to, scale, j == first, limit, low, lead, edge, anyw[f], badw + 4 * f, mref, l);
+            softmax_tile<INT2, FP8>(ts, to, sc, j == first, limit, low, lead, edge, anyw[f], badw + 4 * f, mref, l);
           give();
         }
         // O is complete.  A row sees all positions up to its own, so it sees a NaN or an
@@ -1350,6 +1417,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         copy_v = itv;
       }
       int id[2];
+      [[maybe_unused]] int tid8 = -1;
       uint4 x[8];
       auto records = [&](int j) {
 #pragma unroll
@@ -1358,19 +1426,34 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           id[y] = pages.id(first(j + 1) + y, j + 1 < st.tiles);
         }
       };
+      // 8-bit cache: lane l < 8 has the id of the page l of the tile that is loaded next
+      [[maybe_unused]] Fp8Meta meta;
+      auto tile_id = [&](int j) {
+        return pages.id(w.tile<FP8>(j) * kTilePages + lane, lane < kTilePages && j < st.tiles);
+      };
+      auto tile_records = [&](int j) {      // the pair's records and the lane's page's meta of tile j
+        meta = fp8_meta(pages.record(tid8));
+        rec[0] = pages.record(__shfl_sync(0xffffffffu, tid8, 2 * pw));
+        rec[1] = pages.record(__shfl_sync(0xffffffffu, tid8, 2 * pw + 1));
+        tid8 = tile_id(j + 1);
+      };
+      if constexpr (FP8) {
+        tid8 = tile_id(0);
+        tile_records(0);
+      } else {
 #pragma unroll
-      for (int y = 0; y < 2; ++y) id[y] = pages.id(first(0) + y, st.tiles > 0);
-      [[maybe_unused]] Fp8Meta meta[2];
-      records(0);
+        for (int y = 0; y < 2; ++y) id[y] = pages.id(first(0) + y, st.tiles > 0);
+        records(0);
+      }
       if constexpr (INT2) {
 #pragma unroll
         for (int y = 0; y < 2; ++y) int2_load(raw, y, rec[y], lane);
       } else if constexpr (FP8) {
-        fp8_load_half(x, meta, rec, 0, lane);
+        fp8_load_half(x, rec, 0, lane);
       } else {
         bf16_load_key(x, rec[0], lane);
       }
-      load_q<INT2>(a, w, smem);
+      load_q<INT2, FP8>(a, w, smem);
       sync_cta();                   // Q is there
       for (int j = 0; j < st.tiles && alive; ++j) {
         const uint32_t k = itk + st.pre + j, kv = itv + st.pre + j;
@@ -1404,14 +1487,32 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           poison = int2_store_v(now, vbuf(kv), pw, lane);
         } else if constexpr (FP8) {
           uint4 values[8];
-          Fp8Meta now[2] = {meta[0], meta[1]};
-          fp8_load_half(values, now, rec, 2048, lane);
-          fp8_store_k(x, meta, key_base(kbuf(k), pw, lane));
+          fp8_load_half(values, rec, 2048, lane);
+          const uint8_t* const old[2] = {rec[0], rec[1]};
+          // exponent of the lane's page and the tile's largest (a page that is not there: -127)
+          const int e = static_cast<int>(meta.scale_k >> 23) - 127;
+          const int top = __reduce_max_sync(0xffffffffu, lane < kTilePages ? e : -127);
+          uint32_t fk[2], fv[2];
+          bool plain = true;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            fk[y] = half_pow2(top - __shfl_sync(0xffffffffu, e, 2 * pw + y));
+            const uint32_t s = __shfl_sync(0xffffffffu, meta.scale_v, 2 * pw + y);
+            plain = plain && fp8_plain(s, __shfl_sync(0xffffffffu, meta.flags, 2 * pw + y));
+            fv[y] = fp8_factor(s);
+          }
+          if (pw == 0 && lane == 0)
+            reinterpret_cast<volatile float*>(smem + Smem::kTileExp)[slot] =
+                __int_as_float((min(max(top, -126), 127) + 127) << 23);
+          fp8_store_k(x, fk, key_base(kbuf(k), pw, lane));
           give(kKFull, k);
-          records(j + 1);
-          fp8_load_half(x, meta, rec, 0, lane);
+          tile_records(j + 1);
+          fp8_load_half(x, rec, 0, lane);
           if (!wait_empty(kVEmpty, kv)) break;
-          poison = fp8_store_v(values, now, vbuf(kv), pw, lane);
+          poison = 0;
+          const uint32_t row = value_base(vbuf(kv), pw, lane);
+          if (plain) fp8_store_v(values, fv, row);
+          else poison = fp8_store_v_any(old[0], old[1], row, lane);
           if (poison) {
             Look& look = looks[i & 1];
             for (uint32_t m = poison; m != 0; m &= m - 1) {
@@ -1479,7 +1580,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const Steps<INT2> st(w, a);
       sync_cta();                   // Q is there
       if (warp == kMmaWarp && st.tiles > 0) {
-        constexpr uint32_t idesc = idesc_f16(INT2 ? 0 : 1), idesc_bf = idesc_f16(1);
+        constexpr uint32_t idesc = idesc_f16(INT2 || FP8 ? 0 : 1), idesc_bf = idesc_f16(1);   // scores, q R_K
+        constexpr uint32_t idesc_v = idesc_f16(INT2 ? 0 : 1);
         const bool both = __shfl_sync(0xffffffffu, st.split ? 0 : 1, 0) != 0;
         const int tiles = __shfl_sync(0xffffffffu, st.tiles, 0);
         auto full = [&](int bar, uint32_t k) {
@@ -1513,7 +1615,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         auto weighted = [&](int t, uint32_t v, bool add) {     // O_t += P_t V
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            tc_mma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * k, v + desc_step(k), idesc,
+            tc_mma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * k, v + desc_step(k), idesc_v,
                       add || k != 0, one);
         };
         uint32_t k = __shfl_sync(0xffffffffu, itk, 0), v = __shfl_sync(0xffffffffu, itv, 0);
