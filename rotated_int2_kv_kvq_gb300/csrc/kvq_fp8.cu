@@ -117,11 +117,6 @@ __device__ __forceinline__ bool scale_exponent(uint32_t bits, int& e) {
   return (bits & 0x807fffffu) == 0 && e >= kFp8MinExp && e <= kFp8MaxExp;
 }
 
-__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // Codes of what the four codes of w stand for on a scale 2^k times larger (f as two fp16
 // numbers 2^-k): exact products unless they round to zero codes anyway.
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, uint32_t f) {
@@ -214,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_append_kernel(const __grid_co
         unpack8(v, x[j], ik);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-          *reinterpret_cast<uint16_t*>(at + 64 * j + 16 * t) = static_cast<uint16_t>(encode2(v[2 * t], v[2 * t + 1]));
+          *reinterpret_cast<uint16_t*>(at + 64 * j + 16 * t) = fp8_encode(v[2 * t], v[2 * t + 1]);
       }
     }
     {
@@ -229,9 +224,9 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_append_kernel(const __grid_co
         unpack8(v1, y[2 * t + 1], iv);
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
-          const uint32_t code = encode2(v0[g], v1[g]);
+          const uint16_t code = fp8_encode(v0[g], v1[g]);
           uint8_t* to = at + 64 * g + 16 * t;
-          if (both == 3) *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(code);
+          if (both == 3) *reinterpret_cast<uint16_t*>(to) = code;
           else if (both == 1) to[0] = static_cast<uint8_t>(code);
           else to[1] = static_cast<uint8_t>(code >> 8);
         }

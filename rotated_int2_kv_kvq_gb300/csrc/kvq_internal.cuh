@@ -465,6 +465,12 @@ __device__ __forceinline__ uint32_t fp8_pair(uint16_t codes) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
   return h;
 }
+// The nearest codes of two numbers (|x| above 448: 448), the first in the low byte.
+__device__ __forceinline__ uint16_t fp8_encode(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ uint32_t fp8_lo(uint32_t w) { return fp8_pair(static_cast<uint16_t>(w)); }
 __device__ __forceinline__ uint32_t fp8_hi(uint32_t w) { return fp8_pair(static_cast<uint16_t>(w >> 16)); }
 

@@ -4,6 +4,8 @@
 // The including file defines kRegLaunch, the registers a thread at launch.
 #pragma once
 
+#include <type_traits>
+
 #include "kvq_internal.cuh"
 
 namespace kvq {
@@ -16,9 +18,10 @@ constexpr int kThreads = 512;
 constexpr int kProdWarp0 = 8, kMmaWarp = 12, kSchedWarp = 13;
 // Registers a thread, after the roles part (warpgroups: two softmax, producers, one for
 // issue and schedule), of kRegLaunch a thread at launch.
-template <bool INT2>
+template <bool INT2, bool FP8>
 struct Regs {
-  static constexpr int kSoftmax = INT2 ? 184 : 176, kProducer = INT2 ? 96 : 112, kIssue = 48;
+  static constexpr int kSoftmax = FP8 ? 168 : INT2 ? 184 : 176, kProducer = INT2 ? 96 : 112,
+                       kIssue = FP8 ? 64 : 48;
   static_assert(2 * kSoftmax + kProducer + kIssue <= 4 * kRegLaunch, "register split");
 };
 constexpr int kStages = 2;
@@ -47,9 +50,10 @@ struct Smem {
   static constexpr int kTmem = kLine + 48;
   static constexpr int kPair = kTmem + 16;                  // float2 [128]: a split row's scale, then (max, sum) of its odd tiles
   static constexpr int kLook = kPair + 1024;                // Look [2] (8-bit cache)
-  static constexpr int kTileExp = kLook + 96;               // float [kFlags] 2^e of a tile's keys (8-bit cache)
-  static constexpr int kQScale = kLook + 128;               // float [256] a query row's power of two (8-bit cache)
-  static constexpr int kBytes = kQScale + 1024;
+  // 8-bit cache: a query row's power of two; the keys' scales of a tile's pages
+  static constexpr int kQScale = kLook + 128;               // float [256]
+  static constexpr int kPageScale = kQScale + 1024;         // float [kFlags][8]
+  static constexpr int kBytes = kPageScale + 32 * kFlags;
   static constexpr int kAlloc = kBytes + 1024;              // base rounded up to 1024
 };
 
@@ -65,7 +69,7 @@ using Cut = PrefillArgs::Cut;
 struct Look {
   uint32_t first, before, rows[8];
 };
-static_assert(2 * sizeof(Look) <= 96 && 4 * kFlags <= 32, "Look, tile exponents");
+static_assert(2 * sizeof(Look) <= 128, "Look");
 
 struct Line {               // a CTA's range of the line of work
   long long cur, end;       // its next unit, its end
@@ -129,6 +133,16 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, ui
       "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
       "mov.b64 y, {%2, %6};\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(one), "n"(kDescHi)
+      : "memory");
+}
+// Both operands e4m3, 32 columns a step.
+__device__ __forceinline__ void tc_mma_ss_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                             uint32_t acc, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 x, {%1, %6};\n\tmov.b64 y, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n\t}" ::"r"(d),
       "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(one), "n"(kDescHi)
       : "memory");
 }
@@ -589,59 +603,25 @@ __device__ __forceinline__ uint32_t bf16_store_value(uint4 (&x)[8], int p0, int 
   return poison;
 }
 
-// 8-bit pages.  Keys become fp16: code * 2^(e - E) with E the largest e of the tile's eight pages,
-// whose 2^E goes into the scores' scale.  Exact unless a page is 2^15 and more below its tile's
-// largest; what that loses is 2^-24 of the tile's largest entry at most.  Values become bf16,
-// exactly, because their sum spans tiles.
-// What lane l < 8 knows of the tile's page l: bits of the scales, flags.
-struct Fp8Meta {
-  uint32_t scale_k, scale_v, flags;
-};
-__device__ __forceinline__ Fp8Meta fp8_meta(const uint8_t* rec) {
-  const uint4 w = rec ? *reinterpret_cast<const uint4*>(rec + 4096) : make_uint4(0, 0, 0, 0);
-  return Fp8Meta{w.x, w.y, w.z};
+// 8-bit pages.  Key codes are operands as they are (kind::f8f6f4, against two e4m3 parts of the
+// query: as many tensor cycles as 16-bit operands take, and no conversion), moved from the record's
+// order to rows: chunk 2t + h of a token's 128-byte row holds the words (t, h) of the record's four
+// loads, that is, element d = 16 w + 8 h + 2 t + e at byte 2 w + e.  A page's 2^e goes into its
+// columns' scores.  Values become bf16, exactly, because their sum spans pages.
+//
+// What a lane knows of a page: exponents + 128 of the keys and of the values, flags.
+__device__ __forceinline__ uint32_t fp8_meta(const uint8_t* rec) {
+  const uint4 w = rec ? *reinterpret_cast<const uint4*>(rec + 4096) : make_uint4(0x3f800000u, 0, 0, 0);
+  return ((w.x >> 23) + 1) | ((w.y >> 23) + 1) << 9 | w.z << 18;
 }
-// Codes at byte `at` of two pages.
-__device__ __forceinline__ void fp8_load_half(uint4 (&x)[8], const uint8_t* const (&rec)[2], int at, int lane) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    x[i] = rec[i >> 2] ? *reinterpret_cast<const uint4*>(rec[i >> 2] + at + 512 * (i & 3) + 16 * lane)
-                       : make_uint4(0, 0, 0, 0);
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
+__device__ __forceinline__ uint32_t meta_k(uint32_t m) { return (m & 511u) - 1; }          // biased as fp32's
+__device__ __forceinline__ uint32_t meta_v(uint32_t m) { return ((m >> 9) & 511u) - 1; }
+__device__ __forceinline__ uint32_t meta_flags(uint32_t m) { return m >> 18; }
 __device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// 2^-d, d >= 0, as two fp16 numbers (0 below the smallest).
-__device__ __forceinline__ uint32_t half_pow2(int d) {
-  const uint32_t h = d <= 14 ? static_cast<uint32_t>(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
-  return h * 0x10001u;
-}
-
-// The pair's keys, each page times its fp16 factor f.
-__device__ __forceinline__ void fp8_store_k(const uint4 (&x)[8], const uint32_t (&f)[2], uint32_t base) {
-#pragma unroll
-  for (int pi = 0; pi < 2; ++pi)
-#pragma unroll
-    for (int th = 0; th < 2; ++th)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {           // chunk j = 2h + (w >> 2): words th + 2h of two loads
-        auto word = [&](int i) {
-          const uint4& q = x[4 * pi + i];
-          return (j >> 1) ? (th ? q.w : q.z) : (th ? q.y : q.x);
-        };
-        const uint32_t a = word(2 * (j & 1)), b = word(2 * (j & 1) + 1);
-        sts128(key_at(base, j, 4 * pi + 2 * th), hmul2(fp8_lo(a), f[pi]), hmul2(fp8_hi(a), f[pi]),
-               hmul2(fp8_lo(b), f[pi]), hmul2(fp8_hi(b), f[pi]));
-      }
-}
-
 // Four codes as bf16: sign, exponent and mantissa bits moved to their places, which is code *
 // 2^-120, then times f = 2^(120 + e) (two bf16 numbers).  NaN codes come out as numbers.
 __device__ __forceinline__ void fp8_wide(uint32_t w, uint32_t f, uint32_t& lo, uint32_t& hi) {
@@ -649,57 +629,33 @@ __device__ __forceinline__ void fp8_wide(uint32_t w, uint32_t f, uint32_t& lo, u
   lo = hmul2_bf16(__byte_perm(l, h, 0x5140), f);
   hi = hmul2_bf16(__byte_perm(l, h, 0x7362), f);
 }
-// Whether that form holds a page's values, and the factor.
-__device__ __forceinline__ bool fp8_plain(uint32_t scale, uint32_t flags) {
-  return (flags & 2u) == 0 && scale <= 0x43000000u;      // 2^7: f is at most 2^127
+// Whether that form holds a page's values (f is at most 2^127: e up to 7), and the factor; a
+// page that is not there gives zeros.
+__device__ __forceinline__ bool fp8_plain(uint32_t meta) {
+  return (meta_flags(meta) & 2u) == 0 && meta_v(meta) <= 127u + 7u;
 }
-__device__ __forceinline__ uint32_t fp8_factor(uint32_t scale) { return ((scale >> 23) + 120u) * 0x00800080u; }
+__device__ __forceinline__ uint32_t fp8_factor(uint32_t meta) {
+  const uint32_t e = meta_v(meta);
+  return e == 0 ? 0u : (e + 120u) * 0x00800080u;
+}
 
 // Where the value rows of a page pair go.
 __device__ __forceinline__ uint32_t value_base(uint32_t vs, int pw, int lane) {
   const int g64 = pw >> 1, pp = pw & 1, g = lane >> 2, t = lane & 3;
   return vs + g64 * (kTileBytes / 2) + g * 128 + (((2 * t + pp) ^ g) << 4);
 }
-__device__ __forceinline__ void fp8_store_v(const uint4 (&x)[8], const uint32_t (&f)[2], uint32_t row) {
+__device__ __forceinline__ void fp8_store_v(const uint4 (&x)[8], uint32_t f0, uint32_t f1, uint32_t row) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {             // element 16 (2i + (r >> 1)) + 8 (r & 1) + g
       const uint4 &p = x[i], &q = x[4 + i];
       uint32_t e[4];
-      fp8_wide(r == 0 ? p.x : r == 1 ? p.y : r == 2 ? p.z : p.w, f[0], e[0], e[1]);
-      fp8_wide(r == 0 ? q.x : r == 1 ? q.y : r == 2 ? q.z : q.w, f[1], e[2], e[3]);
+      fp8_wide(r == 0 ? p.x : r == 1 ? p.y : r == 2 ? p.z : p.w, f0, e[0], e[1]);
+      fp8_wide(r == 0 ? q.x : r == 1 ? q.y : r == 2 ? q.z : q.w, f1, e[2], e[3]);
       sts128(row + (32 * i + 8 * r) * 128, e[0], e[1], e[2], e[3]);
     }
 }
-// The same from the records, for any scales and codes: through fp32, a word at a time.  Returns
-// the lane's bits of tokens (16 pi + tau) with a value that is not finite; zeros are stored in its
-// place.
-__device__ __noinline__ uint32_t fp8_store_v_any(const uint8_t* rec0, const uint8_t* rec1, uint32_t row, int lane) {
-  uint32_t poison = 0;
-#pragma unroll 1
-  for (int i = 0; i < 16; ++i) {
-    uint32_t e[4];
-#pragma unroll
-    for (int pi = 0; pi < 2; ++pi) {
-      const uint8_t* rec = pi ? rec1 : rec0;
-      uint32_t w = 0;
-      float s = 0.0f;
-      if (rec) {
-        w = *reinterpret_cast<const uint32_t*>(rec + 2048 + 512 * (i >> 2) + 16 * lane + 4 * (i & 3));
-        s = *reinterpret_cast<const float*>(rec + 4100);
-      }
-      const uint32_t lo = fp8_lo(w), hi = fp8_hi(w);
-      e[2 * pi] = pack_bf162(half_lo(lo) * s, half_hi(lo) * s);
-      e[2 * pi + 1] = pack_bf162(half_lo(hi) * s, half_hi(hi) * s);
-      poison |= bf16_clean(e[2 * pi]) << (16 * pi + 2 * (lane & 3));
-      poison |= bf16_clean(e[2 * pi + 1]) << (16 * pi + 8 + 2 * (lane & 3));
-    }
-    sts128(row + (32 * (i >> 2) + 8 * (i & 3)) * 128, e[0], e[1], e[2], e[3]);
-  }
-  return poison;
-}
-
 // A warp's wait for a phase, given up after two seconds of the global timer (its low
 // word wraps after 4.3): all lanes have seen the phase complete, or none goes on (the
 // tcgen05 loads and stores that follow are warp-wide).  Kept short: some twenty of
@@ -795,32 +751,21 @@ struct Steps {
 };
 
 // The pages of an item's sequence and KV head.
-template <bool INT2, bool FP8>
+template <bool INT2>
 struct Pages {
   const int32_t* table;
   const uint8_t* pool;
   size_t stride;
   int count, ids;
-  int lo, sinks;         // 8-bit cache: nothing in [sinks, lo) is visible to the item's rows
-  static constexpr int kRec = INT2 ? kInt2Rec : FP8 ? kFp8Rec : kBf16Rec;
   __device__ __forceinline__ Pages(const PrefillArgs& a, const Item& w)
       : table(a.page_table + static_cast<size_t>(w.b) * a.max_pages),
-        pool(a.pool + static_cast<size_t>(w.kv) * kRec),
-        stride(static_cast<size_t>(a.Hkv) * kRec),
+        pool(a.pool + static_cast<size_t>(w.kv) * (INT2 ? kInt2Rec : kBf16Rec)),
+        stride(static_cast<size_t>(a.Hkv) * (INT2 ? kInt2Rec : kBf16Rec)),
         count((w.key_end + kPage - 1) / kPage),
-        ids(a.num_pool_pages) {
-    if constexpr (FP8) {
-      lo = a.window == 0 ? 0 : max(0, w.pos0 - a.window + 1);
-      sinks = a.sinks;
-    }
-  }
-  // whether a row of the item sees part of page p (behind the last page: no)
-  __device__ __forceinline__ bool seen(int p) const {
-    return p < count && (!FP8 || (p + 1) * kPage > lo || p * kPage < sinks);
-  }
-  // id of the sequence's page p; -1 if no row sees it, or where `wanted` is false
+        ids(a.num_pool_pages) {}
+  // id of the sequence's page p; -1 behind its last page, or where `wanted` is false
   __device__ __forceinline__ int id(int p, bool wanted) const {
-    return wanted && seen(p) ? table[p] : -1;
+    return wanted && p < count ? table[p] : -1;
   }
   __device__ __forceinline__ const uint8_t* record(int i) const {
     return i >= 0 && i < ids ? pool + static_cast<size_t>(i) * stride : nullptr;
@@ -842,7 +787,8 @@ template <bool INT2, bool FP8>
 __device__ __forceinline__ void load_q(const PrefillArgs& a, const Item& w, uint8_t* smem) {
   const int lg = a.G >> 1, rows = w.tokens << lg;         // log2 of 1, 2, 4
   const int pieces = (rows > 128 ? 256 : 128) * 16;
-  constexpr int kStep = kMmaWarp * 32, kBatch = 6;        // loads in flight a thread
+  constexpr int kStep = kMmaWarp * 32, kBatch = FP8 ? 2 : 6;   // loads in flight a thread (8-bit cache:
+                                        // beside the producers' pages; 6 spill, 1931 against 1728 us)
 #pragma unroll 1
   for (int base = threadIdx.x; base < pieces; base += kBatch * kStep) {
     uint4 v[kBatch];
@@ -859,21 +805,33 @@ __device__ __forceinline__ void load_q(const PrefillArgs& a, const Item& w, uint
     for (int y = 0; y < kBatch; ++y) {
       const int idx = base + y * kStep, row = idx >> 4, c = idx & 15;
       if (idx >= pieces) break;
-      if constexpr (FP8) {          // to fp16, a power of two a row apart (a row is 16 lanes)
-        uint32_t x[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+      if constexpr (FP8) {
+        // two e4m3 parts of q times a power of two a row (its largest in [128, 256)): 8 bits, so exact
+        // but for elements below 2^-9 of the largest, which keep 2^-18 of it
+        const uint32_t x[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
         float mx = 0.0f;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           mx = max3(mx, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xffff0000u)));
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const uint32_t ex = min((__float_as_uint(mx) >> 23) & 255u, 253u);
-        const float down = __uint_as_float((254u - ex) << 23);
-        if (c == 0) reinterpret_cast<float*>(smem + Smem::kQScale)[row] = __uint_as_float(ex << 23);
+        for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));   // a row is 16 lanes
+        const uint32_t ex = min(max((__float_as_uint(mx) >> 23) & 255u, 8u), 253u);
+        const float down = __uint_as_float((261u - ex) << 23);
+        if (c == 0) reinterpret_cast<float*>(smem + Smem::kQScale)[row] = __uint_as_float((ex - 7u) << 23);
+        uint8_t* to = smem + Smem::kQ + (row >> 7) * kTileBytes + (row & 127) * 128 + 2 * (c >> 1);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          x[e] = pack_half2(__uint_as_float(x[e] << 16) * down, __uint_as_float(x[e] & 0xffff0000u) * down);
-        v[y] = make_uint4(x[0], x[1], x[2], x[3]);
+        for (int t = 0; t < 4; ++t) {
+          float q0 = __uint_as_float(x[t] << 16) * down, q1 = __uint_as_float(x[t] & 0xffff0000u) * down;
+          q0 += q0 - q0;            // an infinity becomes NaN
+          q1 += q1 - q1;
+          const uint16_t hi = fp8_encode(q0, q1);
+          const uint32_t back = fp8_pair(hi);
+          const uint16_t lo = fp8_encode(q0 - half_lo(back), q1 - half_hi(back));
+          const int at = ((2 * t + (c & 1)) ^ (row & 7)) << 4;
+          *reinterpret_cast<uint16_t*>(to + at) = hi;
+          *reinterpret_cast<uint16_t*>(to + kTileBytes / 2 + at) = lo;
+        }
+        continue;
       }
       uint8_t* at = smem + Smem::kQ + (row >> 7) * kTileBytes + (row & 127) * 128;
       if constexpr (INT2) {         // d in order: the left operand of q R_K
@@ -906,10 +864,12 @@ __device__ __forceinline__ uint32_t visible(int limit, int k) {
 // against 64 bits on two 4093-token prompts 0.0022 against 0.0023; 279 us against 282).
 // INT2: the fp16 rounding is an eighth of that and the sum of the unrounded ones (the two
 // conversions would cost 5 to 11 % there) as good, 0.0018 either way.
-// low, lead (8-bit cache): positions of the tile from `lead` on and before `low` are hidden too.
+// low, lead (8-bit cache): positions of the tile from `lead` on and before `low` are hidden too;
+// pages: the keys' scales of its pages (those of column 64 a + 8 b + 4 c + .. are of page 4a + 2b + c,
+// b and c modulo 2).
 template <bool INT2, bool FP8>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float scale, bool first,
-                                             int limit, int low, int lead, bool edge, uint32_t any, const volatile uint32_t* bad,
+                                             int limit, int low, int lead, const float* pages, bool edge, uint32_t any, const volatile uint32_t* bad,
                                              float& mref, float& l) {
   if (edge || any != 0) {
     // Hidden scores become -inf in TMEM first, 32 columns a step: rolled and apart from
@@ -936,17 +896,49 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sca
     }
     tc_wait_st();
   }
+  [[maybe_unused]] float sc_all[8];      // of the columns of each page
+  if constexpr (FP8) {
+    const float4 x = *reinterpret_cast<const float4*>(pages), y = *reinterpret_cast<const float4*>(pages + 4);
+    sc_all[0] = x.x, sc_all[1] = x.y, sc_all[2] = x.z, sc_all[3] = x.w;
+    sc_all[4] = y.x, sc_all[5] = y.y, sc_all[6] = y.z, sc_all[7] = y.w;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sc_all[i] *= scale;
+    if (edge || any != 0) {              // a hidden column's 0 * -inf would be NaN
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sc_all[i] = fmaxf(sc_all[i], 1.17549435e-38f);
+    }
+  }
   uint32_t v[4][32];
   tc_ld_row(v, ts);
-  float m[4];                    // four chains, a quarter of the columns each
+  float mnew;
+  if constexpr (FP8) {
+    float m[8];                  // a chain a page
 #pragma unroll
-  for (int c = 0; c < 4; ++c) m[c] = fmaxf(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]));
+    for (int i = 0; i < 32; i += 2)
 #pragma unroll
-  for (int i = 2; i < 32; i += 2)
+      for (int c = 0; c < 4; ++c) {
+        const int pg = 4 * (c >> 1) + ((i >> 2) & 3);          // bits 3 and 2 of the column: 2b + c
+        const float x = __uint_as_float(v[c][i]), y = __uint_as_float(v[c][i + 1]);
+        m[pg] = (c & 1) == 0 && i == ((i >> 2) & 3) * 4 ? fmaxf(x, y) : max3(m[pg], x, y);
+      }
+    mnew = mref;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      m[c] = max3(m[c], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
-  const float mnew = fmaxf(mref, fmaxf(max3(m[0], m[1], m[2]), m[3]) * scale);
+    for (int h = 0; h < 2; ++h) {
+      const float* sc = sc_all + 4 * h;
+      mnew = max3(mnew, m[4 * h] * sc[0], m[4 * h + 1] * sc[1]);
+      mnew = max3(mnew, m[4 * h + 2] * sc[2], m[4 * h + 3] * sc[3]);
+    }
+  } else {
+    float m[4];                  // four chains, a quarter of the columns each
+#pragma unroll
+    for (int c = 0; c < 4; ++c) m[c] = fmaxf(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]));
+#pragma unroll
+    for (int i = 2; i < 32; i += 2)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        m[c] = max3(m[c], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
+    mnew = fmaxf(mref, fmaxf(max3(m[0], m[1], m[2]), m[3]) * scale);
+  }
   // The reference is a whole power of two at or below the maximum, so that two references
   // of a row differ by an exact factor and its weights are rounded alike whichever part of
   // the work, and so whichever batch or chunking, they fall in (a sequence's outputs alone and
@@ -973,13 +965,21 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sca
     }
   }
   const float neg = mref == -INFINITY ? 0.0f : (INT2 ? kBias : 0.0f) - mref;
-  const uint64_t sc2 = pair2(scale, scale), ng2 = pair2(neg, neg);
+  const uint64_t ng2 = pair2(neg, neg);
+  [[maybe_unused]] const uint64_t one2 = pair2(scale, scale);
   uint64_t s0 = 0, s1 = 0;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t pk[32];
+    uint64_t page2[4] = {one2, one2, one2, one2};
+    if constexpr (FP8) {
+      const float* sc = sc_all + 4 * h;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) page2[i] = pair2(sc[i], sc[i]);
+    }
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
+      const uint64_t sc2 = page2[(i >> 1) & 3];
       const uint32_t* x = &v[2 * h + (i >> 4)][2 * (i & 15)];
       float x0, x1;
       split2(fma2(pair2(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, ng2), x0, x1);
@@ -1090,6 +1090,166 @@ __device__ __noinline__ void start_line(const PrefillArgs& a, Line* line, long l
   }
 }
 
+// The 8-bit cache's producer warp `pw`: an item's key and value operands.  Key codes go straight
+// into their rows by 4-byte asynchronous copies, a tile ahead; registers hold the values' codes of
+// two pages, a tile ahead too, and there is no room for more (a spill is a round trip to L2, as
+// shared memory leaves L1 next to nothing), so everything else is read again from shared memory
+// or worked out where it is used.  it: stages and tiles before the item.
+// Measured, 4096 tokens at 32K: keys through registers too 1657 us (this 1620), keys and values
+// staged by bulk copies in shared memory 1940 and more (its bandwidth is what the products need).
+__device__ __forceinline__ bool fp8_produce(const PrefillArgs& a, const Item& w, uint8_t* smem, Look& look, int pw,
+                                            uint32_t it) {
+  const uint32_t sb = smem_u32(smem), bar = sb + Smem::kBar;
+  const int lane = threadIdx.x & 31;
+  const int tiles = w.tiles;
+  // lane l has page l % 8 of tile l / 8 of a block of four tiles: its id (-1: not there, or not
+  // seen by any row), of the tile's block and the next; likewise what its record says
+  auto block_ids = [&](int j0) {
+    const int j = j0 + (lane >> 3), p = w.tile<true>(j) * kTilePages + (lane & 7);
+    const int lo = a.window == 0 ? 0 : w.pos0 - a.window + 1;
+    int id = -1;
+    if (j < tiles && p * kPage < w.key_end && ((p + 1) * kPage > lo || p * kPage < a.sinks)) {
+      id = a.page_table[static_cast<size_t>(w.b) * a.max_pages + p];
+      if (id < 0 || id >= a.num_pool_pages) id = -2;          // bad
+    }
+    return id;
+  };
+  const uint8_t* pool = a.pool + static_cast<size_t>(w.kv) * kFp8Rec;
+  auto record = [&](int id) { return id < 0 ? nullptr : pool + static_cast<size_t>(id) * (a.Hkv * kFp8Rec); };
+  int ids0 = block_ids(0), ids1 = block_ids(4);
+  uint32_t meta0 = fp8_meta(record(ids0)), meta1 = 0;
+  auto pair_id = [&](int j, int y, bool next) {               // next: j is in the block behind
+    return __shfl_sync(0xffffffffu, next ? ids1 : ids0, 8 * (j & 3) + 2 * pw + y);
+  };
+  uint4 v[8];
+  // the pair's keys of tile j: word r of load i of the record's lane is token half r & 1, element
+  // half r >> 1 (pages that are not there: zeros)
+  const uint32_t krow = 64 * (pw >> 1) + 16 * (lane >> 3) + 8 * (pw & 1) + ((lane >> 2) & 1);
+  auto copy_k = [&](int j, bool next, uint32_t ks) {
+    const uint32_t base = ks + krow * 128 + (((2 * (lane & 3)) ^ ((lane >> 2) & 1)) << 4);
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const uint8_t* r = record(pair_id(j, y, next));
+      const uint32_t n = r ? 4u : 0u;
+      if (!r) r = a.pool;
+      r += 16 * lane;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint32_t ro = 4 * y + 2 * (g & 1);
+        const uint32_t to = (base ^ ((ro ^ (g >> 1)) << 4)) + ro * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + 4 * i), "l"(r + 512 * i + 4 * g),
+                       "r"(n)
+                       : "memory");
+      }
+    }
+  };
+  auto give_k = [&](uint32_t k) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async();
+    __syncwarp();
+    arrive_if(bar + 8 * (kKFull + k % kStages), lane == 0);
+  };
+  // what the softmax has to know of tile j: pages that are missing, the keys' scales
+  auto flags = [&](int j, bool next) {
+    const uint32_t k = it + j, slot = k % kFlags;
+    const uint32_t bad = (pair_id(j, 0, next) == -2 ? 0xffffu : 0u) | (pair_id(j, 1, next) == -2 ? 0xffff0000u : 0u);
+    if (lane == 0) {
+      reinterpret_cast<volatile uint32_t*>(smem + Smem::kBad)[4 * slot + pw] = bad;
+      reinterpret_cast<volatile uint8_t*>(smem + Smem::kAny)[4 * slot + pw] = bad != 0;
+      if (bad) atomicOr(a.status, KVQ_STATUS_BAD_PAGE);
+    }
+    if (pw == 0 && (lane >> 3) == (j & 3))
+      reinterpret_cast<volatile float*>(smem + Smem::kPageScale)[8 * slot + (lane & 7)] =
+          __uint_as_float(meta_k(next ? meta1 : meta0) << 23);
+  };
+  auto load_v = [&](int j, bool next) {
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const uint8_t* r = record(pair_id(j, y, next));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[4 * y + i] = r ? *reinterpret_cast<const uint4*>(r + 2048 + 512 * i + 16 * lane) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto wait_empty = [&](int empty, uint32_t k) {
+    if (warp_wait(bar + 8 * (empty + k % kStages), ((k / kStages) & 1) ^ 1)) return true;
+    asm volatile("cp.async.wait_all;" ::: "memory");       // nothing may be under way when the CTA leaves
+    return false;
+  };
+  load_v(0, false);
+  load_q<false, true>(a, w, smem);
+  sync_cta();                   // Q is there
+  if (tiles > 0) {
+    if (!wait_empty(kKEmpty, it)) return false;
+    flags(0, false);
+    copy_k(0, false, sb + Smem::kK + (it % kStages) * (kTileBytes / 2));
+    give_k(it);
+  }
+#pragma unroll 1
+  for (int j = 0; j < tiles; ++j) {
+    if (j > 0 && (j & 3) == 0) {
+      ids0 = ids1;
+      meta0 = meta1;
+      ids1 = block_ids(j + 4);
+    }
+    if ((j & 3) == 1) meta1 = fp8_meta(record(ids1));
+    const uint32_t k = it + j;
+    if (j + 1 < tiles) {
+      if (!wait_empty(kKEmpty, k + 1)) return false;
+      flags(j + 1, (j & 3) == 3);
+      copy_k(j + 1, (j & 3) == 3, sb + Smem::kK + ((k + 1) % kStages) * (kTileBytes / 2));
+    }
+    if (!wait_empty(kVEmpty, k)) return false;
+    const uint32_t row = value_base(sb + Smem::kV + (k % kStages) * kTileBytes, pw, lane);
+    const uint32_t m0 = __shfl_sync(0xffffffffu, meta0, 8 * (j & 3) + 2 * pw);
+    const uint32_t m1 = __shfl_sync(0xffffffffu, meta0, 8 * (j & 3) + 2 * pw + 1);
+    if (fp8_plain(m0) && fp8_plain(m1)) {
+      fp8_store_v(v, fp8_factor(m0), fp8_factor(m1), row);
+    } else {
+      // any scales and codes: from the records, through fp32, a word at a time; a value that is not
+      // finite is stored as zero and noted
+      uint32_t poison = 0;
+      const uint8_t *r0 = record(pair_id(j, 0, false)), *r1 = record(pair_id(j, 1, false));
+#pragma unroll 1
+      for (int i = 0; i < 16; ++i) {
+        uint32_t e[4];
+#pragma unroll
+        for (int pi = 0; pi < 2; ++pi) {
+          const uint8_t* r = pi ? r1 : r0;
+          uint32_t c = 0;
+          float s = 0.0f;
+          if (r) {
+            c = *reinterpret_cast<const uint32_t*>(r + 2048 + 512 * (i >> 2) + 16 * lane + 4 * (i & 3));
+            s = *reinterpret_cast<const float*>(r + 4100);
+          }
+          const uint32_t lo = fp8_lo(c), hi = fp8_hi(c);
+          e[2 * pi] = pack_bf162(half_lo(lo) * s, half_hi(lo) * s);
+          e[2 * pi + 1] = pack_bf162(half_lo(hi) * s, half_hi(hi) * s);
+          poison |= bf16_clean(e[2 * pi]) << (16 * pi + 2 * (lane & 3));
+          poison |= bf16_clean(e[2 * pi + 1]) << (16 * pi + 8 + 2 * (lane & 3));
+        }
+        sts128(row + (32 * (i >> 2) + 8 * (i & 3)) * 128, e[0], e[1], e[2], e[3]);
+      }
+#pragma unroll 1
+      for (; poison != 0; poison &= poison - 1) {
+        const int p = (w.tile<true>(j) * kTilePages + 2 * pw) * kPage + __ffs(poison) - 1;
+        if (p >= w.key_end) continue;
+        atomicMin(&look.first, static_cast<uint32_t>(p));
+        if (p < w.pos0) atomicMax(&look.before, static_cast<uint32_t>(p) + 1);
+        else atomicOr(&look.rows[(p - w.pos0) >> 5], 1u << ((p - w.pos0) & 31));
+      }
+    }
+    load_v(j + 1, (j & 3) == 3);
+    fence_proxy_async();
+    __syncwarp();
+    arrive_if(bar + 8 * (kVFull + k % kStages), lane == 0);
+    if (j + 1 < tiles) give_k(k + 1);
+  }
+  return true;
+}
+
 template <bool INT2, bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -1144,7 +1304,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 
   if (warp < kProdWarp0) {
     // ======================= softmax: a thread a row =======================
-    reg_set<Regs<INT2>::kSoftmax>();
+    reg_set<Regs<INT2, FP8>::kSoftmax>();
     const int t = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
@@ -1165,9 +1325,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const bool valid = row < rows, some = (row & ~31) < rows;
       const int first = st.split ? t : 0, step = st.split ? 2 : 1;    // this group's key tiles
       float mref = -INFINITY, l = 0.0f, scale = a.log2_scale;
-      // (a row of zeros: 0 * -inf would be NaN)
-      if constexpr (FP8)
-        scale = fmaxf(scale * reinterpret_cast<const float*>(smem + Smem::kQScale)[row], 1.17549435e-38f);
+      if constexpr (FP8) scale *= reinterpret_cast<const float*>(smem + Smem::kQScale)[row];
       auto wait_s = [&]() {
         alive = warp_wait(B(kSFull + t), ns & 1);
         ++ns;
@@ -1228,12 +1386,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           // the tile's missing pages, written before its operands were handed over; the slot
           // is written again four tiles later, which weights of two tiles later precede
           const uint32_t f = (itf + j) % kFlags;
-          float sc = scale;
-          if constexpr (FP8)
-            sc = fminf(fmaxf(scale * reinterpret_cast<const volatile float*>(smem + Smem::kTileExp)[f], 1.17549435e-38f),
-                       1.7014118e38f);
           if (some)
-            softmax_tile<INT2, FP8>(ts, to, sc, j == first, limit, low, lead, edge, anyw[f], badw + 4 * f, mref, l);
+            softmax_tile<INT2, FP8>(ts, to, scale, j == first, limit, low, lead,
+                                    reinterpret_cast<const float*>(smem + Smem::kPageScale) + 8 * f, edge, anyw[f], badw + 4 * f, mref, l);
           give();
         }
         // O is complete.  A row sees all positions up to its own, so it sees a NaN or an
@@ -1371,16 +1526,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
   } else if (warp < kMmaWarp) {
     // ======================= producers =======================
-    reg_set<Regs<INT2>::kProducer>();
+    reg_set<Regs<INT2, FP8>::kProducer>();
     const int pw = warp - kProdWarp0;
-    uint32_t copy_k = 0, copy_v = 0;       // stages of the last bulk copies
-    for (uint32_t i = 0;; ++i) {
+    uint32_t stage_k = 0, stage_v = 0;     // stages of the last bulk copies
+    if constexpr (FP8) {
+      for (uint32_t i = 0;; ++i) {
+        sync_cta();
+        const Item& w = items[i & 1];
+        if (w.done) break;
+        alive = fp8_produce(a, w, smem, looks[i & 1], pw, itk);
+        itk += w.tiles;
+        if (!item_end(alive, a, abort)) break;
+      }
+    } else for (uint32_t i = 0;; ++i) {
       sync_cta();
       const Item w = items[i & 1];
       if (w.done) break;
       const Steps<INT2> st(w, a);
-      const Pages<INT2, FP8> pages(a, w);
-      auto first = [&](int j) { return w.tile<FP8>(j) * kTilePages + 2 * pw; };   // tile j's pair: this page and the next
+      const Pages<INT2> pages(a, w);
+      const int first = w.tile_begin * kTilePages + 2 * pw;       // the pair: first + 8 j, + 1
       auto wait_empty = [&](int empty, uint32_t k) {
         alive = alive && warp_wait(B(empty + k % kStages), ((k / kStages) & 1) ^ 1);
         return alive;
@@ -1413,43 +1577,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (st.pre && wait_empty(kKEmpty, itk) && wait_empty(kVEmpty, itv)) {
         give_copy(kKFull, itk, kbuf(itk), a.rk_hi + mat);
         give_copy(kVFull, itv, vbuf(itv), a.rk_lo + mat);
-        copy_k = itk;
-        copy_v = itv;
+        stage_k = itk;
+        stage_v = itv;
       }
       int id[2];
-      [[maybe_unused]] int tid8 = -1;
       uint4 x[8];
       auto records = [&](int j) {
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           rec[y] = pages.record(id[y]);
-          id[y] = pages.id(first(j + 1) + y, j + 1 < st.tiles);
+          id[y] = pages.id(first + kTilePages * (j + 1) + y, j + 1 < st.tiles);
         }
       };
-      // 8-bit cache: lane l < 8 has the id of the page l of the tile that is loaded next
-      [[maybe_unused]] Fp8Meta meta;
-      auto tile_id = [&](int j) {
-        return pages.id(w.tile<FP8>(j) * kTilePages + lane, lane < kTilePages && j < st.tiles);
-      };
-      auto tile_records = [&](int j) {      // the pair's records and the lane's page's meta of tile j
-        meta = fp8_meta(pages.record(tid8));
-        rec[0] = pages.record(__shfl_sync(0xffffffffu, tid8, 2 * pw));
-        rec[1] = pages.record(__shfl_sync(0xffffffffu, tid8, 2 * pw + 1));
-        tid8 = tile_id(j + 1);
-      };
-      if constexpr (FP8) {
-        tid8 = tile_id(0);
-        tile_records(0);
-      } else {
 #pragma unroll
-        for (int y = 0; y < 2; ++y) id[y] = pages.id(first(0) + y, st.tiles > 0);
-        records(0);
-      }
+      for (int y = 0; y < 2; ++y) id[y] = pages.id(first + y, st.tiles > 0);
+      records(0);
       if constexpr (INT2) {
 #pragma unroll
         for (int y = 0; y < 2; ++y) int2_load(raw, y, rec[y], lane);
-      } else if constexpr (FP8) {
-        fp8_load_half(x, rec, 0, lane);
       } else {
         bf16_load_key(x, rec[0], lane);
       }
@@ -1458,7 +1603,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       for (int j = 0; j < st.tiles && alive; ++j) {
         const uint32_t k = itk + st.pre + j, kv = itv + st.pre + j;
         const uint32_t f = itf + j, slot = f % kFlags;
-        const int p0 = first(j) * kPage;
+        const int p0 = (first + kTilePages * j) * kPage;
         uint32_t bad = 0, poison;
         auto key_flags = [&]() {
           if (lane == 0) {
@@ -1469,7 +1614,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         };
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-          if (!rec[y] && (FP8 ? pages.seen(first(j) + y) : p0 + kPage * y < w.key_end)) bad |= 0xffffu << (16 * y);
+          if (!rec[y] && p0 + kPage * y < w.key_end) bad |= 0xffffu << (16 * y);
         if (!wait_empty(kKEmpty, k)) break;
         key_flags();
         if constexpr (INT2) {
@@ -1485,45 +1630,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           for (int y = 0; y < 2; ++y) int2_load(raw, y, rec[y], lane);
           if (!wait_empty(kVEmpty, kv)) break;
           poison = int2_store_v(now, vbuf(kv), pw, lane);
-        } else if constexpr (FP8) {
-          uint4 values[8];
-          fp8_load_half(values, rec, 2048, lane);
-          const uint8_t* const old[2] = {rec[0], rec[1]};
-          // exponent of the lane's page and the tile's largest (a page that is not there: -127)
-          const int e = static_cast<int>(meta.scale_k >> 23) - 127;
-          const int top = __reduce_max_sync(0xffffffffu, lane < kTilePages ? e : -127);
-          uint32_t fk[2], fv[2];
-          bool plain = true;
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            fk[y] = half_pow2(top - __shfl_sync(0xffffffffu, e, 2 * pw + y));
-            const uint32_t s = __shfl_sync(0xffffffffu, meta.scale_v, 2 * pw + y);
-            plain = plain && fp8_plain(s, __shfl_sync(0xffffffffu, meta.flags, 2 * pw + y));
-            fv[y] = fp8_factor(s);
-          }
-          if (pw == 0 && lane == 0)
-            reinterpret_cast<volatile float*>(smem + Smem::kTileExp)[slot] =
-                __int_as_float((min(max(top, -126), 127) + 127) << 23);
-          fp8_store_k(x, fk, key_base(kbuf(k), pw, lane));
-          give(kKFull, k);
-          tile_records(j + 1);
-          fp8_load_half(x, rec, 0, lane);
-          if (!wait_empty(kVEmpty, kv)) break;
-          poison = 0;
-          const uint32_t row = value_base(vbuf(kv), pw, lane);
-          if (plain) fp8_store_v(values, fv, row);
-          else poison = fp8_store_v_any(old[0], old[1], row, lane);
-          if (poison) {
-            Look& look = looks[i & 1];
-            for (uint32_t m = poison; m != 0; m &= m - 1) {
-              const int p = p0 + __ffs(m) - 1;
-              if (p >= w.key_end) continue;
-              atomicMin(&look.first, static_cast<uint32_t>(p));
-              if (p < w.pos0) atomicMax(&look.before, static_cast<uint32_t>(p) + 1);
-              else atomicOr(&look.rows[(p - w.pos0) >> 5], 1u << ((p - w.pos0) & 31));
-            }
-            poison = 0;
-          }
         } else {
           uint4 ahead[8];
           bf16_load_key(ahead, rec[1], lane);
@@ -1545,7 +1651,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (st.post && alive && wait_empty(kKEmpty, itk + st.pre + st.tiles)) {
         const uint32_t k = itk + st.pre + st.tiles;
         give_copy(kKFull, k, kbuf(k), a.rv_tile + mat);
-        copy_k = k;
+        stage_k = k;
       }
       itk += st.keys();
       itv += st.values();
@@ -1554,12 +1660,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
     // after a wait gave up: a copy may still be under way that nobody waited for
     if (INT2 && *abort) {
-      (void)warp_wait(B(kKFull + copy_k % kStages), (copy_k / kStages) & 1);
-      (void)warp_wait(B(kVFull + copy_v % kStages), (copy_v / kStages) & 1);
+      (void)warp_wait(B(kKFull + stage_k % kStages), (stage_k / kStages) & 1);
+      (void)warp_wait(B(kVFull + stage_v % kStages), (stage_v / kStages) & 1);
     }
   } else {
     // ======================= tensor-core issue, schedule =======================
-    reg_set<Regs<INT2>::kIssue>();
+    reg_set<Regs<INT2, FP8>::kIssue>();
     uint32_t np0 = 0, np1 = 0;      // P_full phases
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), one = elect_one();
     if (warp == kSchedWarp && lane == 0) {
@@ -1567,11 +1673,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       next_item<FP8>(a, *line, items[0]);
     }
     __syncwarp();
+    auto work = [&](auto issue, auto schedule) {
     for (uint32_t i = 0;; ++i) {
       sync_cta();
       const Item w = items[i & 1];
       if (w.done) break;
-      if (warp == kSchedWarp && lane == 0) {
+      if (schedule.value && warp == kSchedWarp && lane == 0) {
         first_bad[(i + 1) & 1] = 0xffffffffu;
         if constexpr (FP8) looks[(i + 1) & 1] = Look{0xffffffffu, 0u, {}};
         next_item<FP8>(a, *line, items[(i + 1) & 1]);
@@ -1579,9 +1686,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       __syncwarp();
       const Steps<INT2> st(w, a);
       sync_cta();                   // Q is there
-      if (warp == kMmaWarp && st.tiles > 0) {
-        constexpr uint32_t idesc = idesc_f16(INT2 || FP8 ? 0 : 1), idesc_bf = idesc_f16(1);   // scores, q R_K
-        constexpr uint32_t idesc_v = idesc_f16(INT2 ? 0 : 1);
+      if (issue.value && warp == kMmaWarp && st.tiles > 0) {
+        constexpr uint32_t idesc = idesc_f16(INT2 ? 0 : 1), idesc_bf = idesc_f16(1);
         const bool both = __shfl_sync(0xffffffffu, st.split ? 0 : 1, 0) != 0;
         const int tiles = __shfl_sync(0xffffffffu, st.tiles, 0);
         auto full = [&](int bar, uint32_t k) {
@@ -1606,16 +1712,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         // S_t = Q_t X^T, X a stage's K (or V) operand
         auto product = [&](int t, uint32_t x, uint32_t id, bool add) {
           const uint32_t q = tile_desc(sb + Smem::kQ + (both ? t : 0) * kTileBytes);
+          if constexpr (FP8) {      // the query's two parts, 32 columns a step
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc_mma_ss(tm + t * 128, q + desc_step(k), x + desc_step(k), id, add || k != 0, one);
+            for (int k = 0; k < 8; ++k)
+              tc_mma_ss_f8(tm + t * 128, q + (k >> 2) * (kTileBytes / 2 >> 4) + 2 * (k & 3), x + 2 * (k & 3),
+                           idesc_f16(0), k != 0, one);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              tc_mma_ss(tm + t * 128, q + desc_step(k), x + desc_step(k), id, add || k != 0, one);
+          }
         };
-        auto kdesc = [&](uint32_t k) { return tile_desc(sb + Smem::kK + (k % kStages) * kTileBytes); };
+        auto kdesc = [&](uint32_t k) {
+          return tile_desc(sb + Smem::kK + (k % kStages) * (FP8 ? kTileBytes / 2 : kTileBytes));
+        };
         auto vdesc = [&](uint32_t k) { return tile_desc(sb + Smem::kV + (k % kStages) * kTileBytes); };
         auto weighted = [&](int t, uint32_t v, bool add) {     // O_t += P_t V
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            tc_mma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * k, v + desc_step(k), idesc_v,
+            tc_mma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * k, v + desc_step(k), idesc,
                       add || k != 0, one);
         };
         uint32_t k = __shfl_sync(0xffffffffu, itk, 0), v = __shfl_sync(0xffffffffu, itv, 0);
@@ -1674,6 +1789,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       itv += st.values();
       itf += st.tiles;
       if (!item_end(alive, a, abort)) break;
+    }
+    };
+    // apart where registers are short (8-bit cache): the scheduler's call would keep the issuing
+    // warp's in memory
+    if constexpr (FP8) {
+      if (warp == kMmaWarp) work(std::true_type(), std::false_type());
+      else work(std::false_type(), std::true_type());
+    } else {
+      work(std::true_type(), std::true_type());
     }
   }
 
@@ -1827,12 +1951,14 @@ __global__ void __launch_bounds__(128) prefill_combine_kernel(const __grid_const
 
 template <bool INT2, bool FP8 = false>
 cudaError_t launch(const PrefillArgs& a, int num_sms, cudaStream_t st) {
+  constexpr int kSmem = Smem::kAlloc;
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
   static bool attr_set[64] = {};       // per device: the attributes are per context
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
     cudaError_t e = cudaFuncSetAttribute(prefill_kernel<INT2, FP8>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::kAlloc);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, prefill_kernel<INT2, FP8>);
@@ -1841,7 +1967,7 @@ cudaError_t launch(const PrefillArgs& a, int num_sms, cudaStream_t st) {
     if (fa.numRegs != kRegLaunch) return cudaErrorInvalidConfiguration;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  prefill_kernel<INT2, FP8><<<num_sms, kThreads, Smem::kAlloc, st>>>(a);
+  prefill_kernel<INT2, FP8><<<num_sms, kThreads, kSmem, st>>>(a);
   if (num_sms > 1) {
     // a programmatic dependent: it is launched while the first kernel ends
     cudaLaunchConfig_t cfg = {};

@@ -158,6 +158,51 @@ def test_several_nan_values_and_keys():
         assert torch.equal(torch.isnan(out[:, 1]).all(1), bad1) and torch.equal(torch.isnan(out[:, 1]).any(1), bad1)
 
 
+@pytest.mark.parametrize("n", [9, 200])
+def test_nonfinite_queries(n):
+    """A query with a NaN or an infinity spoils its own row and head, and no other."""
+    c = Cache8(4, 2, [300])
+    q = c.randn(n, 4)
+    want = c.prefill(q, [n])
+    q[3, 1, 5], q[n - 1, 2, 77] = float("nan"), float("inf")
+    out = c.prefill(q, [n])
+    bad = torch.zeros(n, 4, dtype=torch.bool, device="cuda")
+    bad[3, 1] = bad[n - 1, 2] = True
+    assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], want[~bad])
+
+
+def test_queries_of_uneven_elements():
+    """One element far larger than the others, against keys that cancel it: what the query's 8-bit
+    parts keep of the small ones (2^-18 of the largest) enters the scores."""
+    c = Cache8(2, 1, [256], seed=14, fill=False)
+    c.k[:, :, 0] = 0
+    c.append(c.k, c.v, [256])
+    for big in (16.0, 256.0):
+        q = c.randn(130, 2)
+        q[:, :, 0] = big
+        out = c.prefill(q, [130])
+        # a score moves by at most scale * 2^-18 big sum |k_d|, its weight by that factor, twice
+        k = c.entries(0)[0].abs().sum(-1).max()
+        extra = 2 * 2.0 ** -18 * 2 * big * float(k) / math.sqrt(D)
+        keys, vals = c.entries(0)
+        mask = seen(256, 130, 0, 0)
+        for h in range(2):
+            o, mag, _ = attend(q[:, h].double(), keys[0], vals[0], mask)
+            err = (out[:, h].double() - o).norm(dim=1)
+            assert torch.all(err <= 2.0 ** -8 * o.norm(dim=1) + (2.0 ** -8 + 2.0 ** -11 + extra) * mag.norm(dim=1))
+
+
+def test_pages_of_very_different_keys():
+    """Keys of one page 2^20 times those of the next, in one tile: each page's scale is its own."""
+    c = Cache8(2, 1, [400], seed=15, fill=False)
+    size = torch.tensor([2.0 ** (20 * (i // 16 % 2) - 20) for i in range(400)], device="cuda")[:, None, None]
+    c.k = (c.k.float() * size * 3).bfloat16()
+    c.append(c.k, c.v, [400])
+    q = c.randn(300, 2)
+    check(c, c.prefill(q, [300]), q, [300])
+    check(c, c.prefill(q, [300], 60, 3), q, [300], 60, 3)
+
+
 def test_behind_the_end():
     """A shorter length: what lies behind it in the last page, NaN or not, is not seen."""
     c = Cache8(4, 2, [90], seed=8, fill=False)
