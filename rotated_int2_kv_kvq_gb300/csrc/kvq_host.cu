@@ -530,7 +530,7 @@ bool norm_rows(kvq::NormRows* r, const uint16_t* x, long long x_stride, bool bac
 
 size_t norm_backward_bytes(const kvq_handle* h, int n) {
   if (!h || n < 0) return 0;
-  return static_cast<size_t>(2) * kvq::norm_backward_parts(n, h->num_sms) * kDim * sizeof(float);
+  return static_cast<size_t>(kvq::norm_backward_ctas(h->num_sms)) * kDim * sizeof(float);
 }
 
 // Each pair's turns per position as a 64-bit fraction, from the base and the
@@ -878,7 +878,7 @@ int kvq_norm_rope(kvq_handle* h, const uint16_t* q, long long q_stride, const ui
   a.n = n;
   a.eps = eps;
   a.status = h->status;
-  return cuda_rc(kvq::launch_norm_rope(a, S(stream)));
+  return cuda_rc(kvq::launch_norm_rope(a, h->num_sms, S(stream)));
 }
 
 size_t kvq_norm_rope_backward_workspace_bytes(const kvq_handle* h, int n) { return norm_backward_bytes(h, n); }

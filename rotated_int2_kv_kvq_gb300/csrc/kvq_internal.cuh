@@ -181,11 +181,12 @@ struct NormArgs {
   RopeArgs rope;
   float eps;
   uint32_t* status;
-  float* part = nullptr;         // backward: [2][CTAs][128]
+  float* part = nullptr;         // backward: [CTAs][128]
+  int q_ctas = 0;                // backward: the CTAs of the queries, before those of the keys
 };
-int norm_backward_parts(int n, int num_sms);
-cudaError_t launch_norm_rope(const NormArgs& a, cudaStream_t st);
-cudaError_t launch_norm_rope_backward(const NormArgs& a, int num_sms, cudaStream_t st);
+int norm_backward_ctas(int num_sms);      // at most
+cudaError_t launch_norm_rope(const NormArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_norm_rope_backward(NormArgs a, int num_sms, cudaStream_t st);
 
 // One kvq_fp8_append / kvq_fp8_read call: row i of sequence b is position
 // seq_lens[b] - cu[b + 1] + i.

@@ -7,33 +7,36 @@
 //   dx = r (g - xh mean_d(g_d xh_d)),   dw_d = sum over rows of dn_d xh_d.
 // Everything is fp32 between the bf16 loads and the one rounding of y or dx.
 //
-// A row (token, head) is worked on by 8 lanes, 16 elements each, so that a pair of the
-// rotation is in one lane and the sums over a row are three shuffles.
+// A row (token, head) is worked on by 8 lanes, 16 elements each (backward: 16 lanes of 8), so that
+// a pair of the rotation is in one lane and the sums over a row are a few shuffles.
+#include <type_traits>
+
 #include "kvq_internal.cuh"
 
 namespace kvq {
 namespace {
 
-// How a lane's 16 elements lie in the row:
-//   kHalfVec  : 8 of the first half of the rotated part and their 8 partners, or 16 behind it;
-//   kInterVec : 8 elements (four pairs) in each half of the head;
-//   kScalar   : eight pairs of the rotated part or behind it (any even rot_dim).
+// How a lane's E elements (16, 8 lanes a row, or 8, 16 lanes a row) lie in the row, U = E / 2:
+//   kHalfVec  : U of the first half of the rotated part and their U partners, or E behind it;
+//   kInterVec : U elements (U / 2 pairs) in each half of the head;
+//   kScalar   : U pairs of the rotated part or behind it (any even rot_dim).
 enum NormMode { kHalfVec, kInterVec, kScalar };
 
-template <int MODE>
+template <int MODE, int E>
 struct Lane {
-  int u;             // lane of the row, 0 .. 7
-  int at0, at1;      // first elements of the two 8-element units (vector forms)
-  __device__ __forceinline__ Lane(int lane, const RopeArgs& r) : u(lane & 7), at0(8 * u), at1(64 + 8 * u) {
+  static constexpr int U = E / 2, kLanes = kDim / E;
+  int u;             // lane of the row
+  int at0, at1;      // first elements of the two units (vector forms)
+  __device__ __forceinline__ Lane(int lane, const RopeArgs& r) : u(lane % kLanes), at0(U * u), at1(64 + U * u) {
     if (MODE == kHalfVec) {
-      const int turned = r.rot_dim >> 4;
-      at0 = u < turned ? 8 * u : r.rot_dim + 16 * (u - turned);
-      at1 = u < turned ? (r.rot_dim >> 1) + 8 * u : at0 + 8;
+      const int turned = r.rot_dim / E;
+      at0 = u < turned ? U * u : r.rot_dim + E * (u - turned);
+      at1 = u < turned ? (r.rot_dim >> 1) + U * u : at0 + U;
     }
   }
-  // first and second element of pair i of the lane's eight (kScalar)
+  // first and second element of pair i of the lane's U (kScalar)
   __device__ __forceinline__ void pair(int i, const RopeArgs& r, int& d0, int& d1) const {
-    const int j = u + 8 * i, half = r.rot_dim >> 1;
+    const int j = u + kLanes * i, half = r.rot_dim >> 1;
     const bool inter = r.style == KVQ_ROPE_INTERLEAVED, turned = j < half;
     d0 = !turned ? r.rot_dim + 2 * (j - half) : inter ? 2 * j : j;
     d1 = turned && !inter ? j + half : d0 + 1;
@@ -45,17 +48,26 @@ struct Lane {
       pair(e >> 1, r, d0, d1);
       return (e & 1) ? d1 : d0;
     } else {
-      return e < 8 ? at0 + e : at1 + e - 8;
+      return e < U ? at0 + e : at1 + e - U;
     }
   }
-  // cos and sin of the lane's eight pairs; 1 and 0 where nothing turns
-  __device__ __forceinline__ void angles(float (&c)[8], float (&s)[8], const float* row, float sign,
+  // cos and sin of the lane's U pairs; 1 and 0 where nothing turns
+  __device__ __forceinline__ void angles(float (&c)[U], float (&s)[U], const float* row, float sign,
                                          const RopeArgs& r) const {
     const int half = r.rot_dim >> 1;
-    auto four = [&](int k, int i, bool on) {
+    // two pairs at a time: half is even in the vector forms
+    auto two = [&](int k, int i, bool on) {
+      float2 x = make_float2(1.f, 1.f), y = make_float2(0.f, 0.f);
+      if (on) {
+        x = *reinterpret_cast<const float2*>(row + i);
+        y = *reinterpret_cast<const float2*>(row + half + i);
+      }
+      c[k] = x.x, c[k + 1] = x.y;
+      s[k] = sign * y.x, s[k + 1] = sign * y.y;
+    };
+    auto four = [&](int k, int i, bool on) {      // half is a multiple of 4
       float4 x = make_float4(1.f, 1.f, 1.f, 1.f), y = make_float4(0.f, 0.f, 0.f, 0.f);
       if (on) {
-        // half is a multiple of 4 in the vector forms
         x = *reinterpret_cast<const float4*>(row + i);
         y = *reinterpret_cast<const float4*>(row + half + i);
       }
@@ -63,16 +75,18 @@ struct Lane {
       s[k] = sign * y.x, s[k + 1] = sign * y.y, s[k + 2] = sign * y.z, s[k + 3] = sign * y.w;
     };
     if constexpr (MODE == kHalfVec) {
-      const bool on = u < (r.rot_dim >> 4);
-      four(0, 8 * u, on);
-      four(4, 8 * u + 4, on);
-    } else if constexpr (MODE == kInterVec) {
+#pragma unroll
+      for (int k = 0; k < U; k += 4) four(k, U * u + k, u < r.rot_dim / E);
+    } else if constexpr (MODE == kInterVec && E == 16) {
       four(0, 4 * u, at0 < r.rot_dim);
       four(4, 32 + 4 * u, at1 < r.rot_dim);
+    } else if constexpr (MODE == kInterVec) {
+      two(0, 2 * u, at0 < r.rot_dim);
+      two(2, 32 + 2 * u, at1 < r.rot_dim);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int j = u + 8 * i;
+      for (int i = 0; i < U; ++i) {
+        const int j = u + kLanes * i;
         c[i] = j < half ? row[j] : 1.0f;
         s[i] = j < half ? sign * row[half + j] : 0.0f;
       }
@@ -80,98 +94,114 @@ struct Lane {
   }
 };
 
-// The raw bf16 elements of a lane: 8 words, words 0-3 and 4-7 its two units (vector forms),
-// word i its pair i (kScalar).
-template <int MODE>
-__device__ __forceinline__ void load_raw(uint32_t (&w)[8], const uint16_t* row, const Lane<MODE>& l,
+// The raw bf16 elements of a lane: U words, the first and second half its two units (vector
+// forms), word i its pair i (kScalar).
+template <int MODE, int E>
+__device__ __forceinline__ void load_raw(uint32_t (&w)[E / 2], const uint16_t* row, const Lane<MODE, E>& l,
                                          const RopeArgs& r) {
   if constexpr (MODE == kScalar) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < E / 2; ++i) {
       int d0, d1;
       l.pair(i, r, d0, d1);
       w[i] = row[d0] | static_cast<uint32_t>(row[d1]) << 16;
     }
-  } else {
+  } else if constexpr (E == 16) {
     const uint4 a = *reinterpret_cast<const uint4*>(row + l.at0);
     const uint4 b = *reinterpret_cast<const uint4*>(row + l.at1);
     w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
     w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  } else {
+    const uint2 a = *reinterpret_cast<const uint2*>(row + l.at0);
+    const uint2 b = *reinterpret_cast<const uint2*>(row + l.at1);
+    w[0] = a.x, w[1] = a.y, w[2] = b.x, w[3] = b.y;
   }
 }
-__device__ __forceinline__ void unpack(float (&v)[16], const uint32_t (&w)[8]) {
+template <int E>
+__device__ __forceinline__ void unpack(float (&v)[E], const uint32_t (&w)[E / 2]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < E / 2; ++i) {
     v[2 * i] = __uint_as_float(w[i] << 16);
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-template <int MODE>
-__device__ __forceinline__ void store_row(uint16_t* row, const float (&v)[16], const Lane<MODE>& l,
+template <int MODE, int E>
+__device__ __forceinline__ void store_row(uint16_t* row, const float (&v)[E], const Lane<MODE, E>& l,
                                           const RopeArgs& r) {
-  uint32_t w[8];
+  uint32_t w[E / 2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = pack_bf162(v[2 * i], v[2 * i + 1]);
+  for (int i = 0; i < E / 2; ++i) w[i] = pack_bf162(v[2 * i], v[2 * i + 1]);
   if constexpr (MODE == kScalar) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < E / 2; ++i) {
       int d0, d1;
       l.pair(i, r, d0, d1);
       row[d0] = static_cast<uint16_t>(w[i]);
       row[d1] = static_cast<uint16_t>(w[i] >> 16);
     }
-  } else {
+  } else if constexpr (E == 16) {
     *reinterpret_cast<uint4*>(row + l.at0) = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint4*>(row + l.at1) = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+    *reinterpret_cast<uint2*>(row + l.at0) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(row + l.at1) = make_uint2(w[2], w[3]);
   }
 }
 
 // v's pairs turned by (c, s).
-template <int MODE>
-__device__ __forceinline__ void turn(float (&v)[16], const float (&c)[8], const float (&s)[8]) {
+template <int MODE, int E>
+__device__ __forceinline__ void turn(float (&v)[E], const float (&c)[E / 2], const float (&s)[E / 2]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int a = MODE == kHalfVec ? i : 2 * i, b = MODE == kHalfVec ? 8 + i : 2 * i + 1;
+  for (int i = 0; i < E / 2; ++i) {
+    const int a = MODE == kHalfVec ? i : 2 * i, b = MODE == kHalfVec ? E / 2 + i : 2 * i + 1;
     const float x = v[a], y = v[b];
     v[a] = x * c[i] - y * s[i];
     v[b] = y * c[i] + x * s[i];
   }
 }
 
-__device__ __forceinline__ float sum8(float x) {      // over the 8 lanes of a row
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  x += __shfl_xor_sync(0xffffffffu, x, 2);
-  return x + __shfl_xor_sync(0xffffffffu, x, 4);
+template <int LANES>
+__device__ __forceinline__ float sum_row(float x) {      // over the lanes of a row
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
 }
 
-template <int MODE>
-__device__ __forceinline__ void load_weight(float (&w)[16], const float* weight, const Lane<MODE>& l,
+template <int MODE, int E>
+__device__ __forceinline__ void load_weight(float (&w)[E], const float* weight, const Lane<MODE, E>& l,
                                             const RopeArgs& r) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e) w[e] = weight ? weight[l.dim(e, r)] : 1.0f;
+  for (int e = 0; e < E; ++e) w[e] = weight ? weight[l.dim(e, r)] : 1.0f;
 }
 
 // ---- forward ---------------------------------------------------------------------------
-// A warp takes one token's queries or keys, kHeads at a time a row group: the token's angles
-// and the weight are in registers for all of them.
+// A warp takes 4 ROWS heads of one token, queries or keys: the token's angles and the weight are
+// in registers for all of them, and the elements are asked for before the position, so that its two
+// dependent loads (position, table row) overlap them.
 constexpr int kFwdThreads = 128;
 
-template <int MODE>
-__global__ void __launch_bounds__(kFwdThreads) norm_rope_kernel(const __grid_constant__ NormArgs a, int rows) {
+template <int MODE, int ROWS>
+__global__ void __launch_bounds__(kFwdThreads) norm_rope_kernel(const __grid_constant__ NormArgs a) {
   const int lane = threadIdx.x & 31;
+  // tasks of a token: blockIdx.y the runs of 4 ROWS query heads, then of key heads
   const long long task = static_cast<long long>(blockIdx.x) * (kFwdThreads / 32) + (threadIdx.x >> 5);
-  // tasks of a token: runs of 4 * rows query heads, then of key heads
-  const int per = 4 * rows, nq = a.q.x ? (a.q.heads + per - 1) / per : 0,
-            nk = a.k.x ? (a.k.heads + per - 1) / per : 0;
-  const int tok = static_cast<int>(task / (nq + nk)), part = static_cast<int>(task % (nq + nk));
-  if (tok >= a.n) return;
+  if (task >= a.n) return;
+  const int tok = static_cast<int>(task);
+  constexpr int kPer = 4 * ROWS;
+  const int nq = a.q.x ? (a.q.heads + kPer - 1) / kPer : 0, part = blockIdx.y;
   const bool is_q = part < nq;
   const NormRows& x = is_q ? a.q : a.k;
-  const int first = (is_q ? part : part - nq) * per + (lane >> 3);
+  const int first = (is_q ? part : part - nq) * kPer + (lane >> 3);
   const uint16_t* xr = x.x + static_cast<size_t>(tok) * x.x_stride;
   uint16_t* yr = x.y + static_cast<size_t>(tok) * x.y_stride;
-  const Lane<MODE> l(lane, a.rope);
+  const Lane<MODE, 16> l(lane, a.rope);
   const int pos = a.positions[tok];
+  uint32_t raw[ROWS][8];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int head = first + 4 * i;
+    load_raw(raw[i], xr + (head < x.heads ? head : 0) * kDim, l, a.rope);
+  }
   if (pos < 0 || pos >= a.rope.table_len) {
     if (lane == 0) atomicOr(a.status, KVQ_STATUS_BAD_POS);
     return;
@@ -179,106 +209,172 @@ __global__ void __launch_bounds__(kFwdThreads) norm_rope_kernel(const __grid_con
   float c[8], s[8], w[16];
   l.angles(c, s, a.rope.table + static_cast<size_t>(pos) * a.rope.rot_dim, 1.0f, a.rope);
   load_weight(w, x.weight, l, a.rope);
-  for (int i = 0; i < rows; ++i) {
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
     const int head = first + 4 * i;
-    const bool on = head < x.heads;
-    uint32_t raw[8];
-    load_raw(raw, xr + (on ? head : 0) * kDim, l, a.rope);
     float v[16];
-    unpack(v, raw);
+    unpack<16>(v, raw[i]);
     float ss = 0.0f;
 #pragma unroll
     for (int e = 0; e < 16; ++e) ss = fmaf(v[e], v[e], ss);
-    const float r = rsqrtf(sum8(ss) * (1.0f / kDim) + a.eps);
+    const float r = rsqrtf(sum_row<8>(ss) * (1.0f / kDim) + a.eps);
 #pragma unroll
     for (int e = 0; e < 16; ++e) v[e] = v[e] * r * w[e];
-    turn<MODE>(v, c, s);
-    if (on) store_row(yr + head * kDim, v, l, a.rope);
+    turn<MODE, 16>(v, c, s);
+    if (head < x.heads) store_row(yr + head * kDim, v, l, a.rope);
   }
 }
 
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+
 // ---- backward --------------------------------------------------------------------------
-// blockIdx.y: queries or keys.  Row groups stride over the rows (token, head); each lane keeps
-// its 16 elements' share of dw, summed over the CTA at the end and over the CTAs by a second
-// kernel, always in the same order.
+// The first a.q_ctas CTAs take the queries, the others the keys.  A row group takes a run of rows
+// (token, head), so that a token's angles serve several of them; each lane keeps its 16 elements'
+// share of dw, summed over the CTA at the end and over the CTAs by a second kernel, always in the
+// same order.  The elements of the next rows are under way into shared memory by asynchronous
+// copies (a lane reads back its own, so nothing is waited for but them); with the next row in
+// registers instead 4099 tokens of 40 heads took 32.2 us, not 29.0.  4 CTAs an SM spill (32.9),
+// 2 CTAs of 16 elements a lane are as fast.
 constexpr int kBwdThreads = 256;
+constexpr int kBwdE = 8;              // elements of a row a lane has
+constexpr int kAhead = 4;             // rows a lane has under way
+constexpr int kBwdCtas = 3;           // CTAs an SM
 
 template <int MODE>
-__global__ void __launch_bounds__(kBwdThreads) norm_rope_backward_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kBwdThreads, kBwdCtas) norm_rope_backward_kernel(const __grid_constant__ NormArgs a) {
+  extern __shared__ __align__(16) uint8_t ring_raw[];
   __shared__ float red[kBwdThreads / 32][kDim];
-  const bool is_q = blockIdx.y == 0;
+  const bool is_q = static_cast<int>(blockIdx.x) < a.q_ctas;
   const NormRows& x = is_q ? a.q : a.k;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Lane<MODE> l(lane, a.rope);
-  float w[16], dw[16];
+  const Lane<MODE, kBwdE> l(lane, a.rope);
+  constexpr int U = kBwdE / 2, kLanes = kDim / kBwdE, kRowsCta = kBwdThreads / kLanes;
+  using Unit = std::conditional_t<kBwdE == 16, uint4, uint2>;      // U elements
+  Unit* ring = reinterpret_cast<Unit*>(ring_raw);                  // [kAhead][4][kBwdThreads]
+  float w[kBwdE], dw[kBwdE], c[U], s[U];
   load_weight(w, x.weight, l, a.rope);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) dw[e] = 0.0f;
-  const long long rows = x.x ? static_cast<long long>(a.n) * x.heads : 0;
-  const long long step = static_cast<long long>(gridDim.x) * (kBwdThreads / 8);
-  const long long first = static_cast<long long>(blockIdx.x) * (kBwdThreads / 8) + (threadIdx.x >> 3);
-  for (long long base = first - (lane >> 3); base < rows; base += step) {     // uniform in the warp
-    const long long row = base + (lane >> 3);
-    const bool in = row < rows;
-    const int tok = in ? static_cast<int>(row / x.heads) : 0, head = in ? static_cast<int>(row % x.heads) : 0;
-    const int pos = a.positions[tok];
-    const bool good = pos >= 0 && pos < a.rope.table_len, on = in && good;
-    if (in && !good && l.u == 0) atomicOr(a.status, KVQ_STATUS_BAD_POS);
-    uint32_t rx[8], rd[8];
-    load_raw(rx, x.x + static_cast<size_t>(tok) * x.x_stride + head * kDim, l, a.rope);
-    load_raw(rd, x.dy + static_cast<size_t>(tok) * x.dy_stride + head * kDim, l, a.rope);
-    float c[8], s[8], v[16], d[16];
-    l.angles(c, s, a.rope.table + static_cast<size_t>(good ? pos : 0) * a.rope.rot_dim, -1.0f, a.rope);
-    unpack(v, rx);
-    unpack(d, rd);
-    turn<MODE>(d, c, s);
+  for (int e = 0; e < kBwdE; ++e) dw[e] = 0.0f;
+#pragma unroll
+  for (int e = 0; e < U; ++e) c[e] = s[e] = 0.0f;
+  const int ctas = is_q ? a.q_ctas : static_cast<int>(gridDim.x) - a.q_ctas;
+  const long long rows = static_cast<long long>(a.n) * x.heads;
+  const long long groups = static_cast<long long>(ctas) * kRowsCta;
+  const long long per = (rows + groups - 1) / groups;          // uniform: the loop's shuffles
+  const long long r0 = ((static_cast<long long>(blockIdx.x) - (is_q ? 0 : a.q_ctas)) * kRowsCta +
+                        threadIdx.x / kLanes) * per;
+  const int mine = static_cast<int>(max(0ll, min(per, rows - r0)));
+  int tok = mine > 0 ? static_cast<int>(r0 / x.heads) : 0, head = mine > 0 ? static_cast<int>(r0 % x.heads) : 0;
+  bool fresh = true, good = false;
+  int tok_ahead = tok, head_ahead = head;          // of the row that is asked for next
+  auto ask = [&](int i) {
+    if (MODE != kScalar && i < mine) {
+      const uint16_t* xr = x.x + static_cast<size_t>(tok_ahead) * x.x_stride + head_ahead * kDim;
+      const uint16_t* dr = x.dy + static_cast<size_t>(tok_ahead) * x.dy_stride + head_ahead * kDim;
+      const uint32_t to = smem_u32(ring + (i % kAhead) * 4 * kBwdThreads + threadIdx.x);
+      constexpr int kStep = static_cast<int>(sizeof(Unit)) * kBwdThreads;
+      copy_async<sizeof(Unit)>(to, xr + l.at0);
+      copy_async<sizeof(Unit)>(to + kStep, xr + l.at1);
+      copy_async<sizeof(Unit)>(to + 2 * kStep, dr + l.at0);
+      copy_async<sizeof(Unit)>(to + 3 * kStep, dr + l.at1);
+      if (++head_ahead == x.heads) {
+        head_ahead = 0;
+        ++tok_ahead;
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int i = 0; i < kAhead - 1; ++i) ask(i);
+#pragma unroll 1
+  for (int i = 0; i < per; ++i) {
+    const bool in = i < mine;
+    ask(i + kAhead - 1);
+    if (in && fresh) {
+      const int pos = a.positions[tok];
+      good = pos >= 0 && pos < a.rope.table_len;
+      if (!good && l.u == 0) atomicOr(a.status, KVQ_STATUS_BAD_POS);
+      l.angles(c, s, a.rope.table + static_cast<size_t>(good ? pos : 0) * a.rope.rot_dim, -1.0f, a.rope);
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    uint32_t rx[U] = {}, rd[U] = {};
+    if (in) {
+      if constexpr (MODE == kScalar) {
+        load_raw(rx, x.x + static_cast<size_t>(tok) * x.x_stride + head * kDim, l, a.rope);
+        load_raw(rd, x.dy + static_cast<size_t>(tok) * x.dy_stride + head * kDim, l, a.rope);
+      } else {
+        const Unit* from = ring + (i % kAhead) * 4 * kBwdThreads + threadIdx.x;
+        const Unit e[4] = {from[0], from[kBwdThreads], from[2 * kBwdThreads], from[3 * kBwdThreads]};
+        const uint32_t* ew = reinterpret_cast<const uint32_t*>(e);
+#pragma unroll
+        for (int x2 = 0; x2 < U; ++x2) {
+          rx[x2] = ew[x2];
+          rd[x2] = ew[U + x2];
+        }
+      }
+    }
+    float v[kBwdE], d[kBwdE];
+    unpack<kBwdE>(v, rx);
+    unpack<kBwdE>(d, rd);
+    uint16_t* to = x.y + static_cast<size_t>(tok) * x.y_stride + head * kDim;
+    fresh = head + 1 == x.heads;
+    head = fresh ? 0 : head + 1;
+    tok += fresh ? 1 : 0;
+    turn<MODE, kBwdE>(d, c, s);
     float ss = 0.0f, gx = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
+    for (int e = 0; e < kBwdE; ++e) {
       ss = fmaf(v[e], v[e], ss);
       gx = fmaf(d[e] * w[e], v[e], gx);
     }
-    const float r = rsqrtf(sum8(ss) * (1.0f / kDim) + a.eps);
-    const float m = sum8(gx) * r * (1.0f / kDim);
-    if (on) {
+    const float r = rsqrtf(sum_row<kLanes>(ss) * (1.0f / kDim) + a.eps);
+    const float m = sum_row<kLanes>(gx) * r * (1.0f / kDim);
+    if (in && good) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
+      for (int e = 0; e < kBwdE; ++e) {
         const float xh = v[e] * r;
         dw[e] = fmaf(d[e], xh, dw[e]);
         v[e] = r * (d[e] * w[e] - xh * m);
       }
-      store_row(x.y + static_cast<size_t>(tok) * x.y_stride + head * kDim, v, l, a.rope);
+      store_row(to, v, l, a.rope);
     }
   }
+  dependents_begin();
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], 8);
-    dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], 16);
-    if (lane < 8) red[warp][l.dim(e, a.rope)] = dw[e];
+  for (int e = 0; e < kBwdE; ++e) {
+#pragma unroll
+    for (int o = kLanes; o < 32; o <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
+    if (lane < kLanes) red[warp][l.dim(e, a.rope)] = dw[e];
   }
   __syncthreads();
   if (threadIdx.x < kDim) {
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < kBwdThreads / 32; ++i) sum += red[i][threadIdx.x];
-    a.part[(static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kDim + threadIdx.x] = sum;
+    a.part[static_cast<size_t>(blockIdx.x) * kDim + threadIdx.x] = sum;
   }
 }
 
 // dw of the queries or the keys: 32 elements a CTA, the CTAs' parts in order.
-__global__ void __launch_bounds__(256) norm_weight_kernel(const __grid_constant__ NormArgs a, int parts) {
-  __shared__ float red[8][32];
+__global__ void __launch_bounds__(1024) norm_weight_kernel(const __grid_constant__ NormArgs a, int ctas) {
+  __shared__ float red[32][32];
+  dependency_wait();
   float* dw = blockIdx.y == 0 ? a.q.dw : a.k.dw;
   if (!dw) return;
+  const int first = blockIdx.y == 0 ? 0 : a.q_ctas, parts = (blockIdx.y == 0 ? a.q_ctas : ctas) - first;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float* p = a.part + static_cast<size_t>(blockIdx.y) * parts * kDim + blockIdx.x * 32 + lane;
+  const float* p = a.part + static_cast<size_t>(first) * kDim + blockIdx.x * 32 + lane;
   float sum = 0.0f;
-  for (int i = warp; i < parts; i += 8) sum += p[static_cast<size_t>(i) * kDim];
+#pragma unroll 8
+  for (int i = warp; i < parts; i += 32) sum += p[static_cast<size_t>(i) * kDim];
   red[warp][lane] = sum;
   __syncthreads();
   if (warp == 0) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) sum += red[i][lane];
+    for (int i = 1; i < 32; ++i) sum += red[i][lane];
     dw[blockIdx.x * 32 + lane] = sum;
   }
 }
@@ -290,38 +386,76 @@ NormMode mode_of(const RopeArgs& r) {
 
 }  // namespace
 
-int norm_backward_parts(int n, int num_sms) {
-  // at most four CTAs an SM; a row group each for the rows of few tokens
-  const long long most = 4LL * num_sms;
-  return static_cast<int>(n < most ? (n < 1 ? 1 : n) : most);
-}
+int norm_backward_ctas(int num_sms) { return kBwdCtas * num_sms; }
 
-cudaError_t launch_norm_rope(const NormArgs& a, cudaStream_t st) {
-  const int rows = 1;
-  const int per = 4 * rows;
-  const long long tasks = static_cast<long long>(a.n) * ((a.q.x ? (a.q.heads + per - 1) / per : 0) +
-                                                         (a.k.x ? (a.k.heads + per - 1) / per : 0));
-  const long long grid = (tasks + kFwdThreads / 32 - 1) / (kFwdThreads / 32);
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const int g = static_cast<int>(grid);
-  switch (mode_of(a.rope)) {
-    case kHalfVec: norm_rope_kernel<kHalfVec><<<g, kFwdThreads, 0, st>>>(a, rows); break;
-    case kInterVec: norm_rope_kernel<kInterVec><<<g, kFwdThreads, 0, st>>>(a, rows); break;
-    default: norm_rope_kernel<kScalar><<<g, kFwdThreads, 0, st>>>(a, rows);
-  }
+template <int MODE>
+static cudaError_t forward(const NormArgs& a, int num_sms, cudaStream_t st) {
+  // two rows a group where tokens alone make several waves of warps, else one
+  const bool wide = a.n >= 16 * num_sms;
+  const int per = wide ? 8 : 4;
+  const dim3 grid((static_cast<unsigned>(a.n) + kFwdThreads / 32 - 1) / (kFwdThreads / 32),
+                  (a.q.x ? (a.q.heads + per - 1) / per : 0) + (a.k.x ? (a.k.heads + per - 1) / per : 0));
+  if (wide) norm_rope_kernel<MODE, 2><<<grid, kFwdThreads, 0, st>>>(a);
+  else norm_rope_kernel<MODE, 1><<<grid, kFwdThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_norm_rope_backward(const NormArgs& a, int num_sms, cudaStream_t st) {
-  const int parts = norm_backward_parts(a.n, num_sms);
-  const dim3 grid(parts, 2);
+cudaError_t launch_norm_rope(const NormArgs& a, int num_sms, cudaStream_t st) {
   switch (mode_of(a.rope)) {
-    case kHalfVec: norm_rope_backward_kernel<kHalfVec><<<grid, kBwdThreads, 0, st>>>(a); break;
-    case kInterVec: norm_rope_backward_kernel<kInterVec><<<grid, kBwdThreads, 0, st>>>(a); break;
-    default: norm_rope_backward_kernel<kScalar><<<grid, kBwdThreads, 0, st>>>(a);
+    case kHalfVec: return forward<kHalfVec>(a, num_sms, st);
+    case kInterVec: return forward<kInterVec>(a, num_sms, st);
+    default: return forward<kScalar>(a, num_sms, st);
   }
-  norm_weight_kernel<<<dim3(kDim / 32, 2), 256, 0, st>>>(a, parts);
+}
+
+template <int MODE>
+static cudaError_t backward(const NormArgs& a, int ctas, cudaStream_t st) {
+  constexpr int kSmem = MODE == kScalar ? 0 : kAhead * 4 * kBwdThreads * kBwdE;
+  static bool attr_set[64] = {};       // per device: the attributes are per context
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (kSmem > 0 && (dev < 0 || dev >= 64 || !attr_set[dev])) {
+    const cudaError_t e = cudaFuncSetAttribute(norm_rope_backward_kernel<MODE>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  norm_rope_backward_kernel<MODE><<<ctas, kBwdThreads, kSmem, st>>>(a);
   return cudaGetLastError();
+}
+
+cudaError_t launch_norm_rope_backward(NormArgs a, int num_sms, cudaStream_t st) {
+  // a row a group at least, shared out between queries and keys by their rows
+  const long long hq = a.q.x ? a.q.heads : 0, hk = a.k.x ? a.k.heads : 0;
+  const long long groups = kBwdThreads / (kDim / kBwdE);
+  long long ctas = ((hq + hk) * a.n + groups - 1) / groups + 1;
+  if (ctas > norm_backward_ctas(num_sms)) ctas = norm_backward_ctas(num_sms);
+  long long q = hq + hk > 0 ? (ctas * hq + (hq + hk) / 2) / (hq + hk) : 0;
+  if (hq > 0 && q < 1) q = 1;
+  if (hk > 0 && q > ctas - 1) q = ctas - 1;
+  a.q_ctas = static_cast<int>(q);
+  const int g = static_cast<int>(ctas);
+  if (a.n > 0) {
+    cudaError_t e;
+    switch (mode_of(a.rope)) {
+      case kHalfVec: e = backward<kHalfVec>(a, g, st); break;
+      case kInterVec: e = backward<kInterVec>(a, g, st); break;
+      default: e = backward<kScalar>(a, g, st);
+    }
+    if (e != cudaSuccess) return e;
+  }
+  // a programmatic dependent: it is launched while the first kernel ends
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kDim / 32, 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_weight_kernel, a, a.n > 0 ? g : 0);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace kvq
