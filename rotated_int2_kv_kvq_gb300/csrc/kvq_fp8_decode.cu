@@ -22,6 +22,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;
 constexpr int kCtasPerSm = 2;
 constexpr int kMinUnits = kWarps;       // pages of a CTA's range at least: one a warp
+constexpr int kItemCost = 32;           // pages that an item counts for beside its own
 constexpr int kFlush = 16;              // pages of a warp between flushes of the accumulators
 constexpr int kMaxCtas = 1024;          // of the grid: sizes the joining kernel's arrays
 constexpr float kLazy = 8.0f;           // log2 by which a reference may lag behind its maximum
@@ -81,7 +82,11 @@ struct Start {            // a CTA's range of the line of work
   int b;
 };
 
-// An item counts its pages, at least one.
+// An item counts its pages, at least one, and kItemCost more for what it costs a CTA whatever its
+// length (query, page ids and first records to wait for, the warps' states to join): in the line,
+// those units come before its first page.  (64 ragged sequences up to 16K: without 138 us, 8: 119,
+// 16: 108, 32: 98; 64 windows of 4100: 97, 93, 90, 88; 16 x 32K: 185 to 187 whatever.)
+__device__ __forceinline__ int item_units(const Seen& s) { return max(s.pages, 1) + kItemCost; }
 __device__ __forceinline__ void start_line(const Fp8DecodeArgs& a, Start* line, long long* red) {
   const int tid = threadIdx.x;
   const int per_thread = (a.batch + kThreads - 1) / kThreads;
@@ -90,7 +95,7 @@ __device__ __forceinline__ void start_line(const Fp8DecodeArgs& a, Start* line, 
   for (int b = b_lo; b < b_hi; ++b) {
     const Seen s = seen_of(a, b);
     if (s.bad && blockIdx.x == 0) atomicOr(a.status, KVQ_STATUS_BAD_SEQLEN);
-    mine += static_cast<long long>(max(s.pages, 1)) * a.Hkv;
+    mine += static_cast<long long>(item_units(s)) * a.Hkv;
   }
   long long total;
   const long long before = block_prefix(mine, red, &total);
@@ -104,7 +109,7 @@ __device__ __forceinline__ void start_line(const Fp8DecodeArgs& a, Start* line, 
   if (u0 < u1 && before <= u0 && u0 < before + mine) {
     long long u = before;
     for (int b = b_lo; b < b_hi; ++b) {
-      const long long su = static_cast<long long>(max(seen_of(a, b).pages, 1)) * a.Hkv;
+      const long long su = static_cast<long long>(item_units(seen_of(a, b))) * a.Hkv;
       if (u0 < u + su) {
         line->b = b;
         line->b_first = u;
@@ -163,15 +168,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_fp8_kernel(const 
 
   while (cur < end) {
     Seen s = seen_of(a, b);
-    while (cur >= b_first + static_cast<long long>(max(s.pages, 1)) * a.Hkv) {     // ends: cur < total
-      b_first += static_cast<long long>(max(s.pages, 1)) * a.Hkv;
+    while (cur >= b_first + static_cast<long long>(item_units(s)) * a.Hkv) {     // ends: cur < total
+      b_first += static_cast<long long>(item_units(s)) * a.Hkv;
       s = seen_of(a, ++b);
     }
     const int units = max(s.pages, 1);
-    const long long item = b_first + (cur - b_first) / units * units;       // its first unit
-    const int kv = static_cast<int>((cur - b_first) / units);
-    const int j0 = static_cast<int>(cur - item);
+    const int kv = static_cast<int>((cur - b_first) / item_units(s));
+    const long long item = b_first + static_cast<long long>(kv) * item_units(s) + kItemCost;   // its first page
+    const int j0 = static_cast<int>(max(cur - item, 0ll));
     const int j1 = static_cast<int>(min(static_cast<long long>(units), end - item));
+    if (j1 <= 0) break;                // the range ends before the item's first page
     const int jp = min(j1, s.pages);                                        // pages j0 .. jp - 1
     const int count = jp - j0 > warp ? (jp - j0 - warp + kWarps - 1) / kWarps : 0;
     const int32_t* ptab = a.page_table + static_cast<size_t>(b) * a.max_pages;

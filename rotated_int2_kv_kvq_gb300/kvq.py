@@ -398,25 +398,33 @@ def _raw_stream(stream, device: int) -> int:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _at(t, dtypes, device, name):
-    """Address of a contiguous tensor of one of `dtypes` on CUDA device `device`."""
+def _wrong(t, dtypes, device, name):
+    """Raise what is wrong with a tensor: its type, place or layout."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, the handle on cuda:{device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
+    raise ValueError(f"{name}: must be contiguous")
+
+
+def _at(t, dtypes, device, name):
+    """Address of a contiguous tensor of one of `dtypes` on CUDA device `device`."""
+    if (not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.get_device() != device
+            or not t.is_contiguous()):
+        _wrong(t, dtypes, device, name)
     return t.data_ptr()
 
 
 def _vec(t, n, device, name):
     """Address of an int32 [n] tensor."""
-    at = _at(t, _I32, device, name)
-    if t.dim() != 1 or t.numel() != n:
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != device
+            or not t.is_contiguous()):
+        _wrong(t, _I32, device, name)
+    if t.shape != (n,):
         raise ValueError(f"{name}: expected [{n}], got {tuple(t.shape)}")
-    return at
+    return t.data_ptr()
 
 
 def _table2(t, device):
@@ -431,16 +439,14 @@ def _table2(t, device):
 def _rows(t, device, name, heads=None):
     """(address, token stride, n, heads) of bf16 rows [n, heads, 128]; only the tokens may be
     strided."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name}: expected a CUDA tensor")
-    if t.dtype not in _BF16:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {_BF16}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, the handle on cuda:{device}")
+    if not isinstance(t, torch.Tensor) or t.dtype not in _BF16 or t.get_device() != device:
+        _wrong(t, _BF16, device, name)
     shape = t.shape
     if len(shape) != 3 or shape[2] != 128 or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name}: expected [n, {heads or 'heads'}, 128], got {tuple(shape)}")
     n, hh = shape[0], shape[1]
+    if t.is_contiguous():
+        return t.data_ptr(), hh * 128, n, hh
     s0, s1, s2 = t.stride()
     if n and (s2 != 1 or (hh > 1 and s1 != 128)):
         raise ValueError(f"{name}: the heads of a token must be adjacent and contiguous")
@@ -475,18 +481,12 @@ def kvq_rope(h, x, y, positions, rope: Rope, inverse=False, stream=None):
         1 if inverse else 0, _raw_stream(stream, dev)))
 
 
-def _norm_rows(x, others, heads, dev, names):
-    """[address, stride] of x and each of `others` (rows of one shape), and n; x may be None."""
-    if x is None:
-        return [None, 0] * (1 + len(others)), None
-    p, s, n, _ = _rows(x, dev, names[0], heads)
-    got = [p, s]
-    for t, name in zip(others, names[1:]):
-        p, s, m, _ = _rows(t, dev, name, heads)
-        if m != n:
-            raise ValueError(f"{name} must have the shape of {names[0]}")
-        got += [p, s]
-    return got, n
+def _like(t, n, heads, device, name, of):
+    """(address, token stride) of rows like those of `of`."""
+    at, stride, m, _ = _rows(t, device, name, heads)
+    if m != n:
+        raise ValueError(f"{name} must have the shape of {of}")
+    return at, stride
 
 
 def _weight(t, device, name):
@@ -494,17 +494,25 @@ def _weight(t, device, name):
     if t is None:
         return None
     at = _at(t, _F32, device, name)
-    if t.dim() != 1 or t.numel() != 128:
+    if t.shape != (128,):
         raise ValueError(f"{name}: expected [128], got {tuple(t.shape)}")
     return at
 
 
-def _one_length(nq, nk):
-    if nq is None and nk is None:
+def _norm_rows(q, k, lay, dev):
+    """(address, token stride) of q and of k (None: NULL, 0), and their number of tokens."""
+    if q is None and k is None:
         raise ValueError("q and k must not both be None")
-    if nq is not None and nk is not None and nq != nk:
-        raise ValueError("q and k must have the same number of tokens")
-    return nk if nq is None else nq
+    pq = pk = None
+    sq = sk = 0
+    if q is not None:
+        pq, sq, n, _ = _rows(q, dev, "q", lay.num_heads)
+    if k is not None:
+        pk, sk, m, _ = _rows(k, dev, "k", lay.num_kv_heads)
+        if q is not None and m != n:
+            raise ValueError("q and k must have the same number of tokens")
+        n = m
+    return pq, sq, pk, sk, n
 
 
 def kvq_norm_rope(h, q, k, q_out, k_out, q_weight, k_weight, eps, positions, rope: Rope,
@@ -514,13 +522,18 @@ def kvq_norm_rope(h, q, k, q_out, k_out, q_weight, k_weight, eps, positions, rop
     q_out may be q, k_out may be k); either pair may be None; weights: fp32 [128] or None (ones);
     positions: int32 [n]."""
     dev, lay = h.device, h.layout
-    aq, nq = _norm_rows(q, [q_out], lay.num_heads, dev, ["q", "q_out"])
-    ak, nk = _norm_rows(k, [k_out], lay.num_kv_heads, dev, ["k", "k_out"])
-    n = _one_length(nq, nk)
-    _check("kvq_norm_rope", load_library().kvq_norm_rope(
-        h.ptr, *aq[:2], *ak[:2], *aq[2:], *ak[2:], _weight(q_weight, dev, "q_weight"),
+    pq, sq, pk, sk, n = _norm_rows(q, k, lay, dev)
+    oq = ok = None, 0
+    if pq is not None:
+        oq = _like(q_out, n, lay.num_heads, dev, "q_out", "q")
+    if pk is not None:
+        ok = _like(k_out, n, lay.num_kv_heads, dev, "k_out", "k")
+    rc = load_library().kvq_norm_rope(
+        h.ptr, pq, sq, pk, sk, oq[0], oq[1], ok[0], ok[1], _weight(q_weight, dev, "q_weight"),
         _weight(k_weight, dev, "k_weight"), eps, _vec(positions, n, dev, "positions"), n,
-        _rope_on(rope, dev), _raw_stream(stream, dev)))
+        _rope_on(rope, dev), _raw_stream(stream, dev))
+    if rc:
+        _check("kvq_norm_rope", rc)
 
 
 def kvq_norm_rope_backward_workspace_bytes(h: Handle, n: int) -> int:
@@ -533,15 +546,22 @@ def kvq_norm_rope_backward(h, q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, 
     and dq_weight, dk_weight (fp32 [128], written; None: not wanted) from dq_out, dk_out.
     workspace: uint8, >= kvq_norm_rope_backward_workspace_bytes(h, n)."""
     dev, lay = h.device, h.layout
-    aq, nq = _norm_rows(q, [dq_out, dq], lay.num_heads, dev, ["q", "dq_out", "dq"])
-    ak, nk = _norm_rows(k, [dk_out, dk], lay.num_kv_heads, dev, ["k", "dk_out", "dk"])
-    n = _one_length(nq, nk)
-    _check("kvq_norm_rope_backward", load_library().kvq_norm_rope_backward(
-        h.ptr, *aq[:2], *ak[:2], *aq[2:4], *ak[2:4], *aq[4:], *ak[4:],
+    pq, sq, pk, sk, n = _norm_rows(q, k, lay, dev)
+    gq = gk = oq = ok = None, 0
+    if pq is not None:
+        gq = _like(dq_out, n, lay.num_heads, dev, "dq_out", "q")
+        oq = _like(dq, n, lay.num_heads, dev, "dq", "q")
+    if pk is not None:
+        gk = _like(dk_out, n, lay.num_kv_heads, dev, "dk_out", "k")
+        ok = _like(dk, n, lay.num_kv_heads, dev, "dk", "k")
+    rc = load_library().kvq_norm_rope_backward(
+        h.ptr, pq, sq, pk, sk, gq[0], gq[1], gk[0], gk[1], oq[0], oq[1], ok[0], ok[1],
         _weight(q_weight, dev, "q_weight"), _weight(k_weight, dev, "k_weight"),
         _weight(dq_weight, dev, "dq_weight"), _weight(dk_weight, dev, "dk_weight"), eps,
         _vec(positions, n, dev, "positions"), n, _rope_on(rope, dev),
-        _at(workspace, _U8, dev, "workspace"), workspace.numel(), _raw_stream(stream, dev)))
+        _at(workspace, _U8, dev, "workspace"), workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        _check("kvq_norm_rope_backward", rc)
 
 
 def _append_rope(int2, h, pool, num_pool_pages, K, V, seq_idx, positions, page_table, rope,
@@ -623,26 +643,27 @@ def kvq_bf16_prefill(h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out
 
 # ---- the 8-bit cache --------------------------------------------------------------
 
-def _fp8_rows(fn, h, pool, num_pool_pages, K, V, names, cu, page_table, seq_lens, stream):
+def _fp8_rows(fn, h, pool, num_pool_pages, k, v, names, cu, page_table, seq_lens, stream):
     dev, hkv = h.device, h.layout.num_kv_heads
-    at, n = [], None
-    for t, name in zip((K, V), names):
-        if t is None and fn == "kvq_fp8_read":
-            at += [None, 0]
-            continue
-        p, s, m, _ = _rows(t, dev, name, hkv)
-        if n is not None and m != n:
+    pk = pv = None
+    sk = sv = 0
+    if k is not None or fn == "kvq_fp8_append":
+        pk, sk, n, _ = _rows(k, dev, names[0], hkv)
+    if v is not None or fn == "kvq_fp8_append":
+        pv, sv, m, _ = _rows(v, dev, names[1], hkv)
+        if pk is not None and m != n:
             raise ValueError(f"{names[0]} and {names[1]} must have the same number of tokens")
         n = m
-        at += [p, s]
-    if n is None:
+    elif pk is None:
         raise ValueError(f"{names[0]} and {names[1]} must not both be None")
     pt, batch, max_pages = _table2(page_table, dev)
     pages = int(num_pool_pages)
-    _check(fn, getattr(load_library(), fn)(
-        h.ptr, _pool(pool, pages, hkv * FP8_RECORD_BYTES, dev), pages, *at,
+    rc = getattr(load_library(), fn)(
+        h.ptr, _pool(pool, pages, hkv * FP8_RECORD_BYTES, dev), pages, pk, sk, pv, sv,
         _vec(cu, batch + 1, dev, "cu"), n, pt, max_pages, _vec(seq_lens, batch, dev, "seq_lens"),
-        batch, _raw_stream(stream, dev)))
+        batch, _raw_stream(stream, dev))
+    if rc:
+        _check(fn, rc)
 
 
 def kvq_fp8_append(h, pool, num_pool_pages, K, V, cu, page_table, seq_lens, stream=None):
@@ -672,13 +693,15 @@ def kvq_fp8_decode(h, pool, num_pool_pages, q, page_table, seq_lens, out, worksp
     pt, batch, max_pages = _table2(page_table, dev)
     pages, shape = int(num_pool_pages), (batch, lay.num_heads, 128)
     pq, po = _at(q, _BF16, dev, "q"), _at(out, _F32, dev, "out")
-    if tuple(q.shape) != shape or tuple(out.shape) != shape:
+    if q.shape != shape or out.shape != shape:
         raise ValueError(f"q and out: expected {list(shape)}, got {tuple(q.shape)} and "
                          f"{tuple(out.shape)}")
-    _check("kvq_fp8_decode", load_library().kvq_fp8_decode(
+    rc = load_library().kvq_fp8_decode(
         h.ptr, _pool(pool, pages, lay.num_kv_heads * FP8_RECORD_BYTES, dev), pages, pq, pt,
         max_pages, _vec(seq_lens, batch, dev, "seq_lens"), batch, int(window), int(sinks), po,
-        _at(workspace, _U8, dev, "workspace"), workspace.numel(), _raw_stream(stream, dev)))
+        _at(workspace, _U8, dev, "workspace"), workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        _check("kvq_fp8_decode", rc)
 
 
 def kvq_fp8_prefill_workspace_bytes(h: Handle, batch: int, n: int) -> int:
