@@ -287,7 +287,8 @@ __device__ __forceinline__ long long gaps_before(const PrefillArgs& a, const Seq
   if (a.window == 0 || !s.ok) return 0;
   const long long lead = lead_tiles(a), c = static_cast<long long>(s.p0) - a.window + 1;
   const long long need = kTileKeys * (lead + 1) - c;           // c + i TR >= 128 (lead + 1) from tile i on
-  const long long i = need > 0 ? (need + TR - 1) / TR : 0, m = k - i;
+  const int lg = TR == 64 ? 6 : TR == 128 ? 7 : 8;
+  const long long i = need > 0 ? (need + TR - 1) >> lg : 0, m = k - i;
   if (m <= 0) return 0;
   const long long at = c + i * TR;
   if (TR == 64) {                                              // (a + j) / 2 - lead, j = 0 .. m - 1
@@ -617,6 +618,16 @@ __device__ __forceinline__ uint32_t fp8_meta(const uint8_t* rec) {
 __device__ __forceinline__ uint32_t meta_k(uint32_t m) { return (m & 511u) - 1; }          // biased as fp32's
 __device__ __forceinline__ uint32_t meta_v(uint32_t m) { return ((m >> 9) & 511u) - 1; }
 __device__ __forceinline__ uint32_t meta_flags(uint32_t m) { return m >> 18; }
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint16_t fp8_encode_half(uint32_t h2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+  return r;
+}
 __device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -783,12 +794,11 @@ __device__ __forceinline__ bool item_end(bool alive, const PrefillArgs& a, volat
 }
 
 // The item's query rows into the Q operands, by the first 384 threads.
-template <bool INT2, bool FP8>
+template <bool INT2>
 __device__ __forceinline__ void load_q(const PrefillArgs& a, const Item& w, uint8_t* smem) {
   const int lg = a.G >> 1, rows = w.tokens << lg;         // log2 of 1, 2, 4
   const int pieces = (rows > 128 ? 256 : 128) * 16;
-  constexpr int kStep = kMmaWarp * 32, kBatch = FP8 ? 2 : 6;   // loads in flight a thread (8-bit cache:
-                                        // beside the producers' pages; 6 spill, 1931 against 1728 us)
+  constexpr int kStep = kMmaWarp * 32, kBatch = 6;        // loads in flight a thread
 #pragma unroll 1
   for (int base = threadIdx.x; base < pieces; base += kBatch * kStep) {
     uint4 v[kBatch];
@@ -805,34 +815,6 @@ __device__ __forceinline__ void load_q(const PrefillArgs& a, const Item& w, uint
     for (int y = 0; y < kBatch; ++y) {
       const int idx = base + y * kStep, row = idx >> 4, c = idx & 15;
       if (idx >= pieces) break;
-      if constexpr (FP8) {
-        // two e4m3 parts of q times a power of two a row (its largest in [128, 256)): 8 bits, so exact
-        // but for elements below 2^-9 of the largest, which keep 2^-18 of it
-        const uint32_t x[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
-        float mx = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mx = max3(mx, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xffff0000u)));
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));   // a row is 16 lanes
-        const uint32_t ex = min(max((__float_as_uint(mx) >> 23) & 255u, 8u), 253u);
-        const float down = __uint_as_float((261u - ex) << 23);
-        if (c == 0) reinterpret_cast<float*>(smem + Smem::kQScale)[row] = __uint_as_float((ex - 7u) << 23);
-        uint8_t* to = smem + Smem::kQ + (row >> 7) * kTileBytes + (row & 127) * 128 + 2 * (c >> 1);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          float q0 = __uint_as_float(x[t] << 16) * down, q1 = __uint_as_float(x[t] & 0xffff0000u) * down;
-          q0 += q0 - q0;            // an infinity becomes NaN
-          q1 += q1 - q1;
-          const uint16_t hi = fp8_encode(q0, q1);
-          const uint32_t back = fp8_pair(hi);
-          const uint16_t lo = fp8_encode(q0 - half_lo(back), q1 - half_hi(back));
-          const int at = ((2 * t + (c & 1)) ^ (row & 7)) << 4;
-          *reinterpret_cast<uint16_t*>(to + at) = hi;
-          *reinterpret_cast<uint16_t*>(to + kTileBytes / 2 + at) = lo;
-        }
-        continue;
-      }
       uint8_t* at = smem + Smem::kQ + (row >> 7) * kTileBytes + (row & 127) * 128;
       if constexpr (INT2) {         // d in order: the left operand of q R_K
         *reinterpret_cast<uint4*>(at + (c >> 3) * (kTileBytes / 2) + (((c & 7) ^ (row & 7)) << 4)) = v[y];
@@ -846,6 +828,74 @@ __device__ __forceinline__ void load_q(const PrefillArgs& a, const Item& w, uint
                                        4 * (wq & 3)) = x[t];
         }
       }
+    }
+  }
+  fence_proxy_async();
+}
+
+// 8-bit cache: the query rows as two e4m3 parts, by the softmax's 256 threads.  q is taken times a
+// power of two a row (its largest element in [128, 256)): its 8 bits fill both parts, so that is
+// exact but for elements below 2^-9 of the largest, which keep 2^-18 of it.  A thread takes a
+// 16-byte chunk of both parts, 16 elements 16 w + 8 h + 2 t + {0, 1}; a row is 8 lanes.
+__device__ __forceinline__ void load_q_fp8(const PrefillArgs& a, const Item& w, uint8_t* smem) {
+  const int lg = a.G >> 1, rows = w.tokens << lg;         // log2 of 1, 2, 4
+  const int chunks = (rows > 128 ? 256 : 128) * 8;
+  constexpr int kBatch = 2;
+#pragma unroll 1
+  for (int base = threadIdx.x; base < chunks; base += kBatch * 256) {
+    uint32_t v[kBatch][8];
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      const int idx = base + y * 256, row = idx >> 3, t = (idx >> 1) & 3, h = idx & 1;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[y][i] = 0;
+      if (row < rows) {
+        const uint32_t* from = reinterpret_cast<const uint32_t*>(
+            a.q + static_cast<size_t>(w.row0 + (row >> lg)) * a.q_stride +
+            ((w.kv << lg) + (row & (a.G - 1))) * kDim + 8 * h + 2 * t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[y][i] = from[8 * i];
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      const int idx = base + y * 256, row = idx >> 3;
+      if (idx >= chunks) break;
+      float mx = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        mx = max3(mx, fabsf(__uint_as_float(v[y][i] << 16)), fabsf(__uint_as_float(v[y][i] & 0xffff0000u)));
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const uint32_t raw = (__float_as_uint(mx) >> 23) & 255u;
+      if (raw == 255u) {             // an infinity becomes NaN (e4m3 has none)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if ((v[y][i] & 0x7f80u) == 0x7f80u) v[y][i] |= 0x40u;
+          if ((v[y][i] & 0x7f800000u) == 0x7f800000u) v[y][i] |= 0x400000u;
+        }
+      }
+      const uint32_t ex = min(max(raw, 8u), 253u);
+      const float down = __uint_as_float((261u - ex) << 23);
+      if ((idx & 7) == 0) reinterpret_cast<float*>(smem + Smem::kQScale)[row] = __uint_as_float((ex - 7u) << 23);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t x = pack_half2(__uint_as_float(v[y][i] << 16) * down,
+                                      __uint_as_float(v[y][i] & 0xffff0000u) * down);
+        const uint16_t q1 = fp8_encode_half(x), q2 = fp8_encode_half(hsub2(x, fp8_pair(q1)));
+        if (i & 1) {
+          hi[i >> 1] |= static_cast<uint32_t>(q1) << 16;
+          lo[i >> 1] |= static_cast<uint32_t>(q2) << 16;
+        } else {
+          hi[i >> 1] = q1;
+          lo[i >> 1] = q2;
+        }
+      }
+      const uint32_t to = smem_u32(smem + Smem::kQ + (row >> 7) * kTileBytes + (row & 127) * 128) +
+                          (((idx & 7) ^ (row & 7)) << 4);
+      sts128(to, hi[0], hi[1], hi[2], hi[3]);
+      sts128(to + kTileBytes / 2, lo[0], lo[1], lo[2], lo[3]);
     }
   }
   fence_proxy_async();
@@ -1179,7 +1229,6 @@ __device__ __forceinline__ bool fp8_produce(const PrefillArgs& a, const Item& w,
     return false;
   };
   load_v(0, false);
-  load_q<false, true>(a, w, smem);
   sync_cta();                   // Q is there
   if (tiles > 0) {
     if (!wait_empty(kKEmpty, it)) return false;
@@ -1316,7 +1365,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       sync_cta();                   // the item is there
       const Item w = items[i & 1];
       if (w.done) break;
-      load_q<INT2, FP8>(a, w, smem);
+      if constexpr (FP8) load_q_fp8(a, w, smem);
+      else load_q<INT2>(a, w, smem);
       sync_cta();                   // Q is there
       const Steps<INT2> st(w, a);
       const int rows = w.tokens * a.G;
@@ -1598,7 +1648,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       } else {
         bf16_load_key(x, rec[0], lane);
       }
-      load_q<INT2, FP8>(a, w, smem);
+      load_q<INT2>(a, w, smem);
       sync_cta();                   // Q is there
       for (int j = 0; j < st.tiles && alive; ++j) {
         const uint32_t k = itk + st.pre + j, kv = itv + st.pre + j;
