@@ -551,8 +551,9 @@ int kvq_bf16_prefill(kvq_handle* h, const void* pool, int num_pool_pages, const 
  * not count for e.  A call that writes a page's slot 0 begins the page: what it held counts no
  * more and the slots the call does not write become 0.  So a page serves a new sequence without
  * being cleared, and a sequence that was cut back goes on where it was cut (tokens behind the
- * cut may keep e larger than needed).  Two sequences of one call must not share a page that
- * both write to.
+ * cut may keep e larger than needed).  No page may be written through two places of the page
+ * table in one call.  (A number from 1.9375 * 2^127 on rounds to 2^128, an
+ * infinity.)
  *   K, V : device bf16, row i at K + i * k_stride (elements), KV heads adjacent; 16-byte
  *          aligned, strides multiples of 8 and >= Hkv * 128.
  *   pool : device, 16-byte aligned.
@@ -595,7 +596,9 @@ int kvq_fp8_decode(kvq_handle* h, const void* pool, int num_pool_pages, const ui
 /* The same for chunks of new tokens (prompts, drafts, mixed batches), as kvq_bf16_prefill: row i of
  * sequence b, at position p = seq_lens[b] - n_b + i, attends to the positions t <= p with
  *     t > p - window  or  t < sinks          (window = 0: all of them).
- * Entries and queries enter the products as they are, weights are rounded to bf16, sums are fp32.
+ * Entries enter the products as they are; a query does times a power of two in two 8-bit parts,
+ * which hold it exactly but for elements below 2^-9 of its largest, of which 2^-18 of that is kept;
+ * weights are rounded to bf16, sums are fp32.  A value beyond bf16's range counts as a NaN.
  * Key tiles of 128 positions that no row of a tile of rows sees are not worked on; pages without a
  * visible position are not read, and need not exist.  A value vector that holds a NaN makes NaN
  * the whole output of each row that sees it, and leaves the others alone.

@@ -902,6 +902,7 @@ int kvq_norm_rope_backward(kvq_handle* h, const uint16_t* q, long long q_stride,
                   dk_weight)))
     return KVQ_EINVAL;
   if (n == 0) {        // no rows: the sums are zero
+    if (reinterpret_cast<uintptr_t>(dq_weight) % 4 || reinterpret_cast<uintptr_t>(dk_weight) % 4) return KVQ_EINVAL;
     a.q.dw = dq_weight;
     a.k.dw = dk_weight;
   }
@@ -943,7 +944,9 @@ int kvq_fp8_decode(kvq_handle* h, const void* pool, int num_pool_pages, const ui
                    void* stream) {
   if (!h || !fp8_cache_ok(pool, num_pool_pages, page_table, max_pages, seq_lens, batch)) return KVQ_EINVAL;
   if (!q || !out || !workspace || window < 0 || sinks < 0) return KVQ_EINVAL;
-  if (reinterpret_cast<uintptr_t>(q) % 4 || reinterpret_cast<uintptr_t>(workspace) % 256) return KVQ_EINVAL;
+  if (reinterpret_cast<uintptr_t>(q) % 4 || reinterpret_cast<uintptr_t>(out) % 4 ||
+      reinterpret_cast<uintptr_t>(workspace) % 256)
+    return KVQ_EINVAL;
   const kvq::Fp8DecodeWs w = kvq::fp8_decode_ws_layout(h->num_sms);
   if (ws_bytes < w.total) return KVQ_ENOSPACE;
   kvq::DeviceGuard dev_guard(h->device);

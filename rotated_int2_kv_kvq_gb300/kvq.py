@@ -684,6 +684,11 @@ def kvq_fp8_workspace_bytes(h: Handle, batch: int) -> int:
     return int(load_library().kvq_fp8_workspace_bytes(h.ptr, int(batch)))
 
 
+def _span(window, sinks):
+    """window and sinks as C ints (beyond every position, more is no more)."""
+    return [max(-1, min(int(x), 2 ** 31 - 1)) for x in (window, sinks)]
+
+
 def kvq_fp8_decode(h, pool, num_pool_pages, q, page_table, seq_lens, out, workspace, window=0,
                    sinks=0, stream=None):
     """Attention of each sequence's last token over its 8-bit cache: all positions, or the last
@@ -698,7 +703,7 @@ def kvq_fp8_decode(h, pool, num_pool_pages, q, page_table, seq_lens, out, worksp
                          f"{tuple(out.shape)}")
     rc = load_library().kvq_fp8_decode(
         h.ptr, _pool(pool, pages, lay.num_kv_heads * FP8_RECORD_BYTES, dev), pages, pq, pt,
-        max_pages, _vec(seq_lens, batch, dev, "seq_lens"), batch, int(window), int(sinks), po,
+        max_pages, _vec(seq_lens, batch, dev, "seq_lens"), batch, *_span(window, sinks), po,
         _at(workspace, _U8, dev, "workspace"), workspace.numel(), _raw_stream(stream, dev))
     if rc:
         _check("kvq_fp8_decode", rc)
@@ -713,7 +718,7 @@ def kvq_fp8_prefill(h, pool, num_pool_pages, q, cu_q, page_table, seq_lens, out,
     """kvq_prefill over the 8-bit cache (workspace: kvq_fp8_prefill_workspace_bytes): each row sees
     all positions up to its own, or the last `window` of them and the first `sinks`."""
     _prefill("kvq_fp8_prefill", FP8_RECORD_BYTES, h, pool, num_pool_pages, q, cu_q, page_table, seq_lens,
-             out, workspace, stream, int(window), int(sinks))
+             out, workspace, stream, *_span(window, sinks))
 
 
 def kvq_dequant(h, pool, num_pool_pages, page_table, seq, start, length, K_out=None, V_out=None,

@@ -39,6 +39,16 @@ def test_null_handles(lib):
         assert fn(None, at, 1, at, 128, at, 128, at, 1, at, 1, at, 1, None) == K.KVQ_EINVAL
     assert lib.kvq_fp8_decode(None, at, 1, at, at, 1, at, 1, 0, 0, at, at, 1 << 30,
                               None) == K.KVQ_EINVAL
+    assert lib.kvq_fp8_prefill_workspace_bytes(None, 1, 1) == 0
+    assert lib.kvq_fp8_prefill(None, at, 1, at, 512, at, 1, at, 1, at, 1, 0, 0, at, at, 1 << 30,
+                               None) == K.KVQ_EINVAL
+
+
+def test_window_and_sinks_fit_a_c_int():
+    most = 2 ** 31 - 1
+    assert K._span(7, 3) == [7, 3] and K._span(0, 0) == [0, 0] and K._span(most, most) == [most, most]
+    assert K._span(2 ** 32, 2 ** 40) == [most, most]         # not 0, as the low bits say
+    assert K._span(-2 ** 32, -5) == [-1, -1]                 # refused by the call
 
 
 class _Handle:
@@ -57,6 +67,8 @@ def test_binding_refuses_cpu_tensors(lib):
             fn(h, buf, 1, rows, rows, i, pt, i)
     with pytest.raises(TypeError):
         K.kvq_fp8_decode(h, buf, 1, rows, pt, i, rows.float(), buf)
+    with pytest.raises(TypeError):
+        K.kvq_fp8_prefill(h, buf, 1, rows, i, pt, i, rows, buf)
     with pytest.raises(TypeError):
         K.kvq_norm_rope(h, rows, rows, rows, rows, None, None, 1e-6, i, None)
     with pytest.raises(ValueError):

@@ -235,6 +235,63 @@ def test_bad_lengths_pages_and_rows():
     assert torch.equal(c.prefill(q, [20, 20, 20], 50, 3), want)
 
 
+@pytest.mark.parametrize("n", [3, 200])
+def test_rows_that_see_nothing(n):
+    """A window of one token whose page is missing leaves a row without a position: zeros."""
+    c = Cache8(4, 2, [400], seed=16)
+    q = c.randn(n, 4)
+    want = c.prefill(q, [n], 1, 0)
+    pt = c.pt.clone()
+    pt[0, 24] = -1                         # positions 384 .. 399
+    out = c.prefill(q, [n], 1, 0, pt=pt)
+    lost = min(n, 16)
+    assert (out[n - lost:] == 0).all() and torch.equal(out[:n - lost], want[:n - lost])
+    assert K.kvq_get_status(c.h) == K.KVQ_STATUS_BAD_PAGE
+    one = q[n - 1:].contiguous()
+    assert (c.decode(one, 1, 0, pt=pt) == 0).all() and K.kvq_get_status(c.h) == K.KVQ_STATUS_BAD_PAGE
+    check(c, c.prefill(q, [n], 17, 2, pt=pt), q, [n], 17, 2, drop=slice(384, 400))
+
+
+def test_windows_beyond_a_c_int():
+    c = Cache8(4, 2, [300], seed=17)
+    q = c.randn(40, 4)
+    assert torch.equal(c.prefill(q, [40], 2 ** 32, 2 ** 33), c.prefill(q, [40]))
+    assert torch.equal(c.decode(q[:1], 2 ** 32), c.decode(q[:1]))
+    assert torch.equal(c.prefill(q, [40], 9, 2 ** 32 + 1), c.prefill(q, [40]))
+
+
+def test_calls_at_once():
+    """Attention of both kinds over one cache, and reads of it, on four streams with workspaces of
+    their own: the results are those of one call after the other."""
+    c = Cache8(32, 8, [6000, 33, 900], seed=18)
+    new = [700, 9, 100]
+    cu, q, q1 = cu_of(new), c.randn(809, 32), c.randn(3, 32)
+    size, size1 = K.kvq_fp8_prefill_workspace_bytes(c.h, 3, 809), K.kvq_fp8_workspace_bytes(c.h, 3)
+
+    def calls():
+        kinds = []
+        for _ in range(2):
+            out, ws = torch.zeros_like(q), torch.empty(size, dtype=torch.uint8, device="cuda")
+            kinds.append((out, lambda o=out, w=ws: c.prefill(q, new, 500, 4, out=o, ws=w, cu=cu)))
+        out, ws = torch.zeros(3, 32, D, device="cuda"), torch.empty(size1, dtype=torch.uint8, device="cuda")
+        kinds.append((out, lambda o=out, w=ws: c.decode(q1, 800, 2, out=o, ws=w)))
+        out = torch.zeros(809, 8, D, dtype=torch.bfloat16, device="cuda")
+        kinds.append((out, lambda o=out: K.kvq_fp8_read(c.h, c.pool, c.pages, None, o, cu, c.pt, c.seq_lens)))
+        return kinds
+
+    want = calls()
+    for _, run in want:
+        run()
+    got, streams = calls(), [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (_, run), stream in zip(got, streams):
+            with torch.cuda.stream(stream):
+                run()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for (a, _), (b, _) in zip(got, want)) and K.kvq_get_status(c.h) == 0
+
+
 def test_strided_queries_and_pool_past_32_bits():
     c = Cache8(16, 8, [400], seed=10, extra=400_000)
     assert int(c.pt.max()) * 8 * 4112 > 2 ** 32

@@ -45,9 +45,38 @@ def test_cache_calls():
                 sl=at(c.seq_lens), b=1, w=0, s=0, out=at(o), ws=at(ws), size=size, st=None)
     _refused(lib.kvq_fp8_decode, good, [
         dict(pool=None), dict(pages=0), dict(q=None), dict(q=at(q) + 2), dict(pt=None), dict(mp=0), dict(sl=None),
-        dict(b=0), dict(b=65536), dict(w=-1), dict(s=-1), dict(out=None), dict(ws=None), dict(ws=at(ws) + 16)])
+        dict(b=0), dict(b=65536), dict(w=-1), dict(s=-1), dict(out=None), dict(out=at(o) + 2), dict(ws=None),
+        dict(ws=at(ws) + 16)])
     assert lib.kvq_fp8_decode(*_args(good, size=size - 1)) == K.KVQ_ENOSPACE
     assert K.kvq_fp8_workspace_bytes(c.h, 0) == 0 and K.kvq_fp8_workspace_bytes(c.h, 65536) == 0
+    assert K.kvq_get_status(c.h) == 0
+
+
+def test_prefill_calls():
+    c = Cache8(4, 2, [40], seed=4)
+    lib, at = K.load_library(), lambda t: t.data_ptr()
+    q, cu = c.randn(8, 4), cu_of([8])
+    out = torch.empty_like(q)
+    size = K.kvq_fp8_prefill_workspace_bytes(c.h, 1, 8)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    good = dict(h=c.h.ptr, pool=at(c.pool), pages=c.pages, q=at(q), qs=512, cu=at(cu), n=8, pt=at(c.pt),
+                mp=c.pt.shape[1], sl=at(c.seq_lens), b=1, w=0, s=0, out=at(out), ws=at(ws), size=size, st=None)
+    _refused(lib.kvq_fp8_prefill, good, [
+        dict(h=None), dict(pool=None), dict(pool=at(c.pool) + 8), dict(pages=0), dict(q=None), dict(q=at(q) + 8),
+        dict(qs=511), dict(qs=504), dict(cu=None), dict(n=-1), dict(pt=None), dict(mp=0), dict(mp=(1 << 26) + 1),
+        dict(sl=None), dict(b=0), dict(b=65536), dict(w=-1), dict(s=-1), dict(out=None), dict(out=at(out) + 8),
+        dict(ws=None), dict(ws=at(ws) + 64)])
+    assert lib.kvq_fp8_prefill(*_args(good, size=size - 1)) == K.KVQ_ENOSPACE
+    assert lib.kvq_fp8_prefill(*_args(good, n=0, pool=None)) == K.KVQ_OK      # no rows: nothing is looked at
+    assert K.kvq_fp8_prefill_workspace_bytes(c.h, 0, 8) == 0 and K.kvq_fp8_prefill_workspace_bytes(c.h, 1, -1) == 0
+    for bad in (dict(window=-1), dict(sinks=-2 ** 32), dict(window=-2 ** 32)):
+        with pytest.raises(RuntimeError):
+            c.prefill(q, [8], **bad)
+        with pytest.raises(RuntimeError):
+            c.decode(c.randn(1, 4), **bad)
+    for bad in (dict(out=out[:7]), dict(cu=i32([0, 8, 8])), dict(q=c.randn(8, 2))):
+        with pytest.raises(ValueError):
+            c.prefill(bad.pop("q", q), [8], **bad)
     assert K.kvq_get_status(c.h) == 0
 
 
@@ -74,6 +103,8 @@ def test_norm_calls():
     _refused(lib.kvq_norm_rope_backward, good, bad + [dict(dyq=None), dict(dyks=8), dict(dwq=at(w) + 1),
                                                       dict(ws=None), dict(ws=at(ws) + 64)])
     assert lib.kvq_norm_rope_backward(*_args(good, size=size - 1)) == K.KVQ_ENOSPACE
+    for bad in (dict(dwq=at(w) + 2), dict(dwk=at(w) + 1)):        # no rows: the sums are written all the same
+        assert lib.kvq_norm_rope_backward(*_args(good, n=0, **bad)) == K.KVQ_EINVAL
     assert K.kvq_get_status(h) == 0
 
 
