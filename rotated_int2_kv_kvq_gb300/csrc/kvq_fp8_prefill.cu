@@ -2,10 +2,40 @@
 // all of it or a sliding window and the first tokens.
 //
 // Row r of sequence b sits at position p and attends to the positions t <= p with t > p - window
-// or t < sinks (window 0: all).  The kernel is that of kvq_prefill.cu: the producers turn codes
-// into bf16 operands, which hold an entry code * 2^e exactly, and everything behind them is the
-// BF16 cache's path (query, weights and sums).  Whole key tiles that no row of a row tile sees are
-// left out of the line of work, so a window costs its own length.
+// or t < sinks (window 0: all).  An entry is code * 2^e with one e for a page's keys and one for its
+// values, so that
+//   logit_t = scale 2^x 2^ek (q~ . code_t),   out = sum_t w_t (code_t 2^ev) / sum_t w_t,
+// with q = q~ 2^x.  The kernel is that of kvq_prefill.cu (its roles, its line of work and its joining
+// of cut items), with these differences:
+//   keys    : the codes are the tensor core's 8-bit operand as they are; producers only move them
+//             from the record's order into rows.  The query is two 8-bit parts of 4 bits of mantissa
+//             each, two products of half a 16-bit one's time.  A page's 2^ek goes into its columns'
+//             scores: eight columns' factors a tile in place of one.
+//   values  : bf16, code 2^ev exactly, by bit moves and one product a pair, because their sum spans
+//             pages; weights are bf16 and their sum is that of the rounded ones.
+//   windows : whole key tiles that no row of a row tile sees are left out of the line of work, so a
+//             window costs its own length; partly hidden tiles are masked in TMEM first.
+//   NaN     : a value that is not finite is stored as zero and noted, and spoils the rows that see it.
+//   queries : the next item's rows come into shared memory by bulk copies as soon as the
+//             last product has read this one's, and are made operands from there.
+//   registers: 176 / 96 / 64 a thread (softmax, producers, issue), with the issuing warp's loop apart
+//             from the scheduler's: next to this much shared memory L1 holds nearly nothing, and a
+//             spilled register is a round trip to L2.  Nothing is spilled.
+//
+// Measured (32 query, 8 KV heads): 4096 new tokens at 32K 1560 to 1600 us from one
+// GPU to another, at the power limit (1320 TFLOP/s).  The products alone take 1086 at
+// the rate of a large library product, 1218 at the rate that one keeps up; the BF16 cache takes 1800,
+// the INT2 cache 1450.  A CTA's time for a key tile is 2.3 us: 1.35 of a row tile's softmax and 1.0
+// that it waits for scores behind the other row tile's, so the chain scores -> softmax -> weights ->
+// output bounds it, as it does the other caches'.  Spills and instructions count most: registers
+// 168 / 112 / 64 with 68 bytes of the softmax's spilled 1585, 168 / 120 / 56 with the issuing warp's
+// 1940, 160 / 128 / 64 2270.
+// A prompt of 8191 tokens with a window of 1024: 241 us for products of 68.  Ten key tiles an item where
+// eight hold its window, a third of them partly hidden (2.3 us of softmax for 1.4); and 9 us an item,
+// seven items a CTA, for its queries (3), the first scores (1.5), results (2.4) and the wait for the
+// other row tile's.  Queries by plain loads when the item begins: 273.
+// Eight drafts of five tokens at 8K: 67 us; launches, the line's setup, first loads and the join are
+// about half, and a tile of one row tile takes 1.9 us, as long as its producers need.
 #include "kvq_internal.cuh"
 
 namespace kvq {

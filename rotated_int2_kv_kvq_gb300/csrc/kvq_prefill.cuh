@@ -20,7 +20,7 @@ constexpr int kProdWarp0 = 8, kMmaWarp = 12, kSchedWarp = 13;
 // issue and schedule), of kRegLaunch a thread at launch.
 template <bool INT2, bool FP8>
 struct Regs {
-  static constexpr int kSoftmax = FP8 ? 168 : INT2 ? 184 : 176, kProducer = INT2 ? 96 : 112,
+  static constexpr int kSoftmax = INT2 ? 184 : 176, kProducer = INT2 || FP8 ? 96 : 112,
                        kIssue = FP8 ? 64 : 48;
   static_assert(2 * kSoftmax + kProducer + kIssue <= 4 * kRegLaunch, "register split");
 };
@@ -36,10 +36,14 @@ constexpr float kLazy = 8.0f;              // log2 growth of a row maximum befor
 // 6: 1487, 4: 1519; without the factor 1442).
 constexpr float kBias = 15.0f - kLazy;
 
-struct Smem {
+template <bool FP8>
+struct SmemOf {
+  static constexpr int kKeyTile = FP8 ? kTileBytes / 2 : kTileBytes;
   static constexpr int kQ = 0;                              // [2][32 KB]
-  static constexpr int kK = kQ + 2 * kTileBytes;            // [stages][32 KB]
-  static constexpr int kV = kK + kStages * kTileBytes;      // [stages][32 KB]
+  // 8-bit cache: the next item's queries as they are, from the second half of Q to K
+  static constexpr int kRaw = kQ + kTileBytes;
+  static constexpr int kK = kQ + 2 * kTileBytes + (FP8 ? 48 * 1024 : 0);   // [stages][32 KB, 8-bit: 16 KB]
+  static constexpr int kV = kK + kStages * kKeyTile;        // [stages][32 KB]
   static constexpr int kBar = kV + kStages * kTileBytes;    // mbarriers
   static constexpr int kAny = kBar + 160;                   // u8 [kFlags][4]: a producer warp has set a bit of
   static constexpr int kBad = kAny + 16;                    // u32 [kFlags][4] tokens without a valid page
@@ -56,10 +60,15 @@ struct Smem {
   static constexpr int kBytes = kPageScale + 32 * kFlags;
   static constexpr int kAlloc = kBytes + 1024;              // base rounded up to 1024
 };
+// 8-bit cache: bytes from one token's raw queries to the next: 32 more than they have, so that
+// four tokens' rows lie in different banks.
+__device__ __forceinline__ int raw_pitch(int G) { return 256 * G + 32; }
+static_assert(kRows * (256 + 32) <= SmemOf<true>::kK - SmemOf<true>::kRaw, "raw queries");
 
 // barrier indices
 enum { kKFull = 0, kKEmpty = kKFull + kStages, kVFull = kKEmpty + kStages, kVEmpty = kVFull + kStages,
-       kSFull = kVEmpty + kStages, kPFull = kSFull + 2, kDrain = kPFull + 2, kNumBars };
+       kSFull = kVEmpty + kStages, kPFull = kSFull + 2, kDrain = kPFull + 2, kRawFull, kQFree,
+       kNumBars };
 static_assert(kNumBars * 8 <= 160, "barriers");
 
 using Cut = PrefillArgs::Cut;
@@ -783,6 +792,13 @@ struct Pages {
   }
 };
 
+// Those that wait for an item's queries; the 8-bit cache's producers go on.
+template <bool FP8>
+__device__ __forceinline__ void sync_q() {
+  if constexpr (FP8) asm volatile("barrier.sync 2, 384;" ::: "memory");
+  else sync_cta();
+}
+
 // A wait gave up somewhere in the CTA: every role leaves after the same item.
 __device__ __forceinline__ bool item_end(bool alive, const PrefillArgs& a, volatile uint32_t* abort) {
   if (!alive) {
@@ -815,7 +831,7 @@ __device__ __forceinline__ void load_q(const PrefillArgs& a, const Item& w, uint
     for (int y = 0; y < kBatch; ++y) {
       const int idx = base + y * kStep, row = idx >> 4, c = idx & 15;
       if (idx >= pieces) break;
-      uint8_t* at = smem + Smem::kQ + (row >> 7) * kTileBytes + (row & 127) * 128;
+      uint8_t* at = smem + SmemOf<false>::kQ + (row >> 7) * kTileBytes + (row & 127) * 128;
       if constexpr (INT2) {         // d in order: the left operand of q R_K
         *reinterpret_cast<uint4*>(at + (c >> 3) * (kTileBytes / 2) + (((c & 7) ^ (row & 7)) << 4)) = v[y];
       } else {                      // the 16-byte piece holds the pairs t = 0 .. 3 of one (w, h)
@@ -833,56 +849,54 @@ __device__ __forceinline__ void load_q(const PrefillArgs& a, const Item& w, uint
   fence_proxy_async();
 }
 
-// 8-bit cache: the query rows as two e4m3 parts, by the softmax's 256 threads.  q is taken times a
-// power of two a row (its largest element in [128, 256)): its 8 bits fill both parts, so that is
-// exact but for elements below 2^-9 of the largest, which keep 2^-18 of it.  A thread takes a
-// 16-byte chunk of both parts, 16 elements 16 w + 8 h + 2 t + {0, 1}; a row is 8 lanes.
-__device__ __forceinline__ void load_q_fp8(const PrefillArgs& a, const Item& w, uint8_t* smem) {
-  const int lg = a.G >> 1, rows = w.tokens << lg;         // log2 of 1, 2, 4
-  const int chunks = (rows > 128 ? 256 : 128) * 8;
-  constexpr int kBatch = 2;
+// 8-bit cache: asks for an item's queries, by a whole warp: a copy a token, all on kRawFull.
+__device__ __forceinline__ void ask_queries(const PrefillArgs& a, const Item& w, uint32_t sb, int lane) {
+  using Smem = SmemOf<true>;
+  const uint32_t bytes = 256 * a.G, bar = sb + Smem::kBar + 8 * kRawFull;
+  const int tokens = w.tokens;
+  const uint16_t* from = a.q + static_cast<size_t>(w.row0) * a.q_stride + w.kv * a.G * kDim;
+  if (lane == 0) mbar_arrive_expect_tx(bar, tokens * bytes);
+  __syncwarp();
+  for (int i = lane; i < tokens; i += 32)
+    bulk_g2s(sb + Smem::kRaw + i * raw_pitch(a.G), from + i * a.q_stride, bytes, bar);
+}
+
+// 8-bit cache: the query rows, raw in shared memory, as two e4m3 parts, by the softmax's 256 threads.
+// q is taken times a power of two a row (its largest element in [128, 256)): its 8 bits fill both
+// parts, so that is exact but for elements below 2^-9 of the largest, which keep 2^-18 of it; a row
+// with an infinity or a NaN is NaN.  A thread takes a 16-byte chunk of both parts, 16 elements
+// 16 w + 8 h + 2 t + {0, 1}; a row is 8 lanes, a warp's four rows are one head of four tokens.  The
+// first tile's parts lie before the raw rows, the second's over those of the first.
+// Called, and a row at a time, because the roles' loops need the instruction cache (two rows at a
+// time: a window's 8191 tokens 251 us, not 244; inlined: 4096 tokens at 32K 1620, not 1603).
+__device__ __noinline__ void load_q_fp8(const PrefillArgs& a, const Item& w, uint8_t* smem) {
+  using Smem = SmemOf<true>;
+  const int lg = a.G >> 1, tokens = w.tokens, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tiles = tokens << lg > 128 ? 2 : 1;             // lg: log2 of 1, 2, 4
 #pragma unroll 1
-  for (int base = threadIdx.x; base < chunks; base += kBatch * 256) {
-    uint32_t v[kBatch][8];
+  for (int tile = 0; tile < tiles; ++tile) {
+    if (tile != 0) asm volatile("barrier.sync 1, 256;" ::: "memory");
+#pragma unroll 1
+    for (int u = 32 * tile + 4 * warp, end = u + 4; u < end; ++u) {       // four rows
+      const int tok = 4 * (u >> lg) + (lane >> 3), head = u & (a.G - 1), row = (tok << lg) + head;
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(smem + Smem::kRaw + tok * raw_pitch(a.G) +
+                                                               256 * head + 16 * (lane & 1)) + ((lane >> 1) & 3);
+      uint32_t v[8], top = 0;
 #pragma unroll
-    for (int y = 0; y < kBatch; ++y) {
-      const int idx = base + y * 256, row = idx >> 3, t = (idx >> 1) & 3, h = idx & 1;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[y][i] = 0;
-      if (row < rows) {
-        const uint32_t* from = reinterpret_cast<const uint32_t*>(
-            a.q + static_cast<size_t>(w.row0 + (row >> lg)) * a.q_stride +
-            ((w.kv << lg) + (row & (a.G - 1))) * kDim + 8 * h + 2 * t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[y][i] = from[8 * i];
+      for (int i = 0; i < 8; ++i) {
+        v[i] = tok < tokens ? from[8 * i] : 0u;
+        top = __vmaxu2(top, v[i] & 0x7fff7fffu);
       }
-    }
 #pragma unroll
-    for (int y = 0; y < kBatch; ++y) {
-      const int idx = base + y * 256, row = idx >> 3;
-      if (idx >= chunks) break;
-      float mx = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        mx = max3(mx, fabsf(__uint_as_float(v[y][i] << 16)), fabsf(__uint_as_float(v[y][i] & 0xffff0000u)));
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const uint32_t raw = (__float_as_uint(mx) >> 23) & 255u;
-      if (raw == 255u) {             // an infinity becomes NaN (e4m3 has none)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if ((v[y][i] & 0x7f80u) == 0x7f80u) v[y][i] |= 0x40u;
-          if ((v[y][i] & 0x7f800000u) == 0x7f800000u) v[y][i] |= 0x400000u;
-        }
-      }
-      const uint32_t ex = min(max(raw, 8u), 253u);
-      const float down = __uint_as_float((261u - ex) << 23);
-      if ((idx & 7) == 0) reinterpret_cast<float*>(smem + Smem::kQScale)[row] = __uint_as_float((ex - 7u) << 23);
+      for (int o = 1; o < 8; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const uint32_t raw = max(top & 0xffffu, top >> 16) >> 7, ex = min(max(raw, 8u), 253u);
+      const float down = __uint_as_float(raw == 255u ? 0x7fc00000u : (261u - ex) << 23);
+      if ((lane & 7) == 0) reinterpret_cast<float*>(smem + Smem::kQScale)[row] = __uint_as_float((ex - 7u) << 23);
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t x = pack_half2(__uint_as_float(v[y][i] << 16) * down,
-                                      __uint_as_float(v[y][i] & 0xffff0000u) * down);
+        const uint32_t x = pack_half2(__uint_as_float(v[i] << 16) * down,
+                                      __uint_as_float(v[i] & 0xffff0000u) * down);
         const uint16_t q1 = fp8_encode_half(x), q2 = fp8_encode_half(hsub2(x, fp8_pair(q1)));
         if (i & 1) {
           hi[i >> 1] |= static_cast<uint32_t>(q1) << 16;
@@ -893,7 +907,7 @@ __device__ __forceinline__ void load_q_fp8(const PrefillArgs& a, const Item& w, 
         }
       }
       const uint32_t to = smem_u32(smem + Smem::kQ + (row >> 7) * kTileBytes + (row & 127) * 128) +
-                          (((idx & 7) ^ (row & 7)) << 4);
+                          (((lane & 7) ^ (row & 7)) << 4);
       sts128(to, hi[0], hi[1], hi[2], hi[3]);
       sts128(to + kTileBytes / 2, lo[0], lo[1], lo[2], lo[3]);
     }
@@ -919,8 +933,9 @@ __device__ __forceinline__ uint32_t visible(int limit, int k) {
 // b and c modulo 2).
 template <bool INT2, bool FP8>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float scale, bool first,
-                                             int limit, int low, int lead, const float* pages, bool edge, uint32_t any, const volatile uint32_t* bad,
-                                             float& mref, float& l) {
+                                             int limit, int low, int lead, const float* pages, bool edge,
+                                             uint32_t any, const volatile uint32_t* bad, float& mref,
+                                             float& l) {
   if (edge || any != 0) {
     // Hidden scores become -inf in TMEM first, 32 columns a step: rolled and apart from
     // the tiles' common path, whose code it would double.  Column 32c + i stands for
@@ -946,18 +961,20 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sca
     }
     tc_wait_st();
   }
-  [[maybe_unused]] float sc_all[8];      // of the columns of each page
-  if constexpr (FP8) {
-    const float4 x = *reinterpret_cast<const float4*>(pages), y = *reinterpret_cast<const float4*>(pages + 4);
-    sc_all[0] = x.x, sc_all[1] = x.y, sc_all[2] = x.z, sc_all[3] = x.w;
-    sc_all[4] = y.x, sc_all[5] = y.y, sc_all[6] = y.z, sc_all[7] = y.w;
+  // 8-bit cache: the scales of the columns of pages 4 h .. 4 h + 3.  Read once for the maximum and
+  // again for the weights: eight registers less in between, which are all that this role has.
+  [[maybe_unused]] auto page_scales = [&](float (&sc)[4], int h) {
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(sc[0]), "=f"(sc[1]), "=f"(sc[2]), "=f"(sc[3])
+                 : "r"(smem_u32(pages + 4 * h))
+                 : "memory");
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sc_all[i] *= scale;
+    for (int i = 0; i < 4; ++i) sc[i] *= scale;
     if (edge || any != 0) {              // a hidden column's 0 * -inf would be NaN
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sc_all[i] = fmaxf(sc_all[i], 1.17549435e-38f);
+      for (int i = 0; i < 4; ++i) sc[i] = fmaxf(sc[i], 1.17549435e-38f);
     }
-  }
+  };
   uint32_t v[4][32];
   tc_ld_row(v, ts);
   float mnew;
@@ -974,7 +991,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sca
     mnew = mref;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float* sc = sc_all + 4 * h;
+      float sc[4];
+      page_scales(sc, h);
       mnew = max3(mnew, m[4 * h] * sc[0], m[4 * h + 1] * sc[1]);
       mnew = max3(mnew, m[4 * h + 2] * sc[2], m[4 * h + 3] * sc[3]);
     }
@@ -1023,7 +1041,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sca
     uint32_t pk[32];
     uint64_t page2[4] = {one2, one2, one2, one2};
     if constexpr (FP8) {
-      const float* sc = sc_all + 4 * h;
+      float sc[4];
+      page_scales(sc, h);
 #pragma unroll
       for (int i = 0; i < 4; ++i) page2[i] = pair2(sc[i], sc[i]);
     }
@@ -1145,10 +1164,13 @@ __device__ __noinline__ void start_line(const PrefillArgs& a, Line* line, long l
 // two pages, a tile ahead too, and there is no room for more (a spill is a round trip to L2, as
 // shared memory leaves L1 next to nothing), so everything else is read again from shared memory
 // or worked out where it is used.  it: stages and tiles before the item.
-// Measured, 4096 tokens at 32K: keys through registers too 1657 us (this 1620), keys and values
-// staged by bulk copies in shared memory 1940 and more (its bandwidth is what the products need).
+// Measured, 4096 tokens at 32K (when this took 1620 us): keys through registers too 1657, keys and
+// values staged by bulk copies in shared memory 1940 and more (its bandwidth is what the products
+// need).  At 1585: pages fetched into L2 four tiles ahead 1623, the copies' words in an order
+// without bank conflicts 1630 (an instruction more a copy: issue slots are scarcer than banks).
 __device__ __forceinline__ bool fp8_produce(const PrefillArgs& a, const Item& w, uint8_t* smem, Look& look, int pw,
                                             uint32_t it) {
+  using Smem = SmemOf<true>;
   const uint32_t sb = smem_u32(smem), bar = sb + Smem::kBar;
   const int lane = threadIdx.x & 31;
   const int tiles = w.tiles;
@@ -1229,11 +1251,10 @@ __device__ __forceinline__ bool fp8_produce(const PrefillArgs& a, const Item& w,
     return false;
   };
   load_v(0, false);
-  sync_cta();                   // Q is there
   if (tiles > 0) {
     if (!wait_empty(kKEmpty, it)) return false;
     flags(0, false);
-    copy_k(0, false, sb + Smem::kK + (it % kStages) * (kTileBytes / 2));
+    copy_k(0, false, sb + Smem::kK + (it % kStages) * Smem::kKeyTile);
     give_k(it);
   }
 #pragma unroll 1
@@ -1248,7 +1269,7 @@ __device__ __forceinline__ bool fp8_produce(const PrefillArgs& a, const Item& w,
     if (j + 1 < tiles) {
       if (!wait_empty(kKEmpty, k + 1)) return false;
       flags(j + 1, (j & 3) == 3);
-      copy_k(j + 1, (j & 3) == 3, sb + Smem::kK + ((k + 1) % kStages) * (kTileBytes / 2));
+      copy_k(j + 1, (j & 3) == 3, sb + Smem::kK + ((k + 1) % kStages) * Smem::kKeyTile);
     }
     if (!wait_empty(kVEmpty, k)) return false;
     const uint32_t row = value_base(sb + Smem::kV + (k % kStages) * kTileBytes, pw, lane);
@@ -1301,6 +1322,7 @@ __device__ __forceinline__ bool fp8_produce(const PrefillArgs& a, const Item& w,
 
 template <bool INT2, bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs a) {
+  using Smem = SmemOf<FP8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sb = smem_u32(smem);
@@ -1330,6 +1352,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       mbar_init(B(kPFull + i), 4);
     }
     mbar_init(B(kDrain), 1);
+    mbar_init(B(kRawFull), 1);
+    mbar_init(B(kQFree), 1);
     fence_mbar_init();
     *abort = 0;
     first_bad[0] = 0xffffffffu;
@@ -1365,9 +1389,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       sync_cta();                   // the item is there
       const Item w = items[i & 1];
       if (w.done) break;
-      if constexpr (FP8) load_q_fp8(a, w, smem);
-      else load_q<INT2>(a, w, smem);
-      sync_cta();                   // Q is there
+      if constexpr (FP8) {
+        alive = warp_wait(B(kRawFull), i & 1);
+        load_q_fp8(a, w, smem);      // all warps' barriers, whatever was waited for
+      } else {
+        load_q<INT2>(a, w, smem);
+      }
+      sync_q<FP8>();                // Q is there
       const Steps<INT2> st(w, a);
       const int rows = w.tokens * a.G;
       const int row = st.split ? (tid & 127) : tid;
@@ -1438,7 +1466,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           const uint32_t f = (itf + j) % kFlags;
           if (some)
             softmax_tile<INT2, FP8>(ts, to, scale, j == first, limit, low, lead,
-                                    reinterpret_cast<const float*>(smem + Smem::kPageScale) + 8 * f, edge, anyw[f], badw + 4 * f, mref, l);
+                                    reinterpret_cast<const float*>(smem + Smem::kPageScale) + 8 * f, edge,
+                                    anyw[f], badw + 4 * f, mref, l);
           give();
         }
         // O is complete.  A row sees all positions up to its own, so it sees a NaN or an
@@ -1604,7 +1633,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         __syncwarp();
         arrive_if(B(full + k % kStages), lane == 0);
       };
-      auto kbuf = [&](uint32_t k) { return sb + Smem::kK + (k % kStages) * kTileBytes; };
+      auto kbuf = [&](uint32_t k) { return sb + Smem::kK + (k % kStages) * Smem::kKeyTile; };
       auto vbuf = [&](uint32_t k) { return sb + Smem::kV + (k % kStages) * kTileBytes; };
       // the pair's records (of the tile that is loaded next) and the ids behind them
       const uint8_t* rec[2];
@@ -1723,129 +1752,151 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       next_item<FP8>(a, *line, items[0]);
     }
     __syncwarp();
+    uint32_t asked = 0, freed = 0;  // items whose queries were asked for, whose last product was seen
     auto work = [&](auto issue, auto schedule) {
-    for (uint32_t i = 0;; ++i) {
-      sync_cta();
-      const Item w = items[i & 1];
-      if (w.done) break;
-      if (schedule.value && warp == kSchedWarp && lane == 0) {
-        first_bad[(i + 1) & 1] = 0xffffffffu;
-        if constexpr (FP8) looks[(i + 1) & 1] = Look{0xffffffffu, 0u, {}};
-        next_item<FP8>(a, *line, items[(i + 1) & 1]);
-      }
-      __syncwarp();
-      const Steps<INT2> st(w, a);
-      sync_cta();                   // Q is there
-      if (issue.value && warp == kMmaWarp && st.tiles > 0) {
-        constexpr uint32_t idesc = idesc_f16(INT2 ? 0 : 1), idesc_bf = idesc_f16(1);
-        const bool both = __shfl_sync(0xffffffffu, st.split ? 0 : 1, 0) != 0;
-        const int tiles = __shfl_sync(0xffffffffu, st.tiles, 0);
-        auto full = [&](int bar, uint32_t k) {
-          alive = alive && warp_wait(B(bar + k % kStages), (k / kStages) & 1);
-          tc_fence_after();
-          return alive;
-        };
-        // S_t (or O_t) once the products before are done; the plain arrival passes on what
-        // this warp saw of the producers' flags
-        auto scored = [&](int t) {
-          tc_commit(B(kSFull + t), one);
-          arrive_if(B(kSFull + t), one);
-        };
-        auto empty = [&](int bar, uint32_t k) { tc_commit(B(bar + k % kStages), one); };
-        auto operand = [&](int t) {      // Q, P or o of row tile t
-          uint32_t& n = t ? np1 : np0;
-          alive = alive && warp_wait(B(kPFull + t), n & 1);
-          ++n;
-          tc_fence_after();
-          return alive;
-        };
-        // S_t = Q_t X^T, X a stage's K (or V) operand
-        auto product = [&](int t, uint32_t x, uint32_t id, bool add) {
-          const uint32_t q = tile_desc(sb + Smem::kQ + (both ? t : 0) * kTileBytes);
-          if constexpr (FP8) {      // the query's two parts, 32 columns a step
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc_mma_ss_f8(tm + t * 128, q + (k >> 2) * (kTileBytes / 2 >> 4) + 2 * (k & 3), x + 2 * (k & 3),
-                           idesc_f16(0), k != 0, one);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc_mma_ss(tm + t * 128, q + desc_step(k), x + desc_step(k), id, add || k != 0, one);
-          }
-        };
-        auto kdesc = [&](uint32_t k) {
-          return tile_desc(sb + Smem::kK + (k % kStages) * (FP8 ? kTileBytes / 2 : kTileBytes));
-        };
-        auto vdesc = [&](uint32_t k) { return tile_desc(sb + Smem::kV + (k % kStages) * kTileBytes); };
-        auto weighted = [&](int t, uint32_t v, bool add) {     // O_t += P_t V
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc_mma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * k, v + desc_step(k), idesc,
-                      add || k != 0, one);
-        };
-        uint32_t k = __shfl_sync(0xffffffffu, itk, 0), v = __shfl_sync(0xffffffffu, itv, 0);
-        if (st.pre && full(kKFull, k) && full(kVFull, v)) {
-#pragma unroll 1
-          for (int t = 0; t < 2; ++t)
-            if (t == 0 || both) {
-              product(t, kdesc(k), idesc_bf, false);
-              product(t, vdesc(v), idesc_bf, true);
-              scored(t);
-            }
-          empty(kKEmpty, k);
-          empty(kVEmpty, v);
-          ++k;
-          ++v;
+      for (uint32_t i = 0;; ++i) {
+        sync_cta();
+        const Item w = items[i & 1];
+        if (w.done) break;
+        if (FP8 && schedule.value && warp == kSchedWarp && i == 0) {
+          ask_queries(a, w, sb, lane);
+          asked = 1;
         }
-        if (st.pre) {
-          operand(0);
-          if (both) operand(1);
+        if (schedule.value && warp == kSchedWarp && lane == 0) {
+          first_bad[(i + 1) & 1] = 0xffffffffu;
+          if constexpr (FP8) looks[(i + 1) & 1] = Look{0xffffffffu, 0u, {}};
+          next_item<FP8>(a, *line, items[(i + 1) & 1]);
         }
-        // Step s: O_t += P_t V, then row tile t's next scores, t = s % 2.  Both row tiles:
-        // tile s / 2 each; one row tile: tile s, to group t.  Two scores ahead.
-        const int total = both ? 2 * tiles : tiles;
-        for (int s0 = -2; s0 < total && alive; s0 += 2) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int s = s0 + t;
-            if (s >= total) break;
-            const bool last = t == 1 || !both;       // of the stages' users
-            if (s0 >= 0) {
-              if (!full(kVFull, v) || !operand(t)) break;
-              weighted(t, vdesc(v), s0 != 0);
-              if (last) empty(kVEmpty, v++);
+        __syncwarp();
+        const Steps<INT2> st(w, a);
+        sync_q<FP8>();                // Q is there
+        if constexpr (FP8) {
+          // the next item's queries, once the last product has read this one's
+          if (schedule.value && warp == kSchedWarp && !items[(i + 1) & 1].done) {
+            if (st.tiles > 0) {         // a longer item gets more than one wait's limit
+              int more = st.tiles >> 16;
+              while (!(alive = warp_wait(B(kQFree), freed & 1)) && more-- > 0 && *abort == 0) {}
+              ++freed;
             }
-            const bool more = s + 2 < total;
-            if (more) {
-              if (!full(kKFull, k)) break;
-              product(t, kdesc(k), idesc, false);
-              if (last) empty(kKEmpty, k++);
+            if (alive) {
+              ask_queries(a, items[(i + 1) & 1], sb, lane);
+              ++asked;
             }
-            if (s0 >= 0 || more) scored(t);          // the next scores, or O
           }
         }
-        if (st.post && alive && full(kKFull, k)) {
-#pragma unroll 1
-          for (int t = 0; t < 2; ++t)
-            if ((t == 0 || both) && operand(t)) {
-              product(t, kdesc(k), idesc, false);
-              scored(t);
+        if (issue.value && warp == kMmaWarp && st.tiles > 0) {
+          constexpr uint32_t idesc = idesc_f16(INT2 ? 0 : 1), idesc_bf = idesc_f16(1);
+          const bool both = __shfl_sync(0xffffffffu, st.split ? 0 : 1, 0) != 0;
+          const int tiles = __shfl_sync(0xffffffffu, st.tiles, 0);
+          auto full = [&](int bar, uint32_t k) {
+            alive = alive && warp_wait(B(bar + k % kStages), (k / kStages) & 1);
+            tc_fence_after();
+            return alive;
+          };
+          // S_t (or O_t) once the products before are done; the plain arrival passes on what
+          // this warp saw of the producers' flags
+          auto scored = [&](int t) {
+            tc_commit(B(kSFull + t), one);
+            arrive_if(B(kSFull + t), one);
+          };
+          auto empty = [&](int bar, uint32_t k) { tc_commit(B(bar + k % kStages), one); };
+          auto operand = [&](int t) {      // Q, P or o of row tile t
+            uint32_t& n = t ? np1 : np0;
+            alive = alive && warp_wait(B(kPFull + t), n & 1);
+            ++n;
+            tc_fence_after();
+            return alive;
+          };
+          // S_t = Q_t X^T, X a stage's K (or V) operand
+          auto product = [&](int t, uint32_t x, uint32_t id, bool add) {
+            const uint32_t q = tile_desc(sb + Smem::kQ + (both ? t : 0) * kTileBytes);
+            if constexpr (FP8) {      // the query's two parts, 32 columns a step
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                tc_mma_ss_f8(tm + t * 128, q + (k >> 2) * (kTileBytes / 2 >> 4) + 2 * (k & 3), x + 2 * (k & 3),
+                             idesc_f16(0), k != 0, one);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                tc_mma_ss(tm + t * 128, q + desc_step(k), x + desc_step(k), id, add || k != 0, one);
             }
-          empty(kKEmpty, k);
+          };
+          auto kdesc = [&](uint32_t k) {
+            return tile_desc(sb + Smem::kK + (k % kStages) * Smem::kKeyTile);
+          };
+          auto vdesc = [&](uint32_t k) { return tile_desc(sb + Smem::kV + (k % kStages) * kTileBytes); };
+          auto weighted = [&](int t, uint32_t v, bool add) {     // O_t += P_t V
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              tc_mma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * k, v + desc_step(k), idesc,
+                        add || k != 0, one);
+          };
+          uint32_t k = __shfl_sync(0xffffffffu, itk, 0), v = __shfl_sync(0xffffffffu, itv, 0);
+          if (st.pre && full(kKFull, k) && full(kVFull, v)) {
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t)
+              if (t == 0 || both) {
+                product(t, kdesc(k), idesc_bf, false);
+                product(t, vdesc(v), idesc_bf, true);
+                scored(t);
+              }
+            empty(kKEmpty, k);
+            empty(kVEmpty, v);
+            ++k;
+            ++v;
+          }
+          if (st.pre) {
+            operand(0);
+            if (both) operand(1);
+          }
+          // Step s: O_t += P_t V, then row tile t's next scores, t = s % 2.  Both row tiles:
+          // tile s / 2 each; one row tile: tile s, to group t.  Two scores ahead.
+          const int total = both ? 2 * tiles : tiles;
+          for (int s0 = -2; s0 < total && alive; s0 += 2) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int s = s0 + t;
+              if (s >= total) break;
+              const bool last = t == 1 || !both;       // of the stages' users
+              if (s0 >= 0) {
+                if (!full(kVFull, v) || !operand(t)) break;
+                weighted(t, vdesc(v), s0 != 0);
+                if (last) empty(kVEmpty, v++);
+              }
+              const bool more = s + 2 < total;
+              if (more) {
+                if (!full(kKFull, k)) break;
+                product(t, kdesc(k), idesc, false);
+                if (last) empty(kKEmpty, k++);
+                if (FP8 && s + 3 == total) tc_commit(B(kQFree), one);      // the last of them
+              }
+              if (s0 >= 0 || more) scored(t);          // the next scores, or O
+            }
+          }
+          if (st.post && alive && full(kKFull, k)) {
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t)
+              if ((t == 0 || both) && operand(t)) {
+                product(t, kdesc(k), idesc, false);
+                scored(t);
+              }
+            empty(kKEmpty, k);
+          }
         }
+        __syncwarp();
+        itk += st.keys();
+        itv += st.values();
+        itf += st.tiles;
+        if (!item_end(alive, a, abort)) break;
       }
-      __syncwarp();
-      itk += st.keys();
-      itv += st.values();
-      itf += st.tiles;
-      if (!item_end(alive, a, abort)) break;
-    }
     };
     // apart where registers are short (8-bit cache): the scheduler's call would keep the issuing
     // warp's in memory
     if constexpr (FP8) {
       if (warp == kMmaWarp) work(std::true_type(), std::false_type());
       else work(std::false_type(), std::true_type());
+      // after a wait gave up: nothing may be under way when the CTA leaves
+      if (asked > 0) (void)warp_wait(B(kRawFull), (asked - 1) & 1);
     } else {
       work(std::true_type(), std::true_type());
     }
@@ -2001,7 +2052,7 @@ __global__ void __launch_bounds__(128) prefill_combine_kernel(const __grid_const
 
 template <bool INT2, bool FP8 = false>
 cudaError_t launch(const PrefillArgs& a, int num_sms, cudaStream_t st) {
-  constexpr int kSmem = Smem::kAlloc;
+  constexpr int kSmem = SmemOf<FP8>::kAlloc;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
   static bool attr_set[64] = {};       // per device: the attributes are per context
   int dev = 0;
