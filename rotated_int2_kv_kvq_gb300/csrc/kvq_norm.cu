@@ -9,6 +9,12 @@
 //
 // A row (token, head) is worked on by 8 lanes, 16 elements each (backward: 16 lanes of 8), so that
 // a pair of the rotation is in one lane and the sums over a row are a few shuffles.
+//
+// Both directions are bound by HBM: each element is read once and written once (backward: two read).
+// Measured, 32 query and 8 key heads, rot_dim 128: forward of 8191 tokens 29.5 us (172 MB, 5.8 TB/s, 86 %
+// of the copy rate); backward of 4099 tokens 28.5 us (128 MB), of which 24 are the rows (5.3 TB/s: a CTA
+// has 23 rows a group, so that its start is an eighth) and 4.5 the weights' sum behind them.  16 tokens
+// 1.6 us, 257 tokens' backward 4.9 (8 and 2 heads, interleaved): launches and dependent loads.
 #include <type_traits>
 
 #include "kvq_internal.cuh"
@@ -160,6 +166,26 @@ __device__ __forceinline__ void turn(float (&v)[E], const float (&c)[E / 2], con
   }
 }
 
+// The same of neighbouring elements in pairs.
+template <int MODE, int U>
+__device__ __forceinline__ void turn_pairs(uint64_t (&v)[U], const float (&c)[U], const float (&s)[U]) {
+  if constexpr (MODE == kHalfVec) {
+#pragma unroll
+    for (int i = 0; i < U / 2; ++i) {
+      const uint64_t x = v[i], y = v[U / 2 + i], cc = pair2(c[2 * i], c[2 * i + 1]);
+      v[i] = fma2(x, cc, mul2(y, pair2(-s[2 * i], -s[2 * i + 1])));
+      v[U / 2 + i] = fma2(y, cc, mul2(x, pair2(s[2 * i], s[2 * i + 1])));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      float x, y;
+      split2(v[i], x, y);
+      v[i] = pair2(x * c[i] - y * s[i], y * c[i] + x * s[i]);
+    }
+  }
+}
+
 template <int LANES>
 __device__ __forceinline__ float sum_row(float x) {      // over the lanes of a row
 #pragma unroll
@@ -177,7 +203,7 @@ __device__ __forceinline__ void load_weight(float (&w)[E], const float* weight, 
 // ---- forward ---------------------------------------------------------------------------
 // A warp takes 4 ROWS heads of one token, queries or keys: the token's angles and the weight are
 // in registers for all of them, and the elements are asked for before the position, so that its two
-// dependent loads (position, table row) overlap them.
+// dependent loads (position, table row) overlap them (8191 tokens 29.6 us, after it 33.0).
 constexpr int kFwdThreads = 128;
 
 template <int MODE, int ROWS>
@@ -237,8 +263,8 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
 // share of dw, summed over the CTA at the end and over the CTAs by a second kernel, always in the
 // same order.  The elements of the next rows are under way into shared memory by asynchronous
 // copies (a lane reads back its own, so nothing is waited for but them); with the next row in
-// registers instead 4099 tokens of 40 heads took 32.2 us, not 29.0.  4 CTAs an SM spill (32.9),
-// 2 CTAs of 16 elements a lane are as fast.
+// registers instead 4099 tokens of 40 heads took 32.2 us where this took 29.0, 28.5 since two
+// elements share an instruction.  4 CTAs an SM spill (34.5), 2 CTAs of 16 elements a lane: 29.7.
 constexpr int kBwdThreads = 256;
 constexpr int kBwdE = 8;              // elements of a row a lane has
 constexpr int kAhead = 4;             // rows a lane has under way
@@ -255,12 +281,15 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) norm_rope_backward_kern
   constexpr int U = kBwdE / 2, kLanes = kDim / kBwdE, kRowsCta = kBwdThreads / kLanes;
   using Unit = std::conditional_t<kBwdE == 16, uint4, uint2>;      // U elements
   Unit* ring = reinterpret_cast<Unit*>(ring_raw);                  // [kAhead][4][kBwdThreads]
-  float w[kBwdE], dw[kBwdE], c[U], s[U];
-  load_weight(w, x.weight, l, a.rope);
+  float wf[kBwdE], c[U], s[U];
+  load_weight(wf, x.weight, l, a.rope);
+  uint64_t w[U], dw[U];                // pairs of neighbouring elements
 #pragma unroll
-  for (int e = 0; e < kBwdE; ++e) dw[e] = 0.0f;
-#pragma unroll
-  for (int e = 0; e < U; ++e) c[e] = s[e] = 0.0f;
+  for (int e = 0; e < U; ++e) {
+    w[e] = pair2(wf[2 * e], wf[2 * e + 1]);
+    dw[e] = 0;
+    c[e] = s[e] = 0.0f;
+  }
   const int ctas = is_q ? a.q_ctas : static_cast<int>(gridDim.x) - a.q_ctas;
   const long long rows = static_cast<long long>(a.n) * x.heads;
   const long long groups = static_cast<long long>(ctas) * kRowsCta;
@@ -270,20 +299,26 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) norm_rope_backward_kern
   const int mine = static_cast<int>(max(0ll, min(per, rows - r0)));
   int tok = mine > 0 ? static_cast<int>(r0 / x.heads) : 0, head = mine > 0 ? static_cast<int>(r0 % x.heads) : 0;
   bool fresh = true, good = false;
-  int tok_ahead = tok, head_ahead = head;          // of the row that is asked for next
+  // of the row that is asked for next, and of the one that is written
+  int head_ahead = head;
+  const uint16_t* xr = x.x + static_cast<size_t>(tok) * x.x_stride + head * kDim;
+  const uint16_t* dr = x.dy + static_cast<size_t>(tok) * x.dy_stride + head * kDim;
+  uint16_t* to = x.y + static_cast<size_t>(tok) * x.y_stride + head * kDim;
+  const long long gap = static_cast<long long>(x.heads) * kDim;
   auto ask = [&](int i) {
     if (MODE != kScalar && i < mine) {
-      const uint16_t* xr = x.x + static_cast<size_t>(tok_ahead) * x.x_stride + head_ahead * kDim;
-      const uint16_t* dr = x.dy + static_cast<size_t>(tok_ahead) * x.dy_stride + head_ahead * kDim;
-      const uint32_t to = smem_u32(ring + (i % kAhead) * 4 * kBwdThreads + threadIdx.x);
+      const uint32_t at = smem_u32(ring + (i % kAhead) * 4 * kBwdThreads + threadIdx.x);
       constexpr int kStep = static_cast<int>(sizeof(Unit)) * kBwdThreads;
-      copy_async<sizeof(Unit)>(to, xr + l.at0);
-      copy_async<sizeof(Unit)>(to + kStep, xr + l.at1);
-      copy_async<sizeof(Unit)>(to + 2 * kStep, dr + l.at0);
-      copy_async<sizeof(Unit)>(to + 3 * kStep, dr + l.at1);
+      copy_async<sizeof(Unit)>(at, xr + l.at0);
+      copy_async<sizeof(Unit)>(at + kStep, xr + l.at1);
+      copy_async<sizeof(Unit)>(at + 2 * kStep, dr + l.at0);
+      copy_async<sizeof(Unit)>(at + 3 * kStep, dr + l.at1);
+      xr += kDim;
+      dr += kDim;
       if (++head_ahead == x.heads) {
         head_ahead = 0;
-        ++tok_ahead;
+        xr += x.x_stride - gap;
+        dr += x.dy_stride - gap;
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -316,38 +351,52 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) norm_rope_backward_kern
         }
       }
     }
-    float v[kBwdE], d[kBwdE];
-    unpack<kBwdE>(v, rx);
-    unpack<kBwdE>(d, rd);
-    uint16_t* to = x.y + static_cast<size_t>(tok) * x.y_stride + head * kDim;
-    fresh = head + 1 == x.heads;
-    head = fresh ? 0 : head + 1;
-    tok += fresh ? 1 : 0;
-    turn<MODE, kBwdE>(d, c, s);
-    float ss = 0.0f, gx = 0.0f;
+    uint64_t v[U], d[U];
 #pragma unroll
-    for (int e = 0; e < kBwdE; ++e) {
-      ss = fmaf(v[e], v[e], ss);
-      gx = fmaf(d[e] * w[e], v[e], gx);
+    for (int e = 0; e < U; ++e) {
+      v[e] = bf16_pair(rx[e]);
+      d[e] = bf16_pair(rd[e]);
     }
+    turn_pairs<MODE>(d, c, s);
+    uint64_t ss2 = 0, gx2 = 0;
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      ss2 = fma2(v[e], v[e], ss2);
+      gx2 = fma2(mul2(d[e], w[e]), v[e], gx2);
+    }
+    float ss, gx, x1;
+    split2(ss2, ss, x1);
+    ss += x1;
+    split2(gx2, gx, x1);
+    gx += x1;
     const float r = rsqrtf(sum_row<kLanes>(ss) * (1.0f / kDim) + a.eps);
     const float m = sum_row<kLanes>(gx) * r * (1.0f / kDim);
     if (in && good) {
+      const uint64_t r2 = pair2(r, r), m2 = pair2(-m, -m);
+      float y[kBwdE];
 #pragma unroll
-      for (int e = 0; e < kBwdE; ++e) {
-        const float xh = v[e] * r;
-        dw[e] = fmaf(d[e], xh, dw[e]);
-        v[e] = r * (d[e] * w[e] - xh * m);
+      for (int e = 0; e < U; ++e) {
+        const uint64_t xh = mul2(v[e], r2);
+        dw[e] = fma2(d[e], xh, dw[e]);
+        split2(mul2(fma2(xh, m2, mul2(d[e], w[e])), r2), y[2 * e], y[2 * e + 1]);
       }
-      store_row(to, v, l, a.rope);
+      store_row(to, y, l, a.rope);
     }
+    fresh = head + 1 == x.heads;
+    head = fresh ? 0 : head + 1;
+    tok += fresh ? 1 : 0;
+    to += kDim;
+    if (fresh) to += x.y_stride - gap;
   }
   dependents_begin();
+  float sums[kBwdE];
+#pragma unroll
+  for (int e = 0; e < U; ++e) split2(dw[e], sums[2 * e], sums[2 * e + 1]);
 #pragma unroll
   for (int e = 0; e < kBwdE; ++e) {
 #pragma unroll
-    for (int o = kLanes; o < 32; o <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
-    if (lane < kLanes) red[warp][l.dim(e, a.rope)] = dw[e];
+    for (int o = kLanes; o < 32; o <<= 1) sums[e] += __shfl_xor_sync(0xffffffffu, sums[e], o);
+    if (lane < kLanes) red[warp][l.dim(e, a.rope)] = sums[e];
   }
   __syncthreads();
   if (threadIdx.x < kDim) {
@@ -390,8 +439,11 @@ int norm_backward_ctas(int num_sms) { return kBwdCtas * num_sms; }
 
 template <int MODE>
 static cudaError_t forward(const NormArgs& a, int num_sms, cudaStream_t st) {
-  // two rows a group where tokens alone make several waves of warps, else one
-  const bool wide = a.n >= 16 * num_sms;
+  // Two rows a group where one each would be a warp a scheduler or more, else one, for more warps
+  // (tokens of 32 and 8 heads, two rows against one: 8191 29.6 and 33.2 us, 1024 5.0 and 5.9, 256 2.4
+  // and 2.5, 64 the same, 16 1.7 and 1.5; four rows, 8191: 29.2)
+  const int quads = (a.q.x ? (a.q.heads + 3) / 4 : 0) + (a.k.x ? (a.k.heads + 3) / 4 : 0);
+  const bool wide = static_cast<long long>(a.n) * quads >= 4 * num_sms;
   const int per = wide ? 8 : 4;
   const dim3 grid((static_cast<unsigned>(a.n) + kFwdThreads / 32 - 1) / (kFwdThreads / 32),
                   (a.q.x ? (a.q.heads + per - 1) / per : 0) + (a.k.x ? (a.k.heads + per - 1) / per : 0));

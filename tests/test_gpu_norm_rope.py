@@ -118,6 +118,13 @@ def test_large(H, Hkv, n, rot, style):
     Case(H, Hkv, n, rot, style, fused=True, seed=n).check()
 
 
+@pytest.mark.parametrize("rot,style", [(128, "half"), (64, "interleaved"), (20, "half"), (2, "interleaved")])
+@pytest.mark.parametrize("H,Hkv,n", [(5, 5, 700), (6, 3, 401), (10, 5, 203), (9, 9, 101)])
+def test_heads_that_leave_groups_short(rot, style, H, Hkv, n):
+    """Enough tokens for two rows a group, heads that are no multiple of what a warp takes."""
+    Case(H, Hkv, n, rot, style, fused=True, seed=rot + n).check()
+
+
 @pytest.mark.parametrize("weight", [True, False])
 @pytest.mark.parametrize("size,eps", [(1e-4, 1e-6), (1e-4, 0.0), (3e4, 1e-5), (1.0, 0.5), (1e-15, 1e-6)])
 def test_sizes(weight, size, eps):
