@@ -14,12 +14,13 @@
 // ranges, one a CTA; an item that a border cuts leaves partial states for the joining kernel.
 //
 // HBM bounds it: every visible page is read once, by a bulk copy a page into a warp's own ring of
-// three.  Measured, 32 query and 8 KV heads: 16 x 32K 185 us (1.08 GB, 5.8 TB/s, 86 % of the copy
-// rate); the SMs of the GPU's larger clusters get some 15 % less bandwidth each, so equal ranges end
+// three; when a CTA's part of an item ends, the next part's ids and first two pages are under way while
+// the warps wait for one another and join.  Measured, 32 query and 8 KV heads: 16 x 32K 181 us (1.08
+// GB, 6.0 TB/s, 88 % of the copy rate; 187 with the parts one after the other); the SMs of the GPU's larger clusters get some 15 % less bandwidth each, so equal ranges end
 // after 143 to 183 us, and what would even that out costs as much: 2 to 6 times as many CTAs 185 to
 // 193, ranges that shrink towards the end 181 to 200 (windows more), pages by tickets 186 to 213.
-// 64 windows of 4100 positions 88 us (462 MB, 5.2 TB/s): 512 items, 3.4 of their borders a CTA.
-// 1 x 1K 8.2 us on the GPU, two launches and a chain of loads.
+// 64 windows of 4100 positions 86 us (462 MB, 5.4 TB/s; 89 likewise): 512 items, so two or three
+// parts a CTA.  1 x 1K 8.3 us on the GPU, two launches and a chain of loads.
 #include "kvq_internal.cuh"
 
 namespace kvq {
@@ -30,7 +31,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;
 constexpr int kCtasPerSm = 2;
 constexpr int kMinUnits = kWarps;       // pages of a CTA's range at least: one a warp
-constexpr int kItemCost = 32;           // pages that an item counts for beside its own
+constexpr int kItemCost = 40;           // pages that an item counts for beside its own
 constexpr int kFlush = 16;              // pages of a warp between flushes of the accumulators
 constexpr int kMaxCtas = 1024;          // of the grid: sizes the joining kernel's arrays
 constexpr float kLazy = 8.0f;           // log2 by which a reference may lag behind its maximum
@@ -41,6 +42,7 @@ struct __align__(16) Smem {
   int ids[kWarps][kStages];
   float m[kWarps][kMaxG], mv[kWarps][kMaxG], l[kWarps][kMaxG];
   long long red[kWarps];
+  int state[kWarps];                    // the stage that a warp's state is in
 };
 
 // What a sequence's query sees: positions [0, lead) and [first, len), in pages 0 .. sp - 1 and
@@ -93,7 +95,8 @@ struct Start {            // a CTA's range of the line of work
 // An item counts its pages, at least one, and kItemCost more for what it costs a CTA whatever its
 // length (query, page ids and first records to wait for, the warps' states to join): in the line,
 // those units come before its first page.  (64 ragged sequences up to 16K: without 138 us, 8: 119,
-// 16: 108, 32: 98; 64 windows of 4100: 97, 93, 90, 88; 16 x 32K: 185 to 187 whatever.)
+// 16: 108, 32: 98; 64 windows of 4100: 97, 93, 90, 88; 16 x 32K the same whatever.  Since parts
+// overlap: 32: 96.5 and 87.8, 40: 96.2 and 87.0, 48: 96.4 and 87.4.)
 __device__ __forceinline__ int item_units(const Seen& s) { return max(s.pages, 1) + kItemCost; }
 __device__ __forceinline__ void start_line(const Fp8DecodeArgs& a, Start* line, long long* red) {
   const int tid = threadIdx.x;
@@ -166,65 +169,120 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_fp8_kernel(const 
   }
   dependency_wait();
   start_line(a, &line, sm.red);
-  long long cur = line.cur, b_first = line.b_first;
-  const long long end = line.end, per = line.per;
-  int b = line.b;
   if (tid == 0) a.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
   const size_t page_stride = static_cast<size_t>(a.Hkv) * kFp8Rec;
   uint32_t used = 0;                 // ring stages so far
   bool alive = true;
 
-  while (cur < end) {
-    Seen s = seen_of(a, b);
+  // The part of an item that this CTA works on, and the warp's pages of it.
+  long long cur = line.cur, b_first = line.b_first;
+  int b = line.b, kv = 0, j0 = 0, j1 = 0, count = 0;
+  Seen s = {};
+  int blk = 0, ids = -1, ids_next = -1;
+  auto page_of = [&](int i) {        // the warp's i-th page
+    const int j = j0 + warp + kWarps * i;
+    return j < s.sp ? j : j + s.skip;
+  };
+  auto load_ids = [&](int k) {
+    const int i = 32 * k + lane;
+    return i < count ? a.page_table[static_cast<size_t>(b) * a.max_pages + page_of(i)] : -1;
+  };
+  auto first_page = [&]() { return b_first + static_cast<long long>(kv) * item_units(s) + kItemCost; };   // in the line
+  // the part at `cur`, false where the range ends (before the item's first page)
+  auto begin = [&]() {
+    if (cur >= line.end) return false;
+    s = seen_of(a, b);
     while (cur >= b_first + static_cast<long long>(item_units(s)) * a.Hkv) {     // ends: cur < total
       b_first += static_cast<long long>(item_units(s)) * a.Hkv;
       s = seen_of(a, ++b);
     }
-    const int units = max(s.pages, 1);
-    const int kv = static_cast<int>((cur - b_first) / item_units(s));
-    const long long item = b_first + static_cast<long long>(kv) * item_units(s) + kItemCost;   // its first page
-    const int j0 = static_cast<int>(max(cur - item, 0ll));
-    const int j1 = static_cast<int>(min(static_cast<long long>(units), end - item));
-    if (j1 <= 0) break;                // the range ends before the item's first page
-    const int jp = min(j1, s.pages);                                        // pages j0 .. jp - 1
-    const int count = jp - j0 > warp ? (jp - j0 - warp + kWarps - 1) / kWarps : 0;
-    const int32_t* ptab = a.page_table + static_cast<size_t>(b) * a.max_pages;
-    const uint8_t* pool_kv = a.pool + static_cast<size_t>(kv) * kFp8Rec;
-    auto page_of = [&](int i) {      // the warp's i-th page
-      const int j = j0 + warp + kWarps * i;
-      return j < s.sp ? j : j + s.skip;
-    };
-    auto load_ids = [&](int blk) {
-      const int i = 32 * blk + lane;
-      return i < count ? ptab[page_of(i)] : -1;
-    };
-    int blk = 0, ids = load_ids(0), ids_next = load_ids(1);
-    auto issue = [&](int i) {
-      if ((i >> 5) != blk) {
-        blk = i >> 5;
-        ids = ids_next;
-        ids_next = load_ids(blk + 1);
+    kv = static_cast<int>((cur - b_first) / item_units(s));
+    const long long item = first_page();
+    j0 = static_cast<int>(max(cur - item, 0ll));
+    j1 = static_cast<int>(min(static_cast<long long>(max(s.pages, 1)), line.end - item));
+    if (j1 <= 0) return false;
+    const int jp = min(j1, s.pages);                                             // pages j0 .. jp - 1
+    count = jp - j0 > warp ? (jp - j0 - warp + kWarps - 1) / kWarps : 0;
+    blk = 0;
+    ids = load_ids(0);
+    ids_next = load_ids(1);
+    return true;
+  };
+  auto issue = [&](int i) {
+    if ((i >> 5) != blk) {
+      blk = i >> 5;
+      ids = ids_next;
+      ids_next = load_ids(blk + 1);
+    }
+    const int id = __shfl_sync(0xffffffffu, ids, i & 31);
+    if (lane == 0) {
+      const int slot = (used + i) % kStages;
+      const uint32_t bar = smem_u32(&sm.bar[warp][slot]);
+      const bool ok = id >= 0 && id < a.num_pool_pages;
+      sm.ids[warp][slot] = ok ? id : -1;
+      if (ok) {
+        mbar_arrive_expect_tx(bar, kFp8Rec);
+        bulk_g2s(smem_u32(sm.ring[warp][slot]),
+                 a.pool + static_cast<size_t>(kv) * kFp8Rec + static_cast<size_t>(id) * page_stride, kFp8Rec, bar);
+      } else {
+        atomicOr(a.status, KVQ_STATUS_BAD_PAGE);
+        mbar_arrive(bar);
       }
-      const int id = __shfl_sync(0xffffffffu, ids, i & 31);
-      if (lane == 0) {
-        const int slot = (used + i) % kStages;
-        const uint32_t bar = smem_u32(&sm.bar[warp][slot]);
-        const bool ok = id >= 0 && id < a.num_pool_pages;
-        sm.ids[warp][slot] = ok ? id : -1;
-        if (ok) {
-          mbar_arrive_expect_tx(bar, kFp8Rec);
-          bulk_g2s(smem_u32(sm.ring[warp][slot]), pool_kv + static_cast<size_t>(id) * page_stride, kFp8Rec, bar);
+    }
+  };
+  bool have = false, whole = false;  // a part whose states are to be joined; into `to`: all of an item
+  float* to = nullptr;
+  while (true) {
+    // the next part's ids and first copies are under way while the warps wait for one another and join
+    const bool more = alive && begin();
+    __syncwarp();
+    if (have && lane == 0) fence_proxy_async();      // the stages were read
+    if (more)
+#pragma unroll 1
+      for (int k = 0; k < kStages - 1 && k < count; ++k) issue(k);
+    if (have) {
+      const bool stop = __syncthreads_or(!alive);
+      for (int e = tid; e < a.G * kDim; e += kThreads) {
+        const int h = e / kDim, d = e % kDim;
+        float M = -INFINITY, MV = -INFINITY, L = 0.0f, o = 0.0f, state[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          state[w] = reinterpret_cast<const float*>(sm.ring[w][sm.state[w]])[e];
+          M = fmaxf(M, sm.m[w][h]);
+          MV = fmaxf(MV, sm.mv[w][h]);
+        }
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          // a warp without a token has l = 0 (one that met a NaN logit has l = NaN and no maximum)
+          const float x = sm.m[w][h], y = sm.mv[w][h], lw = sm.l[w][h];
+          if (lw == 0.0f) continue;
+          L = fmaf(x == M ? 1.0f : fast_exp2(x - M), lw, L);
+          o = fmaf(y == MV ? 1.0f : fast_exp2(y - MV), state[w], o);
+        }
+        if (whole) {
+          to[e] = L == 0.0f ? 0.0f : o * (MV == M ? 1.0f : fast_exp2(MV - M)) / L;
         } else {
-          atomicOr(a.status, KVQ_STATUS_BAD_PAGE);
-          mbar_arrive(bar);
+          float* p = to + h * kPartStride;
+          p[4 + d] = o;
+          if (d == 0) {
+            p[0] = M;
+            p[1] = L;
+            p[2] = MV;
+          }
         }
       }
-    };
-    if (lane == 0) fence_proxy_async();      // the last item's state was written over the ring
+      __syncthreads();
+      if (stop) {                  // a wait ran out: what this warp asked for has to land
+        if (more)
+          for (int k = 0; k < kStages - 1 && k < count; ++k)
+            mbar_drain(smem_u32(&sm.bar[warp][(used + k) % kStages]), ((used + k) / kStages) & 1);
+        break;
+      }
+    }
+    if (!more) break;
+    if (have && lane == 0) fence_proxy_async();      // a state was written over the last stage
     __syncwarp();
-    for (int i = 0; i < kStages && i < count; ++i) issue(i);
-    __syncwarp();
-
+    if (count >= kStages) issue(kStages - 1);
     uint32_t qf[16];
     const float up = query_frags(a, b, kv, lane, qf);
     const float kq = a.log2_scale * up;
@@ -334,8 +392,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_fp8_kernel(const 
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
 
-    // the warps' states, each over its own ring (its copies have landed), then joined
-    float* mine = reinterpret_cast<float*>(sm.ring[warp][0]);
+    // the warps' states, each in a stage of its own ring (its copies have landed), then joined
+    float* mine = reinterpret_cast<float*>(sm.ring[warp][(used + kStages - 1) % kStages]);
+    if (lane == 0) sm.state[warp] = (used + kStages - 1) % kStages;
     if (t < a.G) {
 #pragma unroll
       for (int mb = 0; mb < 8; ++mb) {
@@ -348,42 +407,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_fp8_kernel(const 
         sm.l[warp][t] = l;
       }
     }
-    const bool stop = __syncthreads_or(!alive);
-    const bool whole = j0 == 0 && j1 == units;
-    for (int e = tid; e < a.G * kDim; e += kThreads) {
-      const int h = e / kDim, d = e % kDim;
-      float M = -INFINITY, MV = -INFINITY, L = 0.0f, o = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        M = fmaxf(M, sm.m[w][h]);
-        MV = fmaxf(MV, sm.mv[w][h]);
-      }
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        // a warp without a token has l = 0 (one that met a NaN logit has l = NaN and no maximum)
-        const float x = sm.m[w][h], y = sm.mv[w][h], lw = sm.l[w][h];
-        if (lw == 0.0f) continue;
-        L = fmaf(x == M ? 1.0f : fast_exp2(x - M), lw, L);
-        o = fmaf(y == MV ? 1.0f : fast_exp2(y - MV), reinterpret_cast<const float*>(sm.ring[w][0])[e], o);
-      }
-      if (whole) {
-        a.out[(static_cast<size_t>(b) * a.H + kv * a.G + h) * kDim + d] =
-            L == 0.0f ? 0.0f : o * (MV == M ? 1.0f : fast_exp2(MV - M)) / L;
-      } else {
-        float* p = a.part + (static_cast<size_t>(2 * blockIdx.x + (j0 == 0 ? 1 : 0)) * kMaxG + h) * kPartStride;
-        p[4 + d] = o;
-        if (d == 0) {
-          p[0] = M;
-          p[1] = L;
-          p[2] = MV;
-        }
-      }
-    }
+    // where the joined state goes
+    const int units = max(s.pages, 1);
+    const long long item = first_page();
+    whole = j0 == 0 && j1 == units;
+    to = whole ? a.out + (static_cast<size_t>(b) * a.H + kv * a.G) * kDim
+               : a.part + static_cast<size_t>(2 * blockIdx.x + (j0 == 0 ? 1 : 0)) * kMaxG * kPartStride;
     if (tid == 0 && j0 > 0)     // an item that CTAs before this one began: what joining it takes
-      a.cuts[blockIdx.x] = make_int4(b, kv, static_cast<int>(item / per), static_cast<int>((item + units - 1) / per));
-    __syncthreads();
-    if (stop) break;
+      a.cuts[blockIdx.x] = make_int4(b, kv, static_cast<int>(item / line.per),
+                                     static_cast<int>((item + units - 1) / line.per));
     cur = item + j1;
+    have = true;
   }
   dependents_begin();
 }
