@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_append_kernel(const __grid_co
   __shared__ int count;
   __shared__ __align__(16) uint8_t stages[kWarps][2][kStage];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  dependency_wait();
   const int n_units = find_units<false>(a, blockIdx.x * rows, rows, units, &count);
   const int kv0 = blockIdx.y * kWarps, heads = min(kWarps, a.Hkv - kv0);
   uint8_t *sk = stages[warp][0], *sv = stages[warp][1];
@@ -298,6 +299,7 @@ __global__ void __launch_bounds__(kThreads) fp8_read_kernel(const __grid_constan
   __shared__ int count;
   __shared__ __align__(16) uint8_t stages[kWarps][kPage * kPitch];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  dependency_wait();
   const int n_units = find_units<true>(a, blockIdx.x * rows, rows, units, &count);
   const int kv0 = blockIdx.y * kWarps, heads = min(kWarps, a.Hkv - kv0);
   uint8_t* stage = stages[warp];
@@ -366,15 +368,13 @@ int rows_per_cta(const Fp8RowArgs& a, int num_sms) {
 cudaError_t launch_fp8_append(const Fp8RowArgs& a, int num_sms, cudaStream_t st) {
   const int rows = rows_per_cta(a, num_sms);
   const dim3 grid((static_cast<unsigned>(a.n) + rows - 1) / rows, (a.Hkv + kWarps - 1) / kWarps);
-  fp8_append_kernel<<<grid, kThreads, 0, st>>>(a, rows);
-  return cudaGetLastError();
+  return launch_dependent(fp8_append_kernel, grid, dim3(kThreads), 0, st, a, rows);
 }
 
 cudaError_t launch_fp8_read(const Fp8RowArgs& a, int num_sms, cudaStream_t st) {
   const int rows = rows_per_cta(a, num_sms);
   const dim3 grid((static_cast<unsigned>(a.n) + rows - 1) / rows, (a.Hkv + kWarps - 1) / kWarps);
-  fp8_read_kernel<<<grid, kThreads, 0, st>>>(a, rows);
-  return cudaGetLastError();
+  return launch_dependent(fp8_read_kernel, grid, dim3(kThreads), 0, st, a, rows);
 }
 
 }  // namespace kvq

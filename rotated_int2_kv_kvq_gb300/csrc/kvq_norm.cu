@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(kFwdThreads) norm_rope_kernel(const __grid_con
   const uint16_t* xr = x.x + static_cast<size_t>(tok) * x.x_stride;
   uint16_t* yr = x.y + static_cast<size_t>(tok) * x.y_stride;
   const Lane<MODE, 16> l(lane, a.rope);
+  dependency_wait();
   const int pos = a.positions[tok];
   uint32_t raw[ROWS][8];
 #pragma unroll
@@ -281,6 +282,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) norm_rope_backward_kern
   constexpr int U = kBwdE / 2, kLanes = kDim / kBwdE, kRowsCta = kBwdThreads / kLanes;
   using Unit = std::conditional_t<kBwdE == 16, uint4, uint2>;      // U elements
   Unit* ring = reinterpret_cast<Unit*>(ring_raw);                  // [kAhead][4][kBwdThreads]
+  dependency_wait();
   float wf[kBwdE], c[U], s[U];
   load_weight(wf, x.weight, l, a.rope);
   uint64_t w[U], dw[U];                // pairs of neighbouring elements
@@ -447,9 +449,8 @@ static cudaError_t forward(const NormArgs& a, int num_sms, cudaStream_t st) {
   const int per = wide ? 8 : 4;
   const dim3 grid((static_cast<unsigned>(a.n) + kFwdThreads / 32 - 1) / (kFwdThreads / 32),
                   (a.q.x ? (a.q.heads + per - 1) / per : 0) + (a.k.x ? (a.k.heads + per - 1) / per : 0));
-  if (wide) norm_rope_kernel<MODE, 2><<<grid, kFwdThreads, 0, st>>>(a);
-  else norm_rope_kernel<MODE, 1><<<grid, kFwdThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(wide ? norm_rope_kernel<MODE, 2> : norm_rope_kernel<MODE, 1>, grid, dim3(kFwdThreads), 0,
+                          st, a);
 }
 
 cudaError_t launch_norm_rope(const NormArgs& a, int num_sms, cudaStream_t st) {
@@ -472,8 +473,7 @@ static cudaError_t backward(const NormArgs& a, int ctas, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  norm_rope_backward_kernel<MODE><<<ctas, kBwdThreads, kSmem, st>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(norm_rope_backward_kernel<MODE>, dim3(ctas), dim3(kBwdThreads), kSmem, st, a);
 }
 
 cudaError_t launch_norm_rope_backward(NormArgs a, int num_sms, cudaStream_t st) {
@@ -496,18 +496,8 @@ cudaError_t launch_norm_rope_backward(NormArgs a, int num_sms, cudaStream_t st) 
     }
     if (e != cudaSuccess) return e;
   }
-  // a programmatic dependent: it is launched while the first kernel ends
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kDim / 32, 2);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = st;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_weight_kernel, a, a.n > 0 ? g : 0);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  // launched while the first kernel ends
+  return launch_dependent(norm_weight_kernel, dim3(kDim / 32, 2), dim3(1024), 0, st, a, a.n > 0 ? g : 0);
 }
 
 }  // namespace kvq

@@ -1335,6 +1335,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     first_bad[0] = 0xffffffffu;
     if constexpr (FP8) looks[0] = Look{0xffffffffu, 0u, {}};
   }
+  if constexpr (FP8) dependency_wait();
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      sb + Smem::kTmem)
@@ -2044,19 +2045,17 @@ cudaError_t launch(const PrefillArgs& a, int num_sms, cudaStream_t st) {
     if (fa.numRegs != kRegLaunch) return cudaErrorInvalidConfiguration;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  prefill_kernel<INT2, FP8><<<num_sms, kThreads, kSmem, st>>>(a);
+  if constexpr (FP8) {
+    const cudaError_t e =
+        launch_dependent(prefill_kernel<INT2, FP8>, dim3(num_sms), dim3(kThreads), kSmem, st, a);
+    if (e != cudaSuccess) return e;
+  } else {
+    prefill_kernel<INT2, FP8><<<num_sms, kThreads, kSmem, st>>>(a);
+  }
   if (num_sms > 1) {
     // a programmatic dependent: it is launched while the first kernel ends
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(num_sms - 1, kRows / kJoinRows);
-    cfg.blockDim = dim3(128);
-    cfg.stream = st;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_combine_kernel, a);
+    const cudaError_t e =
+        launch_dependent(prefill_combine_kernel, dim3(num_sms - 1, kRows / kJoinRows), dim3(128), 0, st, a);
     if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();
