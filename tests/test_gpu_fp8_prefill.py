@@ -407,3 +407,54 @@ def test_prompt_in_chunks_then_steps(window, sinks):
                                    * float(yq[:, h].double().abs().sum(-1).max()) / math.sqrt(D)
                                    * float(vals.abs().max())) * math.sqrt(D)
         assert torch.all(err <= 2.0 ** -8 * o.norm(dim=1) + (2.0 ** -8 + 2.0 ** -11) * mag.norm(dim=1) + late)
+
+
+def test_each_call_sees_what_came_before_it():
+    """Calls back to back, each on what the last one or a torch kernel has just written, eagerly and in a
+    graph, give the bits that they give with the GPU idle before each."""
+    total = 3000
+    c = Cache8(8, 2, [total], seed=19, fill=False)
+    table = torch.randn(total, D, generator=c.g, device="cuda")
+    rope = K.make_rope(table, "half")
+    x, k, v = c.randn(total, 8), c.randn(total, 2), c.randn(total, 2)
+    pos, chunks = i32(range(total)), [(0, 1500), (1500, 1501), (1501, 2200), (2200, 3000)]
+    fixed = [(cu_of([b - a]), i32([b])) for a, b in chunks]
+    ws = [torch.empty(max(K.kvq_fp8_prefill_workspace_bytes(c.h, 1, total), K.kvq_fp8_workspace_bytes(c.h, 1)),
+                      dtype=torch.uint8, device="cuda") for _ in range(2)]
+
+    def chain(after=lambda: None):
+        got, pool = [], torch.full_like(c.pool, 255)
+        after()
+        for (a, b), (cu, sl) in zip(chunks, fixed):
+            n = b - a
+            q0, k0 = x[a:b] * 2, k[a:b] * 0.5                      # torch kernels write what the norms read
+            yq, yk = torch.empty_like(q0), torch.empty_like(k0)
+            after()
+            K.kvq_norm_rope(c.h, q0, k0, yq, yk, None, None, 1e-6, pos[a:b], rope)
+            after()
+            yk.mul_(1.5)
+            after()
+            K.kvq_fp8_append(c.h, pool, c.pages, yk, v[a:b], cu, c.pt, sl)
+            after()
+            out, one = torch.zeros_like(yq), torch.zeros(1, 8, D, device="cuda")
+            back = [torch.zeros_like(yk) for _ in range(2)]
+            after()
+            K.kvq_fp8_read(c.h, pool, c.pages, back[0], back[1], cu, c.pt, sl)
+            after()
+            K.kvq_fp8_prefill(c.h, pool, c.pages, yq, cu, c.pt, sl, out, ws[0], window=800, sinks=3)
+            after()
+            K.kvq_fp8_decode(c.h, pool, c.pages, out[n - 1:], c.pt, sl, one, ws[1], window=90)
+            after()
+            got += [yq, yk, *back, out, one * 1]
+        return got
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(chain(), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and K.kvq_get_status(c.h) == 0
