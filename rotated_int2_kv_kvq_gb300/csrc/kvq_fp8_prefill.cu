@@ -30,12 +30,13 @@
 // output bounds it, as it does the other caches'.  Spills and instructions count most: registers
 // 168 / 112 / 64 with 68 bytes of the softmax's spilled 1585, 168 / 120 / 56 with the issuing warp's
 // 1940, 160 / 128 / 64 2270.
-// A prompt of 8191 tokens with a window of 1024: 241 us for products of 68.  Ten key tiles an item where
+// A prompt of 8191 tokens with a window of 1024: 238 us for products of 68.  Ten key tiles an item where
 // eight hold its window, a third of them partly hidden (2.3 us of softmax for 1.4); and 9 us an item,
 // seven items a CTA, for its queries (3), the first scores (1.5), results (2.4) and the wait for the
 // other row tile's.  Queries by plain loads when the item begins: 273.
-// Eight drafts of five tokens at 8K: 67 us; launches, the line's setup, first loads and the join are
-// about half, and a tile of one row tile takes 1.9 us, as long as its producers need.
+// Eight drafts of five tokens at 8K: 64 us, 27 key tiles a CTA of 1.65 us each: with one row tile the
+// chain stage free -> values converted -> product, two stages deep, is the longest (the conversion left
+// out: 59; waiting for nothing but values: no change).
 #include "kvq_internal.cuh"
 
 namespace kvq {

@@ -11,10 +11,10 @@
 // a pair of the rotation is in one lane and the sums over a row are a few shuffles.
 //
 // Both directions are bound by HBM: each element is read once and written once (backward: two read).
-// Measured, 32 query and 8 key heads, rot_dim 128: forward of 8191 tokens 29.5 us (172 MB, 5.8 TB/s, 86 %
-// of the copy rate); backward of 4099 tokens 28.5 us (128 MB), of which 24 are the rows (5.3 TB/s: a CTA
+// Measured, 32 query and 8 key heads, rot_dim 128: forward of 8191 tokens 29.3 us (172 MB, 5.9 TB/s, 86 %
+// of the copy rate); backward of 4099 tokens 28.2 us (128 MB), of which 24 are the rows (5.3 TB/s: a CTA
 // has 23 rows a group, so that its start is an eighth) and 4.5 the weights' sum behind them.  16 tokens
-// 1.6 us, 257 tokens' backward 4.9 (8 and 2 heads, interleaved): launches and dependent loads.
+// 1.4 us, 257 tokens' backward 4.7 (8 and 2 heads, interleaved): launches and dependent loads.
 #include <type_traits>
 
 #include "kvq_internal.cuh"
