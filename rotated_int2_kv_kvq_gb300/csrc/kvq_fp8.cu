@@ -12,9 +12,9 @@
 //
 // Both directions move bytes; what bounds them is the chain of a short CTA's loads (sequence, its
 // lengths, page id, rows) and their instructions.  Measured, 3 ragged prompts of 32767 tokens in all,
-// 8 KV heads: append 39 us (201 MB, 5.1 TB/s), reading 49152 positions 48 us (302 MB, 6.3 TB/s, 93 % of
-// the copy rate).  Append: pages that a call fills whole without the masks of part pages (44 us with
-// them).  Tried and slower: keys and values one after the other with 3 or 4 CTAs an SM in place of 2
+// 8 KV heads: append 37 us (201 MB, 5.5 TB/s), reading 49152 positions 48 us (302 MB, 6.2 TB/s, 92 % of
+// the copy rate).  Append: pages that a call fills whole without the masks of part pages (5 us less), a
+// sequence's rows and lengths in one load (1.4 less).  Tried and slower: keys and values one after the other with 3 or 4 CTAs an SM in place of 2
 // (+1 to +2 us), 32 to 128 rows a CTA (+0.3 to +12), one warp that finds all of a CTA's units (+4).
 // A step of 64 sequences: 10 us for both, nearly all of it launches and that chain.
 #include <type_traits>
@@ -34,16 +34,24 @@ struct Unit {
   int page;                             // id, or -1
 };
 
-// The sequence of row i: the last b with cu[b] <= i, by 32 probes a step.
-__device__ __forceinline__ int find_sequence(const int32_t* cu, int batch, int i, int lane) {
-  int lo = 0, hi = batch;
-  while (hi - lo > 1) {
+// The sequence of row i, the last b with cu[b] <= i: by 32 probes a step down to 32 candidates, whose
+// rows and lengths are read at once (a load less in a chain of five).
+struct Owner {
+  int b, r0, r1, len;
+};
+__device__ __forceinline__ Owner find_owner(const Fp8RowArgs& a, int i, int lane) {
+  int lo = 0, hi = a.batch;
+  while (hi - lo > 32) {
     const int step = (hi - lo + 31) / 32, p = lo + (lane + 1) * step;
-    const unsigned below = __ballot_sync(0xffffffffu, p < hi && cu[p] <= i);
+    const unsigned below = __ballot_sync(0xffffffffu, p < hi && a.cu[p] <= i);
     lo += __popc(below) * step;
     hi = min(lo + step, hi);
   }
-  return lo;
+  const int p = min(lo + lane, hi - 1);
+  const int r0 = a.cu[p], r1 = a.cu[p + 1], len = a.seq_lens[p];
+  const int own = max(__popc(__ballot_sync(0xffffffffu, lo + lane < hi && r0 <= i)) - 1, 0);
+  return Owner{lo + own, __shfl_sync(0xffffffffu, r0, own), __shfl_sync(0xffffffffu, r1, own),
+               __shfl_sync(0xffffffffu, len, own)};
 }
 
 // The leaders among rows [row0, row0 + rows) as units in shared memory.  A sequence whose
@@ -64,8 +72,8 @@ __device__ __forceinline__ int find_units(const Fp8RowArgs& a, int row0, int row
   for (int k = warp; k < rows; k += kWarps) {
     const int i = row0 + k;
     if (i >= a.n) break;
-    const int b = find_sequence(a.cu, a.batch, i, lane);
-    const int r0 = a.cu[b], r1 = a.cu[b + 1], len = a.seq_lens[b];
+    const Owner o = find_owner(a, i, lane);
+    const int b = o.b, r0 = o.r0, r1 = o.r1, len = o.len;
     if (r0 < 0 || i < r0 || i >= r1 || r1 > a.n) continue;
     const bool ok = len >= r1 - r0 && len <= a.max_pages * kPage;
     if (!ok && !KEEP_BAD) continue;
