@@ -12,9 +12,9 @@
 //
 // Both directions are bound by HBM: each element is read once and written once (backward: two read).
 // Measured, 32 query and 8 key heads, rot_dim 128: forward of 8191 tokens 29.3 us (172 MB, 5.9 TB/s, 86 %
-// of the copy rate); backward of 4099 tokens 28.2 us (128 MB), of which 24 are the rows (5.3 TB/s: a CTA
-// has 23 rows a group, so that its start is an eighth) and 4.5 the weights' sum behind them.  16 tokens
-// 1.4 us, 257 tokens' backward 4.7 (8 and 2 heads, interleaved): launches and dependent loads.
+// of the copy rate); backward of 4099 tokens 27.8 us (128 MB), of which 24 are the rows (5.3 TB/s: a CTA
+// has 23 rows a group, so that its start is an eighth) and 4 the weights' sum behind them.  16 tokens
+// 1.4 us, 257 tokens' backward 4.0 (8 and 2 heads, interleaved): launches and dependent loads.
 #include <type_traits>
 
 #include "kvq_internal.cuh"
@@ -409,24 +409,30 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) norm_rope_backward_kern
   }
 }
 
-// dw of the queries or the keys: 32 elements a CTA, the CTAs' parts in order.
+// dw of the queries or the keys: 8 elements a CTA, a warp 4 of the CTAs' parts at a time, always in the
+// same order (32 elements a CTA, a part a warp: 0.5 us more).
 __global__ void __launch_bounds__(1024) norm_weight_kernel(const __grid_constant__ NormArgs a, int ctas) {
-  __shared__ float red[32][32];
+  __shared__ float red[32][8];
   dependency_wait();
   float* dw = blockIdx.y == 0 ? a.q.dw : a.k.dw;
   if (!dw) return;
   const int first = blockIdx.y == 0 ? 0 : a.q_ctas, parts = (blockIdx.y == 0 ? a.q_ctas : ctas) - first;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float* p = a.part + static_cast<size_t>(first) * kDim + blockIdx.x * 32 + lane;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 8 + (lane & 7);
+  const float* p = a.part + static_cast<size_t>(first) * kDim + col;
   float sum = 0.0f;
-#pragma unroll 8
-  for (int i = warp; i < parts; i += 32) sum += p[static_cast<size_t>(i) * kDim];
-  red[warp][lane] = sum;
+#pragma unroll 4
+  for (int i = 4 * warp + (lane >> 3); i < parts; i += 128) sum += p[static_cast<size_t>(i) * kDim];
+  sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+  if (lane < 8) red[warp][lane] = sum;
   __syncthreads();
   if (warp == 0) {
+    sum = 0.0f;
 #pragma unroll
-    for (int i = 1; i < 32; ++i) sum += red[i][lane];
-    dw[blockIdx.x * 32 + lane] = sum;
+    for (int i = 0; i < 8; ++i) sum += red[8 * (lane >> 3) + i][lane & 7];
+    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+    if (lane < 8) dw[col] = sum;
   }
 }
 
@@ -497,7 +503,7 @@ cudaError_t launch_norm_rope_backward(NormArgs a, int num_sms, cudaStream_t st) 
     if (e != cudaSuccess) return e;
   }
   // launched while the first kernel ends
-  return launch_dependent(norm_weight_kernel, dim3(kDim / 32, 2), dim3(1024), 0, st, a, a.n > 0 ? g : 0);
+  return launch_dependent(norm_weight_kernel, dim3(kDim / 8, 2), dim3(1024), 0, st, a, a.n > 0 ? g : 0);
 }
 
 }  // namespace kvq
