@@ -390,6 +390,7 @@ def kvq_rope_table(table: torch.Tensor, scaling: KvqRopeScaling, stream=None) ->
 
 # The calls of a decode step are bound by this module's own time, so the functions
 # below look at each tensor once and hand plain integers to ctypes.
+_TENSOR = torch.Tensor        # its type compared first: isinstance is slower
 
 def _raw_stream(stream, device: int) -> int:
     """`stream`, or the current stream of the device the tensors are on."""
@@ -411,16 +412,16 @@ def _wrong(t, dtypes, device, name):
 
 def _at(t, dtypes, device, name):
     """Address of a contiguous tensor of one of `dtypes` on CUDA device `device`."""
-    if (not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.get_device() != device
-            or not t.is_contiguous()):
+    if ((type(t) is not _TENSOR and not isinstance(t, _TENSOR)) or t.dtype not in dtypes
+            or t.get_device() != device or not t.is_contiguous()):
         _wrong(t, dtypes, device, name)
     return t.data_ptr()
 
 
 def _vec(t, n, device, name):
     """Address of an int32 [n] tensor."""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != device
-            or not t.is_contiguous()):
+    if ((type(t) is not _TENSOR and not isinstance(t, _TENSOR)) or t.dtype not in _I32
+            or t.get_device() != device or not t.is_contiguous()):
         _wrong(t, _I32, device, name)
     if t.shape != (n,):
         raise ValueError(f"{name}: expected [{n}], got {tuple(t.shape)}")
@@ -439,12 +440,15 @@ def _table2(t, device):
 def _rows(t, device, name, heads=None):
     """(address, token stride, n, heads) of bf16 rows [n, heads, 128]; only the tokens may be
     strided."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in _BF16 or t.get_device() != device:
+    if ((type(t) is not _TENSOR and not isinstance(t, _TENSOR)) or t.dtype not in _BF16
+            or t.get_device() != device):
         _wrong(t, _BF16, device, name)
-    shape = t.shape
-    if len(shape) != 3 or shape[2] != 128 or (heads is not None and shape[1] != heads):
-        raise ValueError(f"{name}: expected [n, {heads or 'heads'}, 128], got {tuple(shape)}")
-    n, hh = shape[0], shape[1]
+    try:
+        n, hh, d = t.shape
+    except ValueError:
+        d = 0
+    if d != 128 or (heads is not None and hh != heads):
+        raise ValueError(f"{name}: expected [n, {heads or 'heads'}, 128], got {tuple(t.shape)}")
     if t.is_contiguous():
         return t.data_ptr(), hh * 128, n, hh
     s0, s1, s2 = t.stride()
