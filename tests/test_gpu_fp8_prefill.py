@@ -458,3 +458,59 @@ def test_each_call_sees_what_came_before_it():
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and K.kvq_get_status(c.h) == 0
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_behind_copies_and_other_streams(captured):
+    """What a call reads comes from a copy, a memset and kernels of another stream that its own stream waits
+    for; what it writes is read in another stream."""
+    n = 600
+    c = Cache8(8, 2, [n], seed=20, fill=False)
+    rope = K.make_rope(torch.randn(n, D, generator=c.g, device="cuda"), "half")
+    x, k, v = c.randn(n, 8, scale=2.0), c.randn(n, 2), c.randn(n, 2)
+    pos, cu, sl = i32(range(n)), cu_of([n]), c.seq_lens
+    ws = torch.empty(K.kvq_fp8_prefill_workspace_bytes(c.h, 1, n), dtype=torch.uint8, device="cuda")
+    q0, v0, yq, yk, out = (torch.empty_like(t) for t in (x, v, x, k, x))
+    big, res = torch.empty(1 << 26, device="cuda"), torch.empty_like(x)
+    side = torch.cuda.Stream()
+
+    def run():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        q0.copy_(x)                                # a copy right before the norms
+        K.kvq_norm_rope(c.h, q0, k, yq, yk, None, None, 1e-6, pos, rope)
+        with torch.cuda.stream(side):
+            big.fill_(1.0)                         # long enough for the main stream to be ahead
+            v0.copy_(v * big[0])
+        c.pool.zero_()                             # a memset
+        main.wait_stream(side)
+        K.kvq_fp8_append(c.h, c.pool, c.pages, yk, v0, cu, c.pt, sl)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            K.kvq_fp8_prefill(c.h, c.pool, c.pages, yq, cu, c.pt, sl, out, ws, window=100)
+            res.copy_(out)
+        main.wait_stream(side)
+
+    run()
+    torch.cuda.synchronize()
+    c.pool.zero_()
+    torch.cuda.synchronize()
+    K.kvq_norm_rope(c.h, x, k, yq, yk, None, None, 1e-6, pos, rope)
+    torch.cuda.synchronize()
+    c.append(yk, v, [n])
+    torch.cuda.synchronize()
+    want = c.prefill(yq, [n], 100)
+    torch.cuda.synchronize()
+    assert torch.equal(res, want)
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+    for _ in range(3):
+        for t in (q0, v0, yq, yk, out, res):
+            t.fill_(7.0)
+        torch.cuda.synchronize()
+        graph.replay() if captured else run()
+        torch.cuda.synchronize()
+        assert torch.equal(res, want)
+    assert K.kvq_get_status(c.h) == 0
