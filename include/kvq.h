@@ -576,7 +576,8 @@ int kvq_fp8_read(kvq_handle* h, const void* pool, int num_pool_pages, uint16_t* 
  *     t >= len - window  or  t < sinks          (window = 0: all of them)
  * that is, a sliding window that holds the token itself and the first `sinks` tokens, which stay
  * visible.  Pages without a visible position are not read, and need not exist.  Products are of
- * fp32 accuracy, sums and statistics fp32.  A NaN among the visible keys makes a head's output
+ * fp32 accuracy, whatever the pages' scales (a weight's error is 2^-23 of it, or 2^-30 of the largest
+ * weight if that is more), sums and statistics fp32.  A NaN among the visible keys makes a head's output
  * NaN, one among the values its element.
  *   q         : device bf16 [batch][H][D], 4-byte aligned.   out : device fp32 [batch][H][D].
  *   window, sinks : >= 0 (sinks has no effect without a window).

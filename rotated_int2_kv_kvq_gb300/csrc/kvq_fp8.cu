@@ -128,7 +128,6 @@ __device__ __forceinline__ int exponent_for(uint32_t bits) {
   const int e = static_cast<int>(bits >> 7) - 127 - ((bits & 0x7fu) <= 0x60u ? 8 : 7);
   return max(e, kFp8MinExp);
 }
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 // Whether a stored scale is one of this library's, and its exponent.
 __device__ __forceinline__ bool scale_exponent(uint32_t bits, int& e) {
   e = static_cast<int>(bits >> 23) - 127;

@@ -5,10 +5,12 @@
 // and a page is the M = 16 tokens of an mma.sync tile, so no entry is ever scaled: codes become
 // fp16 operands by one conversion a pair, and the two factors go into the page's scores,
 //   logit_t = scale 2^ek (q . code_t),
-// and its weights, w_t = 2^(logit_t + ev - mv).  mv is the running maximum of logit + ev, so w
-// fits fp16 whatever the pages' scales; the softmax's own maximum m and sum l are kept apart,
-// and the result is (sum w code) 2^(mv - m) / l.  Query and weights enter as an fp16 part and a
-// residual in a column of its own (times 2^11): products of fp32 accuracy, as kvq_decode's.
+// and its weights, w_t = 2^(logit_t - m + ev - er), m the running maximum.  er is that of a run of
+// pages whose ev lies within er - 6 .. er + 7: where a page's does not, what the run has summed goes
+// times 2^er into the fp32 totals and the page begins the next run.  So a weight's range is spent on
+// logits alone, whatever the scales of other pages: w fits fp16.  Query and weights enter as an fp16
+// part and a residual in a column of its own (times 2^11): products of fp32 accuracy, as kvq_decode's;
+// a weight's error is 2^-23 of it, or 2^-30 of the largest weight's.
 //
 // All visible pages of all (sequence, KV head) items form one line of work, cut into equal
 // ranges, one a CTA; an item that a border cuts leaves partial states for the joining kernel.
@@ -34,14 +36,19 @@ constexpr int kMinUnits = kWarps;       // pages of a CTA's range at least: one 
 constexpr int kItemCost = 40;           // pages that an item counts for beside its own
 constexpr int kFlush = 16;              // pages of a warp between flushes of the accumulators
 constexpr int kMaxCtas = 1024;          // of the grid: sizes the joining kernel's arrays
-constexpr float kLazy = 8.0f;           // log2 by which a reference may lag behind its maximum
+constexpr float kLazy = 8.0f;           // log2 by which the reference may lag behind the maximum
+constexpr int kBelow = 6, kAbove = 7;   // of a run's er: 2^(kLazy + kAbove) fits fp16
+// Totals are in units of 2^u, u = 0 until an exponent passes kUnitTop: then values of up to 2^128,
+// times weights of up to 2^kLazy, summed over any length, fit fp32.
+constexpr int kUnitTop = 86;
 
 struct __align__(16) Smem {
   uint8_t ring[kWarps][kStages][kFp8Rec];
   uint64_t bar[kWarps][kStages];
   int ids[kWarps][kStages];
-  float m[kWarps][kMaxG], mv[kWarps][kMaxG], l[kWarps][kMaxG];
+  float m[kWarps][kMaxG], l[kWarps][kMaxG];
   long long red[kWarps];
+  int u[kWarps];                        // the unit of a warp's totals
   int state[kWarps];                    // the stage that a warp's state is in
 };
 
@@ -244,30 +251,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_fp8_kernel(const 
       const bool stop = __syncthreads_or(!alive);
       for (int e = tid; e < a.G * kDim; e += kThreads) {
         const int h = e / kDim, d = e % kDim;
-        float M = -INFINITY, MV = -INFINITY, L = 0.0f, o = 0.0f, state[kWarps];
+        float M = -INFINITY, U = 0.0f, L = 0.0f, o = 0.0f, state[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           state[w] = reinterpret_cast<const float*>(sm.ring[w][sm.state[w]])[e];
           M = fmaxf(M, sm.m[w][h]);
-          MV = fmaxf(MV, sm.mv[w][h]);
+          U = fmaxf(U, static_cast<float>(sm.u[w]));
         }
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           // a warp without a token has l = 0 (one that met a NaN logit has l = NaN and no maximum)
-          const float x = sm.m[w][h], y = sm.mv[w][h], lw = sm.l[w][h];
+          const float x = sm.m[w][h], lw = sm.l[w][h];
           if (lw == 0.0f) continue;
-          L = fmaf(x == M ? 1.0f : fast_exp2(x - M), lw, L);
-          o = fmaf(y == MV ? 1.0f : fast_exp2(y - MV), state[w], o);
+          const float f = x == M ? 1.0f : fast_exp2(x - M);
+          L = fmaf(f, lw, L);
+          o = fmaf(f, state[w] * fast_exp2(static_cast<float>(sm.u[w]) - U), o);
         }
         if (whole) {
-          to[e] = L == 0.0f ? 0.0f : o * (MV == M ? 1.0f : fast_exp2(MV - M)) / L;
+          to[e] = L == 0.0f ? 0.0f : o / L * fast_exp2(U);
         } else {
           float* p = to + h * kPartStride;
           p[4 + d] = o;
           if (d == 0) {
             p[0] = M;
             p[1] = L;
-            p[2] = MV;
+            p[2] = U;
           }
         }
       }
@@ -294,12 +302,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_fp8_kernel(const 
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[mb][k] = 0.0f;
     }
-    float m = -INFINITY, mv = -INFINITY, l = 0.0f;      // of head t
+    float m = -INFINITY, l = 0.0f;      // of head t
+    int er = 0;                         // the run's exponent
+    if (lane == 0) sm.u[warp] = 0;
+    __syncwarp();
     auto flush = [&]() {
+      const float f = pow2(-sm.u[warp]), fe = pow2(er);
 #pragma unroll
       for (int mb = 0; mb < 8; ++mb) {
-        tot[mb][0] += fmaf(acc[mb][1], 0x1p-11f, acc[mb][0]);
-        tot[mb][1] += fmaf(acc[mb][3], 0x1p-11f, acc[mb][2]);
+        tot[mb][0] = fmaf(fmaf(acc[mb][1], 0x1p-11f, acc[mb][0]) * f, fe, tot[mb][0]);
+        tot[mb][1] = fmaf(fmaf(acc[mb][3], 0x1p-11f, acc[mb][2]) * f, fe, tot[mb][1]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[mb][k] = 0.0f;
       }
@@ -338,19 +350,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_fp8_kernel(const 
         return p < s.len && (p >= s.first || p < s.lead);
       };
       const float sk = __uint_as_float(meta.x);
-      const float ev = static_cast<float>(static_cast<int>(meta.y >> 23) - 127);
+      const int ev = static_cast<int>(meta.y >> 23) - 127;
+      if (ev < er - kBelow || ev > er + kAbove) {      // alike in all lanes
+        flush();
+        er = ev;
+        if (const int u = sm.u[warp]; ev > u + kUnitTop) {
+          __syncwarp();
+          const float f = pow2(u + kUnitTop - ev);
+#pragma unroll
+          for (int mb = 0; mb < 8; ++mb) {
+            tot[mb][0] *= f;
+            tot[mb][1] *= f;
+          }
+          if (lane == 0) sm.u[warp] = ev - kUnitTop;
+          __syncwarp();
+        }
+      }
       const float l0 = visible(g) ? fmaf(sa[1] + sb[1], 0x1p-11f, sa[0] + sb[0]) * sk * kq : -INFINITY;
       const float l1 = visible(g + 8) ? fmaf(sa[3] + sb[3], 0x1p-11f, sa[2] + sb[2]) * sk * kq : -INFINITY;
       float pm = fmaxf(l0, l1);
       pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 4));
       pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 8));
       pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 16));
-      if (__any_sync(0xffffffffu, pm > m + kLazy || pm + ev > mv + kLazy)) {
-        // whole powers of two: their differences, and ev's, are exact, and a weight is rounded alike
-        // whichever reference it meets
-        const float mn = fmaxf(m, floorf(pm)), mvn = fmaxf(mv, floorf(pm) + ev);
-        l *= m == mn ? 1.0f : fast_exp2(m - mn);
-        const float f = mv == mvn ? 1.0f : fast_exp2(mv - mvn);
+      if (__any_sync(0xffffffffu, pm > m + kLazy)) {
+        // whole powers of two: their differences are exact, and a weight is rounded alike whichever
+        // reference it meets
+        const float mn = fmaxf(m, floorf(pm)), f = m == mn ? 1.0f : fast_exp2(m - mn);
+        l *= f;
 #pragma unroll
         for (int mb = 0; mb < 8; ++mb) {
           tot[mb][0] *= f;
@@ -359,9 +385,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_fp8_kernel(const 
           for (int k = 0; k < 4; ++k) acc[mb][k] *= f;
         }
         m = mn;
-        mv = mvn;
       }
-      const float mr = m == -INFINITY ? 0.0f : m, wr = (mv == -INFINITY ? 0.0f : mv) - ev;
+      const float mr = m == -INFINITY ? 0.0f : m, wr = mr - static_cast<float>(ev - er);
       l += fast_exp2(l0 - mr) + fast_exp2(l1 - mr);
       const float w0 = fast_exp2(l0 - wr), w1 = fast_exp2(l1 - wr);
       const uint32_t hi = pack_half2(w0, w1);
@@ -403,7 +428,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_fp8_kernel(const 
       }
       if (g == 0) {
         sm.m[warp][t] = m;
-        sm.mv[warp][t] = mv;
         sm.l[warp][t] = l;
       }
     }
@@ -435,10 +459,10 @@ __global__ void __launch_bounds__(kDim) join_fp8_kernel(const __grid_constant__ 
   auto part = [&](int i) {
     return a.part + (static_cast<size_t>(2 * (c.z + i) + (i == 0 ? 1 : 0)) * kMaxG + h) * kPartStride;
   };
-  float M = -INFINITY, MV = -INFINITY, L = 0.0f;
+  float M = -INFINITY, U = 0.0f, L = 0.0f;
   for (int i = tid; i < parts; i += kDim) {
     M = fmaxf(M, part(i)[0]);
-    MV = fmaxf(MV, part(i)[2]);
+    U = fmaxf(U, part(i)[2]);
   }
   auto all = [&](float x, int which, bool sum) {
 #pragma unroll
@@ -452,18 +476,18 @@ __global__ void __launch_bounds__(kDim) join_fp8_kernel(const __grid_constant__ 
                : fmaxf(fmaxf(red[which][0], red[which][1]), fmaxf(red[which][2], red[which][3]));
   };
   M = all(M, 0, false);
-  MV = all(MV, 1, false);
+  U = all(U, 1, false);
   for (int i = tid; i < parts; i += kDim) {
-    const float x = part(i)[0], lw = part(i)[1], y = part(i)[2];
-    L += lw == 0.0f ? 0.0f : (x == M ? 1.0f : fast_exp2(x - M)) * lw;
-    f[i] = lw == 0.0f ? 0.0f : y == MV ? 1.0f : fast_exp2(y - MV);
+    const float x = part(i)[0], lw = part(i)[1], g = x == M ? 1.0f : fast_exp2(x - M);
+    L += lw == 0.0f ? 0.0f : g * lw;
+    f[i] = lw == 0.0f ? 0.0f : g * fast_exp2(part(i)[2] - U);
   }
   L = all(L, 2, true);        // its barrier is also that of f
   float o = 0.0f;
 #pragma unroll 8
   for (int i = 0; i < parts; ++i) o = fmaf(f[i], part(i)[4 + tid], o);
   a.out[(static_cast<size_t>(c.x) * a.H + c.y * a.G + h) * kDim + tid] =
-      L == 0.0f ? 0.0f : o * (MV == M ? 1.0f : fast_exp2(MV - M)) / L;
+      L == 0.0f ? 0.0f : o / L * fast_exp2(U);
 }
 
 int grid_of(int num_sms) {

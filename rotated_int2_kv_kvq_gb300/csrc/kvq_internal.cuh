@@ -221,7 +221,7 @@ struct Fp8DecodeArgs {
   float log2_scale;
   uint32_t* status;
   int4* cuts;                // [CTAs] {sequence, KV head, first, last CTA}; sequence -1: none
-  float* part;               // [2 * CTAs][kMaxG][kPartStride]: m, l, mv, -, o[128]
+  float* part;               // [2 * CTAs][kMaxG][kPartStride]: m, l, u, -, o[128]
 };
 struct Fp8DecodeWs {
   size_t cuts_off, part_off, total;
@@ -427,6 +427,9 @@ __device__ __forceinline__ float fast_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
 // log2(x) via the SFU (lg2.approx.ftz): log2(0) = -inf.
 __device__ __forceinline__ float fast_log2(float x) {
