@@ -599,7 +599,10 @@ int kvq_fp8_decode(kvq_handle* h, const void* pool, int num_pool_pages, const ui
  *     t > p - window  or  t < sinks          (window = 0: all of them).
  * Entries enter the products as they are; a query does times a power of two in two 8-bit parts,
  * which hold it exactly but for elements below 2^-9 of its largest, of which 2^-18 of that is kept;
- * weights are rounded to bf16, sums are fp32.  A value beyond bf16's range counts as a NaN.
+ * sums are fp32.  Weights are rounded to fp16 (to 11 bits, those below 2^-21 of the row's largest to
+ * 2^-32 of it), in a tile of 128 positions that holds a page with a V scale outside 2^-21 .. 2^1 (a
+ * largest value below 0.0002 or above 896) to bf16; where a row sees a page of the latter kind, 2^-32
+ * above is 2^-19.  A value beyond bf16's range counts as a NaN.
  * Key tiles of 128 positions that no row of a tile of rows sees are not worked on; pages without a
  * visible position are not read, and need not exist.  A value vector that holds a NaN makes NaN
  * the whole output of each row that sees it, and leaves the others alone.

@@ -11,8 +11,9 @@
 //             from the record's order into rows.  The query is two 8-bit parts of 4 bits of mantissa
 //             each, two products of half a 16-bit one's time.  A page's 2^ek goes into its columns'
 //             scores: eight columns' factors a tile in place of one.
-//   values  : bf16, code 2^ev exactly, by bit moves and one product a pair, because their sum spans
-//             pages; weights are bf16 and their sum is that of the rounded ones.
+//   values  : fp16, code 2^ev exactly, by bit moves and one product a pair, because their sum spans
+//             pages; weights are fp16 then.  A tile with a page that fp16 does not hold (2^ev outside
+//             2^-21 .. 2^1) is bf16, and so are its weights, whose sum is that of the rounded ones.
 //   windows : whole key tiles that no row of a row tile sees are left out of the line of work, so a
 //             window costs its own length; partly hidden tiles are masked in TMEM first.
 //   NaN     : a value that is not finite is stored as zero and noted, and spoils the rows that see it.

@@ -54,7 +54,8 @@ struct SmemOf {
   static constexpr int kTmem = kLine + 48;
   static constexpr int kPair = kTmem + 16;                  // float2 [128]: a split row's scale, then (max, sum) of its odd tiles
   static constexpr int kLook = kPair + 1024;                // Look [2] (8-bit cache)
-  // 8-bit cache: a query row's power of two; the keys' scales of a tile's pages
+  // 8-bit cache: a query row's power of two; the keys' scales of a tile's pages, the first one's sign
+  // set where fp16 does not hold the tile's values (bf16 does), the second one's where they lie above it
   static constexpr int kQScale = kLook + 128;               // float [256]
   static constexpr int kPageScale = kQScale + 1024;         // float [kFlags][8]
   static constexpr int kBytes = kPageScale + 32 * kFlags;
@@ -239,6 +240,9 @@ constexpr uint32_t idesc_f16(int bf16) {
          ((128u >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+// The same of two e4m3 operands.
+constexpr uint32_t kIdescF8 = idesc_f16(0);
+
 // One lane's arrival, as a predicated instruction: no branch for the warp to diverge at
 // (the tcgen05 loads that follow are warp-wide).
 __device__ __forceinline__ void arrive_if(uint32_t bar, bool on) {
@@ -415,6 +419,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // Nonzero bits where a half of x is infinite or NaN (fp16 / bf16).
 __device__ __forceinline__ uint32_t nonfinite_f16(uint32_t x) {
   return ((x & 0x7c00u) == 0x7c00u ? 1u : 0u) | ((x & 0x7c000000u) == 0x7c000000u ? 2u : 0u);
+}
+// Those halves as zeros, and their bits.
+__device__ __forceinline__ uint32_t f16_clean(uint32_t& x) {
+  const uint32_t bad = nonfinite_f16(x);
+  x &= (bad & 1u ? 0u : 0xffffu) | (bad & 2u ? 0u : 0xffff0000u);
+  return bad;
 }
 
 __device__ __forceinline__ void int2_load(RawInt2& r, int i, const uint8_t* rec, int lane) {
@@ -617,11 +627,11 @@ __device__ __forceinline__ uint32_t bf16_store_value(uint4 (&x)[8], int p0, int 
 // query: as many tensor cycles as 16-bit operands take, and no conversion), moved from the record's
 // order to rows: chunk 2t + h of a token's 128-byte row holds the words (t, h) of the record's four
 // loads, that is, element d = 16 w + 8 h + 2 t + e at byte 2 w + e.  A page's 2^e goes into its
-// columns' scores.  Values become bf16, exactly, because their sum spans pages.
+// columns' scores.  Values become 16-bit numbers, exactly, because their sum spans pages.
 //
 // What a lane knows of a page: exponents + 128 of the keys and of the values, flags.
 __device__ __forceinline__ uint32_t fp8_meta(const uint8_t* rec) {
-  const uint4 w = rec ? *reinterpret_cast<const uint4*>(rec + 4096) : make_uint4(0x3f800000u, 0, 0, 0);
+  const uint4 w = rec ? *reinterpret_cast<const uint4*>(rec + 4096) : make_uint4(0x3f800000u, 0x3f800000u, 0, 0);
   return ((w.x >> 23) + 1) | ((w.y >> 23) + 1) << 9 | w.z << 18;
 }
 __device__ __forceinline__ uint32_t meta_k(uint32_t m) { return (m & 511u) - 1; }          // biased as fp32's
@@ -642,21 +652,43 @@ __device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// Four codes as bf16: sign, exponent and mantissa bits moved to their places, which is code *
-// 2^-120, then times f = 2^(120 + e) (two bf16 numbers).  NaN codes come out as numbers.
+__device__ __forceinline__ uint32_t hmul2_f16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Values are held as fp16, which leaves weights their 11 bits, and times 2^kLift, so that the range lies
+// around what models' values are: code * 2^e is exact for e = -21 (codes are multiples of 2^-9) to 1 (up
+// to 448), pages of a largest value of 0.0002 to 896.  A tile with another page is bf16, weights too.
+// Whether a page's values lie elsewhere, and whether above.
+constexpr int kLift = 6;
+constexpr uint32_t kHalfLow = 127 - 15 - kLift, kHalfTop = 127 + 7 - kLift;
+__device__ __forceinline__ bool fp8_beyond_half(uint32_t meta) {
+  return meta_v(meta) - kHalfLow > kHalfTop - kHalfLow;
+}
+__device__ __forceinline__ bool fp8_above_half(uint32_t meta) { return meta_v(meta) > kHalfTop; }
+// Four codes as fp16: sign, exponent and mantissa bits moved to their places, which is code * 2^-8,
+// times f = 2^(8 + e + kLift) (two fp16 numbers).  NaN codes come out as numbers.
+__device__ __forceinline__ void fp8_half(uint32_t w, uint32_t f, uint32_t& lo, uint32_t& hi) {
+  const uint32_t h = (w & 0x80808080u) | ((w >> 1) & 0x3f3f3f3fu), l = (w << 7) & 0x80808080u;
+  lo = hmul2_f16(__byte_perm(l, h, 0x5140), f);
+  hi = hmul2_f16(__byte_perm(l, h, 0x7362), f);
+}
+__device__ __forceinline__ uint32_t fp8_factor(uint32_t meta) {
+  return (meta_v(meta) + 8 + kLift + 15 - 127) * 0x04000400u;
+}
+// As bf16, without the lift (such a tile's weights have it): code * 2^-120, times f = 2^(120 + e) (two
+// bf16 numbers: e up to 7), and which pages that does.
 __device__ __forceinline__ void fp8_wide(uint32_t w, uint32_t f, uint32_t& lo, uint32_t& hi) {
   const uint32_t h = (w & 0x80808080u) | ((w >> 4) & 0x07070707u), l = (w << 4) & 0xf0f0f0f0u;
   lo = hmul2_bf16(__byte_perm(l, h, 0x5140), f);
   hi = hmul2_bf16(__byte_perm(l, h, 0x7362), f);
 }
-// Whether that form holds a page's values (f is at most 2^127: e up to 7), and the factor; a
-// page that is not there gives zeros.
 __device__ __forceinline__ bool fp8_plain(uint32_t meta) {
   return (meta_flags(meta) & 2u) == 0 && meta_v(meta) <= 127u + 7u;
 }
-__device__ __forceinline__ uint32_t fp8_factor(uint32_t meta) {
-  const uint32_t e = meta_v(meta);
-  return e == 0 ? 0u : (e + 120u) * 0x00800080u;
+__device__ __forceinline__ uint32_t fp8_wide_factor(uint32_t meta) {
+  return meta_v(meta) == 0 ? 0u : (meta_v(meta) + 120u) * 0x00800080u;    // a scale never written: zeros
 }
 
 // Where the value rows of a page pair go.
@@ -671,8 +703,8 @@ __device__ __forceinline__ void fp8_store_v(const uint4 (&x)[8], uint32_t f0, ui
     for (int r = 0; r < 4; ++r) {             // element 16 (2i + (r >> 1)) + 8 (r & 1) + g
       const uint4 &p = x[i], &q = x[4 + i];
       uint32_t e[4];
-      fp8_wide(r == 0 ? p.x : r == 1 ? p.y : r == 2 ? p.z : p.w, f0, e[0], e[1]);
-      fp8_wide(r == 0 ? q.x : r == 1 ? q.y : r == 2 ? q.z : q.w, f1, e[2], e[3]);
+      fp8_half(r == 0 ? p.x : r == 1 ? p.y : r == 2 ? p.z : p.w, f0, e[0], e[1]);
+      fp8_half(r == 0 ? q.x : r == 1 ? q.y : r == 2 ? q.z : q.w, f1, e[2], e[3]);
       sts128(row + (32 * i + 8 * r) * 128, e[0], e[1], e[2], e[3]);
     }
 }
@@ -904,6 +936,11 @@ __device__ __forceinline__ uint32_t visible(int limit, int k) {
 // against 64 bits on two 4093-token prompts 0.0022 against 0.0023; 279 us against 282).
 // INT2: the fp16 rounding is an eighth of that and the sum of the unrounded ones (the two
 // conversions would cost 5 to 11 % there) as good, 0.0018 either way.
+// 8-bit cache: as INT2 where fp16 holds the tile's values, else as BF16 (error against 64 bits of the
+// timed cases 0.0017 with fp16 weights, as with fp32 ones, 0.0023 with bf16 ones throughout; 4096
+// tokens at 32K 1550 us against 1562, and 1755 where every tile is bf16).  The sums carry kBias and
+// kLift either way; a tile of values above fp16's raises the reference by both, so that the sums keep
+// the room that those values need.
 // low, lead (8-bit cache): positions of the tile from `lead` on and before `low` are hidden too;
 // pages: the keys' scales of its pages (those of column 64 a + 8 b + 4 c + .. are of page 4a + 2b + c,
 // b and c modulo 2).
@@ -937,23 +974,21 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sca
     }
     tc_wait_st();
   }
-  // 8-bit cache: the scales of the columns of pages 4 h .. 4 h + 3.  Read once for the maximum and
-  // again for the weights: eight registers less in between, which are all that this role has.
-  [[maybe_unused]] auto page_scales = [&](float (&sc)[4], int h) {
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(sc[0]), "=f"(sc[1]), "=f"(sc[2]), "=f"(sc[3])
-                 : "r"(smem_u32(pages + 4 * h))
-                 : "memory");
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sc[i] *= scale;
-    if (edge || any != 0) {              // a hidden column's 0 * -inf would be NaN
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sc[i] = fmaxf(sc[i], 1.17549435e-38f);
-    }
+  // 8-bit cache: what a page's scores are multiplied by, from its scale x (or -x).  Scales are read for
+  // the maximum and again, one by one, for the weights: this role has no registers to keep them in.
+  [[maybe_unused]] auto factor = [&](float x) {
+    x = fabsf(x) * scale;
+    return edge || any != 0 ? fmaxf(x, 1.17549435e-38f) : x;      // a hidden column's 0 * -inf would be NaN
+  };
+  [[maybe_unused]] auto page_scale = [&](int p) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(smem_u32(pages + p)) : "memory");
+    return x;
   };
   uint32_t v[4][32];
   tc_ld_row(v, ts);
   float mnew;
+  [[maybe_unused]] bool bf16_tile = false;      // alike in all lanes
   if constexpr (FP8) {
     float m[8];                  // a chain a page
 #pragma unroll
@@ -964,14 +999,21 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sca
         const float x = __uint_as_float(v[c][i]), y = __uint_as_float(v[c][i + 1]);
         m[pg] = (c & 1) == 0 && i == ((i >> 2) & 3) * 4 ? fmaxf(x, y) : max3(m[pg], x, y);
       }
-    mnew = mref;
+    float big = 0.0f;
+    mnew = -INFINITY;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float sc[4];
-      page_scales(sc, h);
-      mnew = max3(mnew, m[4 * h] * sc[0], m[4 * h + 1] * sc[1]);
-      mnew = max3(mnew, m[4 * h + 2] * sc[2], m[4 * h + 3] * sc[3]);
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(sc[0]), "=f"(sc[1]), "=f"(sc[2]), "=f"(sc[3])
+                   : "r"(smem_u32(pages + 4 * h))
+                   : "memory");
+      if (h == 0) big = sc[1], bf16_tile = __float_as_int(sc[0]) < 0;
+      mnew = max3(mnew, m[4 * h] * factor(sc[0]), m[4 * h + 1] * factor(sc[1]));
+      mnew = max3(mnew, m[4 * h + 2] * factor(sc[2]), m[4 * h + 3] * factor(sc[3]));
     }
+    if (__float_as_int(big) < 0) mnew += kBias + kLift;
+    mnew = fmaxf(mnew, mref);
   } else {
     float m[4];                  // four chains, a quarter of the columns each
 #pragma unroll
@@ -1008,33 +1050,55 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sca
       if (grow) mref = top;
     }
   }
-  const float neg = mref == -INFINITY ? 0.0f : (INT2 ? kBias : 0.0f) - mref;
+  const float neg = mref == -INFINITY ? 0.0f : (INT2 || FP8 ? kBias : 0.0f) - mref;
   const uint64_t ng2 = pair2(neg, neg);
-  [[maybe_unused]] const uint64_t one2 = pair2(scale, scale);
   uint64_t s0 = 0, s1 = 0;
+  if (bf16_tile) {
+    // seldom: from TMEM again, 32 columns a step, in little code (the roles share the instruction
+    // cache); a step's 16 columns of P lie in what was read
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t x[32], pk[16];
+      tc_ld32(x, ts + 32 * c);
+      tc_wait_ld(x);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t pk[32];
-    uint64_t page2[4] = {one2, one2, one2, one2};
-    if constexpr (FP8) {
-      float sc[4];
-      page_scales(sc, h);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) page2[i] = pair2(sc[i], sc[i]);
+      for (int i = 0; i < 16; ++i) {
+        const float f = factor(page_scale(4 * (c >> 1) + ((i >> 1) & 3)));
+        pk[i] = pack_bf162(fast_exp2(fmaf(__uint_as_float(x[2 * i]), f, neg + kLift)),
+                           fast_exp2(fmaf(__uint_as_float(x[2 * i + 1]), f, neg + kLift)));
+        s0 = add2(s0, bf16_pair(pk[i]));
+      }
+      tc_st16(ts + 16 * c, pk);
     }
+    s0 = mul2(s0, pair2(1.0f / (1 << kLift), 1.0f / (1 << kLift)));
+  } else {
+    // 8-bit cache: columns go page by page, so that one factor is held at a time, and weights are
+    // added in pairs first, so that none waits for the sum's chain
+    constexpr bool kHalf = INT2 || FP8;
+    uint64_t sc2 = pair2(scale, scale), even = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const uint64_t sc2 = page2[(i >> 1) & 3];
-      const uint32_t* x = &v[2 * h + (i >> 4)][2 * (i & 15)];
-      float x0, x1;
-      split2(fma2(pair2(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, ng2), x0, x1);
-      const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-      pk[i] = INT2 ? pack_half2(p0, p1) : pack_bf162(p0, p1);
-      const uint64_t w = INT2 ? pair2(p0, p1) : bf16_pair(pk[i]);
-      if (i & 1) s1 = add2(s1, w);
-      else s0 = add2(s0, w);
+    for (int h = 0; h < 2; ++h) {
+      uint32_t pk[32];
+#pragma unroll
+      for (int n = 0; n < 32; ++n) {
+        const int i = FP8 ? 2 * (n >> 3) + 8 * ((n >> 1) & 3) + (n & 1) : n;
+        if (FP8 && (n & 7) == 0) {
+          const float f = factor(page_scale(4 * h + (n >> 3)));
+          sc2 = pair2(f, f);
+        }
+        const uint32_t* x = &v[2 * h + (i >> 4)][2 * (i & 15)];
+        float x0, x1;
+        split2(fma2(pair2(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, ng2), x0, x1);
+        const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+        pk[i] = kHalf ? pack_half2(p0, p1) : pack_bf162(p0, p1);
+        const uint64_t w = kHalf ? pair2(p0, p1) : bf16_pair(pk[i]);
+        if (FP8 && (n & 1) == 0) even = w;
+        else if (FP8) s0 = add2(s0, add2(even, w));
+        else if (i & 1) s1 = add2(s1, w);
+        else s0 = add2(s0, w);
+      }
+      tc_st32(ts + 32 * h, pk);     // all of S is in registers: P may overwrite it
     }
-    tc_st32(ts + 32 * h, pk);     // all of S is in registers: P may overwrite it
   }
   float a0, a1;
   split2(add2(s0, s1), a0, a1);
@@ -1199,18 +1263,28 @@ __device__ __forceinline__ bool fp8_produce(const PrefillArgs& a, const Item& w,
     __syncwarp();
     arrive_if(bar + 8 * (kKFull + k % kStages), lane == 0);
   };
-  // what the softmax has to know of tile j: pages that are missing, the keys' scales
+  // what softmax and issue have to know of tile j: pages that are missing, the keys' scales, the
+  // type of the values
+  bool wide = false, ahead_wide = false;      // bf16: the tile whose values are stored next, and the one behind
   auto flags = [&](int j, bool next) {
     const uint32_t k = it + j, slot = k % kFlags;
     const uint32_t bad = (pair_id(j, 0, next) == -2 ? 0xffffu : 0u) | (pair_id(j, 1, next) == -2 ? 0xffff0000u : 0u);
+    const uint32_t meta = next ? meta1 : meta0;
+    const bool mine = (lane >> 3) == (j & 3);
+    uint32_t sign = 0;
+    ahead_wide = __any_sync(0xffffffffu, mine && fp8_beyond_half(meta));
+    if (ahead_wide) {
+      const bool big = __any_sync(0xffffffffu, mine && fp8_above_half(meta));
+      sign = (lane & 7) == 0 || ((lane & 7) == 1 && big) ? 0x80000000u : 0u;
+    }
     if (lane == 0) {
       reinterpret_cast<volatile uint32_t*>(smem + Smem::kBad)[4 * slot + pw] = bad;
       reinterpret_cast<volatile uint8_t*>(smem + Smem::kAny)[4 * slot + pw] = bad != 0;
       if (bad) atomicOr(a.status, KVQ_STATUS_BAD_PAGE);
     }
-    if (pw == 0 && (lane >> 3) == (j & 3))
-      reinterpret_cast<volatile float*>(smem + Smem::kPageScale)[8 * slot + (lane & 7)] =
-          __uint_as_float(meta_k(next ? meta1 : meta0) << 23);
+    if (pw == 0 && mine)
+      reinterpret_cast<volatile uint32_t*>(smem + Smem::kPageScale)[8 * slot + (lane & 7)] =
+          (meta_k(meta) & 255u) << 23 | sign;
   };
   auto load_v = [&](int j, bool next) {
 #pragma unroll
@@ -1242,6 +1316,7 @@ __device__ __forceinline__ bool fp8_produce(const PrefillArgs& a, const Item& w,
     }
     if ((j & 3) == 1) meta1 = fp8_meta(record(ids1));
     const uint32_t k = it + j;
+    wide = ahead_wide;
     if (j + 1 < tiles) {
       if (!wait_empty(kKEmpty, k + 1)) return false;
       flags(j + 1, (j & 3) == 3);
@@ -1251,32 +1326,53 @@ __device__ __forceinline__ bool fp8_produce(const PrefillArgs& a, const Item& w,
     const uint32_t row = value_base(sb + Smem::kV + (k % kStages) * kTileBytes, pw, lane);
     const uint32_t m0 = __shfl_sync(0xffffffffu, meta0, 8 * (j & 3) + 2 * pw);
     const uint32_t m1 = __shfl_sync(0xffffffffu, meta0, 8 * (j & 3) + 2 * pw + 1);
-    if (fp8_plain(m0) && fp8_plain(m1)) {
+    if (!wide && ((meta_flags(m0) | meta_flags(m1)) & 2u) == 0) {
       fp8_store_v(v, fp8_factor(m0), fp8_factor(m1), row);
+    } else if (wide && fp8_plain(m0) && fp8_plain(m1)) {
+      // seldom: a word of each load a step
+      const uint32_t f0 = fp8_wide_factor(m0), f1 = fp8_wide_factor(m1);
+#pragma unroll 2
+      for (int r = 0; r < 4; ++r) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t e[4];
+          fp8_wide(v[i].x, f0, e[0], e[1]);
+          fp8_wide(v[4 + i].x, f1, e[2], e[3]);
+          sts128(row + (32 * i + 8 * r) * 128, e[0], e[1], e[2], e[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = make_uint4(v[i].y, v[i].z, v[i].w, 0);
+      }
     } else {
       // any scales and codes: from the records, through fp32, a word at a time; a value that is not
       // finite is stored as zero and noted
       uint32_t poison = 0;
       const uint8_t *r0 = record(pair_id(j, 0, false)), *r1 = record(pair_id(j, 1, false));
+      const float lift = wide ? 1.0f : pow2(kLift);
+      const float s0 = r0 ? *reinterpret_cast<const float*>(r0 + 4100) * lift : 0.0f;
+      const float s1 = r1 ? *reinterpret_cast<const float*>(r1 + 4100) * lift : 0.0f;
+      auto put = [&](uint32_t c, float s, uint32_t& lo, uint32_t& hi) {
+        const uint32_t a = fp8_lo(c), b = fp8_hi(c);
+        const float x[4] = {half_lo(a) * s, half_hi(a) * s, half_lo(b) * s, half_hi(b) * s};
+        lo = wide ? pack_bf162(x[0], x[1]) : pack_half2(x[0], x[1]);
+        hi = wide ? pack_bf162(x[2], x[3]) : pack_half2(x[2], x[3]);
+        const uint32_t bad = wide ? bf16_clean(lo) | bf16_clean(hi) << 8 : f16_clean(lo) | f16_clean(hi) << 8;
+        return bad << (2 * (lane & 3));
+      };
 #pragma unroll 1
-      for (int i = 0; i < 16; ++i) {
-        uint32_t e[4];
-#pragma unroll
-        for (int pi = 0; pi < 2; ++pi) {
-          const uint8_t* r = pi ? r1 : r0;
-          uint32_t c = 0;
-          float s = 0.0f;
-          if (r) {
-            c = *reinterpret_cast<const uint32_t*>(r + 2048 + 512 * (i >> 2) + 16 * lane + 4 * (i & 3));
-            s = *reinterpret_cast<const float*>(r + 4100);
-          }
-          const uint32_t lo = fp8_lo(c), hi = fp8_hi(c);
-          e[2 * pi] = pack_bf162(half_lo(lo) * s, half_hi(lo) * s);
-          e[2 * pi + 1] = pack_bf162(half_lo(hi) * s, half_hi(hi) * s);
-          poison |= bf16_clean(e[2 * pi]) << (16 * pi + 2 * (lane & 3));
-          poison |= bf16_clean(e[2 * pi + 1]) << (16 * pi + 8 + 2 * (lane & 3));
+      for (int i = 0; i < 4; ++i) {
+        uint4 p = make_uint4(0, 0, 0, 0), q = p;
+        if (r0) p = *reinterpret_cast<const uint4*>(r0 + 2048 + 512 * i + 16 * lane);
+        if (r1) q = *reinterpret_cast<const uint4*>(r1 + 2048 + 512 * i + 16 * lane);
+#pragma unroll 1
+        for (int r = 0; r < 4; ++r) {
+          uint32_t e[4];
+          poison |= put(p.x, s0, e[0], e[1]);
+          poison |= put(q.x, s1, e[2], e[3]) << 16;
+          sts128(row + (32 * i + 8 * r) * 128, e[0], e[1], e[2], e[3]);
+          p = make_uint4(p.y, p.z, p.w, 0);
+          q = make_uint4(q.y, q.z, q.w, 0);
         }
-        sts128(row + (32 * (i >> 2) + 8 * (i & 3)) * 128, e[0], e[1], e[2], e[3]);
       }
 #pragma unroll 1
       for (; poison != 0; poison &= poison - 1) {
@@ -1364,7 +1460,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     uint32_t ns = 0;                // S_full phases
     for (uint32_t i = 0;; ++i) {
       sync_cta();                   // the item is there
-      const Item w = items[i & 1];
+      // 8-bit cache: read where it is used, as registers are short and shared memory is nearer than a
+      // spilled one
+      std::conditional_t<FP8, const Item&, const Item> w = items[i & 1];
       if (w.done) break;
       if constexpr (FP8) {
         alive = warp_wait(B(kRawFull), i & 1);
@@ -1425,13 +1523,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           give();
         }
         const int pos = w.pos0 + tok;
-        for (int j = first; j < st.tiles && alive; j += step) {
-          const int base = w.tile<FP8>(j) * kTileKeys;
-          const int limit = valid ? pos - base : kTileKeys;
+        for (int j = first; j < (FP8 ? w.tiles : st.tiles) && alive;
+             j += FP8 ? (w.tokens * a.G <= 128 ? 2 : 1) : step) {
+          const bool in = FP8 ? row < w.tokens * a.G : valid;
+          const int base = w.template tile<FP8>(j) * kTileKeys, at = FP8 ? w.pos0 + tok : pos;
+          const int limit = in ? at - base : kTileKeys;
           int low = 0, lead = 0;
           if constexpr (FP8) {
             // a window of none: the row's starts at 0, or before
-            low = valid && a.window > 0 ? pos - a.window + 1 - base : 0;
+            low = in && a.window > 0 ? at - a.window + 1 - base : 0;
             lead = max(a.sinks - base, 0);
           }
           const bool edge =
@@ -1441,7 +1541,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           // the tile's missing pages, written before its operands were handed over; the slot
           // is written again four tiles later, which weights of two tiles later precede
           const uint32_t f = (itf + j) % kFlags;
-          if (some)
+          if (FP8 ? (row & ~31) < w.tokens * a.G : some)
             softmax_tile<INT2, FP8>(ts, to, scale, j == first, limit, low, lead,
                                     reinterpret_cast<const float*>(smem + Smem::kPageScale) + 8 * f, edge,
                                     anyw[f], badw + 4 * f, mref, l);
@@ -1466,6 +1566,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           } else {
             spoiled = poison[i & 1] <= static_cast<uint32_t>(pos);
           }
+          if constexpr (FP8) l *= pow2(kLift);        // O has it
           if (spoiled) l = __int_as_float(0x7fffffff);
         }
       }
@@ -1762,7 +1863,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           }
         }
         if (issue.value && warp == kMmaWarp && st.tiles > 0) {
-          constexpr uint32_t idesc = idesc_f16(INT2 ? 0 : 1), idesc_bf = idesc_f16(1);
+          constexpr uint32_t idesc = idesc_f16(INT2 || FP8 ? 0 : 1), idesc_bf = idesc_f16(1);
           const bool both = __shfl_sync(0xffffffffu, st.split ? 0 : 1, 0) != 0;
           const int tiles = __shfl_sync(0xffffffffu, st.tiles, 0);
           auto full = [&](int bar, uint32_t k) {
@@ -1791,7 +1892,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
               for (int k = 0; k < 8; ++k)
                 tc_mma_ss_f8(tm + t * 128, q + (k >> 2) * (kTileBytes / 2 >> 4) + 2 * (k & 3), x + 2 * (k & 3),
-                             idesc_f16(0), k != 0, one);
+                             kIdescF8, k != 0, one);
             } else {
 #pragma unroll
               for (int k = 0; k < 8; ++k)
@@ -1802,10 +1903,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             return tile_desc(sb + Smem::kK + (k % kStages) * Smem::kKeyTile);
           };
           auto vdesc = [&](uint32_t k) { return tile_desc(sb + Smem::kV + (k % kStages) * kTileBytes); };
-          auto weighted = [&](int t, uint32_t v, bool add) {     // O_t += P_t V
+          auto weighted = [&](int t, uint32_t v, uint32_t id, bool add) {     // O_t += P_t V
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              tc_mma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * k, v + desc_step(k), idesc,
+              tc_mma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * k, v + desc_step(k), id,
                         add || k != 0, one);
           };
           uint32_t k = __shfl_sync(0xffffffffu, itk, 0), v = __shfl_sync(0xffffffffu, itv, 0);
@@ -1836,8 +1937,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
               if (s >= total) break;
               const bool last = t == 1 || !both;       // of the stages' users
               if (s0 >= 0) {
-                if (!full(kVFull, v) || !operand(t)) break;
-                weighted(t, vdesc(v), s0 != 0);
+                if (!full(kVFull, v)) break;
+                uint32_t id = idesc;
+                if constexpr (FP8) {        // of the tile's weights and values
+                  const uint32_t f = (itf + (both ? s0 >> 1 : s)) % kFlags;
+                  const float x = reinterpret_cast<const volatile float*>(smem + Smem::kPageScale)[8 * f];
+                  if (__any_sync(0xffffffffu, __float_as_int(x) < 0)) id = idesc_bf;
+                }
+                if (!operand(t)) break;
+                weighted(t, vdesc(v), id, s0 != 0);
                 if (last) empty(kVEmpty, v++);
               }
               const bool more = s + 2 < total;
