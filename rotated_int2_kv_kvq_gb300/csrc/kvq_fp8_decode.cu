@@ -154,7 +154,7 @@ __device__ __forceinline__ float query_frags(const Fp8DecodeArgs& a, int b, int 
   }
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-  const uint32_t ex = min((__float_as_uint(mx) >> 23) & 255u, 253u);
+  const uint32_t ex = min(max((__float_as_uint(mx) >> 23) & 255u, 1u), 253u);   // 1: subnormal ones too
   const float down = __uint_as_float((254u - ex) << 23), up = __uint_as_float(ex << 23);
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -293,8 +293,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_fp8_kernel(const 
     if (count >= kStages) issue(kStages - 1);
     uint32_t qf[16];
     const float up = query_frags(a, b, kv, lane, qf);
-    const float kq = a.log2_scale * up;
-
     float acc[8][4], tot[8][2];
 #pragma unroll
     for (int mb = 0; mb < 8; ++mb) {
@@ -349,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_fp8_kernel(const 
         const int p = pos + tau;
         return p < s.len && (p >= s.first || p < s.lead);
       };
-      const float sk = __uint_as_float(meta.x);
+      // the powers of two first: a sum of products times 2^ek alone may overflow where the score does not
+      const float kf = fminf(__uint_as_float(meta.x) * up * a.log2_scale, 3.4028235e38f);
       const int ev = static_cast<int>(meta.y >> 23) - 127;
       if (ev < er - kBelow || ev > er + kAbove) {      // alike in all lanes
         flush();
@@ -366,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_fp8_kernel(const 
           __syncwarp();
         }
       }
-      const float l0 = visible(g) ? fmaf(sa[1] + sb[1], 0x1p-11f, sa[0] + sb[0]) * sk * kq : -INFINITY;
-      const float l1 = visible(g + 8) ? fmaf(sa[3] + sb[3], 0x1p-11f, sa[2] + sb[2]) * sk * kq : -INFINITY;
+      const float l0 = visible(g) ? fmaf(sa[1] + sb[1], 0x1p-11f, sa[0] + sb[0]) * kf : -INFINITY;
+      const float l1 = visible(g + 8) ? fmaf(sa[3] + sb[3], 0x1p-11f, sa[2] + sb[2]) * kf : -INFINITY;
       float pm = fmaxf(l0, l1);
       pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 4));
       pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 8));

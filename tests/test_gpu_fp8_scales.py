@@ -119,3 +119,17 @@ def test_decode_flat_tail(drop, first):
     c, q = flat_tail(drop, first)
     one = q[:1].contiguous()
     check_decode(c, c.decode(one), one, extra=2.0 ** (drop - 35))
+
+
+@pytest.mark.parametrize("sk,sq", [(2.0 ** 124, 2.0 ** -124), (2.0 ** 124, 2.0 ** -130), (2.0 ** -90, 2.0 ** 90),
+                                   (2.0 ** 116, 2.0 ** -112)])
+@pytest.mark.parametrize("length", [20, 900])
+def test_decode_keys_and_queries_at_the_ends_of_the_range(sk, sq, length):
+    """Scores of ordinary size from keys and queries that are not, all of a score's products of one sign: no partial
+    product overflows, nor do queries below the smallest normal number count as zeros."""
+    c = Cache8(4, 2, [length], seed=7, fill=False)
+    sign = torch.where(torch.rand(D, generator=c.g, device="cuda") < 0.5, -1.0, 1.0)
+    size = 0.5 + 0.5 * torch.rand(length, 2, 1, generator=c.g, device="cuda")
+    c.append((sign * sk * size).bfloat16(), c.v, [length])
+    q = (sign * sq * torch.rand(1, 4, D, generator=c.g, device="cuda")).bfloat16()
+    check_decode(c, c.decode(q), q)
