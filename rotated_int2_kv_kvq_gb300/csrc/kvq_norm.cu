@@ -15,8 +15,6 @@
 // of the copy rate); backward of 4099 tokens 27.8 us (128 MB), of which 24 are the rows (5.3 TB/s: a CTA
 // has 23 rows a group, so that its start is an eighth) and 4 the weights' sum behind them.  16 tokens
 // 1.4 us, 257 tokens' backward 4.0 (8 and 2 heads, interleaved): launches and dependent loads.
-#include <type_traits>
-
 #include "kvq_internal.cuh"
 
 namespace kvq {
@@ -252,15 +250,13 @@ __global__ void __launch_bounds__(kFwdThreads) norm_rope_kernel(const __grid_con
   }
 }
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
-  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+__device__ __forceinline__ void copy_async8(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
 }
 
 // ---- backward --------------------------------------------------------------------------
 // The first a.q_ctas CTAs take the queries, the others the keys.  A row group takes a run of rows
-// (token, head), so that a token's angles serve several of them; each lane keeps its 16 elements'
+// (token, head), so that a token's angles serve several of them; each lane keeps its 8 elements'
 // share of dw, summed over the CTA at the end and over the CTAs by a second kernel, always in the
 // same order.  The elements of the next rows are under way into shared memory by asynchronous
 // copies (a lane reads back its own, so nothing is waited for but them); with the next row in
@@ -280,8 +276,8 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) norm_rope_backward_kern
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Lane<MODE, kBwdE> l(lane, a.rope);
   constexpr int U = kBwdE / 2, kLanes = kDim / kBwdE, kRowsCta = kBwdThreads / kLanes;
-  using Unit = std::conditional_t<kBwdE == 16, uint4, uint2>;      // U elements
-  Unit* ring = reinterpret_cast<Unit*>(ring_raw);                  // [kAhead][4][kBwdThreads]
+  static_assert(U == 4, "a uint2 of the ring");
+  uint2* ring = reinterpret_cast<uint2*>(ring_raw);                // [kAhead][4][kBwdThreads]
   dependency_wait();
   float wf[kBwdE], c[U], s[U];
   load_weight(wf, x.weight, l, a.rope);
@@ -310,11 +306,11 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) norm_rope_backward_kern
   auto ask = [&](int i) {
     if (MODE != kScalar && i < mine) {
       const uint32_t at = smem_u32(ring + (i % kAhead) * 4 * kBwdThreads + threadIdx.x);
-      constexpr int kStep = static_cast<int>(sizeof(Unit)) * kBwdThreads;
-      copy_async<sizeof(Unit)>(at, xr + l.at0);
-      copy_async<sizeof(Unit)>(at + kStep, xr + l.at1);
-      copy_async<sizeof(Unit)>(at + 2 * kStep, dr + l.at0);
-      copy_async<sizeof(Unit)>(at + 3 * kStep, dr + l.at1);
+      constexpr int kStep = static_cast<int>(sizeof(uint2)) * kBwdThreads;
+      copy_async8(at, xr + l.at0);
+      copy_async8(at + kStep, xr + l.at1);
+      copy_async8(at + 2 * kStep, dr + l.at0);
+      copy_async8(at + 3 * kStep, dr + l.at1);
       xr += kDim;
       dr += kDim;
       if (++head_ahead == x.heads) {
@@ -343,14 +339,10 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) norm_rope_backward_kern
         load_raw(rx, x.x + static_cast<size_t>(tok) * x.x_stride + head * kDim, l, a.rope);
         load_raw(rd, x.dy + static_cast<size_t>(tok) * x.dy_stride + head * kDim, l, a.rope);
       } else {
-        const Unit* from = ring + (i % kAhead) * 4 * kBwdThreads + threadIdx.x;
-        const Unit e[4] = {from[0], from[kBwdThreads], from[2 * kBwdThreads], from[3 * kBwdThreads]};
-        const uint32_t* ew = reinterpret_cast<const uint32_t*>(e);
-#pragma unroll
-        for (int x2 = 0; x2 < U; ++x2) {
-          rx[x2] = ew[x2];
-          rd[x2] = ew[U + x2];
-        }
+        const uint2* from = ring + (i % kAhead) * 4 * kBwdThreads + threadIdx.x;
+        const uint2 e[4] = {from[0], from[kBwdThreads], from[2 * kBwdThreads], from[3 * kBwdThreads]};
+        rx[0] = e[0].x, rx[1] = e[0].y, rx[2] = e[1].x, rx[3] = e[1].y;
+        rd[0] = e[2].x, rd[1] = e[2].y, rd[2] = e[3].x, rd[3] = e[3].y;
       }
     }
     uint64_t v[U], d[U];
