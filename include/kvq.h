@@ -338,8 +338,8 @@ int kvq_norm_rope(kvq_handle* h, const uint16_t* q, long long q_stride, const ui
  *   workspace  : device, >= kvq_norm_rope_backward_workspace_bytes(h, n) bytes, 256-byte
  *                aligned; contents on entry do not matter.  Calls (and captured graphs) that can
  *                run at the same time need one each.
- * A token whose position is outside the table adds nothing to dw.  n == 0 sets dw to 0.  The same
- * call on the same GPU gives the same bits.  Returns KVQ_ENOSPACE if ws_bytes is too small. */
+ * A token whose position is outside the table adds nothing to dw.  n == 0 sets each dw that is given
+ * to 0.  The same call on the same GPU gives the same bits.  Returns KVQ_ENOSPACE if ws_bytes is too small. */
 size_t kvq_norm_rope_backward_workspace_bytes(const kvq_handle* h, int n);
 int kvq_norm_rope_backward(kvq_handle* h, const uint16_t* q, long long q_stride, const uint16_t* k,
                            long long k_stride, const uint16_t* dq_out, long long dq_out_stride,

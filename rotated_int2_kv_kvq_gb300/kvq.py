@@ -552,6 +552,10 @@ def kvq_norm_rope_backward(h, q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, 
     dev, lay = h.device, h.layout
     pq, sq, pk, sk, n = _norm_rows(q, k, lay, dev)
     gq = gk = oq = ok = None, 0
+    if pq is None:      # of no tokens the library cannot tell a missing side from an empty one
+        dq_weight = None
+    if pk is None:
+        dk_weight = None
     if pq is not None:
         gq = _like(dq_out, n, lay.num_heads, dev, "dq_out", "q")
         oq = _like(dq, n, lay.num_heads, dev, "dq", "q")

@@ -69,3 +69,17 @@ def test_a_bad_position_among_many():
     for dw, x, dy in ((got[0], c.q, c.dq), (got[1], c.k, c.dk)):
         want, mag = weight_gradient(x[keep], dy[keep], c.table, c.pos[keep], "half", c.eps)
         assert torch.all((dw.double() - want).abs() <= 2.0 ** -17 * mag)
+
+
+@pytest.mark.parametrize("n", [0, 5])
+def test_a_missing_side_keeps_its_gradient(n):
+    """Without queries (keys), the other arguments of that side are not looked at, with no tokens either."""
+    c = Case(4, 2, n, 128, "half")
+    ws = torch.empty(K.kvq_norm_rope_backward_workspace_bytes(c.h, n), dtype=torch.uint8, device="cuda")
+    for q, k in ((None, c.k), (c.q, None)):
+        dw = [torch.full((D,), 9.0, device="cuda") for _ in range(2)]
+        dq, dk = (None if x is None else torch.empty_like(x) for x in (q, k))
+        K.kvq_norm_rope_backward(c.h, q, k, None if q is None else c.dq, None if k is None else c.dk, dq, dk, c.wq, c.wk,
+                                 *dw, c.eps, c.pos, c.rope, ws)
+        assert (dw[0 if q is None else 1] == 9).all() and not (dw[1 if q is None else 0] == 9).any()
+        assert n > 0 or (dw[1 if q is None else 0] == 0).all()
