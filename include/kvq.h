@@ -547,7 +547,7 @@ int kvq_bf16_prefill(kvq_handle* h, const void* pool, int num_pool_pages, const 
  *     e = max(e of the page, least e >= -100 with |x| <= 448 * 2^e for the new tokens),
  *     code = x * 2^-e rounded to nearest (ties to even), s = 2^e;
  * where e grew, the older tokens' codes are rounded again from what they stood for (exact but
- * for those below 2^-14 of the page's largest).  Elements that are not finite become NaN and do
+ * for those that become subnormal, below 2^-6 s).  Elements that are not finite become NaN and do
  * not count for e.  A call that writes a page's slot 0 begins the page: what it held counts no
  * more and the slots the call does not write become 0.  So a page serves a new sequence without
  * being cleared, and a sequence that was cut back goes on where it was cut (tokens behind the
@@ -598,8 +598,8 @@ int kvq_fp8_decode(kvq_handle* h, const void* pool, int num_pool_pages, const ui
  * sequence b, at position p = seq_lens[b] - n_b + i, attends to the positions t <= p with
  *     t > p - window  or  t < sinks          (window = 0: all of them).
  * Entries enter the products as they are; a query does times a power of two in two 8-bit parts,
- * which hold it exactly but for elements below 2^-9 of its largest, of which 2^-18 of that is kept;
- * sums are fp32.  Weights are rounded to fp16 (to 11 bits, those below 2^-21 of the row's largest to
+ * which hold it exactly but for elements below 2^-9 of its largest, which are off by up to 2^-17 of
+ * that (2^-136 in a row whose largest is below 2^-119); sums are fp32.  Weights are rounded to fp16 (to 11 bits, those below 2^-21 of the row's largest to
  * 2^-32 of it), in a tile of 128 positions that holds a page with a V scale outside 2^-21 .. 2^1 (a
  * largest value below 0.0002 or above 896) to bf16; where a row sees a page of the latter kind, 2^-32
  * above is 2^-19.  A value beyond bf16's range counts as a NaN.

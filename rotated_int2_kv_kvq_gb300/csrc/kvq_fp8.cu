@@ -4,7 +4,7 @@
 // An entry is code * 2^e: e4m3 codes, one exponent for the 16 x 128 keys and one for the values
 // of a page and KV head.  A power of two makes x * 2^-e exact, so a code has one rounding, and
 // codes that are rounded again because a later token raised e lose bits only where they become
-// subnormal (below 2^-14 of the page's largest): a floating code needs no finer scale.
+// subnormal (below 2^-6 * 2^e, 2^-13 of the page's largest): a floating code needs no finer scale.
 //
 // Work is shared out by pages: a page's tokens of one call are consecutive rows of one
 // sequence, and the CTA that holds the first of them (the leader) does all of them, a warp a

@@ -871,7 +871,7 @@ __device__ __forceinline__ void ask_queries(const PrefillArgs& a, const Item& w,
 
 // 8-bit cache: the query rows, raw in shared memory, as two e4m3 parts, by the softmax's 256 threads.
 // q is taken times a power of two a row (its largest element in [128, 256)): its 8 bits fill both
-// parts, so that is exact but for elements below 2^-9 of the largest, which keep 2^-18 of it; a row
+// parts, so that is exact but for elements below 2^-9 of the largest, off by up to 2^-17 of it; a row
 // with an infinity or a NaN is NaN.  A thread takes a 16-byte chunk of both parts, 16 elements
 // 16 w + 8 h + 2 t + {0, 1}; a row is 8 lanes, a warp's four rows are one head of four tokens.  The
 // first tile's parts lie before the raw rows, the second's over those of the first.

@@ -90,3 +90,23 @@ def test_prefill_flat_tail(drop, first):
     """fp16 has 2^-10 of a weight of 2^-15, with the 2^7 that weights are taken times, left as its half step."""
     c, q = flat_tail(drop, first)
     check_prefill(c, c.prefill(q, [4]), q, 4)
+
+
+@pytest.mark.parametrize("small", [2.0 ** -17, -3 * 2.0 ** -18, 2.0 ** -12 * 1.0078125])
+def test_small_query_elements(small):
+    """127 elements far below a row's largest: each is off by at most 2^-17 of that (half of the second part's step of
+    2^-9, the largest in [128, 256)), which moves a score by scale * 2^-17 sum |k_d| and a weight, and the sum of the
+    weights, by that factor."""
+    length, size = 512, 200.0
+    c = Cache8(2, 1, [length], seed=8, fill=False)
+    second = (torch.arange(length, device="cuda") // 16 % 2) == 1
+    c.k.zero_()
+    c.k[second, :, 1:] = size
+    c.v.fill_(1.0)
+    c.v[second] = -1.0
+    c.append(c.k, c.v, [length])
+    q = torch.full((5, 2, D), small, device="cuda")
+    q[:, :, 0] = 1.0
+    q = q.bfloat16()
+    moved = 2.0 ** -17 * 127 * size / math.sqrt(D)
+    check_prefill(c, c.prefill(q, [5]), q, 5, weight=2.0 ** -11 + 2 * math.expm1(moved))
