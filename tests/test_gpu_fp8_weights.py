@@ -110,3 +110,32 @@ def test_small_query_elements(small):
     q = q.bfloat16()
     moved = 2.0 ** -17 * 127 * size / math.sqrt(D)
     check_prefill(c, c.prefill(q, [5]), q, 5, weight=2.0 ** -11 + 2 * math.expm1(moved))
+
+
+@pytest.mark.parametrize("sv", [1.0, 2.0 ** -40, 2.0 ** 5, 2.0 ** 60])
+@pytest.mark.parametrize("H,Hkv,n", [(4, 1, 20), (2, 2, 300)])
+def test_nan_values_on_any_scale(sv, H, Hkv, n):
+    """Values that are not finite, in pages that are fp16 operands, and bf16 ones, with others of the tile on
+    ordinary scales."""
+    length, at = 500, (3, 215, 350, 490)
+    c = Cache8(H, Hkv, [length], seed=9, fill=False)
+    v = c.v.float()
+    v[::32] *= sv               # a token of every other page
+    for i, p in enumerate(at):
+        v[p, 0, 5 + i] = float("nan") if i % 2 else float("inf")
+    c.append(c.k, v.bfloat16(), [length])
+    q = c.randn(n, H)
+    for window, sinks in ((0, 0), (100, 2), (140, 5), (9, 0)):
+        out = c.prefill(q, [n], window, sinks)
+        mask = seen(length, n, window, sinks)
+        spoiled = mask[:, list(at)].any(1)
+        G = H // Hkv
+        assert torch.isnan(out[spoiled, :G]).all() and not torch.isnan(out[~spoiled, :G]).any()
+        assert not torch.isnan(out[:, G:]).any()
+        keys, vals = c.entries(0)
+        for h in range(H):
+            o, mag, _ = attend(q[:, h].double(), keys[h // G], vals[h // G].nan_to_num(), mask)
+            err = (out[:, h].double() - o).abs()
+            fine = torch.all(err <= 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.0 ** -11) * mag, dim=1)
+            assert fine[~spoiled].all() and (h < G or fine.all())
+    assert K.kvq_get_status(c.h) == 0
