@@ -14,9 +14,12 @@
 // lengths, page id, rows) and their instructions.  Measured, 3 ragged prompts of 32767 tokens in all,
 // 8 KV heads: append 37 us (201 MB, 5.5 TB/s), reading 49152 positions 48 us (302 MB, 6.2 TB/s, 92 % of
 // the copy rate).  Append: pages that a call fills whole without the masks of part pages (5 us less), a
-// sequence's rows and lengths in one load (1.4 less).  Tried and slower: keys and values one after the other with 3 or 4 CTAs an SM in place of 2
-// (+1 to +2 us), 32 to 128 rows a CTA (+0.3 to +12), one warp that finds all of a CTA's units (+4).
-// A step of 64 sequences: 10 us for both, nearly all of it launches and that chain.
+// sequence's rows and lengths in one load (1.4 less).  Tried and slower: keys and values one after the
+// other with 3 or 4 CTAs an SM in place of 2 (+1 to +2 us), 32 to 128 rows a CTA (+0.3 to +12), one warp
+// that finds all of a CTA's units (+4).  At 4, 2 and 1 KV heads append 25, 22 and 15 us (4.0, 2.3 and 1.7
+// TB/s), reading 29, 22 and 18: a CTA's page or two of rows leave some of its eight warps without work.
+// A step of 64 sequences: append 5.3 us, reading the last pages 5.3, nearly all of it launches and the
+// chain, which for the append goes on with the page's scales and its older codes.
 #include <type_traits>
 
 #include "kvq_internal.cuh"

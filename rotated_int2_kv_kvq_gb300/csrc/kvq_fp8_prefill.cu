@@ -23,21 +23,24 @@
 //             from the scheduler's: next to this much shared memory L1 holds nearly nothing, and a
 //             spilled register is a round trip to L2.  Nothing is spilled.
 //
-// Measured (32 query, 8 KV heads): 4096 new tokens at 32K 1560 to 1600 us from one
+// Measured (32 query, 8 KV heads): 4096 new tokens at 32K 1535 to 1590 us from one
 // GPU to another, at the power limit (1320 TFLOP/s).  The products alone take 1086 at
 // the rate of a large library product, 1218 at the rate that one keeps up; the BF16 cache takes 1800,
 // the INT2 cache 1450.  A CTA's time for a key tile is 2.3 us: 1.35 of a row tile's softmax and 1.0
-// that it waits for scores behind the other row tile's, so the chain scores -> softmax -> weights ->
-// output bounds it, as it does the other caches'.  Spills and instructions count most: registers
-// 168 / 112 / 64 with 68 bytes of the softmax's spilled 1585, 168 / 120 / 56 with the issuing warp's
-// 1940, 160 / 128 / 64 2270.
-// A prompt of 8191 tokens with a window of 1024: 238 us for products of 68.  Ten key tiles an item where
+// that it waits for scores behind the other row tile's (timed with bf16 weights), so the chain scores ->
+// softmax -> weights -> output bounds it, as it does the other caches'.  Spills and instructions count
+// most.  With bf16 weights: registers 168 / 112 / 64 with 68 bytes of the softmax's spilled 1585,
+// 168 / 120 / 56 with the issuing warp's 1940, 160 / 128 / 64 2270.  With fp16 ones: their sum in two
+// chains, 96 bytes of the softmax's spilled, 2068; what bf16 tiles need unrolled beside it 1565 to 1595,
+// windows 245, drafts 67.  Where every tile is bf16: 1755, 251 and 66; values above 57344, or not finite,
+// a word at a time: 3500, 347 and 119.
+// A prompt of 8191 tokens with a window of 1024: 236 to 239 us for products of 68.  Ten key tiles an item where
 // eight hold its window, a third of them partly hidden (2.3 us of softmax for 1.4); and 9 us an item,
 // seven items a CTA, for its queries (3), the first scores (1.5), results (2.4) and the wait for the
 // other row tile's.  Queries by plain loads when the item begins: 273.
-// Eight drafts of five tokens at 8K: 64 us, 27 key tiles a CTA of 1.65 us each: with one row tile the
-// chain stage free -> values converted -> product, two stages deep, is the longest (the conversion left
-// out: 59; waiting for nothing but values: no change).
+// Eight drafts of five tokens at 8K: 64 us, 27 key tiles a CTA, at the pace of the producers' loads: two
+// pages a warp, a tile ahead (pages from L2 53; without the values' conversion 57, the keys' copies 59,
+// both 51; without the products 62, the softmax 61; without the four of them 48).
 #include "kvq_internal.cuh"
 
 namespace kvq {
