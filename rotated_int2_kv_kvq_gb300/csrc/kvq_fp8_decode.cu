@@ -18,7 +18,8 @@
 // HBM bounds it: every visible page is read once, by a bulk copy a page into a warp's own ring of
 // three; when a CTA's part of an item ends, the next part's ids and first two pages are under way while
 // the warps wait for one another and join.  Measured, 32 query and 8 KV heads: 16 x 32K 181 us (1.08
-// GB, 6.0 TB/s, 88 % of the copy rate; 187 with the parts one after the other); the SMs of the GPU's larger clusters get some 15 % less bandwidth each, so equal ranges end
+// GB, 6.0 TB/s, 88 % of the copy rate; 187 with the parts one after the other; 4, 2 and 1 KV heads 96, 53
+// and 32); the SMs of the GPU's larger clusters get some 15 % less bandwidth each, so equal ranges end
 // after 143 to 183 us, and what would even that out costs as much: 2 to 6 times as many CTAs 185 to
 // 193, ranges that shrink towards the end 181 to 200 (windows more), pages by tickets 186 to 213.
 // 64 windows of 4100 positions 86 us (462 MB, 5.4 TB/s; 89 likewise): 512 items, so two or three
@@ -103,7 +104,8 @@ struct Start {            // a CTA's range of the line of work
 // length (query, page ids and first records to wait for, the warps' states to join): in the line,
 // those units come before its first page.  (64 ragged sequences up to 16K: without 138 us, 8: 119,
 // 16: 108, 32: 98; 64 windows of 4100: 97, 93, 90, 88; 16 x 32K the same whatever.  Since parts
-// overlap: 32: 96.5 and 87.8, 40: 96.2 and 87.0, 48: 96.4 and 87.4.)
+// overlap: 32: 96.5 and 87.8, 40: 96.2 and 87.0, 48: 96.4 and 87.4; with 1, 2 and 4 KV heads, where 40
+// takes 22.9, 32.4, 53.4 and 21.4, 29.6, 48.5, 32 and 48 are within 2 % of it and 16 5 to 9 % slower.)
 __device__ __forceinline__ int item_units(const Seen& s) { return max(s.pages, 1) + kItemCost; }
 __device__ __forceinline__ void start_line(const Fp8DecodeArgs& a, Start* line, long long* red) {
   const int tid = threadIdx.x;
