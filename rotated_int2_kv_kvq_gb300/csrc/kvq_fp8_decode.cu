@@ -105,7 +105,7 @@ struct Start {            // a CTA's range of the line of work
 // those units come before its first page.  (64 ragged sequences up to 16K: without 138 us, 8: 119,
 // 16: 108, 32: 98; 64 windows of 4100: 97, 93, 90, 88; 16 x 32K the same whatever.  Since parts
 // overlap: 32: 96.5 and 87.8, 40: 96.2 and 87.0, 48: 96.4 and 87.4; with 1, 2 and 4 KV heads, where 40
-// takes 22.9, 32.4, 53.4 and 21.4, 29.6, 48.5, 32 and 48 are within 2 % of it and 16 5 to 9 % slower.)
+// takes 22.9, 32.4, 53.4 and 21.4, 29.6, 48.5, 32 and 48 are within 2 % of it, 16 is 2 to 9 % slower.)
 __device__ __forceinline__ int item_units(const Seen& s) { return max(s.pages, 1) + kItemCost; }
 __device__ __forceinline__ void start_line(const Fp8DecodeArgs& a, Start* line, long long* red) {
   const int tid = threadIdx.x;
